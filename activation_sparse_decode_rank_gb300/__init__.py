@@ -14,6 +14,8 @@ import os
 import subprocess
 import threading
 
+from . import serve
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
@@ -32,10 +34,15 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
               "-Xcompiler", "-fPIC", "-shared"]
 
 
+# Translation units: the FFN library and the serving operators (csrc/serve),
+# compiled side by side and linked into one libpi.so.
+_UNITS = ["pi_abi.cu", "serve/attend.cu", "serve/pages.cu", "serve/logprob.cu"]
+
+
 def _sources():
-    srcs = [os.path.join(_CSRC, f) for f in sorted(os.listdir(_CSRC))
-            if f.endswith((".cu", ".cuh"))]
-    return srcs + [os.path.join(_INCLUDE, "pi.h")]
+    srcs = [os.path.join(d, f) for d in (_CSRC, os.path.join(_CSRC, "serve"))
+            for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))]
+    return srcs + [os.path.join(_INCLUDE, "pi.h"), os.path.join(_INCLUDE, "pi_serve.h")]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -43,11 +50,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     stale = (not os.path.exists(_LIB)) or any(
         os.path.getmtime(p) > os.path.getmtime(_LIB) for p in _sources())
     if force or stale:
+        from concurrent.futures import ThreadPoolExecutor
         tmp = _LIB + f".tmp{os.getpid()}"
-        cmd = ["nvcc", *NVCC_FLAGS, "-o", tmp, os.path.join(_CSRC, "pi_abi.cu")]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-        subprocess.run(cmd, check=True)
+        flags = [f for f in NVCC_FLAGS if f != "-shared"] + (["-Xptxas=-v"] if verbose else [])
+        objs = [f"{tmp}.{i}.o" for i in range(len(_UNITS))]
+
+        def compile_unit(unit, obj):
+            subprocess.run(["nvcc", *flags, "-c", "-o", obj, os.path.join(_CSRC, unit)], check=True)
+
+        try:
+            with ThreadPoolExecutor(len(_UNITS)) as ex:
+                list(ex.map(compile_unit, _UNITS, objs))
+            subprocess.run(["nvcc", *NVCC_FLAGS, "-o", tmp, *objs], check=True)
+        finally:
+            for o in objs:
+                if os.path.exists(o):
+                    os.remove(o)
         os.replace(tmp, _LIB)
     return _LIB
 
@@ -125,6 +143,8 @@ SIGNATURES = {
     "pi_shard_layer": (ctypes.c_int, [_DESC, _W, _I32, _I32, _W, _P]),
     "pi_shard_reduce": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _P]),
 }
+# ... and of include/pi_serve.h, bound in serve.py.
+SIGNATURES.update(serve.SIGNATURES)
 
 
 def lib():
@@ -362,3 +382,9 @@ def pi_shard_layer(desc, src, G, g, dst, stream=None) -> int:
 def pi_shard_reduce(parts, G, batch, d, residual, y, stream=None) -> int:
     return lib().pi_shard_reduce(_ptr(parts), int(G), int(batch), int(d), _ptr(residual), _ptr(y),
                                  _stream(stream))
+
+
+from .serve import (  # noqa: E402
+    PI_CACHE_MAX_SLOTS, PI_F32, PI_TOPK_MAX, cache_workspace, logprob_workspace, make_cache_desc,
+    pi_cache_append, pi_cache_compact, pi_cache_copy, pi_cache_desc, pi_cache_fork,
+    pi_cache_workspace_size, pi_logprob_workspace_size, pi_paged_attention, pi_token_logprobs)
