@@ -91,9 +91,32 @@ pi_status launch(void (*k)(KArgs...), dim3 grid, unsigned block, size_t smem, pi
                                                                                  : PI_ERR_CUDA;
 }
 
-// Byte offsets of the regions of a cache workspace.
+// Raises a kernel's dynamic shared-memory limit on the current device, once.
+inline pi_status ensure_smem(const void* fn, int bytes) {
+  static std::mutex mu;
+  static std::unordered_map<const void*, unsigned long long> done;  // devices, as bits
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PI_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  unsigned long long& bits = done[fn];
+  if (dev < 64 && (bits >> dev & 1)) return PI_OK;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return PI_ERR_CUDA;
+  if (dev < 64) bits |= 1ull << dev;
+  return PI_OK;
+}
+
+constexpr int kAttendGrid = 512;  // most thread blocks of the attention
+
+// Two tiles of eight query heads per unit where the group has them and a
+// head's accumulators leave the registers for it.
+inline bool att_two_tiles(int head_dim, int group) { return group > 8 && head_dim <= 128; }
+
+// Byte offsets of the regions of a cache workspace.  `arrived` is zero
+// between calls and has one place and size for every cache, so that a
+// workspace may serve calls of several shapes; the rest is scratch.
 struct CacheWs {
-  size_t blocks, owner, free_list, total;
+  size_t arrived, part, blocks, owner, free_list, total;
 };
 
 constexpr int kScanPages = 1024;  // pages of one block of the page scans
@@ -107,11 +130,16 @@ inline CacheWs cache_ws(const pi_cache_desc& C, int slots, int heads) {
     return o;
   };
   (void)slots;
-  (void)heads;
+  w.arrived = take(4 * kAttendGrid);
+  const size_t scratch = off;
+  const int rows = heads ? (att_two_tiles(C.head_dim, heads / C.kv_heads) ? 16 : 8) : 0;
+  w.part = take((size_t)kAttendGrid * 2 * rows * (C.head_dim + 4) * 4);
+  const size_t end = off;
+  off = scratch;  // the page calls use the same bytes
   w.blocks = take(4 * (((size_t)C.pages + kScanPages - 1) / kScanPages + 1));
   w.owner = take(4 * (size_t)C.pages);
   w.free_list = take(4 * (size_t)C.pages);
-  w.total = off;
+  w.total = off > end ? off : end;
   return w;
 }
 
