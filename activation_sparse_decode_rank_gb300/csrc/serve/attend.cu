@@ -25,17 +25,21 @@ namespace pis {
 // third part.  fp16's narrow exponent range is met by exact powers of two:
 // q is scaled to [2^13, 2^14) per head, p by 2^14.
 //
-// Work split.  All visible tokens of all (slot, kv head, group of heads)
-// units, in blocks of 64 tokens, form one line; each thread block takes an
-// equal contiguous share of it, found from the lengths on the device, so
-// ragged lengths balance and nothing depends on the host knowing them.  A
-// unit that spans thread blocks leaves partial results; the last of its
-// blocks to arrive joins them in block order (no waiting; order fixed).
+// Work split.  The tiles of all (slot, kv head, head tile) units, each unit
+// preceded by kUnitCost positions that stand for its fixed cost, form one
+// line; each warp takes an equal contiguous share of it, found from the
+// lengths on the device, so ragged lengths balance and nothing depends on the
+// host knowing them.  A unit inside one warp's share is written from that
+// warp's registers.  A unit that spans warps leaves partial results, joined
+// once at the end: within a thread block through shared memory, across
+// thread blocks by the last of them to arrive, in block order (no waiting;
+// the order of the sums is fixed).
 //
-// Data flow.  A warp owns every fourth 16-token tile of its block's share
-// and streams it through its own ring of cp.async stages (no block-wide
-// barrier per tile); page numbers are fetched one tile ahead of their use;
-// rows outside the visible set are never read (zero-filled).
+// Data flow.  A warp streams its tiles through its own ring of cp.async
+// stages, without any block-wide barrier until the end; page numbers are
+// fetched one tile ahead of their use; rows outside the visible set are
+// never read (zero-filled).  Head dimensions below 64, 128 or 256 are padded
+// with zeros in shared memory only.
 struct AttendArgs {
   const float *q, *k_new, *v_new;
   const int *table, *len;
@@ -43,24 +47,27 @@ struct AttendArgs {
   float *y, *lse;
   int* status;
   int* arrived;   // [kAttendGrid] arrivals at the units that begin in a block
-  float* part;    // [grid][2][heads of a unit][head_dim + 4]: o, m, l of split units
+  float* part;    // [grid][2][heads of a unit][head_dim + 4]: o, m, l of units split over blocks
+  float* wpart;   // [4 grid][16][padded dim]: warps' first parts where shared memory lacks the room
   int slots, heads, kv_heads, group, head_dim, page_tokens, pages, max_pages, window, sinks;
   int tiles;      // head tiles per kv head: ceil(group / (8 MT))
-  int min_blocks; // least 64-token blocks of a thread block
+  int page_shift; // log2(page_tokens), or -1
   float scale;    // scale log2(e)
 };
 
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
+constexpr int kUnitCost = 2;  // a unit's start and end, in tiles
+constexpr int kMinTiles = 4;  // a warp's least share, in tiles
 
 // Stages of a warp's ring: two thread blocks per SM (one at 256 dims).
 template <int DP>
 __host__ __device__ constexpr int att_stages() {
   return DP == 64 ? 6 : 3;
 }
-template <int DP>
+template <int DP, int MT>
 __host__ __device__ constexpr int att_smem() {
-  return kAttWarps * att_stages<DP>() * 16 * DP * 4 + kAttWarps * 8 * DP * 4;
+  return kAttWarps * att_stages<DP>() * 16 * DP * 4 + (MT == 1 ? kAttWarps * 8 * DP * 4 : 0);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -70,6 +77,10 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -104,6 +115,22 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c = a b
+template <int DT>
+__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (DT == 0)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -141,42 +168,68 @@ __device__ __forceinline__ Seen seen_of(const AttendArgs& a, int slot) {
   v.tiles = v.n ? v.first_tiles + (int)(((unsigned)v.n + 15u) >> 4) - (v.tail >> 4) : 0;
   return v;
 }
-__device__ __forceinline__ int blocks_of(int tiles) {
-  return (tiles + kAttWarps - 1) / kAttWarps;
-}
-
-// A position on the line of 64-token blocks.
+// A tile on the line.
 struct Cursor {
-  int slot, unit, blk, blocks;  // unit: kv head x head tiles
+  long long pos;
+  int slot, g, ht, tile;  // kv head, its head tile, tile of the unit
   Seen v;
-  __device__ __forceinline__ void enter(const AttendArgs& a, int s) {
-    slot = s;
-    v = seen_of(a, s);
-    blocks = blocks_of(v.tiles);
-  }
   __device__ __forceinline__ void advance(const AttendArgs& a) {
-    if (++blk < blocks) return;
-    blk = 0;
-    if (++unit < a.kv_heads * a.tiles) return;
-    unit = 0;
+    ++pos;
+    if (++tile < v.tiles) return;
+    tile = 0;
+    pos += kUnitCost;
+    if (++ht < a.tiles) return;
+    ht = 0;
+    if (++g < a.kv_heads) return;
+    g = 0;
     do {
-      if (slot + 1 >= a.slots) return;  // past the end: not used any more
-      enter(a, slot + 1);
-    } while (blocks == 0);
+      if (++slot >= a.slots) {  // past the end: not used any more
+        pos = 1ll << 62;
+        return;
+      }
+      v = seen_of(a, slot);
+    } while (v.tiles == 0);
   }
-  // first token of the warp's tile, and the tile's visible rows [r0, r1)
-  __device__ __forceinline__ int tile(int warp, int& r0, int& r1) const {
-    const int i = blk * kAttWarps + warp;
-    if (i < v.first_tiles) {
+  // the tile's first token, and its visible rows as bits
+  __device__ __forceinline__ int rows_of(uint32_t& rows) const {
+    int t, r0, r1;
+    if (tile < v.first_tiles) {
+      t = 16 * tile;
       r0 = 0;
-      r1 = min(16, v.first - 16 * i);
-      return 16 * i;
+      r1 = v.first - t;
+    } else {
+      t = ((v.tail >> 4) + tile - v.first_tiles) << 4;
+      r0 = v.tail - t;
+      r1 = v.n - t;
     }
-    const int t = ((v.tail >> 4) + i - v.first_tiles) << 4;
-    r0 = max(0, v.tail - t);
-    r1 = i < v.tiles ? min(16, v.n - t) : 0;
+    rows = r1 >= 16 ? 0xffffu : 0xffffu >> (16 - r1);
+    if (r0 > 0) rows &= 0xffffu << r0;
     return t;
   }
+};
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void add_scaled(float4& sum, const float4& x, float f) {
+  sum.x = fmaf(x.x, f, sum.x);
+  sum.y = fmaf(x.y, f, sum.y);
+  sum.z = fmaf(x.z, f, sum.z);
+  sum.w = fmaf(x.w, f, sum.w);
+}
+
+// Four elements of an output row from its joined parts (no visible token: 0).
+__device__ __forceinline__ void finish(const AttendArgs& a, size_t row, int d, const float4& sum,
+                                       float top, float lsum, float shift) {
+  const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
+  *reinterpret_cast<float4*>(a.y + row * a.head_dim + d) =
+      make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+  if (d == 0 && a.lse) a.lse[row] = (top + (log2f(lsum) - shift)) * kLn2;
+}
+
+// A warp's part of a unit that it shares with other warps.
+struct Piece {
+  long long at;  // line position of the unit's first tile, -1: none
+  int slot, g, ht, tiles;
 };
 
 template <int DT, int DP, int MT>
@@ -186,16 +239,22 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   constexpr int kRow = DP * 2;             // bytes of a staged row
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
   constexpr float kShift = DT == 0 ? 14.f : 0.f;  // weights carry 2^kShift
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[kAttWarps];
-  __shared__ int s_slot0, s_last;
-  __shared__ long long s_before;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ long long s_scan[kAttWarps], s_before[kAttWarps];
+  __shared__ int s_slot[kAttWarps], s_last;
   __shared__ uint32_t s_mask[kAttWarps][S];
-  __shared__ float s_m[kAttWarps][8], s_l[kAttWarps][8];
+  __shared__ float s_m[kAttWarps][2][8 * MT], s_l[kAttWarps][2][8 * MT];
+  __shared__ Piece s_piece[kAttWarps][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = a.head_dim, P = a.page_tokens;
   const int units = a.kv_heads * a.tiles;
-  float* part = reinterpret_cast<float*>(smem + kAttWarps * S * 2 * kTile);
+  // where a warp leaves its first and its last part
+  auto piece_data = [&](int w, int k) -> float* {
+    if (k) return reinterpret_cast<float*>(smem + w * S * 2 * kTile);
+    if (MT == 1) return reinterpret_cast<float*>(smem + kAttWarps * S * 2 * kTile) + w * 8 * DP;
+    return a.wpart + ((size_t)blockIdx.x * kAttWarps + w) * (8 * MT) * DP;
+  };
+  if (lane < 2) s_piece[warp][lane].at = -1;
   pdl_enter();
 
   // Empty slots, and lengths out of range.
@@ -208,13 +267,19 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       for (int e = tid; e < a.heads; e += kAttThreads) a.lse[(size_t)s * a.heads + e] = -INFINITY;
   }
 
-  // This block's share of the line.  Thread t holds the slots [t k, t k + k).
-  long long share0, share1, total;
+  // The warps' shares of the line.  Thread t sums the slots [t k, t k + k).
+  long long total, share0, share1;
   int grid;
+  auto unit_len = [](int tiles) { return tiles ? tiles + kUnitCost : 0; };
   {
     const int k = (a.slots + kAttThreads - 1) / kAttThreads;
     long long mine = 0;
-    for (int s = tid * k; s < min(a.slots, tid * k + k); ++s) mine += blocks_of(seen_of(a, s).tiles);
+    int used = 0;
+    for (int s = tid * k; s < min(a.slots, tid * k + k); ++s) {
+      const int n = unit_len(seen_of(a, s).tiles);
+      mine += n;
+      used += n > 0;
+    }
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -222,7 +287,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       if (lane >= o) upto += w;
     }
     if (lane == 31) s_scan[warp] = upto;
-    __syncthreads();
+    used = __syncthreads_count(used > 0);  // at most the used slots; exact for up to 128
     long long before = upto - mine;
     total = 0;
     for (int w = 0; w < kAttWarps; ++w) {
@@ -230,113 +295,149 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       total += s_scan[w];
     }
     total *= units;
-    const long long most = (total + a.min_blocks - 1) / a.min_blocks;
-    grid = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
+    if (total == 0) return;
+    long long most = (total + kAttWarps * kMinTiles - 1) / (kAttWarps * kMinTiles);
+    if (most < (long long)gridDim.x) {
+      // few tiles: a multiple of the units, so that equal units begin at a
+      // block's start and need no join across blocks
+      const long long per = (long long)used * units, up = (most + per - 1) / per * per;
+      if (up <= (long long)gridDim.x) most = up;
+      grid = (int)most;
+    } else {
+      grid = gridDim.x;
+    }
+    // no empty share between two warps of one unit
+    if (grid > 1 && total < (long long)grid * kAttWarps) grid = max(1, (int)(total / kAttWarps));
     if ((int)blockIdx.x >= grid) return;
-    share0 = blockIdx.x * total / grid;
-    share1 = (blockIdx.x + 1) * total / grid;
-    // the thread whose slots hold share0 looks for it there
-    long long at = before * units;
-    if (at <= share0 && share0 < at + mine * units) {
-      for (int s = tid * k;; ++s) {
-        const long long n = (long long)blocks_of(seen_of(a, s).tiles) * units;
-        if (share0 < at + n) {
-          s_slot0 = s;
-          s_before = at;
-          break;
+    const long long warps = (long long)grid * kAttWarps;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      // the thread whose slots hold the share's first position looks for it
+      const long long p = ((long long)blockIdx.x * kAttWarps + w) * total / warps;
+      long long at = before * units;
+      if (at <= p && p < at + mine * units) {
+        for (int s = tid * k;; ++s) {
+          const long long n = (long long)unit_len(seen_of(a, s).tiles) * units;
+          if (p < at + n) {
+            s_slot[w] = s;
+            s_before[w] = at;
+            break;
+          }
+          at += n;
         }
-        at += n;
       }
     }
+    const long long me = (long long)blockIdx.x * kAttWarps + warp;
+    share0 = me * total / warps;
+    share1 = (me + 1) * total / warps;
     __syncthreads();
   }
-  const int steps = (int)(share1 - share0);
-  Cursor cc;  // the block being computed
-  cc.enter(a, s_slot0);
-  cc.unit = (int)((share0 - s_before) / cc.blocks);
-  cc.blk = (int)((share0 - s_before) % cc.blocks);
-  long long unit_at = share0 - cc.blk;  // where the unit begins on the line
-  Cursor lc = cc;  // the block being loaded
+  Cursor cc;  // the tile being computed
+  cc.slot = s_slot[warp];
+  cc.v = seen_of(a, cc.slot);
+  {
+    const int len = unit_len(cc.v.tiles);
+    const long long off = share0 - s_before[warp];
+    const int unit = (int)(off / len), r = (int)(off - (long long)unit * len);
+    cc.g = unit / a.tiles;
+    cc.ht = unit % a.tiles;
+    cc.tile = max(0, r - kUnitCost);
+    cc.pos = share0 + max(0, kUnitCost - r);
+  }
+  Cursor lc = cc;  // the tile being loaded
 
   const uint32_t ring = smem_u32(smem) + warp * S * 2 * kTile;
-  const int pieces = D >> 3, ksteps = (D + 15) >> 4;
+  const int pieces = D >> 3;
   const bool one_page = (P & 15) == 0;  // a tile lies in one page
   const size_t v_off = (size_t)a.kv_heads * P * D;
 
-  // Page number of the tile that lc points at (lane r: of its row r).
-  auto fetch = [&]() -> int {
-    int r0, r1;
-    const int t = lc.tile(warp, r0, r1) + (one_page ? 0 : lane & 15);
-    const bool use = one_page ? r1 > 0 : (lane & 15) >= r0 && (lane & 15) < r1;
-    return use ? __ldg(a.table + (size_t)lc.slot * a.max_pages + t / P) : -2;
+  // The tile that lc points at: visible rows, first token (row 0 of lane r's
+  // row where a tile may span pages) as a place in its page, page number.
+  uint32_t next_rows = 0;
+  int next_t = 0, next_row = 0, next_page = 0;
+  auto fetch = [&]() {
+    next_t = lc.rows_of(next_rows);
+    const int t = next_t + (one_page ? 0 : lane & 15);
+    const int j = a.page_shift >= 0 ? t >> a.page_shift : t / P;
+    next_row = t - j * P;
+    const bool use = one_page ? next_rows != 0 : (next_rows >> (lane & 15) & 1u) != 0;
+    next_page = use ? __ldg(a.table + (size_t)lc.slot * a.max_pages + j) : -2;
   };
-  // Sends the tile at lc into a stage.
-  auto issue = [&](int stage, int page) {
-    int r0, r1;
-    const int t = lc.tile(warp, r0, r1);
-    const int g = lc.unit / a.tiles;
-    const bool ok = (unsigned)page < (unsigned)a.pages;
-    if (!ok && page != -2) set_status(a.status, PI_ERR_INDEX);
-    uint32_t mask = 0;  // rows to read: visible, and in a page
-    if (r1 > r0) mask = (0xffffu >> (16 - r1)) & (0xffffu << r0);
+  // Sends that tile into a stage.  A lane's piece of row r = r_lane + i k (k
+  // rows per instruction) goes to piece ^ (r & 7): r_lane < k, so the xor
+  // splits into a lane's part and a constant.
+  constexpr int kRows = 32 / kPieces;  // 4, 2, 1 rows per instruction
+  const uint32_t lane_dst = (lane / kPieces) * kRow + (((lane % kPieces) ^ (lane / kPieces)) << 4);
+  auto issue = [&](int stage) {
+    const bool ok = (unsigned)next_page < (unsigned)a.pages;
+    if (!ok && next_page != -2) set_status(a.status, PI_ERR_INDEX);
+    uint32_t rows = next_rows;  // rows to read: visible, and in a page
     if (one_page)
-      mask = ok ? mask : 0;
+      rows = ok ? rows : 0;
     else
-      mask &= __ballot_sync(~0u, ok);
-    if (lane == 0) s_mask[warp][stage] = mask;
+      rows &= __ballot_sync(~0u, ok);
+    if (lane == 0) s_mask[warp][stage] = rows;
     // the new token's row comes from k_new / v_new when the tile is used
-    if (a.k_new && t < lc.v.n && lc.v.n - t <= 16) mask &= ~(1u << (lc.v.n - 1 - t));
-    const long long row =
-        ok ? ((long long)page * 2 * a.kv_heads + g) * P + (one_page ? t : t + (lane & 15)) % P : 0;
-    const uint32_t k0 = ring + stage * 2 * kTile;
+    if (a.k_new && next_t < lc.v.n && lc.v.n - next_t <= 16) rows &= ~(1u << (lc.v.n - 1 - next_t));
+    const long long row = ok ? ((long long)next_page * 2 * a.kv_heads + lc.g) * P + next_row : 0;
+    const uint32_t dst = ring + stage * 2 * kTile + lane_dst;
     const int pc = lane % kPieces;
+    if (one_page && rows == 0xffffu && D == DP) {  // 16 whole rows side by side
+      const uint16_t* p = a.pool + row * DP + lane * 8;
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        const uint32_t to = (dst ^ (((i * kRows) & 7) << 4)) + i * kRows * kRow;
+        cp16(to, p + i * 256);
+        cp16(to + kTile, p + v_off + i * 256);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
-      const int r = lane / kPieces + i * (32 / kPieces);
+      const int r = lane / kPieces + i * kRows;
       long long src = row + r;
       if (!one_page) src = __shfl_sync(~0u, row, r);
-      if (pc < 2 * ksteps) {
-        const bool take = (mask >> r & 1u) && pc < pieces;
+      if (pc < pieces) {
+        const bool take = rows >> r & 1u;
         const uint16_t* p = a.pool + (take ? (size_t)src * D + 8 * pc : 0);
-        const uint32_t dst = k0 + r * kRow + ((pc ^ (r & 7)) << 4);
-        cp16(dst, p, take ? 16 : 0);
-        cp16(dst + kTile, p + (take ? v_off : 0), take ? 16 : 0);
+        const uint32_t to = (dst ^ (((i * kRows) & 7) << 4)) + i * kRows * kRow;
+        cp16(to, p, take ? 16 : 0);
+        cp16(to + kTile, p + (take ? v_off : 0), take ? 16 : 0);
       }
     }
   };
 
-  int issued = 0;
-  int page = steps > 0 ? fetch() : -2;
+  if (D < DP)  // the padding: zeros that no copy overwrites
+    for (int e = lane; e < S * 2 * kTile / 16; e += 32)
+      *reinterpret_cast<uint4*>(smem + warp * S * 2 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+  __syncwarp();
+  if (lc.pos < share1) fetch();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) {
-    if (issued < steps) {
-      issue(i, page);
-      if (++issued < steps) {
-        lc.advance(a);
-        page = fetch();
-      }
+    if (lc.pos < share1) {
+      issue(i);
+      lc.advance(a);
+      if (lc.pos < share1) fetch();
     }
     cp_commit();
   }
 
   uint32_t qf[MT][DP / 16][4], qf2[DT == 1 ? MT : 1][DP / 16][2];
   float o[MT][DP / 8][2], m[MT], l[MT], unit_scale[MT];
-  int seg0 = cc.blk;  // the segment's first block in its unit
   bool fresh = true;
-
-  for (int i = 0; i < steps; ++i) {
+  int stage = S - 1;
+  while (cc.pos < share1) {
+    stage = stage == S - 1 ? 0 : stage + 1;
     cp_wait<S - 2>();
     __syncwarp();
-    if (issued < steps) {
-      issue((i + S - 1) % S, page);
-      if (++issued < steps) {
-        lc.advance(a);
-        page = fetch();
-      }
+    if (lc.pos < share1) {
+      issue(stage == 0 ? S - 1 : stage - 1);
+      lc.advance(a);
+      if (lc.pos < share1) fetch();
     }
     cp_commit();
 
-    const int g = cc.unit / a.tiles, ht = cc.unit % a.tiles;
+    const int g = cc.g, ht = cc.ht;
     if (fresh) {  // a unit begins: its query heads
       fresh = false;
 #pragma unroll
@@ -377,12 +478,11 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
     }
 
-    const int stage = i % S;
     const uint32_t k0 = ring + stage * 2 * kTile, v0 = k0 + kTile;
     const uint32_t mask = s_mask[warp][stage];
     if (a.k_new) {
-      int r0, r1;
-      const int t = cc.tile(warp, r0, r1);
+      uint32_t rows;
+      const int t = cc.rows_of(rows);
       const int r = cc.v.n - 1 - t;
       if (r >= 0 && r < 16 && (mask >> r & 1u)) {
         // the new token: rounded into the stage, and into its page once
@@ -405,44 +505,47 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
 
     if (mask) {
       // scores of 16 tokens
-      float sc[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+      float sc[MT][2][2][4];  // even and odd steps: shorter chains
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), pc = (lane >> 3) & 1;
+        const uint32_t at = k0 + r * kRow + ((pc ^ (r & 7)) << 4);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
-          if (ks >= ksteps) break;
           uint32_t b[4];
-          ldsm4(b, k0 + r * kRow + (((2 * ks + pc) ^ (r & 7)) << 4));
+          ldsm4(b, at ^ (ks << 5));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma<DT>(sc[mt][0], qf[mt][ks], b[0], b[1]);
-            mma<DT>(sc[mt][1], qf[mt][ks], b[2], b[3]);
-            if (DT == 1) {
-              const uint32_t q2[4] = {0u, qf2[mt][ks][0], 0u, qf2[mt][ks][1]};
-              mma<DT>(sc[mt][0], q2, b[0], b[1]);
-              mma<DT>(sc[mt][1], q2, b[2], b[3]);
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              float(&c)[4] = sc[mt][nt][ks & 1];
+              if (ks < 2)
+                mma0<DT>(c, qf[mt][ks], b[2 * nt], b[2 * nt + 1]);
+              else
+                mma<DT>(c, qf[mt][ks], b[2 * nt], b[2 * nt + 1]);
+              if (DT == 1) {
+                const uint32_t q2[4] = {0u, qf2[mt][ks][0], 0u, qf2[mt][ks][1]};
+                mma<DT>(c, q2, b[2 * nt], b[2 * nt + 1]);
+              }
             }
-          }
         }
       }
       uint32_t pf[MT][4], pf2[MT][2];
       float corr[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float s[4], mx = -INFINITY;
+        float s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int tok = (e >> 1) * 8 + 2 * (lane & 3) + (e & 1);
-          s[e] = sc[mt][e >> 1][e & 1] + sc[mt][e >> 1][2 + (e & 1)];
-          if (!(mask >> tok & 1u)) s[e] = -INFINITY;
-          else mx = fmaxf(mx, s[e] * unit_scale[mt]);
+          const float(&c)[2][4] = sc[mt][e >> 1];
+          s[e] = (c[0][e & 1] + c[1][e & 1]) + (c[0][2 + (e & 1)] + c[1][2 + (e & 1)]);
         }
+        const uint32_t mine = mask >> (2 * (lane & 3));  // rows of s: bits 0, 1, 8, 9
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = mask == 0xffffu || (mine >> ((e >> 1) * 8 + (e & 1)) & 1u) ? s[e] * unit_scale[mt]
+                                                                            : -INFINITY;
+        float mx = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
         const float mn = fmaxf(m[mt], mx);
@@ -452,8 +555,8 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int tok = (e >> 1) * 8 + 2 * (lane & 3) + (e & 1);
-          p[e] = mask >> tok & 1u ? ex2(fmaf(s[e], unit_scale[mt], kShift - ref)) : 0.f;
+          p[e] = ex2(fmaf(s[e], unit_scale[mt], kShift - ref));
+          if (w[e] == -INFINITY) p[e] = 0.f;
         }
         l[mt] = fmaf(l[mt], corr[mt], (p[0] + p[1]) + (p[2] + p[3]));
         split2<DT>(p[0], p[1], pf[mt][0], pf[mt][1], pf2[mt][0]);
@@ -461,17 +564,17 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
       // weighted values; each tile's product is rounded once into the fp32 sums
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), pc = lane >> 4;
+      const uint32_t at = v0 + r * kRow + ((pc ^ (r & 7)) << 4);
 #pragma unroll
       for (int jj = 0; jj < DP / 16; ++jj) {
-        if (jj >= ksteps) break;
         uint32_t b[4];
-        ldsm4t(b, v0 + r * kRow + (((2 * jj + pc) ^ (r & 7)) << 4));
+        ldsm4t(b, at ^ (jj << 5));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma<DT>(c, pf[mt], b[2 * u], b[2 * u + 1]);
+            float c[4];
+            mma0<DT>(c, pf[mt], b[2 * u], b[2 * u + 1]);
             if (DT == 1) {
               const uint32_t p2[4] = {0u, pf2[mt][0], 0u, pf2[mt][1]};
               mma<DT>(c, p2, b[2 * u], b[2 * u + 1]);
@@ -482,117 +585,120 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
     }
 
-    const bool ends = cc.blk + 1 == cc.blocks;
-    if (ends || i + 1 == steps) {  // the segment ends: join the warps
-      const bool whole = ends && seg0 == 0;
-      const int rows = min(8 * MT, a.group - ht * 8 * MT);  // query heads of the unit
-      const int vecs = D >> 2;
-      const int prow = D + 4;
-      // slot 0: the block's share begins in this unit
-      float* mine = a.part + ((size_t)blockIdx.x * 2 + (unit_at <= share0 ? 0 : 1)) * (8 * MT) * prow;
-      const size_t out0 = (size_t)cc.slot * a.heads + g * a.group + ht * 8 * MT;
+    const long long at = cc.pos - cc.tile;  // the unit on the line: [at, at + tiles)
+    const bool ends = cc.tile + 1 == cc.v.tiles;
+    if (ends || cc.pos + 1 == share1) {
+      const bool begins = at >= share0;
+      const int h = lane >> 2;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int live = min(8, rows - 8 * mt);
-        if (live <= 0) break;
-        const int h = lane >> 2;
+        const int hr = 8 * mt + h, hq = ht * 8 * MT + hr;  // head of the unit, of the kv head
         float lt = l[mt];
         lt += __shfl_xor_sync(~0u, lt, 1);
         lt += __shfl_xor_sync(~0u, lt, 2);
-        __syncthreads();  // the previous join has been read
-        if ((lane & 3) == 0) {
-          s_m[warp][h] = m[mt];
-          s_l[warp][h] = lt;
-        }
-        if (h < live) {
+        if (begins && ends) {
+          const size_t row = (size_t)cc.slot * a.heads + g * a.group + hq;
+          if (hq < a.group) {
+            const float inv = lt > 0.f ? 1.f / lt : lt == lt ? 0.f : lt;
+            float* y = a.y + row * D + 2 * (lane & 3);
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j)
-            *reinterpret_cast<float2*>(part + (warp * 8 + h) * DP + ((j ^ h) << 3) + 2 * (lane & 3)) =
-                make_float2(o[mt][j][0], o[mt][j][1]);
-        }
-        __syncthreads();
-        for (int e = tid; e < live * vecs; e += kAttThreads) {
-          const int hh = e / vecs, d = 4 * (e % vecs);
-          float top = -INFINITY;
+            for (int j = 0; j < DP / 8; ++j)
+              if (8 * j < D)
+                *reinterpret_cast<float2*>(y + 8 * j) = make_float2(o[mt][j][0] * inv, o[mt][j][1] * inv);
+            if ((lane & 3) == 0 && a.lse) a.lse[row] = (m[mt] + (log2f(lt) - kShift)) * kLn2;
+          }
+        } else {
+          const int k = begins ? 1 : 0;
+          if (k) {  // into the ring, now idle
+            cp_wait<0>();
+            __syncwarp();
+          }
+          if (hq < a.group) {
+            float* data = piece_data(warp, k) + hr * DP + 2 * (lane & 3);
 #pragma unroll
-          for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_m[w][hh]);
-          const float ref = top == -INFINITY ? 0.f : top;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          float lsum = 0.f;
-#pragma unroll
-          for (int w = 0; w < kAttWarps; ++w) {
-            const float f = ex2(s_m[w][hh] - ref);
-            const float4 x = *reinterpret_cast<const float4*>(
-                part + (w * 8 + hh) * DP + (((d >> 3) ^ hh) << 3) + (d & 7));
-            sum.x = fmaf(x.x, f, sum.x);
-            sum.y = fmaf(x.y, f, sum.y);
-            sum.z = fmaf(x.z, f, sum.z);
-            sum.w = fmaf(x.w, f, sum.w);
-            lsum = fmaf(s_l[w][hh], f, lsum);
+            for (int j = 0; j < DP / 8; ++j)
+              *reinterpret_cast<float2*>(data + ((j ^ h) << 3)) = make_float2(o[mt][j][0], o[mt][j][1]);
           }
-          const int hr = 8 * mt + hh;
-          if (whole) {
-            const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
-            *reinterpret_cast<float4*>(a.y + (out0 + hr) * D + d) =
-                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-            if (d == 0 && a.lse)
-              a.lse[out0 + hr] = (top + (log2f(lsum) - kShift)) * 0.6931471805599453f;
-          } else {
-            float* pr = mine + (size_t)hr * prow;
-            __stcg(reinterpret_cast<float4*>(pr + d), sum);
-            if (d == 0) {
-              __stcg(pr + D, top);
-              __stcg(pr + D + 1, lsum);
-            }
+          if ((lane & 3) == 0) {
+            s_m[warp][k][hr] = m[mt];
+            s_l[warp][k][hr] = lt;
           }
-        }
-      }
-      if (!whole) {
-        // the unit's blocks on the line, and the thread blocks that hold them
-        const long long end = unit_at + cc.blocks;
-        const int b0 = (int)(((unit_at + 1) * grid - 1) / total);
-        const int b1 = (int)((end * grid - 1) / total);
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) s_last = atomicAdd(a.arrived + b0, 1) == b1 - b0;
-        __syncthreads();
-        if (s_last) {
-          __threadfence();
-          if (tid == 0) a.arrived[b0] = 0;
-          const int slot0 = unit_at <= b0 * total / grid ? 0 : 1;
-          for (int e = tid; e < rows * vecs; e += kAttThreads) {
-            const int hr = e / vecs, d = 4 * (e % vecs);
-            auto at = [&](int b) {
-              return a.part + (((size_t)b * 2 + (b == b0 ? slot0 : 0)) * (8 * MT) + hr) * prow;
-            };
-            float top = -INFINITY;
-            for (int b = b0; b <= b1; ++b) top = fmaxf(top, __ldcg(at(b) + D));
-            const float ref = top == -INFINITY ? 0.f : top;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            float lsum = 0.f;
-            for (int b = b0; b <= b1; ++b) {
-              const float* pr = at(b);
-              const float f = ex2(__ldcg(pr + D) - ref);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(pr + d));
-              sum.x = fmaf(x.x, f, sum.x);
-              sum.y = fmaf(x.y, f, sum.y);
-              sum.z = fmaf(x.z, f, sum.z);
-              sum.w = fmaf(x.w, f, sum.w);
-              lsum = fmaf(__ldcg(pr + D + 1), f, lsum);
-            }
-            const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
-            *reinterpret_cast<float4*>(a.y + (out0 + hr) * D + d) =
-                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-            if (d == 0 && a.lse)
-              a.lse[out0 + hr] = (top + (log2f(lsum) - kShift)) * 0.6931471805599453f;
-          }
+          if (lane == 0) s_piece[warp][k] = Piece{at, cc.slot, g, ht, cc.v.tiles};
         }
       }
       fresh = true;
-      seg0 = 0;
-      if (ends) unit_at += cc.blocks;
     }
-    if (i + 1 < steps) cc.advance(a);
+    cc.advance(a);
+  }
+
+  // Units shared by warps.  A unit's warps within the block: the one that
+  // begins it (piece 1) or the block's first (piece 0), then the followers'
+  // pieces 0.
+  cp_wait<0>();
+  __syncthreads();
+  const long long warps = (long long)grid * kAttWarps;
+  const int vecs = D >> 2, prow = D + 4;
+  for (int k = -1; k < kAttWarps; ++k) {
+    const int w0 = max(k, 0);
+    const Piece pc = s_piece[w0][k < 0 ? 0 : 1];
+    if (pc.at < 0) continue;
+    int w1 = w0 + 1;
+    while (w1 < kAttWarps && s_piece[w1][0].at == pc.at) ++w1;
+    const int b0 = (int)(((pc.at + 1) * warps - 1) / total) / kAttWarps;
+    const int b1 = (int)(((pc.at + pc.tiles) * warps - 1) / total) / kAttWarps;
+    const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
+    const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
+    float* mine = a.part + ((size_t)blockIdx.x * 2 + (b0 == (int)blockIdx.x)) * (8 * MT) * prow;
+    for (int e = tid; e < rows * vecs; e += kAttThreads) {
+      const int hr = e / vecs, d = 4 * (e % vecs);
+      float top = -INFINITY;
+      for (int w = w0; w < w1; ++w) top = fmaxf(top, s_m[w][w == k][hr]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float lsum = 0.f;
+      for (int w = w0; w < w1; ++w) {
+        const float f = ex2(s_m[w][w == k][hr] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(
+            piece_data(w, w == k) + hr * DP + (((d >> 3) ^ (hr & 7)) << 3) + (d & 7));
+        add_scaled(sum, x, f);
+        lsum = fmaf(s_l[w][w == k][hr], f, lsum);
+      }
+      if (b0 == b1) {
+        finish(a, out0 + hr, d, sum, top, lsum, kShift);
+      } else {
+        float* pr = mine + (size_t)hr * prow;
+        __stcg(reinterpret_cast<float4*>(pr + d), sum);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(pr + D), make_float2(top, lsum));
+      }
+    }
+    if (b0 == b1) continue;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(a.arrived + b0, 1) == b1 - b0;
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      if (tid == 0) a.arrived[b0] = 0;
+      for (int e = tid; e < rows * vecs; e += kAttThreads) {
+        const int hr = e / vecs, d = 4 * (e % vecs);
+        auto from = [&](int b) { return a.part + (((size_t)b * 2 + (b == b0)) * (8 * MT) + hr) * prow; };
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int b = b0; b <= b1; ++b) top = fmaxf(top, __ldcg(from(b) + D));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lsum = 0.f;
+#pragma unroll 4
+        for (int b = b0; b <= b1; ++b) {
+          const float* pr = from(b);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(pr + D));
+          const float f = ex2(ml.x - ref);
+          add_scaled(sum, __ldcg(reinterpret_cast<const float4*>(pr + d)), f);
+          lsum = fmaf(ml.y, f, lsum);
+        }
+        finish(a, out0 + hr, d, sum, top, lsum, kShift);
+      }
+    }
   }
 }
 
@@ -636,7 +742,7 @@ pi_status launch_attend(const AttendArgs& a, pi_stream stream) {
   DevInfo di;
   pi_status st = dev_info(&di);
   if (st != PI_OK) return st;
-  constexpr int smem = att_smem<DP>();
+  constexpr int smem = att_smem<DP, MT>();
   st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, MT>), smem);
   if (st != PI_OK) return st;
   const int grid = di.sms * (DP == 256 ? 1 : 2);
@@ -687,6 +793,7 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   a.status = dev_status;
   a.arrived = reinterpret_cast<int*>(static_cast<char*>(ws) + w.arrived);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
+  a.wpart = reinterpret_cast<float*>(static_cast<char*>(ws) + w.wpart);
   a.slots = slots;
   a.heads = heads;
   a.kv_heads = C.kv_heads;
@@ -694,10 +801,10 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   a.head_dim = C.head_dim;
   a.page_tokens = C.page_tokens;
   a.pages = C.pages;
+  a.page_shift = C.page_tokens & (C.page_tokens - 1) ? -1 : __builtin_ctz((unsigned)C.page_tokens);
   a.max_pages = max_pages;
   a.window = window;
   a.sinks = sinks;
-  a.min_blocks = 4;
   a.scale = scale * 1.4426950408889634f;
   const bool two = att_two_tiles(C.head_dim, a.group);
   a.tiles = (a.group + (two ? 15 : 7)) / (two ? 16 : 8);

@@ -116,7 +116,7 @@ inline bool att_two_tiles(int head_dim, int group) { return group > 8 && head_di
 // between calls and has one place and size for every cache, so that a
 // workspace may serve calls of several shapes; the rest is scratch.
 struct CacheWs {
-  size_t arrived, part, blocks, owner, free_list, total;
+  size_t arrived, part, wpart, blocks, owner, free_list, total;
 };
 
 constexpr int kScanPages = 1024;  // pages of one block of the page scans
@@ -134,6 +134,7 @@ inline CacheWs cache_ws(const pi_cache_desc& C, int slots, int heads) {
   const size_t scratch = off;
   const int rows = heads ? (att_two_tiles(C.head_dim, heads / C.kv_heads) ? 16 : 8) : 0;
   w.part = take((size_t)kAttendGrid * 2 * rows * (C.head_dim + 4) * 4);
+  w.wpart = take(rows == 16 ? (size_t)kAttendGrid * 4 * 16 * (C.head_dim <= 64 ? 64 : 128) * 4 : 0);
   const size_t end = off;
   off = scratch;  // the page calls use the same bytes
   w.blocks = take(4 * (((size_t)C.pages + kScanPages - 1) / kScanPages + 1));
