@@ -190,21 +190,40 @@ struct Cursor {
       v = seen_of(a, slot);
     } while (v.tiles == 0);
   }
+  __device__ __forceinline__ int first_token() const {
+    return (tile < v.first_tiles ? tile : (v.tail >> 4) + tile - v.first_tiles) << 4;
+  }
   // the tile's first token, and its visible rows as bits
   __device__ __forceinline__ int rows_of(uint32_t& rows) const {
-    int t, r0, r1;
-    if (tile < v.first_tiles) {
-      t = 16 * tile;
-      r0 = 0;
-      r1 = v.first - t;
-    } else {
-      t = ((v.tail >> 4) + tile - v.first_tiles) << 4;
-      r0 = v.tail - t;
-      r1 = v.n - t;
-    }
+    const int t = first_token();
+    const bool sink = tile < v.first_tiles;
+    const int r0 = sink ? 0 : v.tail - t, r1 = (sink ? v.first : v.n) - t;
     rows = r1 >= 16 ? 0xffffu : 0xffffu >> (16 - r1);
     if (r0 > 0) rows &= 0xffffu << r0;
     return t;
+  }
+};
+
+// a / b for a >= 0, b > 0: in 32 bits where a allows it.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// `total` positions over `blocks` blocks: the first `more` take one more.
+struct Line {
+  long long each;
+  int more;
+  __device__ __forceinline__ void set(long long total, int blocks) {
+    each = quotient(total, blocks);
+    more = (int)(total - each * blocks);
+  }
+  __device__ __forceinline__ long long start(int b) const { return b * each + min(b, more); }
+  __device__ __forceinline__ int block_of(long long pos) const {
+    const long long head = more * (each + 1);
+    return pos >= head ? more + (int)divide(pos - head, each) : (int)divide(pos, each + 1);
+  }
+  static __device__ __forceinline__ long long divide(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
   }
 };
 
@@ -240,8 +259,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
   constexpr float kShift = DT == 0 ? 14.f : 0.f;  // weights carry 2^kShift
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ long long s_scan[kAttWarps], s_before[kAttWarps];
-  __shared__ int s_slot[kAttWarps], s_last;
+  __shared__ int s_last[2];
   __shared__ uint32_t s_mask[kAttWarps][S];
   __shared__ float s_m[kAttWarps][2][8 * MT], s_l[kAttWarps][2][8 * MT];
   __shared__ Piece s_piece[kAttWarps][2];
@@ -257,92 +275,72 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   if (lane < 2) s_piece[warp][lane].at = -1;
   pdl_enter();
 
-  // Empty slots, and lengths out of range.
-  for (int s = blockIdx.x; s < a.slots; s += gridDim.x) {
-    const int n = __ldg(a.len + s);
-    if (n > 0 && n <= a.max_pages * P) continue;
-    if (n != 0 && tid == 0) set_status(a.status, PI_ERR_INDEX);
-    for (int e = tid; e < a.heads * D; e += kAttThreads) a.y[(size_t)s * a.heads * D + e] = 0.f;
-    if (a.lse)
-      for (int e = tid; e < a.heads; e += kAttThreads) a.lse[(size_t)s * a.heads + e] = -INFINITY;
-  }
-
-  // The warps' shares of the line.  Thread t sums the slots [t k, t k + k).
+  // The warp's share of the line.  Lane t sums the slots [t k, t k + k).
   long long total, share0, share1;
   int grid;
-  auto unit_len = [](int tiles) { return tiles ? tiles + kUnitCost : 0; };
+  Line line;
+  Cursor cc;  // the tile being computed
   {
-    const int k = (a.slots + kAttThreads - 1) / kAttThreads;
+    auto unit_len = [](int tiles) { return tiles ? tiles + kUnitCost : 0; };
+    auto scan = [&](long long v) {  // sums up to and with this lane
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long w = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += w;
+      }
+      return v;
+    };
+    const int k = (a.slots + 31) >> 5;
     long long mine = 0;
     int used = 0;
-    for (int s = tid * k; s < min(a.slots, tid * k + k); ++s) {
+    for (int s = lane * k; s < min(a.slots, lane * k + k); ++s) {
       const int n = unit_len(seen_of(a, s).tiles);
       mine += n;
       used += n > 0;
     }
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long w = __shfl_up_sync(~0u, upto, o);
-      if (lane >= o) upto += w;
-    }
-    if (lane == 31) s_scan[warp] = upto;
-    used = __syncthreads_count(used > 0);  // at most the used slots; exact for up to 128
-    long long before = upto - mine;
-    total = 0;
-    for (int w = 0; w < kAttWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
-    }
-    total *= units;
-    if (total == 0) return;
-    long long most = (total + kAttWarps * kMinTiles - 1) / (kAttWarps * kMinTiles);
-    if (most < (long long)gridDim.x) {
-      // few tiles: a multiple of the units, so that equal units begin at a
-      // block's start and need no join across blocks
-      const long long per = (long long)used * units, up = (most + per - 1) / per * per;
-      if (up <= (long long)gridDim.x) most = up;
-      grid = (int)most;
-    } else {
-      grid = gridDim.x;
-    }
-    // no empty share between two warps of one unit
-    if (grid > 1 && total < (long long)grid * kAttWarps) grid = max(1, (int)(total / kAttWarps));
-    if ((int)blockIdx.x >= grid) return;
-    const long long warps = (long long)grid * kAttWarps;
-#pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      // the thread whose slots hold the share's first position looks for it
-      const long long p = ((long long)blockIdx.x * kAttWarps + w) * total / warps;
-      long long at = before * units;
-      if (at <= p && p < at + mine * units) {
-        for (int s = tid * k;; ++s) {
-          const long long n = (long long)unit_len(seen_of(a, s).tiles) * units;
-          if (p < at + n) {
-            s_slot[w] = s;
-            s_before[w] = at;
-            break;
-          }
-          at += n;
-        }
+    const long long upto = scan(mine);
+    total = __shfl_sync(~0u, upto, 31) * units;
+    grid = gridDim.x;
+    if (total < (long long)grid * kAttWarps * kMinTiles) {
+      // few tiles: if it can be, a multiple of the units, so that equal units
+      // begin at a block's start and need no join across blocks
+      grid = ((int)total + kAttWarps * kMinTiles - 1) / (kAttWarps * kMinTiles);
+      const int per = (int)__reduce_add_sync(~0u, used) * units;
+      if (per > 0 && per <= (int)gridDim.x) {
+        const int up = (grid + per - 1) / per * per;
+        if (up <= (int)gridDim.x) grid = up;
       }
+      // no empty share between two warps of one unit
+      if (grid > 1 && total < (long long)grid * kAttWarps) grid = max(1, (int)total / kAttWarps);
     }
-    const long long me = (long long)blockIdx.x * kAttWarps + warp;
-    share0 = me * total / warps;
-    share1 = (me + 1) * total / warps;
-    __syncthreads();
-  }
-  Cursor cc;  // the tile being computed
-  cc.slot = s_slot[warp];
-  cc.v = seen_of(a, cc.slot);
-  {
-    const int len = unit_len(cc.v.tiles);
-    const long long off = share0 - s_before[warp];
-    const int unit = (int)(off / len), r = (int)(off - (long long)unit * len);
-    cc.g = unit / a.tiles;
-    cc.ht = unit % a.tiles;
-    cc.tile = max(0, r - kUnitCost);
-    cc.pos = share0 + max(0, kUnitCost - r);
+    cc.pos = share0 = share1 = 0;
+    if ((int)blockIdx.x < grid) {
+      line.set(total, grid);
+      const long long from = line.start(blockIdx.x), n = line.start(blockIdx.x + 1) - from;
+      share0 = from + (warp * n) / kAttWarps;
+      share1 = from + ((warp + 1) * n) / kAttWarps;
+      // its first slot, and where that begins
+      long long at = (upto - mine) * units;
+      int slot = 31 - __clz(__ballot_sync(~0u, mine > 0 && at <= share0));
+      at = __shfl_sync(~0u, at, slot);
+      if (k > 1) {
+        const int s = slot * k + lane;
+        const long long n = lane < k && s < a.slots ? unit_len(seen_of(a, s).tiles) : 0;
+        const long long from = at + (scan(n) - n) * units;
+        const int j = 31 - __clz(__ballot_sync(~0u, n > 0 && from <= share0));
+        at = __shfl_sync(~0u, from, j);
+        slot = slot * k + j;
+      }
+      cc.slot = slot;
+      cc.v = seen_of(a, slot);
+      const int len = unit_len(cc.v.tiles);
+      const int unit = (int)quotient(share0 - at, len);
+      const int r = (int)(share0 - at - (long long)unit * len);
+      cc.g = unit / a.tiles;
+      cc.ht = unit - cc.g * a.tiles;
+      cc.tile = max(0, r - kUnitCost);
+      cc.pos = share0 + max(0, kUnitCost - r);
+    }
   }
   Cursor lc = cc;  // the tile being loaded
 
@@ -351,17 +349,38 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   const bool one_page = (P & 15) == 0;  // a tile lies in one page
   const size_t v_off = (size_t)a.kv_heads * P * D;
 
-  // The tile that lc points at: visible rows, first token (row 0 of lane r's
-  // row where a tile may span pages) as a place in its page, page number.
+  // The tile that lc points at: visible rows, first token, the row within its
+  // page (of lane r's row where a tile may span pages), page number.  Where
+  // it may not, lane i holds the page of the unit's tile page0 + i.
   uint32_t next_rows = 0;
-  int next_t = 0, next_row = 0, next_page = 0;
-  auto fetch = [&]() {
+  int next_t = 0, next_row = 0, next_page = 0, pages32 = 0, page0 = 0;
+  auto page_index = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / P; };
+  auto fetch = [&](bool unit_begins) {
+    if (unit_begins) {  // bring the unit's query rows near: they are read when its first tile is
+      const int rows = min(8 * MT, a.group - lc.ht * 8 * MT);
+      const char* q = reinterpret_cast<const char*>(
+          a.q + ((size_t)lc.slot * a.heads + lc.g * a.group + lc.ht * 8 * MT) * D);
+      for (int e = lane * 128; e < rows * D * 4; e += 32 * 128) {
+        float unused;
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(q + e));
+      }
+    }
     next_t = lc.rows_of(next_rows);
-    const int t = next_t + (one_page ? 0 : lane & 15);
-    const int j = a.page_shift >= 0 ? t >> a.page_shift : t / P;
-    next_row = t - j * P;
-    const bool use = one_page ? next_rows != 0 : (next_rows >> (lane & 15) & 1u) != 0;
-    next_page = use ? __ldg(a.table + (size_t)lc.slot * a.max_pages + j) : -2;
+    const int* row = a.table + (size_t)lc.slot * a.max_pages;
+    if (one_page) {
+      next_row = next_t - page_index(next_t) * P;
+      if (unit_begins || lc.tile - page0 == 32) {
+        page0 = lc.tile;
+        Cursor c = lc;
+        c.tile += lane;
+        pages32 = -2;
+        if (c.tile < c.v.tiles) pages32 = __ldg(row + page_index(c.first_token()));
+      }
+    } else {
+      const int t = next_t + (lane & 15), j = page_index(t);
+      next_row = t - j * P;
+      next_page = next_rows >> (lane & 15) & 1u ? __ldg(row + j) : -2;
+    }
   };
   // Sends that tile into a stage.  A lane's piece of row r = r_lane + i k (k
   // rows per instruction) goes to piece ^ (r & 7): r_lane < k, so the xor
@@ -369,6 +388,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   constexpr int kRows = 32 / kPieces;  // 4, 2, 1 rows per instruction
   const uint32_t lane_dst = (lane / kPieces) * kRow + (((lane % kPieces) ^ (lane / kPieces)) << 4);
   auto issue = [&](int stage) {
+    if (one_page) next_page = __shfl_sync(~0u, pages32, lc.tile - page0);
     const bool ok = (unsigned)next_page < (unsigned)a.pages;
     if (!ok && next_page != -2) set_status(a.status, PI_ERR_INDEX);
     uint32_t rows = next_rows;  // rows to read: visible, and in a page
@@ -392,7 +412,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
       return;
     }
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < DP / 16; ++i) {
       const int r = lane / kPieces + i * kRows;
       long long src = row + r;
@@ -411,31 +431,24 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
     for (int e = lane; e < S * 2 * kTile / 16; e += 32)
       *reinterpret_cast<uint4*>(smem + warp * S * 2 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
   __syncwarp();
-  if (lc.pos < share1) fetch();
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) {
-    if (lc.pos < share1) {
-      issue(i);
-      lc.advance(a);
-      if (lc.pos < share1) fetch();
-    }
-    cp_commit();
-  }
+  if (lc.pos < share1) fetch(true);
 
   uint32_t qf[MT][DP / 16][4], qf2[DT == 1 ? MT : 1][DP / 16][2];
   float o[MT][DP / 8][2], m[MT], l[MT], unit_scale[MT];
   bool fresh = true;
-  int stage = S - 1;
+  int ahead = 0, load_stage = 0, stage = 0;
   while (cc.pos < share1) {
-    stage = stage == S - 1 ? 0 : stage + 1;
-    cp_wait<S - 2>();
-    __syncwarp();
     if (lc.pos < share1) {
-      issue(stage == 0 ? S - 1 : stage - 1);
+      issue(load_stage);
       lc.advance(a);
-      if (lc.pos < share1) fetch();
+      if (lc.pos < share1) fetch(lc.tile == 0);
     }
     cp_commit();
+    load_stage = load_stage == S - 1 ? 0 : load_stage + 1;
+    if (ahead < S - 1) {  // fill the ring first
+      ++ahead;
+      continue;
+    }
 
     const int g = cc.g, ht = cc.ht;
     if (fresh) {  // a unit begins: its query heads
@@ -477,6 +490,9 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
         for (int j = 0; j < DP / 8; ++j) o[mt][j][0] = o[mt][j][1] = 0.f;
       }
     }
+
+    cp_wait<S - 1>();
+    __syncwarp();
 
     const uint32_t k0 = ring + stage * 2 * kTile, v0 = k0 + kTile;
     const uint32_t mask = s_mask[warp][stage];
@@ -629,41 +645,60 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       fresh = true;
     }
     cc.advance(a);
+    stage = stage == S - 1 ? 0 : stage + 1;
+    __syncwarp();  // the stage may be overwritten
   }
 
   // Units shared by warps.  A unit's warps within the block: the one that
   // begins it (piece 1) or the block's first (piece 0), then the followers'
-  // pieces 0.
+  // pieces 0.  Units that other blocks share too (at most one that came in,
+  // one that goes on) are left as one part for the block, and joined by the
+  // last block that arrives.
   cp_wait<0>();
   __syncthreads();
-  const long long warps = (long long)grid * kAttWarps;
   const int vecs = D >> 2, prow = D + 4;
+  int first_block[2] = {0, 0}, last_block[2] = {-1, -1}, cross_k[2] = {0, 0};
+#pragma unroll 1
   for (int k = -1; k < kAttWarps; ++k) {
     const int w0 = max(k, 0);
-    const Piece pc = s_piece[w0][k < 0 ? 0 : 1];
+    const Piece& pc = s_piece[w0][k < 0 ? 0 : 1];
     if (pc.at < 0) continue;
     int w1 = w0 + 1;
     while (w1 < kAttWarps && s_piece[w1][0].at == pc.at) ++w1;
-    const int b0 = (int)(((pc.at + 1) * warps - 1) / total) / kAttWarps;
-    const int b1 = (int)(((pc.at + pc.tiles) * warps - 1) / total) / kAttWarps;
+    // within the block unless its first or last warp is the block's
+    bool local = k >= 0;
+    if (w1 == kAttWarps && pc.at + pc.tiles > line.start(blockIdx.x + 1)) local = false;
+    const int x = k >= 0;  // crossing: 0 came in, 1 goes on
+    if (!local) {
+      const int b0 = line.block_of(pc.at), b1 = line.block_of(pc.at + pc.tiles - 1);
+      first_block[x] = b0;
+      last_block[x] = b1;
+      cross_k[x] = k;
+    }
     const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
     const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
-    float* mine = a.part + ((size_t)blockIdx.x * 2 + (b0 == (int)blockIdx.x)) * (8 * MT) * prow;
+    float* mine = a.part + ((size_t)blockIdx.x * 2 + x) * (8 * MT) * prow;
     for (int e = tid; e < rows * vecs; e += kAttThreads) {
-      const int hr = e / vecs, d = 4 * (e % vecs);
-      float top = -INFINITY;
-      for (int w = w0; w < w1; ++w) top = fmaxf(top, s_m[w][w == k][hr]);
+      const int hr = e / vecs, d = 4 * (e - hr * vecs);
+      float mw[kAttWarps], top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) {
+        mw[w] = w >= w0 && w < w1 ? s_m[w][w == k][hr] : -INFINITY;
+        top = fmaxf(top, mw[w]);
+      }
       const float ref = top == -INFINITY ? 0.f : top;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float lsum = 0.f;
-      for (int w = w0; w < w1; ++w) {
-        const float f = ex2(s_m[w][w == k][hr] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) {
+        if (w < w0 || w >= w1) continue;
+        const float f = ex2(mw[w] - ref);
+        const float4 v = *reinterpret_cast<const float4*>(
             piece_data(w, w == k) + hr * DP + (((d >> 3) ^ (hr & 7)) << 3) + (d & 7));
-        add_scaled(sum, x, f);
+        add_scaled(sum, v, f);
         lsum = fmaf(s_l[w][w == k][hr], f, lsum);
       }
-      if (b0 == b1) {
+      if (local) {
         finish(a, out0 + hr, d, sum, top, lsum, kShift);
       } else {
         float* pr = mine + (size_t)hr * prow;
@@ -671,24 +706,35 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
         if (d == 0) __stcg(reinterpret_cast<float2*>(pr + D), make_float2(top, lsum));
       }
     }
-    if (b0 == b1) continue;
+  }
+  if (last_block[0] >= 0 || last_block[1] >= 0) {
     __threadfence();
     __syncthreads();
-    if (tid == 0) s_last = atomicAdd(a.arrived + b0, 1) == b1 - b0;
-    __syncthreads();
-    if (s_last) {
+    if (tid < 2) {
+      const int b0 = tid ? first_block[1] : first_block[0], b1 = tid ? last_block[1] : last_block[0];
+      s_last[tid] = b1 >= 0 && atomicAdd(a.arrived + b0, 1) == b1 - b0;
+      if (s_last[tid]) a.arrived[b0] = 0;
       __threadfence();
-      if (tid == 0) a.arrived[b0] = 0;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+      if (!s_last[x]) continue;
+      const int b0 = x ? first_block[1] : first_block[0], b1 = x ? last_block[1] : last_block[0];
+      const int k = x ? cross_k[1] : cross_k[0];
+      const Piece& pc = s_piece[max(k, 0)][k < 0 ? 0 : 1];
+      const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
+      const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
       for (int e = tid; e < rows * vecs; e += kAttThreads) {
-        const int hr = e / vecs, d = 4 * (e % vecs);
+        const int hr = e / vecs, d = 4 * (e - hr * vecs);
         auto from = [&](int b) { return a.part + (((size_t)b * 2 + (b == b0)) * (8 * MT) + hr) * prow; };
         float top = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
         for (int b = b0; b <= b1; ++b) top = fmaxf(top, __ldcg(from(b) + D));
         const float ref = top == -INFINITY ? 0.f : top;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         float lsum = 0.f;
-#pragma unroll 4
+#pragma unroll 2
         for (int b = b0; b <= b1; ++b) {
           const float* pr = from(b);
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(pr + D));
@@ -699,6 +745,16 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
         finish(a, out0 + hr, d, sum, top, lsum, kShift);
       }
     }
+  }
+
+  // Empty slots, and lengths out of range.
+  for (int s = blockIdx.x; s < a.slots; s += gridDim.x) {
+    const int n = __ldg(a.len + s);
+    if (n > 0 && n <= a.max_pages * P) continue;
+    if (n != 0 && tid == 0) set_status(a.status, PI_ERR_INDEX);
+    for (int e = tid; e < a.heads * D; e += kAttThreads) a.y[(size_t)s * a.heads * D + e] = 0.f;
+    if (a.lse)
+      for (int e = tid; e < a.heads; e += kAttThreads) a.lse[(size_t)s * a.heads + e] = -INFINITY;
   }
 }
 
@@ -745,9 +801,16 @@ pi_status launch_attend(const AttendArgs& a, pi_stream stream) {
   constexpr int smem = att_smem<DP, MT>();
   st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, MT>), smem);
   if (st != PI_OK) return st;
-  const int grid = di.sms * (DP == 256 ? 1 : 2);
-  return launch(attend_kernel<DT, DP, MT>, dim3((unsigned)(grid < kAttendGrid ? grid : kAttendGrid)),
-                kAttThreads, smem, stream, a);
+  // Two blocks per SM (one at 256 dims), or fewer where the longest slots that
+  // the tables and the window allow cannot use them.
+  long long seen = (long long)a.max_pages * a.page_tokens;
+  if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
+  const long long tiles = (long long)a.slots * a.kv_heads * a.tiles * (seen / 16 + 3 + kUnitCost);
+  const long long useful = tiles / (kAttWarps * kMinTiles) + 1;
+  long long grid = di.sms * (DP == 256 ? 1 : 2);
+  if (grid > kAttendGrid) grid = kAttendGrid;
+  if (grid > useful) grid = useful;
+  return launch(attend_kernel<DT, DP, MT>, dim3((unsigned)grid), kAttThreads, smem, stream, a);
 }
 
 }  // namespace pis
