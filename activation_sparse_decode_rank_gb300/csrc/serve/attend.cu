@@ -204,11 +204,6 @@ struct Cursor {
   }
 };
 
-// a / b for a >= 0, b > 0: in 32 bits where a allows it.
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-
 // `total` positions over `blocks` blocks: the first `more` take one more.
 struct Line {
   long long each;

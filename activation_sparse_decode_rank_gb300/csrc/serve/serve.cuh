@@ -116,7 +116,7 @@ inline bool att_two_tiles(int head_dim, int group) { return group > 8 && head_di
 // between calls and has one place and size for every cache, so that a
 // workspace may serve calls of several shapes; the rest is scratch.
 struct CacheWs {
-  size_t arrived, part, wpart, blocks, owner, free_list, total;
+  size_t arrived, part, wpart, blocks, owner, rank, first, before, src, sums, total;
 };
 
 constexpr int kScanPages = 1024;  // pages of one block of the page scans
@@ -139,7 +139,11 @@ inline CacheWs cache_ws(const pi_cache_desc& C, int slots, int heads) {
   off = scratch;  // the page calls use the same bytes
   w.blocks = take(4 * (((size_t)C.pages + kScanPages - 1) / kScanPages + 1));
   w.owner = take(4 * (size_t)C.pages);
-  w.free_list = take(4 * (size_t)C.pages);
+  w.rank = take(4 * (size_t)C.pages);
+  w.first = take(4 * PI_CACHE_MAX_SLOTS);
+  w.before = take(4 * PI_CACHE_MAX_SLOTS);
+  w.src = take(4 * PI_CACHE_MAX_SLOTS);
+  w.sums = take(16);
   w.total = off > end ? off : end;
   return w;
 }
@@ -176,6 +180,11 @@ __device__ __forceinline__ float from_bits(uint16_t b) {
 template <int DT>
 __device__ __forceinline__ uint32_t pack_bits(float a, float b) {
   return (uint32_t)to_bits<DT>(a) | ((uint32_t)to_bits<DT>(b) << 16);
+}
+
+// a / b for a >= 0, b > 0: in 32 bits where a allows it.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
 __device__ __forceinline__ int pages_of(int tokens, int page_tokens) {
