@@ -1,25 +1,28 @@
 // logprob.cu — log probabilities of given tokens, entropy and the largest
 // alternatives of rows of logits (include/pi_serve.h).
 //
-// Mathematics.  One pass keeps, per thread, a running maximum m and the sums
-// s = sum exp(x - m), t = sum exp(x - m)(x - m), rescaled when m grows; parts
-// join the same way.  Then log p_i = x_i - m - log s and the entropy is
-// log s - t / s, with no large terms to cancel.
+// Mathematics.  In units of log 2, with L = log2(e) and any reference M near
+// the largest logit's L x, one pass keeps s = sum 2^d and t = sum 2^d d with
+// d = L x - M.  Then log p_i = ln 2 (d_i - log2 s) and the entropy is
+// ln 2 (log2 s - t / s): no large terms cancel, and since every d is one
+// fused multiply-add with the same rounded M, what M and L were rounded by
+// drops out.  Each thread's M follows its running maximum.
 //
-// Alternatives without a second pass: order all elements by a unique key
-// (value, then lowest index).  Threads own disjoint sets of elements, and the
-// pass leaves each thread's largest key (the batch that held it is noted when
-// the maximum grows, which is rare).  Let tau be the k-th largest of these.
-// At least k elements are >= tau, so every one of the k largest is; and an
-// element >= tau can only belong to the k threads whose largest key is >= tau.
-// Only their elements are looked at again (k / 256 of the row, from L2).
-// Selection is by sorted lists of 32 keys in the lanes of a warp: sort 32,
-// merge two lists, a tree over the warps.
+// Alternatives without a second pass.  Threads own disjoint sets of elements,
+// so at least k elements are >= tau, the k-th largest of the threads' maxima,
+// and all of the k largest are.  Each thread leaves the maxima of its batches
+// (which the sums need anyway) in shared memory, so that only the batches
+// that reach tau, some k of them, are read again; their elements >= tau are
+// ranked by a unique key (value, then lowest index).  Where ties make more of
+// either than the block has room for, the whole part is read again: slower,
+// as exact.  Selection is by sorted lists of 32 keys in the lanes of a warp:
+// sort 32, merge two lists, a tree over the warps.
 //
 // Bound: HBM bandwidth (each logit read once); for 16-bit logits the pass
-// issues some 7 instructions per logit, near the machine's rate at that
-// bandwidth.  Few rows: a row is split over several blocks, and the last of
-// them to arrive joins the parts in order.
+// issues some 5 instructions per logit, not far from the machine's rate at
+// that bandwidth, hence the packed forms (two FP32 operations per
+// instruction).  Few rows: a row is split over several blocks, and the last
+// of them to arrive joins the parts.
 #include "serve.cuh"
 
 namespace pis {
@@ -44,7 +47,7 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreBlocks = 4;        // per SM
 constexpr int kScoreParts = 2048;      // most parts of rows in flight
 constexpr int kBatch = 4;              // 16-byte vectors of a thread's batch
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int DT>
 __device__ __forceinline__ float logit_at(const void* p, long long i) {
@@ -65,16 +68,22 @@ __device__ __forceinline__ float key_value(u64 k) {
   return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
 }
 
-// ------------------------------------------------------------------ lists of 32 keys
-__device__ __forceinline__ u64 keep(u64 v, u64 w, bool larger) { return (v > w) == larger ? v : w; }
+// A maximum's rank as a thread's; 0 where it has none.
+__device__ __forceinline__ uint32_t value_key(float v) { return (uint32_t)(rank_key(v, 0) >> 32); }
 
-__device__ __forceinline__ u64 merge_down(u64 v) {  // a bitonic sequence, sorted descending
+// ------------------------------------------------------------------ lists of 32 keys
+template <typename K>
+__device__ __forceinline__ K keep(K v, K w, bool larger) { return (v > w) == larger ? v : w; }
+
+template <typename K>
+__device__ __forceinline__ K merge_down(K v) {  // a bitonic sequence, sorted descending
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 16; j > 0; j >>= 1) v = keep(v, __shfl_xor_sync(~0u, v, j), (lane & j) == 0);
   return v;
 }
-__device__ __forceinline__ u64 sort32(u64 v) {
+template <typename K>
+__device__ __forceinline__ K sort32(K v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 2; k < 32; k <<= 1)
@@ -84,77 +93,146 @@ __device__ __forceinline__ u64 sort32(u64 v) {
   return merge_down(v);
 }
 // The 32 largest of two sorted lists, sorted.
-__device__ __forceinline__ u64 merge32(u64 a, u64 b) {
-  const u64 r = __shfl_sync(~0u, b, 31 - (threadIdx.x & 31));
+template <typename K>
+__device__ __forceinline__ K merge32(K a, K b) {
+  const K r = __shfl_sync(~0u, b, 31 - (threadIdx.x & 31));
   return merge_down(a > r ? a : r);
 }
 // The warps' lists into one, left in warp 0.
-__device__ __forceinline__ u64 block_merge(u64 v, u64 (*sh)[32]) {
+template <typename K>
+__device__ __forceinline__ K block_merge(K v, u64 (*sh)[32]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int half = kScoreWarps / 2; half > 0; half >>= 1) {
     if (warp >= half && warp < 2 * half) sh[warp][lane] = v;
     __syncthreads();
-    if (warp < half) v = merge32(v, sh[warp + half][lane]);
+    if (warp < half) v = merge32(v, (K)sh[warp + half][lane]);
   }
   return v;
 }
 
 // ------------------------------------------------------------------ sums
+// Sums relative to the logit m (s = t = 0 for m = -infinity).
 struct Sums {
   float m, s, t;
 };
-// The same sums with the maximum `top` >= a.m.
-__device__ __forceinline__ Sums raised(const Sums& a, float top) {
-  if (a.m == top || a.m == -INFINITY) return Sums{top, a.s, a.m == top ? a.t : 0.f};
-  const float d = a.m - top, f = exp2f(d * kLog2e);
-  return Sums{top, a.s * f, f * fmaf(d, a.s, a.t)};
-}
-
-template <int DT>
-struct Vec {
-  static constexpr int n = DT == 2 ? 4 : 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[n]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == 2) {
-        f[i] = __uint_as_float(w[i]);
-      } else if constexpr (DT == 1) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
-      }
-    }
-  }
-};
-
-__device__ __forceinline__ float max_nan(float a, float b) {
+// L x would overflow beside the reference: differences are taken first.
+__device__ __forceinline__ bool huge(float ref) { return !(fabsf(ref) < 1e38f); }
+// d of a logit x.  At least -1500 (2^d is 0 below -150): keeps 0 * infinity
+// out of t.  NaN stays NaN; +infinity against itself is NaN.
+__device__ __forceinline__ float floor_nan(float d) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(d), "f"(-1500.f));
   return r;
 }
+__device__ __forceinline__ float distance(float x, float ref) {
+  return huge(ref) ? (x - ref) * kLog2e : fmaf(x, kLog2e, -__fmul_rn(ref, kLog2e));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The same sums relative to top >= a.m.
+__device__ __forceinline__ Sums raised(const Sums& a, float top) {
+  if (a.m == top) return a;
+  if (a.m == -INFINITY) return Sums{top, a.s, 0.f};
+  const float d = huge(top) ? (a.m - top) * kLog2e
+                            : __fsub_rn(__fmul_rn(a.m, kLog2e), __fmul_rn(top, kLog2e));
+  const float f = ex2(d);
+  return Sums{top, a.s * f, f > 0.f ? f * fmaf(d, a.s, a.t) : 0.f};
+}
 __device__ __forceinline__ void add_one(Sums& a, float ref, float x) {
-  // exp underflows to 0 below -1000 anyway; keeps 0 * infinity out of t
-  const float d = max_nan(x - ref, -1000.f);
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * kLog2e));
+  const float d = floor_nan(distance(x, ref)), e = ex2(d);
   a.s += e;
   a.t = fmaf(e, d, a.t);
 }
 
+// Two fp32 values in one register pair.
+__device__ __forceinline__ u64 pair(float x, float y) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 halves(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int DT>
+struct Vec {  // 16 bytes of logits
+  static constexpr int n = DT == 2 ? 4 : 8, pairs = n / 2;
+  static __device__ __forceinline__ float2 get(const uint4& v, int i) {  // elements 2i, 2i + 1
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == 2) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else if constexpr (DT == 1) return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+  }
+  // packed lower bound for logits beside a reference: 2^d is 0 there, and no
+  // rounding takes it near the reference; NaN where the type cannot hold it
+  static __device__ __forceinline__ uint32_t floor_at(float ref) {
+    const float f = ref - (1040.f + fabsf(ref) * 0.02f);
+    if constexpr (DT == 2) return __float_as_uint(f);
+    if (DT == 0 && f < -65000.f) return 0x7fff7fffu;
+    return pack_bits<DT>(f, f);
+  }
+  // the larger, NaN if one is NaN
+  static __device__ __forceinline__ uint32_t raise(uint32_t a, uint32_t floor) {
+    uint32_t r;
+    if constexpr (DT == 2) asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(floor));
+    else if constexpr (DT == 1) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(floor));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(floor));
+    return r;
+  }
+  static __device__ __forceinline__ uint4 raise(const uint4& v, uint32_t floor) {
+    return make_uint4(raise(v.x, floor), raise(v.y, floor), raise(v.z, floor), raise(v.w, floor));
+  }
+  // elementwise maximum of packed values (the number where one is NaN)
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == 2) r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else if constexpr (DT == 1) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t max(const uint4& v) {
+    return max(max(v.x, v.y), max(v.z, v.w));
+  }
+  static __device__ __forceinline__ float top(uint32_t w) {
+    if constexpr (DT == 2) return __uint_as_float(w);
+    return fmaxf(from_bits<DT>((uint16_t)w), from_bits<DT>((uint16_t)(w >> 16)));
+  }
+};
+
+constexpr int kGroups = 16;  // groups of batches whose maxima a thread leaves
+constexpr int kPicks = 256;  // groups, then elements, that reach tau
+
 // One block per (row, part).
 template <int DT>
 __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(const ScoreArgs a) {
-  constexpr int VN = Vec<DT>::n, T = kScoreThreads;
+  using V = Vec<DT>;
+  constexpr int VN = V::n, T = kScoreThreads;
   constexpr int kSize = DT == 2 ? 4 : 2;
-  __shared__ u64 sh_keys[kScoreWarps][32], sh_tau;
+  __shared__ u64 sh_keys[kScoreWarps][32];
   __shared__ float sh_sums[kScoreWarps][3];
-  __shared__ int sh_win[32], sh_nwin, sh_last;
+  __shared__ float sh_top[kGroups][T];
+  __shared__ uint32_t sh_group[kPicks];
+  __shared__ u64 sh_pick[kPicks];
+  __shared__ uint32_t sh_tau;
+  __shared__ int sh_groups, sh_picks, sh_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) sh_groups = sh_picks = 0;
   pdl_enter();
   const long long row = blockIdx.x;
   const int part = blockIdx.y;
@@ -166,88 +244,122 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
   const int v0 = (int)((long long)part * nvec / a.parts);
   const int v1 = (int)((long long)(part + 1) * nvec / a.parts);
   // whole vectors [w0, w1); the row's first and last, where cut, go to threads 0 and 1
-  const int w0 = v0 == 0 && shift ? 1 : v0;
+  const bool cut_first = v0 == 0 && shift;
+  const int w0 = cut_first ? 1 : v0;
   const bool cut_last = v1 == nvec && (a.vocab + shift) % VN && nvec - 1 >= w0;
   const int w1 = cut_last ? v1 - 1 : v1;
 
   Sums sum{-INFINITY, 0.f, 0.f};
-  int at = -1;  // batch of the thread's largest element; cut vectors: -2, -3
-  auto raise = [&](float top, int where) {
-    if (top > sum.m || (at == -1 && top == top)) {
-      at = where;
-      if (top > sum.m) sum = raised(sum, top);
-    }
+  bool some = false;  // an element that is not NaN
+  auto raise = [&](float top) {
+    if (top > sum.m) sum = raised(sum, top);
+    some |= top == top;
   };
-  // elements of a cut vector
-  auto cut = [&](int j, auto&& use) {
+  auto cut = [&](int j, auto&& use) {  // elements of a cut vector
     for (int e = 0; e < VN; ++e) {
       const int i = j * VN + e - shift;
       if (i >= 0 && i < a.vocab) use(logit_at<DT>(base, i), i);
     }
   };
+  // The block's k-th largest thread maximum, as a key (0: fewer have one).
+  auto find_tau = [&]() {
+    const uint32_t v = block_merge(sort32(some ? value_key(sum.m) : 0u), sh_keys);
+    if (warp == 0 && lane == a.topk - 1) sh_tau = v;
+    __syncthreads();
+    return sh_tau;
+  };
+
   const int steps = w1 > w0 ? (w1 - w0 + T * kBatch - 1) / (T * kBatch) : 0;
   const uint4* mine = vecs + w0 + tid;
   uint4 raw[kBatch];
   auto load = [&](int it) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int j = (it * kBatch + u) * T;
-      if (w0 + tid + j < w1) raw[u] = __ldcs(mine + j);
-    }
-  };
-  if (steps > 0) load(0);
-  for (int it = 0; it < steps; ++it) {
-    float x[kBatch][VN];
-    bool have[kBatch];
-    float top = -INFINITY;
-    bool any = false;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      have[u] = w0 + tid + (it * kBatch + u) * T < w1;
-      Vec<DT>::unpack(raw[u], x[u]);
-    }
-    const bool full = have[kBatch - 1];
-    if (it + 1 < steps) load(it + 1);
-    if (full) {
-      float m4[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        m4[u] = x[u][0];
-#pragma unroll
-        for (int e = 1; e < VN; ++e) m4[u] = fmaxf(m4[u], x[u][e]);
-      }
-      top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      any = true;
-    } else {
-      top = NAN;
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (have[u]) {
-          any = true;
-#pragma unroll
-          for (int e = 0; e < VN; ++e) top = fmaxf(top, x[u][e]);
-        }
-    }
-    if (any) raise(top, it);
-    const float ref = sum.m == -INFINITY ? 0.f : sum.m;
+    const uint4* p = mine + it * (T * kBatch);
+    const int left = w1 - w0 - tid - it * (T * kBatch);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if (full || have[u]) {
-#pragma unroll
-        for (int e = 0; e < VN; ++e) add_one(sum, ref, x[u][e]);
-      }
-  }
-  if (tid == 0 && w0 > v0) {
+      if (u * T < left) raw[u] = __ldg(p + u * T);
+  };
+  const int group = (steps + kGroups - 1) / kGroups;  // batches of a group
+  float group_top = NAN;
+  int group_left = group, group_at = 0;
+  if (steps > 0) load(0);
+  for (int it = 0; it < steps; ++it) {
+    const int left = w1 - w0 - tid - it * (T * kBatch);
+    const bool full = left > (kBatch - 1) * T;
+    uint4 v[kBatch];
     float top = NAN;
-    cut(0, [&](float x, int) { top = fmaxf(top, x); });
-    raise(top, -2);
+    if (full) {
+      uint32_t w[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        v[u] = raw[u];
+        w[u] = V::max(v[u]);
+      }
+      top = V::top(V::max(V::max(w[0], w[1]), V::max(w[2], w[3])));
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (u * T < left) {
+          v[u] = raw[u];
+          top = fmaxf(top, V::top(V::max(v[u])));
+        }
+    }
+    if (it + 1 < steps) load(it + 1);
+    raise(top);
+    const float ref = sum.m == -INFINITY ? 0.f : sum.m;
+    const uint32_t low = V::floor_at(ref);
+    if (!huge(ref) && (DT != 0 || low != 0x7fff7fffu)) {
+      const float M = -__fmul_rn(ref, kLog2e);
+      const u64 L2 = pair(kLog2e, kLog2e), M2 = pair(M, M);
+      u64 s2 = 0, t2 = 0;
+      auto add_vec = [&](const uint4& raw16) {
+        const uint4 q = V::raise(raw16, low);
+#pragma unroll
+        for (int p = 0; p < V::pairs; ++p) {
+          const float2 x = V::get(q, p);
+          const u64 d2 = fma2(pair(x.x, x.y), L2, M2);
+          const float2 d = halves(d2);
+          const u64 e = pair(ex2(d.x), ex2(d.y));
+          s2 = add2(s2, e);
+          t2 = fma2(e, d2, t2);
+        }
+      };
+      if (full) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) add_vec(v[u]);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u * T < left; ++u) add_vec(u == 0 ? v[0] : u == 1 ? v[1] : v[2]);
+      }
+      const float2 s = halves(s2), t = halves(t2);
+      sum.s += s.x + s.y;
+      sum.t += t.x + t.y;
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kBatch && u * T < left; ++u) {
+        const uint4 q = u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3];
+#pragma unroll 1
+        for (int p = 0; p < V::pairs; ++p) {
+          const float2 x = V::get(q, p);
+          add_one(sum, ref, x.x);
+          add_one(sum, ref, x.y);
+        }
+      }
+    }
+    group_top = fmaxf(group_top, top);
+    if (--group_left == 0 || it + 1 == steps) {
+      sh_top[group_at++][tid] = group_top;
+      group_top = NAN;
+      group_left = group;
+    }
+  }
+  if (tid == 0 && cut_first) {
+    cut(0, [&](float x, int) { raise(x); });
     const float ref = sum.m == -INFINITY ? 0.f : sum.m;
     cut(0, [&](float x, int) { add_one(sum, ref, x); });
   }
   if (tid == 1 && cut_last) {
-    float top = NAN;
-    cut(nvec - 1, [&](float x, int) { top = fmaxf(top, x); });
-    raise(top, -3);
+    cut(nvec - 1, [&](float x, int) { raise(x); });
     const float ref = sum.m == -INFINITY ? 0.f : sum.m;
     cut(nvec - 1, [&](float x, int) { add_one(sum, ref, x); });
   }
@@ -257,7 +369,6 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) sh_sums[warp][0] = top;
-  if (tid == 0) sh_nwin = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kScoreWarps; ++w) top = fmaxf(top, sh_sums[w][0]);
@@ -270,62 +381,72 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
     }
   }
 
-  // elements of thread w's set, one vector at a time
-  auto each = [&](int w, int i, auto&& use) {  // i-th whole vector of thread w
-    const int j = w0 + w + i * T;
-    if (j >= w1) return;
-    float x[VN];
-    Vec<DT>::unpack(__ldg(vecs + j), x);
-#pragma unroll
-    for (int e = 0; e < VN; ++e) use(x[e], j * VN + e - shift);
-  };
   u64 list = 0;  // this warp's 32 largest keys
   if (a.topk > 0) {
-    u64 key = 0;
-    auto best = [&](float x, int i) {
-      const u64 k = rank_key(x, i);
-      key = k > key ? k : key;
-    };
-    if (at == -1) {  // nothing but NaN: the first elements will do
-      if (tid == 0 && w0 > v0) cut(0, best);
-      each(tid, 0, best);
-      if (key == 0 && tid == 1 && cut_last) cut(nvec - 1, best);
-    } else if (at >= 0) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) each(tid, at * kBatch + u, best);
-    } else {
-      cut(at == -2 ? 0 : nvec - 1, best);
-    }
-    // equal values elsewhere in the thread's cut vector may come earlier
-    if (tid == 0 && w0 > v0) cut(0, best);
-    const u64 sorted = block_merge(sort32(key), sh_keys);
-    if (warp == 0 && lane == a.topk - 1) sh_tau = sorted;
-    __syncthreads();
-    const u64 tau = sh_tau;
-    if (key >= tau && key > 0) sh_win[atomicAdd(&sh_nwin, 1)] = tid;
-    __syncthreads();
-    const int nwin = sh_nwin, per = (max(0, w1 - w0) + T - 1) / T;
-    u64 least = tau > 0 ? tau - 1 : 0;  // what enters is larger
+    const uint32_t tau = find_tau();
+    u64 least = (u64)tau << 32;  // a key that enters is larger
     auto enter = [&](u64 k) {
       if (__any_sync(~0u, k > least)) {
-        list = merge32(list, sort32(k > least ? k : 0));
+        list = merge32(list, sort32(k > least ? k : (u64)0));
         const u64 kth = __shfl_sync(~0u, list, a.topk - 1);
         least = kth > least ? kth : least;
       }
     };
-    const int items = nwin * per;
-    for (int i0 = warp * 32; i0 < items; i0 += T) {
-      const int i = i0 + lane, w = min(i, items - 1) / per;
-      const int j = w0 + sh_win[w] + (min(i, items - 1) - w * per) * T;
-      const bool in = i < items && j < w1;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (in) v = __ldg(vecs + j);
-      float x[VN];
-      Vec<DT>::unpack(v, x);
+    auto reaches = [&](float v) { return v == v && value_key(v) >= tau; };
+    bool all = tau == 0;  // then everything counts, NaN too
+    if (!all) {
+      for (int q = 0; q < group_at; ++q)
+        if (reaches(sh_top[q][tid])) {
+          const int i = atomicAdd(&sh_groups, 1);
+          if (i < kPicks) sh_group[i] = (uint32_t)(q * T + tid);
+        }
+      __syncthreads();
+      const int groups = sh_groups, per = group * kBatch, items = groups * per;
+      all = groups > kPicks;
+      if (!all)
+        for (int i = tid; i < items; i += T) {
+          const int q = i / per;
+          const uint32_t who = sh_group[q];
+          const int j = w0 + (int)(who % T) + ((int)(who / T) * per + (i - q * per)) * T;
+          if (j >= w1) continue;
+          const uint4 v = __ldg(vecs + j);
+          if (!reaches(V::top(V::max(v)))) continue;
 #pragma unroll
-      for (int e = 0; e < VN; ++e) enter(in ? rank_key(x[e], j * VN + e - shift) : 0);
+          for (int p = 0; p < V::pairs; ++p) {
+            const float2 x = V::get(v, p);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float y = h ? x.y : x.x;
+              if (!reaches(y)) continue;
+              const int n = atomicAdd(&sh_picks, 1);
+              if (n < kPicks) sh_pick[n] = rank_key(y, j * VN + 2 * p + h - shift);
+            }
+          }
+        }
+      __syncthreads();
+      const int picks = sh_picks;
+      all |= picks > kPicks;
+      if (!all)
+        for (int i0 = warp * 32; i0 < picks; i0 += T)
+          enter(i0 + lane < picks ? sh_pick[i0 + lane] : 0);
     }
-    if (warp == 0 && w0 > v0) {
+    if (all) {
+      for (int j0 = w0 + warp * 32; j0 < w1; j0 += T) {
+        const bool in = j0 + lane < w1;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (in) v = __ldg(vecs + j0 + lane);
+        if (!__any_sync(~0u, in && (tau == 0 || reaches(V::top(V::max(v)))))) continue;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+        for (int e = 0; e < VN; ++e) {
+          float x;
+          if constexpr (DT == 2) x = __uint_as_float(w[e]);
+          else x = from_bits<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+          enter(in ? rank_key(x, (j0 + lane) * VN + e - shift) : 0);
+        }
+      }
+    }
+    if (warp == 0 && cut_first) {
       const int i = lane - shift;
       enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
     }
@@ -358,7 +479,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
     if (!sh_last) return;
     __threadfence();
     if (tid == 0) a.arrived[row] = 0;
-    // all parts, by one warp in order for the sums and by all for the lists
+    // all parts: the sums by one warp, the lists by all
     if (warp == 0) {
       float up = -INFINITY;
       const float4* ps = reinterpret_cast<const float4*>(a.psum) + row * a.parts;
@@ -386,10 +507,12 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
 
   if (warp == 0) {
     const bool bad = sum.s != sum.s, none = sum.m == -INFINITY;
-    const float ls = logf(sum.s);
-    auto lp = [&](float x) { return bad ? NAN : none ? -INFINITY : x - sum.m - ls; };
+    const float ls = log2f(sum.s);
+    auto lp = [&](float x) {
+      return bad ? NAN : none ? -INFINITY : (distance(x, sum.m) - ls) * kLn2;
+    };
     if (lane == 0) {
-      if (a.entropy) a.entropy[row] = bad ? NAN : none ? 0.f : ls - sum.t / sum.s;
+      if (a.entropy) a.entropy[row] = bad ? NAN : none ? 0.f : (ls - sum.t / sum.s) * kLn2;
       if (a.logprob) {
         const int tok = a.tokens[row];
         float r = 0.f;
