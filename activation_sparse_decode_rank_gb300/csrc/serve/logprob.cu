@@ -9,8 +9,8 @@
 // drops out.  Each thread's M follows its running maximum.
 //
 // Alternatives without a second pass.  Threads own disjoint sets of elements,
-// so at least k elements are >= tau, the k-th largest of the threads' maxima,
-// and all of the k largest are.  Each thread leaves the maxima of its batches
+// so at least k elements are >= tau, the k-th largest of the maxima of fours
+// of threads, and all of the k largest are.  Each thread leaves the maxima of its batches
 // (which the sums need anyway) in shared memory, so that only the batches
 // that reach tau, some k of them, are read again; their elements >= tau are
 // ranked by a unique key (value, then lowest index).  Where ties make more of
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
   __shared__ float sh_top[kGroups][T];
   __shared__ uint32_t sh_group[kPicks];
   __shared__ u64 sh_pick[kPicks];
-  __shared__ uint32_t sh_tau;
+  __shared__ uint32_t sh_four[T / 4], sh_tau;
   __shared__ int sh_groups, sh_picks, sh_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) sh_groups = sh_picks = 0;
@@ -261,14 +261,6 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
       if (i >= 0 && i < a.vocab) use(logit_at<DT>(base, i), i);
     }
   };
-  // The block's k-th largest thread maximum, as a key (0: fewer have one).
-  auto find_tau = [&]() {
-    const uint32_t v = block_merge(sort32(some ? value_key(sum.m) : 0u), sh_keys);
-    if (warp == 0 && lane == a.topk - 1) sh_tau = v;
-    __syncthreads();
-    return sh_tau;
-  };
-
   const int steps = w1 > w0 ? (w1 - w0 + T * kBatch - 1) / (T * kBatch) : 0;
   const uint4* mine = vecs + w0 + tid;
   uint4 raw[kBatch];
@@ -369,7 +361,17 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) sh_sums[warp][0] = top;
+  if (a.topk > 0) {  // maxima of fours of threads, as keys (0: only NaN, or nothing)
+    uint32_t k = some ? value_key(sum.m) : 0u;
+    k = max(k, __shfl_xor_sync(~0u, k, 1));
+    k = max(k, __shfl_xor_sync(~0u, k, 2));
+    if ((lane & 3) == 0) sh_four[tid >> 2] = k;
+  }
   __syncthreads();
+  if (a.topk > 0 && warp == 0) {
+    const uint32_t k = merge32(sort32(sh_four[lane]), sort32(sh_four[lane + 32]));
+    if (lane == a.topk - 1) sh_tau = k;
+  }
 #pragma unroll
   for (int w = 0; w < kScoreWarps; ++w) top = fmaxf(top, sh_sums[w][0]);
   {
@@ -383,7 +385,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
 
   u64 list = 0;  // this warp's 32 largest keys
   if (a.topk > 0) {
-    const uint32_t tau = find_tau();
+    __syncthreads();
+    const uint32_t tau = sh_tau;
+    const float tau_value = key_value((u64)tau << 32);
     u64 least = (u64)tau << 32;  // a key that enters is larger
     auto enter = [&](u64 k) {
       if (__any_sync(~0u, k > least)) {
@@ -392,11 +396,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
         least = kth > least ? kth : least;
       }
     };
-    auto reaches = [&](float v) { return v == v && value_key(v) >= tau; };
     bool all = tau == 0;  // then everything counts, NaN too
     if (!all) {
       for (int q = 0; q < group_at; ++q)
-        if (reaches(sh_top[q][tid])) {
+        if (sh_top[q][tid] >= tau_value) {
           const int i = atomicAdd(&sh_groups, 1);
           if (i < kPicks) sh_group[i] = (uint32_t)(q * T + tid);
         }
@@ -410,14 +413,14 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
           const int j = w0 + (int)(who % T) + ((int)(who / T) * per + (i - q * per)) * T;
           if (j >= w1) continue;
           const uint4 v = __ldg(vecs + j);
-          if (!reaches(V::top(V::max(v)))) continue;
+          if (!(V::top(V::max(v)) >= tau_value)) continue;
 #pragma unroll
           for (int p = 0; p < V::pairs; ++p) {
             const float2 x = V::get(v, p);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float y = h ? x.y : x.x;
-              if (!reaches(y)) continue;
+              if (!(y >= tau_value)) continue;
               const int n = atomicAdd(&sh_picks, 1);
               if (n < kPicks) sh_pick[n] = rank_key(y, j * VN + 2 * p + h - shift);
             }
@@ -426,16 +429,15 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
       __syncthreads();
       const int picks = sh_picks;
       all |= picks > kPicks;
-      if (!all)
-        for (int i0 = warp * 32; i0 < picks; i0 += T)
-          enter(i0 + lane < picks ? sh_pick[i0 + lane] : 0);
+      if (!all && warp == 0)
+        for (int i0 = 0; i0 < picks; i0 += 32) enter(i0 + lane < picks ? sh_pick[i0 + lane] : 0);
     }
     if (all) {
       for (int j0 = w0 + warp * 32; j0 < w1; j0 += T) {
         const bool in = j0 + lane < w1;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (in) v = __ldg(vecs + j0 + lane);
-        if (!__any_sync(~0u, in && (tau == 0 || reaches(V::top(V::max(v)))))) continue;
+        if (!__any_sync(~0u, in && (tau == 0 || V::top(V::max(v)) >= tau_value))) continue;
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll 1
         for (int e = 0; e < VN; ++e) {
@@ -445,16 +447,16 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
           enter(in ? rank_key(x, (j0 + lane) * VN + e - shift) : 0);
         }
       }
+      list = block_merge(list, sh_keys);
     }
     if (warp == 0 && cut_first) {
       const int i = lane - shift;
       enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
     }
-    if (warp == 1 && cut_last) {
+    if (warp == 0 && cut_last) {
       const int i = (nvec - 1) * VN + lane - shift;
       enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
     }
-    list = block_merge(list, sh_keys);
   }
   __syncthreads();
   if (warp == 0) {
