@@ -15,9 +15,10 @@
 //           slots, or movers and holes to their pairs
 //   copy    page contents in all layers
 //
-// Bound: for small tables launches and memory latency, so one block runs all
-// passes but the copy; for large ones the reading of the tables; with real
-// pages the copy, at HBM bandwidth (each byte once in, once out).
+// Bound: for small pools launches and memory latency, so one block runs all
+// passes but the copy with the pool's counts in its shared memory; for large
+// ones the chain of dependent reads and the tables; with real pages the copy,
+// at HBM bandwidth (each byte once in, once out).
 #include "serve.cuh"
 
 namespace pis {
@@ -31,12 +32,13 @@ struct PageArgs {
 
 constexpr int kPageThreads = 256;
 constexpr int kNobody = 0x7fffffff;
-enum { kSumNeed, kSumFree, kSumLive, kSumLow };  // places in `sums`
+enum { kSumNeed, kSumLive, kSumLow };  // places in `sums`
 
-// A table this small is left to one block of 1024 threads: its passes take a
-// microsecond or less each, a launch two.
-inline bool one_block(const PageArgs& a) {
-  return a.pages <= 16384 && (long long)a.slots * a.max_pages <= 16384;
+// A pool and tables this small are left to one block of 1024 threads, with
+// both counts of every page in shared memory.
+constexpr int kSmallPages = 8192, kSmallEntries = 16384;
+inline bool is_small(const PageArgs& a) {
+  return a.pages <= kSmallPages && (long long)a.slots * a.max_pages <= kSmallEntries;
 }
 
 // What becomes of slot s (pi_cache_fork): the parent's row, the tokens kept,
@@ -121,34 +123,46 @@ __device__ __forceinline__ void clear_pass(const PageArgs& a, int first, int ste
   }
 }
 
-// Entries [first, ...) of slot s.  Fork: full pages are shared, and the
-// lowest slot bids for each partly filled one.
+// Entries [first, end) of slot s, four at a time where rows are aligned to
+// that.  Fork: full pages are shared, the lowest slot bids for each partly
+// filled one, and the slot's full pages, partly filled page and wanted length
+// are noted.
 template <bool FORK>
-__device__ __forceinline__ void count_pass(const PageArgs& a, int s, int first, int end, int step) {
+__device__ __forceinline__ void count_pass(const PageArgs& a, int s, int first, int end) {
   if (FORK) {
     const Fate f = fate_of(a, s);
     const int whole = f.keep / a.page_tokens;
     const int* src = a.table_in + (size_t)max(f.parent, 0) * a.max_pages;
     int* dst = a.table + (size_t)s * a.max_pages;
-    for (int j = first; j < end; j += step) {
+    if (first == 0 && threadIdx.x == 0) {
       int p = -1;
-      if (j <= whole && f.keep > 0 && (j < whole || f.keep % a.page_tokens)) {
-        p = checked_page(src[j], a.pages, a.status);
-        if (p >= 0) {
-          if (j < whole) {
-            atomicAdd(a.ref + p, 1);
-          } else {
-            atomicMin(a.owner + p, s);
-            p = -1;
-          }
-        }
+      if (f.keep % a.page_tokens) p = checked_page(src[whole], a.pages, a.status);
+      if (p >= 0) atomicMin(a.owner + p, s);
+      a.first[s] = whole;
+      a.src[s] = p;
+      a.before[s] = f.want;
+    }
+    auto take = [&](int j, int p) {
+      if (j >= whole) return -1;
+      p = checked_page(p, a.pages, a.status);
+      if (p >= 0) atomicAdd(a.ref + p, 1);
+      return p;
+    };
+    if ((a.max_pages & 3) == 0) {
+      for (int j = first + 4 * threadIdx.x; j < end; j += 4 * kPageThreads) {
+        int4 p = make_int4(-1, -1, -1, -1);
+        if (j < whole) p = __ldg(reinterpret_cast<const int4*>(src + j));
+        p = make_int4(take(j, p.x), take(j + 1, p.y), take(j + 2, p.z), take(j + 3, p.w));
+        *reinterpret_cast<int4*>(dst + j) = p;
       }
-      dst[j] = p;
+    } else {
+      for (int j = first + threadIdx.x; j < end; j += kPageThreads)
+        dst[j] = take(j, j < whole ? __ldg(src + j) : -1);
     }
   } else {
     const int used = used_pages(a, s);
     const int* src = a.table_in + (size_t)s * a.max_pages;
-    for (int j = first; j < min(end, used); j += step) {
+    for (int j = first + threadIdx.x; j < min(end, used); j += kPageThreads) {
       const int p = checked_page(src[j], a.pages, a.status);
       if (p >= 0) atomicAdd(a.owner + p, 1);
     }
@@ -193,7 +207,7 @@ __device__ void settle(const PageArgs& a, int nb) {
     int low;
     block_scan<T>(n, &low);
     if (threadIdx.x == 0) {
-      low = b < nb ? low + __ldcg(a.blocks + b) : sum;
+      low = b < nb ? low + a.blocks[b] : sum;
       a.sums[kSumLive] = sum;
       a.sums[kSumLow] = low;
       a.counts[0] = sum - low;
@@ -201,39 +215,30 @@ __device__ void settle(const PageArgs& a, int nb) {
     }
     return;
   }
-  int need_sum = 0, pair_sum = 0;
-  for (int s0 = 0; s0 < a.slots; s0 += T) {
-    const int s = s0 + threadIdx.x;
-    int first = 0, need = 0, from = -1, want = 0;
-    if (s < a.slots) {
-      const Fate f = fate_of(a, s);
-      want = f.want;
-      first = f.keep / a.page_tokens;
-      if (f.keep % a.page_tokens) {
-        const int p = a.table_in[(size_t)f.parent * a.max_pages + first];
-        if ((unsigned)p < (unsigned)a.pages) {
-          if (__ldcg(a.owner + p) == s)
-            a.table[(size_t)s * a.max_pages + first++] = p;
-          else
-            from = p;
-        }
-      }
-      need = max(0, pages_of(want, a.page_tokens) - first);
+  // slots <= T
+  const int s = threadIdx.x;
+  int first = 0, need = 0, from = -1, want = 0;
+  if (s < a.slots) {
+    first = __ldcg(a.first + s);
+    want = __ldcg(a.before + s);
+    from = __ldcg(a.src + s);
+    if (from >= 0 && __ldcg(a.owner + from) == s) {
+      a.table[(size_t)s * a.max_pages + first++] = from;
+      from = -1;
     }
-    int total;
-    const int before = need_sum + block_scan<T>(need, &total);
-    need_sum += total;
-    const int got = max(0, min(need, sum - before));
-    const bool copied = from >= 0 && got > 0;
-    const int pair = pair_sum + block_scan<T>(copied, &total);
-    pair_sum += total;
-    if (s < a.slots) {
-      a.first[s] = first;
-      a.before[s] = before;
-      a.src[s] = copied ? pair : -1;
-      if (copied) a.pairs[2 * pair] = from;
-      a.len[s] = got < need ? min(want, (first + got) * a.page_tokens) : want;
-    }
+    need = max(0, pages_of(want, a.page_tokens) - first);
+  }
+  int need_sum, pair_sum;
+  const int before = block_scan<T>(need, &need_sum);
+  const int got = max(0, min(need, sum - before));
+  const bool copied = from >= 0 && got > 0;
+  const int pair = block_scan<T>(copied, &pair_sum);
+  if (s < a.slots) {
+    a.first[s] = first;
+    a.before[s] = before;
+    a.src[s] = copied ? pair : -1;
+    if (copied) a.pairs[2 * pair] = from;
+    a.len[s] = got < need ? min(want, (first + got) * a.page_tokens) : want;
   }
   if (threadIdx.x == 0) {
     a.sums[kSumNeed] = min(need_sum, sum);
@@ -243,32 +248,15 @@ __device__ void settle(const PageArgs& a, int nb) {
   }
 }
 
-// Page p, the at-th of those that count, finds its place.
-template <bool FORK>
-__device__ __forceinline__ void place(const PageArgs& a, int p, int at, bool in) {
-  if (FORK) {
-    if (!in || at >= __ldcg(a.sums + kSumNeed)) return;
-    int lo = 0, hi = a.slots - 1;  // the last slot whose pages begin at or before `at`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldcg(a.before + mid) <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    const int j = at - __ldcg(a.before + lo);
-    a.table[(size_t)lo * a.max_pages + __ldcg(a.first + lo) + j] = p;
-    a.ref[p] = 1;
-    const int pair = __ldcg(a.src + lo);
-    if (j == 0 && pair >= 0) a.pairs[2 * pair + 1] = p;
-  } else {
-    const int live = __ldcg(a.sums + kSumLive);
-    if (in && p >= live) {
-      const int r = at - __ldcg(a.sums + kSumLow);
-      a.rank[p] = r;
-      a.pairs[2 * r] = p;
-    } else if (!in && p < live) {
-      a.pairs[2 * (p - at) + 1] = p;
-    }
+// The last slot whose fresh pages begin at or before the at-th.
+__device__ __forceinline__ int slot_of(const int* before, int slots, int at) {
+  int lo = 0, hi = slots - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] <= at) lo = mid;
+    else hi = mid - 1;
   }
+  return lo;
 }
 
 // Compaction: the new numbers, references and tables.
@@ -308,23 +296,17 @@ __global__ void __launch_bounds__(kPageThreads) count_kernel(const PageArgs a) {
   pdl_enter();
   for (long long at = (long long)blockIdx.y * kCountEntries; at < a.max_pages;
        at += (long long)gridDim.y * kCountEntries)
-    count_pass<FORK>(a, blockIdx.x, (int)at + threadIdx.x,
-                     (int)min((long long)a.max_pages, at + kCountEntries), kPageThreads);
+    count_pass<FORK>(a, blockIdx.x, (int)at, (int)min((long long)a.max_pages, at + kCountEntries));
 }
 
+// A thread per page.
 template <bool FORK>
-__global__ void __launch_bounds__(kPageThreads) rank_kernel(const PageArgs a) {
+__global__ void __launch_bounds__(kScanPages) rank_kernel(const PageArgs a) {
   pdl_enter();
   __shared__ int last;
-  int n = 0;
-  const int p0 = blockIdx.x * kScanPages;
-  for (int p = p0 + threadIdx.x; p < min(a.pages, p0 + kScanPages); p += kPageThreads)
-    n += counts<FORK, true>(a, p);
-  int total;
-  block_scan<kPageThreads>(n, &total);
-  if (threadIdx.x == 0) {
-    a.blocks[blockIdx.x] = total;
-  }
+  const int p = blockIdx.x * kScanPages + threadIdx.x;
+  const int n = __syncthreads_count(p < a.pages && counts<FORK, true>(a, p));
+  if (threadIdx.x == 0) a.blocks[blockIdx.x] = n;
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(a.arrived, 1) == (int)gridDim.x - 1;
@@ -332,53 +314,176 @@ __global__ void __launch_bounds__(kPageThreads) rank_kernel(const PageArgs a) {
   if (!last) return;
   __threadfence();
   if (threadIdx.x == 0) *a.arrived = 0;
-  settle<FORK, kPageThreads>(a, gridDim.x);
+  settle<FORK, kScanPages>(a, gridDim.x);
 }
 
 template <bool FORK>
-__global__ void __launch_bounds__(kPageThreads) place_kernel(const PageArgs a) {
+__global__ void __launch_bounds__(kScanPages) place_kernel(const PageArgs a) {
   pdl_enter();
+  __shared__ int before[PI_CACHE_MAX_SLOTS];
   int at = __ldcg(a.blocks + blockIdx.x);
-  if (FORK && at >= __ldcg(a.sums + kSumNeed)) return;
-  const int p0 = blockIdx.x * kScanPages;
-  for (int q = 0; q < kScanPages; q += kPageThreads) {
-    const int p = p0 + q + threadIdx.x;
-    const bool in = p < a.pages && counts<FORK, false>(a, p);
-    int total;
-    const int mine = block_scan<kPageThreads>(in, &total);
-    if (p < a.pages) place<FORK>(a, p, at + mine, in);
-    at += total;
+  const int need = __ldcg(a.sums + kSumNeed), live = __ldcg(a.sums + kSumLive);
+  const int low = __ldcg(a.sums + kSumLow);
+  if (FORK && at >= need) return;
+  if (FORK && (int)threadIdx.x < a.slots) before[threadIdx.x] = __ldcg(a.before + threadIdx.x);
+  const int p = blockIdx.x * kScanPages + threadIdx.x;
+  const bool in = p < a.pages && counts<FORK, false>(a, p);
+  int total;
+  at += block_scan<kScanPages>(in, &total);
+  if (FORK) {
+    if (!in || at >= need) return;
+    const int s = slot_of(before, a.slots, at), j = at - before[s];
+    a.table[(size_t)s * a.max_pages + __ldcg(a.first + s) + j] = p;
+    a.ref[p] = 1;
+    const int pair = __ldcg(a.src + s);
+    if (j == 0 && pair >= 0) a.pairs[2 * pair + 1] = p;
+  } else if (p < a.pages) {
+    if (in && p >= live) {
+      a.rank[p] = at - low;
+      a.pairs[2 * (at - low)] = p;
+    } else if (!in && p < live) {
+      a.pairs[2 * (p - at) + 1] = p;
+    }
   }
 }
 
-// All passes but the copy, in one block.
+// All passes but the copy in one block, for small pools.  Thread t ranks the
+// pages [t k, t k + k).
 template <bool FORK>
 __global__ void __launch_bounds__(1024) small_kernel(const PageArgs a) {
+  constexpr int T = 1024;
+  extern __shared__ int sh[];
+  int* ref = sh;              // [pages]
+  int* owner = sh + a.pages;  // [pages]: fork: the lowest bidder; else the new number
+  __shared__ int sh_from[T], sh_whole[T], sh_before[T], sh_pair[T];
+  __shared__ int sh_low;
   pdl_enter();
   const int tid = threadIdx.x;
-  clear_pass<FORK>(a, tid, 1024);
-  __syncthreads();
-  for (int s = tid >> 5; s < a.slots; s += 32) count_pass<FORK>(a, s, tid & 31, a.max_pages, 32);
-  __syncthreads();
-  const int nb = (a.pages + kScanPages - 1) / kScanPages;
-  for (int b = 0; b < nb; ++b) {
-    const int p = b * kScanPages + tid;
-    const int n = __syncthreads_count(p < a.pages && counts<FORK, true>(a, p));
-    if (tid == 0) a.blocks[b] = n;
+  const int entries = a.slots * a.max_pages;
+  // what becomes of the slots; the pages' references
+  int last = -1, want = 0;
+  if (tid < a.slots) {
+    if (FORK) {
+      const Fate f = fate_of(a, tid);
+      sh_whole[tid] = f.keep / a.page_tokens;
+      sh_from[tid] = f.parent;
+      want = f.want;
+      if (f.keep % a.page_tokens)
+        last = checked_page(a.table_in[(size_t)f.parent * a.max_pages + f.keep / a.page_tokens],
+                            a.pages, a.status);
+    } else {
+      sh_whole[tid] = used_pages(a, tid);
+      sh_from[tid] = tid;
+    }
+  }
+  for (int p = tid; p < a.pages; p += T) {
+    ref[p] = a.held ? a.held[p] : 0;
+    owner[p] = kNobody;
   }
   __syncthreads();
-  settle<FORK, 1024>(a, nb);
-  __syncthreads();
-  for (int b = 0; b < nb; ++b) {
-    const int p = b * kScanPages + tid;
-    const bool in = p < a.pages && counts<FORK, false>(a, p);
-    int total;
-    const int mine = block_scan<1024>(in, &total);
-    if (p < a.pages) place<FORK>(a, p, __ldcg(a.blocks + b) + mine, in);
+#pragma unroll 4
+  for (int e = tid; e < entries; e += T) {
+    const int s = e / a.max_pages, j = e - s * a.max_pages;
+    int p = -1;
+    if (j < sh_whole[s])
+      p = checked_page(a.table_in[(size_t)sh_from[s] * a.max_pages + j], a.pages, a.status);
+    if (p >= 0) atomicAdd(ref + p, 1);
+    if (FORK) a.table[e] = p;
   }
-  if (!FORK) {
+  if (last >= 0) atomicMin(owner + last, tid);
+  __syncthreads();
+  // ranks
+  const int k = (a.pages + T - 1) / T, p0 = min(a.pages, tid * k), p1 = min(a.pages, p0 + k);
+  int n = 0;
+  for (int p = p0; p < p1; ++p) {
+    if (FORK) {
+      if (ref[p] > 0) owner[p] = kNobody;
+      else if (owner[p] != kNobody) ref[p] = 1;
+    }
+    n += FORK ? ref[p] == 0 : ref[p] > 0;
+  }
+  int sum;
+  int at = block_scan<T>(n, &sum);
+  if (FORK) {
+    int first = 0, need = 0;
+    if (tid < a.slots) {
+      first = sh_whole[tid];
+      if (last >= 0 && owner[last] == tid) {
+        a.table[(size_t)tid * a.max_pages + first++] = last;
+        last = -1;
+      }
+      need = max(0, pages_of(want, a.page_tokens) - first);
+    }
+    int need_sum, pair_sum;
+    const int before = block_scan<T>(need, &need_sum);
+    const int got = max(0, min(need, sum - before));
+    const bool copied = last >= 0 && got > 0;
+    const int pair = block_scan<T>(copied, &pair_sum);
+    if (tid < a.slots) {
+      sh_whole[tid] = first;
+      sh_before[tid] = before;
+      sh_pair[tid] = copied ? pair : -1;
+      if (copied) a.pairs[2 * pair] = last;
+      a.len[tid] = got < need ? min(want, (first + got) * a.page_tokens) : want;
+    }
+    need_sum = min(need_sum, sum);
+    if (tid == 0) {
+      a.counts[0] = pair_sum;
+      a.counts[1] = a.pages - sum + need_sum;
+    }
+    if (got < need) set_status(a.status, PI_ERR_CAPACITY);
     __syncthreads();
-    map_pass(a, tid, 1024);
+    for (int p = p0; p < p1; ++p) {
+      if (ref[p]) continue;
+      if (at < need_sum) {
+        const int s = slot_of(sh_before, a.slots, at), j = at - sh_before[s];
+        a.table[(size_t)s * a.max_pages + sh_whole[s] + j] = p;
+        ref[p] = 1;
+        if (j == 0 && sh_pair[s] >= 0) a.pairs[2 * sh_pair[s] + 1] = p;
+      }
+      ++at;
+    }
+    __syncthreads();
+    for (int p = tid; p < a.pages; p += T) a.ref[p] = ref[p];
+  } else {
+    // `sum` pages are live; `low` of them are below that number
+    if (p0 <= sum && (sum < p1 || tid == T - 1)) {
+      int low = at;
+      for (int p = p0; p < min(p1, sum); ++p) low += ref[p] > 0;
+      if (sum < p1 || p1 == a.pages) sh_low = low;
+    }
+    __syncthreads();
+    const int low = sh_low;
+    if (tid == 0) {
+      a.counts[0] = sum - low;
+      a.counts[1] = sum;
+    }
+    for (int p = p0; p < p1; ++p) {
+      if (ref[p] > 0) {
+        if (p >= sum) a.pairs[2 * (at - low)] = p;
+        owner[p] = p < sum ? p : at - low;  // a mover's place among them
+        ++at;
+      } else if (p < sum) {
+        a.pairs[2 * (p - at) + 1] = p;
+      }
+    }
+    __syncthreads();
+    for (int p = tid; p < a.pages; p += T) {
+      int to = -1;
+      if (ref[p] > 0) {
+        to = p < sum ? p : a.pairs[2 * owner[p] + 1];
+        owner[p] = to;
+        a.ref[to] = ref[p];
+      }
+      a.map[p] = to;
+      if (p >= sum) a.ref[p] = 0;
+    }
+    __syncthreads();
+    for (int e = tid; e < entries; e += T) {
+      const int s = e / a.max_pages, j = e - s * a.max_pages;
+      const int p = j < sh_whole[s] ? a.table_in[e] : -1;
+      a.table[e] = (unsigned)p < (unsigned)a.pages && ref[p] > 0 ? owner[p] : -1;
+    }
   }
 }
 
@@ -444,28 +549,34 @@ static CopyArgs copy_args(const pi_cache_desc& C, const int* pairs, const int* c
                   (int)((page16 + 127) / 128)};
 }
 
-static unsigned copy_grid() {
+// Eight blocks per SM, or what `cap` pairs can use.
+static unsigned copy_grid(const CopyArgs& c) {
   DevInfo di;
-  return dev_info(&di) == PI_OK ? (unsigned)di.sms * 8 : 0;
+  if (dev_info(&di) != PI_OK) return 0;
+  const long long most = ((long long)c.cap * c.layers * c.parts + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+  return (unsigned)(most < di.sms * 8 ? (most > 0 ? most : 1) : di.sms * 8);
 }
 
 static pi_status launch_copy(const CopyArgs& c, pi_stream stream) {
-  const unsigned grid = copy_grid();
+  const unsigned grid = copy_grid(c);
   return grid ? launch(copy_kernel, dim3(grid), kCopyThreads, 0, stream, c) : PI_ERR_CUDA;
 }
 
 // The passes up to `place` (and a small compaction's map).
 template <bool FORK>
 static pi_status launch_passes(const PageArgs& a, pi_stream stream) {
-  if (one_block(a)) return launch(small_kernel<FORK>, dim3(1), 1024, 0, stream, a);
+  if (is_small(a)) {
+    const pi_status st = ensure_smem(reinterpret_cast<const void*>(small_kernel<FORK>), 8 * kSmallPages);
+    return st == PI_OK ? launch(small_kernel<FORK>, dim3(1), 1024, 8 * (size_t)a.pages, stream, a) : st;
+  }
   const unsigned nb = (unsigned)((a.pages + kScanPages - 1) / kScanPages);
-  const unsigned parts = (unsigned)a.max_pages / kCountEntries + 1;
+  const unsigned parts = ((unsigned)a.max_pages + kCountEntries - 1) / kCountEntries;
   const dim3 entries((unsigned)a.slots, parts < 65535 ? parts : 65535);
   const unsigned clear = (unsigned)((a.pages + kPageThreads - 1) / kPageThreads);
   pi_status st = launch(clear_kernel<FORK>, dim3(clear < 1216 ? clear : 1216), kPageThreads, 0, stream, a);
   if (st == PI_OK) st = launch(count_kernel<FORK>, entries, kPageThreads, 0, stream, a);
-  if (st == PI_OK) st = launch(rank_kernel<FORK>, dim3(nb), kPageThreads, 0, stream, a);
-  if (st == PI_OK) st = launch(place_kernel<FORK>, dim3(nb), kPageThreads, 0, stream, a);
+  if (st == PI_OK) st = launch(rank_kernel<FORK>, dim3(nb), kScanPages, 0, stream, a);
+  if (st == PI_OK) st = launch(place_kernel<FORK>, dim3(nb), kScanPages, 0, stream, a);
   return st;
 }
 
@@ -560,8 +671,8 @@ pi_status pi_cache_compact(const pi_cache_desc* cache, int32_t slots, int32_t ma
   st = launch_passes<false>(a, stream);
   if (st != PI_OK) return st;
   const CopyArgs c = copy_args(C, pairs, counts, C.pages / 2, pool, dev_status);
-  if (one_block(a)) return pool ? launch_copy(c, stream) : PI_OK;
-  const unsigned grid = copy_grid();
+  if (is_small(a)) return pool ? launch_copy(c, stream) : PI_OK;
+  const unsigned grid = copy_grid(c);
   return grid ? launch(map_copy_kernel, dim3(grid), kCopyThreads, 0, stream, a, c) : PI_ERR_CUDA;
 }
 

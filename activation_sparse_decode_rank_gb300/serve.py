@@ -40,9 +40,16 @@ SIGNATURES = {
 }
 
 
+_L = None
+
+
 def _pkg():
-    from . import lib
-    return lib()
+    """The loaded libpi.so (looked up once)."""
+    global _L
+    if _L is None:
+        from . import lib
+        _L = lib()
+    return _L
 
 
 def _ptr(t):
@@ -51,15 +58,25 @@ def _ptr(t):
     return t if isinstance(t, int) else t.data_ptr()
 
 
+def _current_stream():
+    """Handle of torch's current stream.  These operators run for a few
+    microseconds, and making torch's stream object alone takes three, so the
+    handle is taken without one where torch offers that."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     return s if isinstance(s, int) else s.cuda_stream
 
 
 def _ws_bytes(ws, ws_bytes):
-    return ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    return ws.nbytes if ws_bytes is None else ws_bytes
 
 
 def make_cache_desc(layers: int, pages: int, kv_heads: int, head_dim: int, page_tokens: int,
