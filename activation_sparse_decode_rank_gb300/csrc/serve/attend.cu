@@ -753,38 +753,70 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   }
 }
 
-// Thread = eight elements of one (token, K or V, kv head) row.
-template <int DT>
-__global__ void __launch_bounds__(256) append_kernel(const float* k, const float* v,
-                                                     const int* slot, const int* pos,
-                                                     const int* table, uint16_t* pool,
-                                                     long long total, int kv_heads, int head_dim,
-                                                     int page_tokens, int pages, int slots,
-                                                     int max_pages, int* status) {
+// A thread stores N pieces of eight elements, 256 pieces apart, of the line
+// (token, K or V, kv head, piece): all its reads are under way before the
+// first store.  Bound: HBM bandwidth (fp32 rows in, 16-bit rows out).  N = 4
+// for prompts (12001 tokens of 32 heads of 128: 97 us, 90 % of the measured
+// copy rate; N = 1: 104.7), 1 where N = 4 would leave SMs without a block (32
+// tokens of 40 heads: 2.4 us against 3.2).
+
+struct AppendArgs {
+  const float *k, *v;
+  const int *slot, *pos, *table;
+  uint16_t* pool;  // the layer's pages
+  int* status;
+  long long total;  // pieces
+  int kv_heads, head_dim, page_tokens, pages, slots, max_pages;
+};
+
+template <int DT, int N>
+__global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
   pdl_enter();
-  const int pieces = head_dim >> 3;
-  for (long long e = blockIdx.x * 256ll + threadIdx.x; e < total; e += gridDim.x * 256ll) {
-    const int pc = (int)(e % pieces);
-    const long long r = e / pieces;  // (token, kind, head)
-    const int g = (int)(r % kv_heads);
-    const long long tk = r / kv_heads;
-    const int kind = (int)(tk & 1);
-    const int i = (int)(tk >> 1);
-    const int s = slot[i], p = pos[i];
-    if (s == -1) continue;
-    if (s < 0 || s >= slots || p < 0 || p >= max_pages * page_tokens) {
-      set_status(status, PI_ERR_INDEX);
-      continue;
+  const int pieces = a.head_dim >> 3, half = a.kv_heads * pieces;
+  for (long long e0 = blockIdx.x * (256ll * N) + threadIdx.x; e0 < a.total;
+       e0 += gridDim.x * (256ll * N)) {
+    float4 f[N][2];
+    int s[N], p[N], r[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const long long e = e0 + u * 256;
+      s[u] = -1;
+      if (e >= a.total) continue;
+      const int i = (int)quotient(e, 2 * half);
+      r[u] = (int)(e - (long long)i * (2 * half));
+      s[u] = __ldg(a.slot + i);
+      p[u] = __ldg(a.pos + i);
+      const bool val = r[u] >= half;
+      const float4* src = reinterpret_cast<const float4*>(val ? a.v : a.k) +
+                          2 * ((size_t)i * half + (r[u] - (val ? half : 0)));
+      f[u][0] = __ldcs(src);
+      f[u][1] = __ldcs(src + 1);
     }
-    const int page = checked_page(table[(size_t)s * max_pages + p / page_tokens], pages, status);
-    if (page < 0) continue;
-    const float4* src = reinterpret_cast<const float4*>((kind ? v : k) +
-                                                        ((size_t)i * kv_heads + g) * head_dim) + 2 * pc;
-    const float4 f0 = src[0], f1 = src[1];
-    uint16_t* dst = pool + ((((size_t)page * 2 + kind) * kv_heads + g) * page_tokens +
-                            p % page_tokens) * head_dim + 8 * pc;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bits<DT>(f0.x, f0.y), pack_bits<DT>(f0.z, f0.w),
-                                                pack_bits<DT>(f1.x, f1.y), pack_bits<DT>(f1.z, f1.w));
+    int page[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (s[u] == -1) continue;
+      if ((unsigned)s[u] >= (unsigned)a.slots || p[u] < 0 || p[u] >= a.max_pages * a.page_tokens) {
+        set_status(a.status, PI_ERR_INDEX);
+        s[u] = -1;
+        continue;
+      }
+      const int j = p[u] / a.page_tokens;
+      page[u] = __ldg(a.table + (size_t)s[u] * a.max_pages + j);
+      p[u] -= j * a.page_tokens;
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (s[u] == -1) continue;
+      if (checked_page(page[u], a.pages, a.status) < 0) continue;
+      const bool val = r[u] >= half;
+      const int q = r[u] - (val ? half : 0), g = q / pieces;
+      uint16_t* dst = a.pool + ((((size_t)page[u] * 2 + val) * a.kv_heads + g) * a.page_tokens + p[u]) *
+                                   a.head_dim + 8 * (q - g * pieces);
+      const float4 x = f[u][0], y = f[u][1];
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bits<DT>(x.x, x.y), pack_bits<DT>(x.z, x.w),
+                                                  pack_bits<DT>(y.x, y.y), pack_bits<DT>(y.z, y.w));
+    }
   }
 }
 
@@ -891,13 +923,19 @@ pi_status pi_cache_append(const pi_cache_desc* cache, int32_t layer, int32_t slo
   if (tokens > 0 && (!slot || !pos || !k || !v)) return PI_ERR_NULL;
   if (!all_aligned(slot, pos, k, v, table, pool, dev_status)) return PI_ERR_ALIGN;
   if (tokens == 0) return PI_OK;
-  const long long total = 2ll * tokens * C.kv_heads * (C.head_dim / 8);
-  const long long blocks = (total + 255) / 256;
-  uint16_t* base = static_cast<uint16_t*>(pool) + (size_t)layer * C.pages * page_elems(C);
-  return launch(C.dtype == PI_F16 ? append_kernel<0> : append_kernel<1>,
-                dim3((unsigned)(blocks < 152 * 64 ? blocks : 152 * 64)), 256, 0, stream, k, v, slot,
-                pos, table, base, total, C.kv_heads, C.head_dim, C.page_tokens, C.pages, slots,
-                max_pages, dev_status);
+  AppendArgs a{k, v, slot, pos, table,
+               static_cast<uint16_t*>(pool) + (size_t)layer * C.pages * page_elems(C), dev_status,
+               2ll * tokens * C.kv_heads * (C.head_dim / 8), C.kv_heads, C.head_dim, C.page_tokens,
+               C.pages, slots, max_pages};
+  DevInfo di;
+  st = dev_info(&di);
+  if (st != PI_OK) return st;
+  const bool many = a.total >= 1024ll * di.sms;
+  const long long blocks = many ? (a.total + 1023) / 1024 : (a.total + 255) / 256;
+  const bool f16 = C.dtype == PI_F16;
+  return launch(many ? (f16 ? append_kernel<0, 4> : append_kernel<1, 4>)
+                     : (f16 ? append_kernel<0, 1> : append_kernel<1, 1>),
+                dim3((unsigned)(blocks < 65536 ? blocks : 65536)), 256, 0, stream, a);
 }
 
 }  // extern "C"
