@@ -1,5 +1,9 @@
 // attend.cu — attention of one new token per slot over a paged cache, and
 // the stores of new keys and values (include/pi_serve.h).
+#include <cuda.h>
+
+#include <cstdlib>
+
 #include "serve.cuh"
 
 namespace pis {
@@ -35,11 +39,14 @@ namespace pis {
 // thread blocks by the last of them to arrive, in block order (no waiting;
 // the order of the sums is fixed).
 //
-// Data flow.  A warp streams its tiles through its own ring of cp.async
-// stages, without any block-wide barrier until the end; page numbers are
-// fetched one tile ahead of their use; rows outside the visible set are
-// never read (zero-filled).  Head dimensions below 64, 128 or 256 are padded
-// with zeros in shared memory only.
+// Data flow.  A warp streams its tiles through its own ring of stages, without
+// any block-wide barrier until the end.  Where pages hold multiples of 16
+// tokens a tile lies in one page: one lane orders its K and V as TMA boxes of
+// 16 rows x 128 bytes, swizzled, that arrive on the stage's mbarrier (rows of
+// a box outside the visible set are cleared before use).  Other page sizes,
+// head dimensions below 64 and pools of 2^31 rows or more gather row pieces
+// with cp.async into the same layout.  Head dimensions below 64, 128 or 256
+// are padded with zeros in shared memory only.
 struct AttendArgs {
   const float *q, *k_new, *v_new;
   const int *table, *len;
@@ -52,7 +59,9 @@ struct AttendArgs {
   int slots, heads, kv_heads, group, head_dim, page_tokens, pages, max_pages, window, sinks;
   int tiles;      // head tiles per kv head: ceil(group / (8 MT))
   int page_shift; // log2(page_tokens), or -1
+  int tma;        // tiles come as TMA boxes
   float scale;    // scale log2(e)
+  unsigned long long limit_ns;  // of a wait for a tile
 };
 
 constexpr int kAttWarps = 4;
@@ -73,14 +82,60 @@ __host__ __device__ constexpr int att_smem() {
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
+// mbarriers (one arrival each: the lane that orders a tile) and TMA boxes.
+__device__ __forceinline__ void mbar_init(uint64_t* m, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(m)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void fence_mbar_init() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Orders this thread's writes to shared memory before later TMA writes there.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* m, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* m, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(m)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase of that parity, for limit_ns at most; the warp agrees.
+__device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, unsigned long long limit_ns) {
+  bool ok = mbar_try(m, parity);
+  if (!__all_sync(~0u, ok)) {
+    const unsigned long long t0 = now_ns();
+    while (!__all_sync(~0u, ok = ok || mbar_try(m, parity)))
+      if (__any_sync(~0u, now_ns() - t0 > limit_ns)) return false;
+  }
+  return true;
+}
+// 16 rows of 64 elements at (x, y) of the pool's rows -> shared memory.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(m))
+      : "memory");
+}
 // 16 bytes global -> shared, or zeros where bytes = 0 (the source is not read).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -247,15 +302,16 @@ struct Piece {
 };
 
 template <int DT, int DP, int MT>
-__global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int S = att_stages<DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
-  constexpr int kRow = DP * 2;             // bytes of a staged row
+  constexpr int kPanel = 16 * 128;         // 16 rows of 64 elements: a tile is DP / 64 panels
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
   constexpr float kShift = DT == 0 ? 14.f : 0.f;  // weights carry 2^kShift
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ int s_last[2];
   __shared__ uint32_t s_mask[kAttWarps][S];
+  __shared__ __align__(8) uint64_t s_bar[kAttWarps][S];
   __shared__ float s_m[kAttWarps][2][8 * MT], s_l[kAttWarps][2][8 * MT];
   __shared__ Piece s_piece[kAttWarps][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -268,6 +324,9 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
     return a.wpart + ((size_t)blockIdx.x * kAttWarps + w) * (8 * MT) * DP;
   };
   if (lane < 2) s_piece[warp][lane].at = -1;
+  if (lane < S) mbar_init(&s_bar[warp][lane], 1);
+  fence_mbar_init();
+  __syncwarp();
   pdl_enter();
 
   // The warp's share of the line.  Lane t sums the slots [t k, t k + k).
@@ -377,11 +436,9 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       next_page = next_rows >> (lane & 15) & 1u ? __ldg(row + j) : -2;
     }
   };
-  // Sends that tile into a stage.  A lane's piece of row r = r_lane + i k (k
-  // rows per instruction) goes to piece ^ (r & 7): r_lane < k, so the xor
-  // splits into a lane's part and a constant.
-  constexpr int kRows = 32 / kPieces;  // 4, 2, 1 rows per instruction
-  const uint32_t lane_dst = (lane / kPieces) * kRow + (((lane % kPieces) ^ (lane / kPieces)) << 4);
+  // Sends that tile into a stage.  Piece pc of row r lies in panel pc / 8 at
+  // piece (pc ^ r) & 7 of its row.
+  constexpr int kRows = 32 / kPieces;  // rows per instruction of the gather: 4, 2, 1
   auto issue = [&](int stage) {
     if (one_page) next_page = __shfl_sync(~0u, pages32, lc.tile - page0);
     const bool ok = (unsigned)next_page < (unsigned)a.pages;
@@ -392,21 +449,25 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
     else
       rows &= __ballot_sync(~0u, ok);
     if (lane == 0) s_mask[warp][stage] = rows;
-    // the new token's row comes from k_new / v_new when the tile is used
-    if (a.k_new && next_t < lc.v.n && lc.v.n - next_t <= 16) rows &= ~(1u << (lc.v.n - 1 - next_t));
     const long long row = ok ? ((long long)next_page * 2 * a.kv_heads + lc.g) * P + next_row : 0;
-    const uint32_t dst = ring + stage * 2 * kTile + lane_dst;
-    const int pc = lane % kPieces;
-    if (one_page && rows == 0xffffu && D == DP) {  // 16 whole rows side by side
-      const uint16_t* p = a.pool + row * DP + lane * 8;
+    const uint32_t k0 = ring + stage * 2 * kTile;
+    if (a.tma) {
+      if (lane == 0) {
+        uint64_t* bar = &s_bar[warp][stage];
+        mbar_expect(bar, rows ? 2 * kTile : 0);
+        if (rows) {
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i) {
-        const uint32_t to = (dst ^ (((i * kRows) & 7) << 4)) + i * kRows * kRow;
-        cp16(to, p + i * 256);
-        cp16(to + kTile, p + v_off + i * 256);
+          for (int c = 0; c < DP / 64; ++c) {
+            tma_box(k0 + c * kPanel, &map, 64 * c, (int)row, bar);
+            tma_box(k0 + kTile + c * kPanel, &map, 64 * c, (int)row + a.kv_heads * P, bar);
+          }
+        }
       }
       return;
     }
+    // the new token's row comes from k_new / v_new when the tile is used
+    if (a.k_new && next_t < lc.v.n && lc.v.n - next_t <= 16) rows &= ~(1u << (lc.v.n - 1 - next_t));
+    const int pc = lane % kPieces;
 #pragma unroll 2
     for (int i = 0; i < DP / 16; ++i) {
       const int r = lane / kPieces + i * kRows;
@@ -415,14 +476,15 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       if (pc < pieces) {
         const bool take = rows >> r & 1u;
         const uint16_t* p = a.pool + (take ? (size_t)src * D + 8 * pc : 0);
-        const uint32_t to = (dst ^ (((i * kRows) & 7) << 4)) + i * kRows * kRow;
+        const uint32_t to = k0 + (pc >> 3) * kPanel + r * 128 + (((pc ^ r) & 7) << 4);
         cp16(to, p, take ? 16 : 0);
         cp16(to + kTile, p + (take ? v_off : 0), take ? 16 : 0);
       }
     }
+    cp_commit();
   };
 
-  if (D < DP)  // the padding: zeros that no copy overwrites
+  if (D < DP && !a.tma)  // the padding: zeros that no copy overwrites
     for (int e = lane; e < S * 2 * kTile / 16; e += 32)
       *reinterpret_cast<uint4*>(smem + warp * S * 2 * kTile + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
   __syncwarp();
@@ -432,13 +494,16 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   float o[MT][DP / 8][2], m[MT], l[MT], unit_scale[MT];
   bool fresh = true;
   int ahead = 0, load_stage = 0, stage = 0;
+  uint32_t parity = 0;
+  bool late = false;
   while (cc.pos < share1) {
     if (lc.pos < share1) {
       issue(load_stage);
       lc.advance(a);
       if (lc.pos < share1) fetch(lc.tile == 0);
+    } else if (!a.tma) {
+      cp_commit();  // an empty group: the count below stays the same
     }
-    cp_commit();
     load_stage = load_stage == S - 1 ? 0 : load_stage + 1;
     if (ahead < S - 1) {  // fill the ring first
       ++ahead;
@@ -486,11 +551,28 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
     }
 
-    cp_wait<S - 1>();
+    if (a.tma) {
+      if (!mbar_wait(&s_bar[warp][stage], parity, a.limit_ns)) {
+        set_status(a.status, PI_ERR_TIMEOUT);
+        late = true;
+        break;
+      }
+    } else {
+      cp_wait<S - 1>();
+    }
     __syncwarp();
 
     const uint32_t k0 = ring + stage * 2 * kTile, v0 = k0 + kTile;
     const uint32_t mask = s_mask[warp][stage];
+    if (a.tma && mask != 0xffffu && mask != 0) {
+      // values of rows that are not visible: 0 x NaN is not 0
+      for (int e = lane; e < 16 * kPieces; e += 32)
+        if (!(mask >> (e >> 3 & 15) & 1u))
+          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + kTile + (e >> 7) * kPanel +
+                                    (e & 127) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async();
+      __syncwarp();
+    }
     if (a.k_new) {
       uint32_t rows;
       const int t = cc.rows_of(rows);
@@ -506,10 +588,11 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
           const float4 x = __ldg(src), y = __ldg(src + 1);
           const uint4 w = make_uint4(pack_bits<DT>(x.x, x.y), pack_bits<DT>(x.z, x.w),
                                      pack_bits<DT>(y.x, y.y), pack_bits<DT>(y.z, y.w));
-          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + kind * kTile + r * kRow +
-                                    ((pc ^ (r & 7)) << 4)) = w;
+          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + kind * kTile +
+                                    (pc >> 3) * kPanel + r * 128 + (((pc ^ r) & 7) << 4)) = w;
           if (ht == 0) *reinterpret_cast<uint4*>(dst + kind * v_off + 8 * pc) = w;
         }
+        fence_async();
         __syncwarp();
       }
     }
@@ -519,11 +602,11 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       float sc[MT][2][2][4];  // even and odd steps: shorter chains
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), pc = (lane >> 3) & 1;
-        const uint32_t at = k0 + r * kRow + ((pc ^ (r & 7)) << 4);
+        const uint32_t at = k0 + r * 128 + ((pc ^ (r & 7)) << 4);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
           uint32_t b[4];
-          ldsm4(b, at ^ (ks << 5));
+          ldsm4(b, (at ^ ((ks & 3) << 5)) + (ks >> 2) * kPanel);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -575,11 +658,11 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
       // weighted values; each tile's product is rounded once into the fp32 sums
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), pc = lane >> 4;
-      const uint32_t at = v0 + r * kRow + ((pc ^ (r & 7)) << 4);
+      const uint32_t at = v0 + r * 128 + ((pc ^ (r & 7)) << 4);
 #pragma unroll
       for (int jj = 0; jj < DP / 16; ++jj) {
         uint32_t b[4];
-        ldsm4t(b, at ^ (jj << 5));
+        ldsm4t(b, (at ^ ((jj & 3) << 5)) + (jj >> 2) * kPanel);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -640,8 +723,19 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       fresh = true;
     }
     cc.advance(a);
-    stage = stage == S - 1 ? 0 : stage + 1;
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
     __syncwarp();  // the stage may be overwritten
+  }
+  // After a wait that ran out: the copies under way land before the block ends.
+  for (int i = 0; late && i < S && (i == 0 || stage != load_stage); ++i) {
+    mbar_wait(&s_bar[warp][stage], parity, 2000000000ull);
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
 
   // Units shared by warps.  A unit's warps within the block: the one that
@@ -820,8 +914,42 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
   }
 }
 
+// Map over a layer's rows (K and V rows of every page and kv head) in boxes of
+// 16 rows x 64 elements, 128-byte swizzle, zeros past the row's end.  False
+// where the driver offers no such map.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static bool make_rows_map(CUtensorMap* m, void* base, long long rows, int head_dim) {
+  static const EncodeFn encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
+  const cuuint32_t box[2] = {64u, 16u}, steps[2] = {1u, 1u};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Limit of a wait: 1 s, or PI_WAIT_LIMIT_NS as for the FFN kernels.
+static unsigned long long wait_limit() {
+  static const unsigned long long limit = [] {
+    const char* e = std::getenv("PI_WAIT_LIMIT_NS");
+    const unsigned long long v = e ? std::strtoull(e, nullptr, 10) : 0;
+    return v >= 1000ull && v <= 10000000000ull ? v : 1000000000ull;
+  }();
+  return limit;
+}
+
 template <int DT, int DP, int MT>
-pi_status launch_attend(const AttendArgs& a, pi_stream stream) {
+pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
   DevInfo di;
   pi_status st = dev_info(&di);
   if (st != PI_OK) return st;
@@ -837,7 +965,8 @@ pi_status launch_attend(const AttendArgs& a, pi_stream stream) {
   long long grid = di.sms * (DP == 256 ? 1 : 2);
   if (grid > kAttendGrid) grid = kAttendGrid;
   if (grid > useful) grid = useful;
-  return launch(attend_kernel<DT, DP, MT>, dim3((unsigned)grid), kAttThreads, smem, stream, a);
+  return launch(attend_kernel<DT, DP, MT>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
+                map);
 }
 
 }  // namespace pis
@@ -896,16 +1025,21 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   a.window = window;
   a.sinks = sinks;
   a.scale = scale * 1.4426950408889634f;
+  const long long rows = (long long)C.pages * 2 * C.kv_heads * C.page_tokens;
+  CUtensorMap map = {};
+  a.limit_ns = wait_limit();
+  a.tma = C.page_tokens % 16 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
+          make_rows_map(&map, a.pool, rows, C.head_dim);
   const bool two = att_two_tiles(C.head_dim, a.group);
   a.tiles = (a.group + (two ? 15 : 7)) / (two ? 16 : 8);
   if (C.dtype == PI_F16) {
-    if (C.head_dim <= 64) return two ? launch_attend<0, 64, 2>(a, stream) : launch_attend<0, 64, 1>(a, stream);
-    if (C.head_dim <= 128) return two ? launch_attend<0, 128, 2>(a, stream) : launch_attend<0, 128, 1>(a, stream);
-    return launch_attend<0, 256, 1>(a, stream);
+    if (C.head_dim <= 64) return two ? launch_attend<0, 64, 2>(a, map, stream) : launch_attend<0, 64, 1>(a, map, stream);
+    if (C.head_dim <= 128) return two ? launch_attend<0, 128, 2>(a, map, stream) : launch_attend<0, 128, 1>(a, map, stream);
+    return launch_attend<0, 256, 1>(a, map, stream);
   }
-  if (C.head_dim <= 64) return two ? launch_attend<1, 64, 2>(a, stream) : launch_attend<1, 64, 1>(a, stream);
-  if (C.head_dim <= 128) return two ? launch_attend<1, 128, 2>(a, stream) : launch_attend<1, 128, 1>(a, stream);
-  return launch_attend<1, 256, 1>(a, stream);
+  if (C.head_dim <= 64) return two ? launch_attend<1, 64, 2>(a, map, stream) : launch_attend<1, 64, 1>(a, map, stream);
+  if (C.head_dim <= 128) return two ? launch_attend<1, 128, 2>(a, map, stream) : launch_attend<1, 128, 1>(a, map, stream);
+  return launch_attend<1, 256, 1>(a, map, stream);
 }
 
 pi_status pi_cache_append(const pi_cache_desc* cache, int32_t layer, int32_t slots,

@@ -142,7 +142,8 @@ class Cache:
 
 SHAPES = [  # heads, kv_heads, head_dim, page
     (4, 4, 64, 16), (8, 1, 128, 16), (6, 2, 80, 24), (32, 2, 128, 32), (5, 5, 96, 7),
-    (3, 1, 256, 128), (12, 1, 8, 1), (40, 2, 72, 16), (14, 2, 200, 8),
+    (3, 1, 256, 128), (12, 1, 8, 1), (40, 2, 72, 16), (14, 2, 200, 8), (2, 1, 136, 16),
+    (4, 2, 96, 48), (18, 2, 112, 64), (64, 4, 256, 16), (33, 1, 64, 32), (4, 2, 40, 16),
 ]
 LENS = [0, 1, 15, 16, 17, 33, 64, 100, 257]
 
