@@ -59,7 +59,7 @@ struct AttendArgs {
   int slots, heads, kv_heads, group, head_dim, page_tokens, pages, max_pages, window, sinks;
   int tiles;      // head tiles per kv head: ceil(group / (8 MT))
   int page_shift; // log2(page_tokens), or -1
-  int tma;        // tiles come as TMA boxes
+  int tma;        // tiles come as TMA boxes: 1 a panel, 2 a whole tile each
   float scale;    // scale log2(e)
   unsigned long long limit_ns;  // of a wait for a tile
 };
@@ -130,6 +130,14 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
       "%3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(m))
+      : "memory");
+}
+// The K and the V tile at row y of the pool's rows (panels, then K / V).
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int y, uint64_t* m) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %2, %2}], [%4];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(y), "r"(smem_u32(m))
       : "memory");
 }
 // 16 bytes global -> shared, or zeros where bytes = 0 (the source is not read).
@@ -252,9 +260,8 @@ struct Cursor {
   __device__ __forceinline__ int rows_of(uint32_t& rows) const {
     const int t = first_token();
     const bool sink = tile < v.first_tiles;
-    const int r0 = sink ? 0 : v.tail - t, r1 = (sink ? v.first : v.n) - t;
-    rows = r1 >= 16 ? 0xffffu : 0xffffu >> (16 - r1);
-    if (r0 > 0) rows &= 0xffffu << r0;
+    const int r1 = (sink ? v.first : v.n) - t, r0 = sink ? 0 : v.tail - t;
+    rows = 0xffffu >> (16 - min(r1, 16)) & 0xffffu << max(r0, 0);
     return t;
   }
 };
@@ -309,7 +316,6 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
   constexpr float kShift = DT == 0 ? 14.f : 0.f;  // weights carry 2^kShift
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ int s_last[2];
   __shared__ uint32_t s_mask[kAttWarps][S];
   __shared__ __align__(8) uint64_t s_bar[kAttWarps][S];
   __shared__ float s_m[kAttWarps][2][8 * MT], s_l[kAttWarps][2][8 * MT];
@@ -455,8 +461,10 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       if (lane == 0) {
         uint64_t* bar = &s_bar[warp][stage];
         mbar_expect(bar, rows ? 2 * kTile : 0);
-        if (rows) {
-#pragma unroll
+        if (rows && a.tma == 2) {
+          tma_tile(k0, &map, (int)row, bar);
+        } else if (rows) {
+#pragma unroll 1
           for (int c = 0; c < DP / 64; ++c) {
             tma_box(k0 + c * kPanel, &map, 64 * c, (int)row, bar);
             tma_box(k0 + kTile + c * kPanel, &map, 64 * c, (int)row + a.kv_heads * P, bar);
@@ -742,94 +750,102 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   // begins it (piece 1) or the block's first (piece 0), then the followers'
   // pieces 0.  Units that other blocks share too (at most one that came in,
   // one that goes on) are left as one part for the block, and joined by the
-  // last block that arrives.
+  // last block that arrives.  A warp joins a row of a unit at a time.
   cp_wait<0>();
   __syncthreads();
-  const int vecs = D >> 2, prow = D + 4;
-  int first_block[2] = {0, 0}, last_block[2] = {-1, -1}, cross_k[2] = {0, 0};
+  const int prow = D + 4;
+  const long long block_end = line.start(blockIdx.x + 1);
+  bool crossing = false;
 #pragma unroll 1
-  for (int k = -1; k < kAttWarps; ++k) {
-    const int w0 = max(k, 0);
+  for (int item = warp; item < (kAttWarps + 1) * 8 * MT; item += kAttWarps) {
+    const int k = item / (8 * MT) - 1, hr = item % (8 * MT), w0 = max(k, 0);
     const Piece& pc = s_piece[w0][k < 0 ? 0 : 1];
-    if (pc.at < 0) continue;
+    if (pc.at < 0 || pc.ht * 8 * MT + hr >= a.group) continue;
     int w1 = w0 + 1;
     while (w1 < kAttWarps && s_piece[w1][0].at == pc.at) ++w1;
-    // within the block unless its first or last warp is the block's
-    bool local = k >= 0;
-    if (w1 == kAttWarps && pc.at + pc.tiles > line.start(blockIdx.x + 1)) local = false;
-    const int x = k >= 0;  // crossing: 0 came in, 1 goes on
-    if (!local) {
-      const int b0 = line.block_of(pc.at), b1 = line.block_of(pc.at + pc.tiles - 1);
-      first_block[x] = b0;
-      last_block[x] = b1;
-      cross_k[x] = k;
+    const bool local = k >= 0 && pc.at + pc.tiles <= block_end;
+    float mw[kAttWarps], top = -INFINITY, lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      mw[w] = w >= w0 && w < w1 ? s_m[w][w == k][hr] : -INFINITY;
+      top = fmaxf(top, mw[w]);
     }
-    const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
-    const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
-    float* mine = a.part + ((size_t)blockIdx.x * 2 + x) * (8 * MT) * prow;
-    for (int e = tid; e < rows * vecs; e += kAttThreads) {
-      const int hr = e / vecs, d = 4 * (e - hr * vecs);
-      float mw[kAttWarps], top = -INFINITY;
+    const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        mw[w] = w >= w0 && w < w1 ? s_m[w][w == k][hr] : -INFINITY;
-        top = fmaxf(top, mw[w]);
-      }
-      const float ref = top == -INFINITY ? 0.f : top;
+    for (int w = 0; w < kAttWarps; ++w) {
+      mw[w] = ex2(mw[w] - ref);
+      if (w >= w0 && w < w1) lsum = fmaf(s_l[w][w == k][hr], mw[w], lsum);
+    }
+    for (int d = 4 * lane; d < D; d += 128) {
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      float lsum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        if (w < w0 || w >= w1) continue;
-        const float f = ex2(mw[w] - ref);
-        const float4 v = *reinterpret_cast<const float4*>(
-            piece_data(w, w == k) + hr * DP + (((d >> 3) ^ (hr & 7)) << 3) + (d & 7));
-        add_scaled(sum, v, f);
-        lsum = fmaf(s_l[w][w == k][hr], f, lsum);
-      }
+      for (int w = 0; w < kAttWarps; ++w)
+        if (w >= w0 && w < w1)
+          add_scaled(sum, *reinterpret_cast<const float4*>(piece_data(w, w == k) + hr * DP +
+                                                           (((d >> 3) ^ (hr & 7)) << 3) + (d & 7)), mw[w]);
       if (local) {
-        finish(a, out0 + hr, d, sum, top, lsum, kShift);
+        finish(a, ((size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT) + hr, d, sum, top, lsum,
+               kShift);
       } else {
-        float* pr = mine + (size_t)hr * prow;
+        float* pr = a.part + (((size_t)blockIdx.x * 2 + (k >= 0)) * (8 * MT) + hr) * prow;
         __stcg(reinterpret_cast<float4*>(pr + d), sum);
         if (d == 0) __stcg(reinterpret_cast<float2*>(pr + D), make_float2(top, lsum));
       }
     }
+    crossing |= !local;
   }
-  if (last_block[0] >= 0 || last_block[1] >= 0) {
-    __threadfence();
-    __syncthreads();
-    if (tid < 2) {
-      const int b0 = tid ? first_block[1] : first_block[0], b1 = tid ? last_block[1] : last_block[0];
-      s_last[tid] = b1 >= 0 && atomicAdd(a.arrived + b0, 1) == b1 - b0;
-      if (s_last[tid]) a.arrived[b0] = 0;
-      __threadfence();
+  if (__syncthreads_or(crossing)) {
+    __shared__ int s_first[2], s_last[2], s_k;
+    if (tid < 2) {  // 0: the unit that came in, 1: the one that goes on
+      int k = tid - 1;
+      if (tid)
+        for (k = kAttWarps - 1; k >= 0; --k)
+          if (s_piece[k][1].at >= 0 && s_piece[k][1].at + s_piece[k][1].tiles > block_end) break;
+      if (tid) s_k = max(k, 0);
+      s_last[tid] = -1;
+      const Piece& pc = s_piece[max(k, 0)][tid];
+      if ((tid == 0 || k >= 0) && pc.at >= 0) {
+        const int b0 = line.block_of(pc.at), b1 = line.block_of(pc.at + pc.tiles - 1);
+        __threadfence();
+        if (atomicAdd(a.arrived + b0, 1) == b1 - b0) {
+          a.arrived[b0] = 0;
+          s_first[tid] = b0;
+          s_last[tid] = b1;
+        }
+        __threadfence();
+      }
     }
     __syncthreads();
+    float2* ml = reinterpret_cast<float2*>(smem);  // [block][row] of the parts, over the ring
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
-      if (!s_last[x]) continue;
-      const int b0 = x ? first_block[1] : first_block[0], b1 = x ? last_block[1] : last_block[0];
-      const int k = x ? cross_k[1] : cross_k[0];
-      const Piece& pc = s_piece[max(k, 0)][k < 0 ? 0 : 1];
-      const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
+      if (s_last[x] < 0) continue;
+      const int b0 = s_first[x], nb = s_last[x] - b0 + 1;
+      const Piece& pc = s_piece[x ? s_k : 0][x];
+      const int rows = min(8 * MT, a.group - pc.ht * 8 * MT), vecs = D >> 2;
       const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
+      // the part of the unit's i-th block
+      auto part = [&](int i, int hr) {
+        return a.part + (((size_t)(b0 + i) * 2 + (i == 0)) * (8 * MT) + hr) * prow;
+      };
+      __syncthreads();  // the pieces in the ring, or ml of the other unit, have been read
+      for (int e = tid; e < nb * rows; e += kAttThreads)
+        ml[e] = __ldcg(reinterpret_cast<const float2*>(part(e / rows, e % rows) + D));
+      __syncthreads();
       for (int e = tid; e < rows * vecs; e += kAttThreads) {
         const int hr = e / vecs, d = 4 * (e - hr * vecs);
-        auto from = [&](int b) { return a.part + (((size_t)b * 2 + (b == b0)) * (8 * MT) + hr) * prow; };
         float top = -INFINITY;
-#pragma unroll 2
-        for (int b = b0; b <= b1; ++b) top = fmaxf(top, __ldcg(from(b) + D));
+        for (int i = 0; i < nb; ++i) top = fmaxf(top, ml[i * rows + hr].x);
         const float ref = top == -INFINITY ? 0.f : top;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         float lsum = 0.f;
-#pragma unroll 2
-        for (int b = b0; b <= b1; ++b) {
-          const float* pr = from(b);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(pr + D));
-          const float f = ex2(ml.x - ref);
-          add_scaled(sum, __ldcg(reinterpret_cast<const float4*>(pr + d)), f);
-          lsum = fmaf(ml.y, f, lsum);
+#pragma unroll 4
+        for (int i = 0; i < nb; ++i) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i, hr) + d));
+          const float2 q = ml[i * rows + hr];
+          const float f = ex2(q.x - ref);
+          add_scaled(sum, v, f);
+          lsum = fmaf(q.y, f, lsum);
         }
         finish(a, out0 + hr, d, sum, top, lsum, kShift);
       }
@@ -914,14 +930,18 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
   }
 }
 
-// Map over a layer's rows (K and V rows of every page and kv head) in boxes of
-// 16 rows x 64 elements, 128-byte swizzle, zeros past the row's end.  False
-// where the driver offers no such map.
+// Map over a layer's rows (K and V rows of every page and kv head), 128-byte
+// swizzle.  Head dimensions that are multiples of 64: {64 elements, rows,
+// panels, K / V}, one box for a whole tile (one request instead of two per
+// panel: a lane's request takes some 100 cycles to issue).  Others: boxes of
+// 16 rows x 64 elements with zeros past the row's end.  False where the driver
+// offers no such map.
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static bool make_rows_map(CUtensorMap* m, void* base, long long rows, int head_dim) {
+static bool make_rows_map(CUtensorMap* m, void* base, long long rows, const pi_cache_desc& C,
+                          int panels) {
   static const EncodeFn encode = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -930,10 +950,13 @@ static bool make_rows_map(CUtensorMap* m, void* base, long long rows, int head_d
     return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
   }();
   if (!encode) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
-  const cuuint32_t box[2] = {64u, 16u}, steps[2] = {1u, 1u};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, steps,
+  const cuuint64_t row = (cuuint64_t)C.head_dim * 2, half = (cuuint64_t)C.kv_heads * C.page_tokens;
+  const bool whole = C.head_dim % 64 == 0;
+  const cuuint64_t dims[4] = {whole ? 64u : (cuuint64_t)C.head_dim, (cuuint64_t)rows - (whole ? half : 0),
+                              (cuuint64_t)C.head_dim / 64, 2u};
+  const cuuint64_t strides[3] = {row, 128u, half * row};
+  const cuuint32_t box[4] = {64u, 16u, (cuuint32_t)panels, 2u}, steps[4] = {1u, 1u, 1u, 1u};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, whole ? 4 : 2, base, dims, strides, box, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1028,8 +1051,10 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   const long long rows = (long long)C.pages * 2 * C.kv_heads * C.page_tokens;
   CUtensorMap map = {};
   a.limit_ns = wait_limit();
+  const int panels = C.head_dim <= 64 ? 1 : C.head_dim <= 128 ? 2 : 4;
   a.tma = C.page_tokens % 16 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
-          make_rows_map(&map, a.pool, rows, C.head_dim);
+          make_rows_map(&map, a.pool, rows, C, panels);
+  if (a.tma && C.head_dim % 64 == 0) a.tma = 2;
   const bool two = att_two_tiles(C.head_dim, a.group);
   a.tiles = (a.group + (two ? 15 : 7)) / (two ? 16 : 8);
   if (C.dtype == PI_F16) {
