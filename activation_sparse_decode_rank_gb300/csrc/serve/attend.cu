@@ -756,43 +756,54 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   const int prow = D + 4;
   const long long block_end = line.start(blockIdx.x + 1);
   bool crossing = false;
+  // lane k + 1 looks at the group that warp k's piece 1 (k = -1: piece 0 of
+  // warp 0) begins; lane w at whether warp w's piece 0 goes on with it
+  const long long begun = lane <= kAttWarps ? s_piece[max(lane - 1, 0)][lane > 0].at : -1;
+  const long long head = lane < kAttWarps ? s_piece[lane][0].at : -1;
+  uint32_t groups = __ballot_sync(~0u, begun >= 0);
+  for (int turn = warp; groups; ++turn, groups &= groups - 1) {
+    const int k = __ffs(groups) - 2, w0 = max(k, 0);
+    const long long at = __shfl_sync(~0u, begun, k + 1);
+    // warps w0 + 1, ... as long as they go on with the unit
+    const uint32_t same = __ballot_sync(~0u, lane > w0 && head == at);
+    const int w1 = w0 + __ffs((int)~(same >> (w0 + 1)));
+    const Piece& pc = s_piece[w0][k >= 0];
+    const bool local = k >= 0 && at + pc.tiles <= block_end;
+    crossing |= !local;
+    const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
+    const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
+    const int w = lane & (kAttWarps - 1);  // the lane's warp: its statistics
+    const bool in = w >= w0 && w < w1;
+    for (int hr = turn & (kAttWarps - 1); hr < rows; hr += kAttWarps) {
+      const float mw = in ? s_m[w][w == k][hr] : -INFINITY, lw = in ? s_l[w][w == k][hr] : 0.f;
+      float top = fmaxf(mw, __shfl_xor_sync(~0u, mw, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      const float f = ex2(mw - (top == -INFINITY ? 0.f : top));
+      float lsum = lw * f;
+      lsum += __shfl_xor_sync(~0u, lsum, 1);
+      lsum += __shfl_xor_sync(~0u, lsum, 2);
+      float fw[kAttWarps];
+#pragma unroll
+      for (int i = 0; i < kAttWarps; ++i) fw[i] = __shfl_sync(~0u, f, i);
 #pragma unroll 1
-  for (int item = warp; item < (kAttWarps + 1) * 8 * MT; item += kAttWarps) {
-    const int k = item / (8 * MT) - 1, hr = item % (8 * MT), w0 = max(k, 0);
-    const Piece& pc = s_piece[w0][k < 0 ? 0 : 1];
-    if (pc.at < 0 || pc.ht * 8 * MT + hr >= a.group) continue;
-    int w1 = w0 + 1;
-    while (w1 < kAttWarps && s_piece[w1][0].at == pc.at) ++w1;
-    const bool local = k >= 0 && pc.at + pc.tiles <= block_end;
-    float mw[kAttWarps], top = -INFINITY, lsum = 0.f;
+      for (int d = 4 * lane; d < D; d += 128) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f), v[kAttWarps];
+        const int at_d = hr * DP + (((d >> 3) ^ (hr & 7)) << 3) + (d & 7);
 #pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      mw[w] = w >= w0 && w < w1 ? s_m[w][w == k][hr] : -INFINITY;
-      top = fmaxf(top, mw[w]);
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
+        for (int i = 0; i < kAttWarps; ++i)
+          if (i >= w0 && i < w1) v[i] = *reinterpret_cast<const float4*>(piece_data(i, i == k) + at_d);
 #pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      mw[w] = ex2(mw[w] - ref);
-      if (w >= w0 && w < w1) lsum = fmaf(s_l[w][w == k][hr], mw[w], lsum);
-    }
-    for (int d = 4 * lane; d < D; d += 128) {
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w)
-        if (w >= w0 && w < w1)
-          add_scaled(sum, *reinterpret_cast<const float4*>(piece_data(w, w == k) + hr * DP +
-                                                           (((d >> 3) ^ (hr & 7)) << 3) + (d & 7)), mw[w]);
-      if (local) {
-        finish(a, ((size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT) + hr, d, sum, top, lsum,
-               kShift);
-      } else {
-        float* pr = a.part + (((size_t)blockIdx.x * 2 + (k >= 0)) * (8 * MT) + hr) * prow;
-        __stcg(reinterpret_cast<float4*>(pr + d), sum);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(pr + D), make_float2(top, lsum));
+        for (int i = 0; i < kAttWarps; ++i)
+          if (i >= w0 && i < w1) add_scaled(sum, v[i], fw[i]);
+        if (local) {
+          finish(a, out0 + hr, d, sum, top, lsum, kShift);
+        } else {
+          float* pr = a.part + (((size_t)blockIdx.x * 2 + (k >= 0)) * (8 * MT) + hr) * prow;
+          __stcg(reinterpret_cast<float4*>(pr + d), sum);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(pr + D), make_float2(top, lsum));
+        }
       }
     }
-    crossing |= !local;
   }
   if (__syncthreads_or(crossing)) {
     __shared__ int s_first[2], s_last[2], s_k;
