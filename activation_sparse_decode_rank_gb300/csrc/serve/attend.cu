@@ -805,60 +805,87 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       }
     }
   }
+  __shared__ int s_first[2], s_last[2];
+  __shared__ const Piece* s_cross[2];
+  if (tid < 2) {  // 0: the unit that came in, 1: the one that goes on
+    const Piece* pc = &s_piece[0][0];
+    if (tid) {
+      pc = &s_piece[kAttWarps - 1][1];
+      for (int w = kAttWarps - 2; w >= 0 && pc->at < 0; --w) pc = &s_piece[w][1];
+      if (pc->at + pc->tiles <= block_end) pc = &s_piece[0][0];
+    }
+    const bool any = pc->at >= 0 && (pc == &s_piece[0][0]) == (tid == 0);
+    s_cross[tid] = pc;
+    s_first[tid] = any ? line.block_of(pc->at) : -1;
+    s_last[tid] = any ? line.block_of(pc->at + pc->tiles - 1) : -1;
+  }
   if (__syncthreads_or(crossing)) {
-    __shared__ int s_first[2], s_last[2], s_k;
-    if (tid < 2) {  // 0: the unit that came in, 1: the one that goes on
-      int k = tid - 1;
-      if (tid)
-        for (k = kAttWarps - 1; k >= 0; --k)
-          if (s_piece[k][1].at >= 0 && s_piece[k][1].at + s_piece[k][1].tiles > block_end) break;
-      if (tid) s_k = max(k, 0);
-      s_last[tid] = -1;
-      const Piece& pc = s_piece[max(k, 0)][tid];
-      if ((tid == 0 || k >= 0) && pc.at >= 0) {
-        const int b0 = line.block_of(pc.at), b1 = line.block_of(pc.at + pc.tiles - 1);
-        __threadfence();
-        if (atomicAdd(a.arrived + b0, 1) == b1 - b0) {
-          a.arrived[b0] = 0;
-          s_first[tid] = b0;
-          s_last[tid] = b1;
-        }
-        __threadfence();
-      }
+    if (tid < 2 && s_first[tid] >= 0) {
+      // releases the block's parts, which the barrier ordered before it, and
+      // acquires the other blocks'
+      int n;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                   : "=r"(n)
+                   : "l"(a.arrived + s_first[tid])
+                   : "memory");
+      if (n == s_last[tid] - s_first[tid])
+        a.arrived[s_first[tid]] = 0;
+      else
+        s_first[tid] = -1;
     }
     __syncthreads();
-    float2* ml = reinterpret_cast<float2*>(smem);  // [block][row] of the parts, over the ring
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
-      if (s_last[x] < 0) continue;
+      if (s_first[x] < 0) continue;
       const int b0 = s_first[x], nb = s_last[x] - b0 + 1;
-      const Piece& pc = s_piece[x ? s_k : 0][x];
-      const int rows = min(8 * MT, a.group - pc.ht * 8 * MT), vecs = D >> 2;
+      const Piece& pc = *s_cross[x];
+      const int rows = min(8 * MT, a.group - pc.ht * 8 * MT), vecs = D >> 2, items = rows * vecs;
       const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
-      // the part of the unit's i-th block
-      auto part = [&](int i, int hr) {
-        return a.part + (((size_t)(b0 + i) * 2 + (i == 0)) * (8 * MT) + hr) * prow;
-      };
-      __syncthreads();  // the pieces in the ring, or ml of the other unit, have been read
-      for (int e = tid; e < nb * rows; e += kAttThreads)
-        ml[e] = __ldcg(reinterpret_cast<const float2*>(part(e / rows, e % rows) + D));
-      __syncthreads();
-      for (int e = tid; e < rows * vecs; e += kAttThreads) {
-        const int hr = e / vecs, d = 4 * (e - hr * vecs);
-        float top = -INFINITY;
-        for (int i = 0; i < nb; ++i) top = fmaxf(top, ml[i * rows + hr].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lsum = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < nb; ++i) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i, hr) + d));
-          const float2 q = ml[i * rows + hr];
-          const float f = ex2(q.x - ref);
-          add_scaled(sum, v, f);
-          lsum = fmaf(q.y, f, lsum);
+      // two items of a thread together, four parts at a time: their reads overlap
+#pragma unroll 1
+      for (int e = tid; e < items; e += 2 * kAttThreads) {
+        float4 sum[2];
+        float top[2], lsum[2];
+        int hr[2], d[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = min(e + i * kAttThreads, items - 1);
+          hr[i] = at / vecs;
+          d[i] = 4 * (at - hr[i] * vecs);
+          sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          top[i] = -INFINITY;
+          lsum[i] = 0.f;
         }
-        finish(a, out0 + hr, d, sum, top, lsum, kShift);
+#pragma unroll 1
+        for (int j0 = 0; j0 < nb; j0 += 4) {
+          float4 v[2][4];
+          float2 q[2][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (j0 + j < nb) {  // the unit's (j0 + j)-th block
+                const float* pr =
+                    a.part + (((size_t)(b0 + j0 + j) * 2 + (j0 + j == 0)) * (8 * MT) + hr[i]) * prow;
+                q[i][j] = __ldcg(reinterpret_cast<const float2*>(pr + D));
+                v[i][j] = __ldcg(reinterpret_cast<const float4*>(pr + d[i]));
+              }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (j0 + j < nb) {
+                const float up = fmaxf(top[i], q[i][j].x), ref = up == -INFINITY ? 0.f : up;
+                const float was = ex2(top[i] - ref), is = ex2(q[i][j].x - ref);
+                sum[i] = make_float4(sum[i].x * was, sum[i].y * was, sum[i].z * was, sum[i].w * was);
+                add_scaled(sum[i], v[i][j], is);
+                lsum[i] = fmaf(lsum[i], was, q[i][j].y * is);
+                top[i] = up;
+              }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (e + i * kAttThreads < items) finish(a, out0 + hr[i], d[i], sum[i], top[i], lsum[i], kShift);
       }
     }
   }
