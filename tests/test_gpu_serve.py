@@ -677,3 +677,39 @@ def test_empty_batches():
     ws = pi.logprob_workspace(0, 10, 0, DEV)
     assert pi.pi_token_logprobs(None, "f32", 0, 10, 10, None, 0, None, None, None, None, st,
                                 ws) == 0
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("beams,window,sinks", [(1, 0, 0), (4, 0, 0), (5, 17, 3)])
+def test_beam_search_scores_hold_without_a_cache(beams, window, sinks):
+    # The example's beams: each sequence's log probability, summed step by step
+    # over forked caches, is that of one pass over the whole sequence.  Both
+    # sides use the same projections and FFN calls; keys, values and scores
+    # differ by fp32 rounding (2^-23 of sums of some hundred terms, three
+    # layers), but a neuron whose predictor logit lies within that of zero may
+    # switch, which moves a logit by its contribution (under 1e-2 here).
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    import beam_decode as ex
+    model = ex.Decoder(seed=3)
+    prompt = torch.randint(0, ex.VOCAB, (37,), generator=torch.Generator().manual_seed(beams))
+    search = ex.BeamSearch(model, beams, 37 + 30, window, sinks)
+    tokens, score = search.run(prompt, 30)
+    assert int(search.status[0]) == 0 and int(model.status[0]) == 0
+    assert (score[:-1] >= score[1:]).all() and len({tuple(t) for t in tokens.tolist()}) == beams
+    for b in range(beams):
+        assert abs(float(score[b]) - ex.rescore(model, tokens[b], 37, window, sinks)) <= 5e-2
+    # after compaction the slots read what they read before
+    before = [search.pool[:, search.table[search.now][b, :5].long()].clone() for b in range(beams)]
+    n = int(search.length[search.now][0])
+    assert n == 66
+    live = search.compact()
+    t = search.table[search.now]
+    assert live == len(set(t.flatten().tolist()) - {-1}) and int(t.max()) < live
+    for b in range(beams):
+        after = search.pool[:, t[b, :5].long()]
+        full = after.permute(0, 1, 4, 2, 3, 5).reshape(ex.LAYERS, -1, 2, 2, 32)[:, :n]
+        was = before[b].permute(0, 1, 4, 2, 3, 5).reshape(ex.LAYERS, -1, 2, 2, 32)[:, :n]
+        assert torch.equal(full, was)
