@@ -15,8 +15,9 @@
 // that reach tau, some k of them, are read again; their elements >= tau are
 // ranked by a unique key (value, then lowest index).  Where ties make more of
 // either than the block has room for, the whole part is read again: slower,
-// as exact.  Selection is by sorted lists of 32 keys in the lanes of a warp:
-// sort 32, merge two lists, a tree over the warps.
+// as exact, by sorted lists of 32 keys in the lanes of a warp.  Few keys are
+// ordered by counting, each thread, the keys larger than its own: one pass
+// of broadcast reads instead of a chain of exchanges (256 keys at most).
 //
 // Bound: HBM bandwidth (each logit read once); for 16-bit logits the pass
 // issues some 5 instructions per logit, not far from the machine's rate at
@@ -215,6 +216,11 @@ struct Vec {  // 16 bytes of logits
   }
 };
 
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+
 constexpr int kGroups = 16;  // groups of batches whose maxima a thread leaves
 constexpr int kPicks = 256;  // groups, then elements, that reach tau
 
@@ -229,7 +235,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
   __shared__ float sh_top[kGroups][T];
   __shared__ uint32_t sh_group[kPicks];
   __shared__ u64 sh_pick[kPicks];
-  __shared__ uint32_t sh_four[T / 4], sh_tau;
+  __shared__ __align__(16) uint32_t sh_four[T / 4];
+  __shared__ uint32_t sh_tau;
+  __shared__ u64 sh_list[32];
   __shared__ int sh_groups, sh_picks, sh_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) sh_groups = sh_picks = 0;
@@ -261,51 +269,42 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
       if (i >= 0 && i < a.vocab) use(logit_at<DT>(base, i), i);
     }
   };
-  const int steps = w1 > w0 ? (w1 - w0 + T * kBatch - 1) / (T * kBatch) : 0;
+  // Batches: `whole` full ones of every thread, then what is left.
+  const int nwhole = max(0, w1 - w0), whole = nwhole / (T * kBatch);
+  const int left = nwhole - whole * (T * kBatch) - tid;  // the thread's vectors: tid, + T, ... < left + tid
+  const int steps = whole + (nwhole > whole * T * kBatch);
   const uint4* mine = vecs + w0 + tid;
+  // batches of a group: the least power of two that kGroups groups suffice for
+  const int group_shift = 32 - __clz((max(steps, 1) - 1) / kGroups), group = 1 << group_shift;
+  float group_top = NAN;
+  auto leave = [&](int it, float top) {
+    group_top = it & (group - 1) ? fmaxf(group_top, top) : top;
+    sh_top[it >> group_shift][tid] = group_top;
+  };
   uint4 raw[kBatch];
   auto load = [&](int it) {
     const uint4* p = mine + it * (T * kBatch);
-    const int left = w1 - w0 - tid - it * (T * kBatch);
+    if (it < whole) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (u * T < left) raw[u] = __ldg(p + u * T);
-  };
-  const int group = (steps + kGroups - 1) / kGroups;  // batches of a group
-  float group_top = NAN;
-  int group_left = group, group_at = 0;
-  if (steps > 0) load(0);
-  for (int it = 0; it < steps; ++it) {
-    const int left = w1 - w0 - tid - it * (T * kBatch);
-    const bool full = left > (kBatch - 1) * T;
-    uint4 v[kBatch];
-    float top = NAN;
-    if (full) {
-      uint32_t w[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        v[u] = raw[u];
-        w[u] = V::max(v[u]);
-      }
-      top = V::top(V::max(V::max(w[0], w[1]), V::max(w[2], w[3])));
+      for (int u = 0; u < kBatch; ++u) raw[u] = __ldg(p + u * T);
     } else {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (u * T < left) {
-          v[u] = raw[u];
-          top = fmaxf(top, V::top(V::max(v[u])));
-        }
+        if (u * T < left) raw[u] = __ldg(p + u * T);
     }
-    if (it + 1 < steps) load(it + 1);
-    raise(top);
+  };
+  // Sums of N vectors beside ref, packed where the type can hold the floor.
+  auto add = [&](const uint4* v, auto n) {
+    constexpr int N = decltype(n)::value;
     const float ref = sum.m == -INFINITY ? 0.f : sum.m;
     const uint32_t low = V::floor_at(ref);
     if (!huge(ref) && (DT != 0 || low != 0x7fff7fffu)) {
       const float M = -__fmul_rn(ref, kLog2e);
       const u64 L2 = pair(kLog2e, kLog2e), M2 = pair(M, M);
       u64 s2 = 0, t2 = 0;
-      auto add_vec = [&](const uint4& raw16) {
-        const uint4 q = V::raise(raw16, low);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const uint4 q = V::raise(v[u], low);
 #pragma unroll
         for (int p = 0; p < V::pairs; ++p) {
           const float2 x = V::get(q, p);
@@ -315,34 +314,48 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
           s2 = add2(s2, e);
           t2 = fma2(e, d2, t2);
         }
-      };
-      if (full) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) add_vec(v[u]);
-      } else {
-#pragma unroll 1
-        for (int u = 0; u * T < left; ++u) add_vec(u == 0 ? v[0] : u == 1 ? v[1] : v[2]);
       }
       const float2 s = halves(s2), t = halves(t2);
       sum.s += s.x + s.y;
       sum.t += t.x + t.y;
     } else {
-#pragma unroll 1
-      for (int u = 0; u < kBatch && u * T < left; ++u) {
-        const uint4 q = u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3];
+#pragma unroll
+      for (int u = 0; u < N; ++u)
 #pragma unroll 1
         for (int p = 0; p < V::pairs; ++p) {
-          const float2 x = V::get(q, p);
+          const float2 x = V::get(v[u], p);
           add_one(sum, ref, x.x);
           add_one(sum, ref, x.y);
         }
-      }
     }
-    group_top = fmaxf(group_top, top);
-    if (--group_left == 0 || it + 1 == steps) {
-      sh_top[group_at++][tid] = group_top;
-      group_top = NAN;
-      group_left = group;
+  };
+  if (steps > 0) load(0);
+#pragma unroll 1
+  for (int it = 0; it < whole; ++it) {
+    uint4 v[kBatch];
+    uint32_t w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      v[u] = raw[u];
+      w[u] = V::max(v[u]);
+    }
+    if (it + 1 < steps) load(it + 1);
+    const float top = V::top(V::max(V::max(w[0], w[1]), V::max(w[2], w[3])));
+    leave(it, top);
+    raise(top);
+    add(v, Count<kBatch>());
+  }
+  if (steps > whole) {
+    float top = NAN;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (u * T < left) top = fmaxf(top, V::top(V::max(raw[u])));
+    leave(whole, top);
+    raise(top);
+#pragma unroll 1
+    for (int u = 0; u * T < left; ++u) {
+      const uint4 q = u == 0 ? raw[0] : u == 1 ? raw[1] : u == 2 ? raw[2] : raw[3];
+      add(&q, Count<1>());
     }
   }
   if (tid == 0 && cut_first) {
@@ -368,9 +381,16 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
     if ((lane & 3) == 0) sh_four[tid >> 2] = k;
   }
   __syncthreads();
-  if (a.topk > 0 && warp == 0) {
-    const uint32_t k = merge32(sort32(sh_four[lane]), sort32(sh_four[lane + 32]));
-    if (lane == a.topk - 1) sh_tau = k;
+  if (a.topk > 0 && tid < T / 4) {  // the one with topk - 1 ahead of it
+    const uint32_t k = sh_four[tid];
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = 0; i < T / 4; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(sh_four + i);
+      ahead += (o.x > k || (o.x == k && i < tid)) + (o.y > k || (o.y == k && i + 1 < tid)) +
+               (o.z > k || (o.z == k && i + 2 < tid)) + (o.w > k || (o.w == k && i + 3 < tid));
+    }
+    if (ahead == a.topk - 1) sh_tau = k;
   }
 #pragma unroll
   for (int w = 0; w < kScoreWarps; ++w) top = fmaxf(top, sh_sums[w][0]);
@@ -383,7 +403,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
     }
   }
 
-  u64 list = 0;  // this warp's 32 largest keys
+  u64 list = 0;  // warp 0: the 32 largest keys (only the first topk count)
   if (a.topk > 0) {
     __syncthreads();
     const uint32_t tau = sh_tau;
@@ -396,9 +416,14 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
         least = kth > least ? kth : least;
       }
     };
+    auto pick = [&](float x, int i) {
+      if (!(x >= tau_value)) return;
+      const int n = atomicAdd(&sh_picks, 1);
+      if (n < kPicks) sh_pick[n] = rank_key(x, i);
+    };
     bool all = tau == 0;  // then everything counts, NaN too
     if (!all) {
-      for (int q = 0; q < group_at; ++q)
+      for (int q = 0; q << group_shift < steps; ++q)
         if (sh_top[q][tid] >= tau_value) {
           const int i = atomicAdd(&sh_groups, 1);
           if (i < kPicks) sh_group[i] = (uint32_t)(q * T + tid);
@@ -419,18 +444,26 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
             const float2 x = V::get(v, p);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float y = h ? x.y : x.x;
-              if (!(y >= tau_value)) continue;
-              const int n = atomicAdd(&sh_picks, 1);
-              if (n < kPicks) sh_pick[n] = rank_key(y, j * VN + 2 * p + h - shift);
+              pick(h ? x.y : x.x, j * VN + 2 * p + h - shift);
             }
           }
         }
+      if (tid == T - 1 && cut_first) cut(0, pick);
+      if (tid == T - 2 && cut_last) cut(nvec - 1, pick);
       __syncthreads();
       const int picks = sh_picks;
       all |= picks > kPicks;
-      if (!all && warp == 0)
-        for (int i0 = 0; i0 < picks; i0 += 32) enter(i0 + lane < picks ? sh_pick[i0 + lane] : 0);
+      if (!all) {
+        if (tid < picks) {
+          const u64 k = sh_pick[tid];
+          int ahead = 0;
+#pragma unroll 4
+          for (int i = 0; i < picks; ++i) ahead += sh_pick[i] > k;
+          if (ahead < 32) sh_list[ahead] = k;
+        }
+        __syncthreads();
+        if (warp == 0) list = lane < picks ? sh_list[lane] : 0;
+      }
     }
     if (all) {
       for (int j0 = w0 + warp * 32; j0 < w1; j0 += T) {
@@ -448,14 +481,14 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
         }
       }
       list = block_merge(list, sh_keys);
-    }
-    if (warp == 0 && cut_first) {
-      const int i = lane - shift;
-      enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
-    }
-    if (warp == 0 && cut_last) {
-      const int i = (nvec - 1) * VN + lane - shift;
-      enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
+      if (warp == 0 && cut_first) {
+        const int i = lane - shift;
+        enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
+      }
+      if (warp == 0 && cut_last) {
+        const int i = (nvec - 1) * VN + lane - shift;
+        enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
+      }
     }
   }
   __syncthreads();
