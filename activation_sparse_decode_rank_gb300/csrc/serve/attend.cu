@@ -55,9 +55,8 @@ struct AttendArgs {
   int* status;
   int* arrived;   // [kAttendGrid] arrivals at the units that begin in a block
   float* part;    // [grid][2][heads of a unit][head_dim + 4]: o, m, l of units split over blocks
-  float* wpart;   // [4 grid][16][padded dim]: warps' first parts where shared memory lacks the room
   int slots, heads, kv_heads, group, head_dim, page_tokens, pages, max_pages, window, sinks;
-  int tiles;      // head tiles per kv head: ceil(group / (8 MT))
+  int tiles;      // head tiles per kv head: ceil(group / 8)
   int page_shift; // log2(page_tokens), or -1
   int tma;        // tiles come as TMA boxes: 1 a panel, 2 a whole tile each
   float scale;    // scale log2(e)
@@ -69,14 +68,23 @@ constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kUnitCost = 2;  // a unit's start and end, in tiles
 constexpr int kMinTiles = 4;  // a warp's least share, in tiles
 
-// Stages of a warp's ring: two thread blocks per SM (one at 256 dims).
-template <int DP>
-__host__ __device__ constexpr int att_stages() {
-  return DP == 64 ? 6 : 3;
+// Thread blocks per SM, and stages of a warp's ring, by measurement.  More
+// warps hide a tile's chain of instructions, more stages its loads; bf16 tiles
+// take half as many instructions again.  32 slots to 4096 tokens, 32 heads of
+// 64: fp16 3 x 3 87 us (2 x 6 116), bf16 4 x 2 96 us (3 x 3 102, 2 x 6 128).
+// 32 slots to 2048, 40 heads of 128: fp16 2 x 2 107 us (2 x 3 114), bf16 2 x 3
+// 109 us (2 x 2 113).
+template <int DT, int DP>
+__host__ __device__ constexpr int att_blocks() {
+  return DP == 256 ? 1 : DP == 64 ? 3 + DT : 2;
 }
-template <int DP, int MT>
+template <int DT, int DP>
+__host__ __device__ constexpr int att_stages() {
+  return DP == 64 ? 3 - DT : DP == 128 ? 2 + DT : 2;
+}
+template <int DT, int DP>
 __host__ __device__ constexpr int att_smem() {
-  return kAttWarps * att_stages<DP>() * 16 * DP * 4 + (MT == 1 ? kAttWarps * 8 * DP * 4 : 0);
+  return kAttWarps * att_stages<DT, DP>() * 16 * DP * 4 + kAttWarps * 8 * DP * 4;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -308,9 +316,9 @@ struct Piece {
   int slot, g, ht, tiles;
 };
 
-template <int DT, int DP, int MT>
-__global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
-  constexpr int S = att_stages<DP>();
+template <int DT, int DP>
+__global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
+  constexpr int S = att_stages<DT, DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
   constexpr int kPanel = 16 * 128;         // 16 rows of 64 elements: a tile is DP / 64 panels
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_mask[kAttWarps][S];
   __shared__ __align__(8) uint64_t s_bar[kAttWarps][S];
-  __shared__ float s_m[kAttWarps][2][8 * MT], s_l[kAttWarps][2][8 * MT];
+  __shared__ float s_m[kAttWarps][2][8], s_l[kAttWarps][2][8];
   __shared__ Piece s_piece[kAttWarps][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = a.head_dim, P = a.page_tokens;
@@ -326,8 +334,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   // where a warp leaves its first and its last part
   auto piece_data = [&](int w, int k) -> float* {
     if (k) return reinterpret_cast<float*>(smem + w * S * 2 * kTile);
-    if (MT == 1) return reinterpret_cast<float*>(smem + kAttWarps * S * 2 * kTile) + w * 8 * DP;
-    return a.wpart + ((size_t)blockIdx.x * kAttWarps + w) * (8 * MT) * DP;
+    return reinterpret_cast<float*>(smem + kAttWarps * S * 2 * kTile) + w * 8 * DP;
   };
   if (lane < 2) s_piece[warp][lane].at = -1;
   if (lane < S) mbar_init(&s_bar[warp][lane], 1);
@@ -417,9 +424,9 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   auto page_index = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / P; };
   auto fetch = [&](bool unit_begins) {
     if (unit_begins) {  // bring the unit's query rows near: they are read when its first tile is
-      const int rows = min(8 * MT, a.group - lc.ht * 8 * MT);
+      const int rows = min(8, a.group - lc.ht * 8);
       const char* q = reinterpret_cast<const char*>(
-          a.q + ((size_t)lc.slot * a.heads + lc.g * a.group + lc.ht * 8 * MT) * D);
+          a.q + ((size_t)lc.slot * a.heads + lc.g * a.group + lc.ht * 8) * D);
       for (int e = lane * 128; e < rows * D * 4; e += 32 * 128) {
         float unused;
         asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(q + e));
@@ -498,8 +505,8 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
   __syncwarp();
   if (lc.pos < share1) fetch(true);
 
-  uint32_t qf[MT][DP / 16][4], qf2[DT == 1 ? MT : 1][DP / 16][2];
-  float o[MT][DP / 8][2], m[MT], l[MT], unit_scale[MT];
+  uint32_t qf[DP / 16][4], qf2[DP / 16][2];
+  float o[DP / 8][2], m, l, unit_scale;
   bool fresh = true;
   int ahead = 0, load_stage = 0, stage = 0;
   uint32_t parity = 0;
@@ -521,42 +528,39 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
     const int g = cc.g, ht = cc.ht;
     if (fresh) {  // a unit begins: its query heads
       fresh = false;
+      const int h = ht * 8 + (lane >> 2);
+      const float* q = a.q + ((size_t)cc.slot * a.heads + g * a.group + min(h, a.group - 1)) * D;
+      float2 f[DP / 16][2];
+      float top = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int h = (ht * MT + mt) * 8 + (lane >> 2);
-        const float* q = a.q + ((size_t)cc.slot * a.heads + g * a.group + min(h, a.group - 1)) * D;
-        float2 f[DP / 16][2];
-        float top = 0.f;
+      for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d = ks * 16 + e * 8 + 2 * (lane & 3);
-            f[ks][e] = h < a.group && d < D ? __ldg(reinterpret_cast<const float2*>(q + d))
-                                            : make_float2(0.f, 0.f);
-            top = fmaxf(top, fmaxf(fabsf(f[ks][e].x), fabsf(f[ks][e].y)));
-          }
-        float up = 1.f;
-        unit_scale[mt] = a.scale;
-        if (DT == 0) {
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-          // exact powers of two; 0, subnormals and infinities are clamped
-          const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 254) - 127 - 13;
-          up = __uint_as_float((uint32_t)(127 - ex) << 23);
-          unit_scale[mt] = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
+        for (int e = 0; e < 2; ++e) {
+          const int d = ks * 16 + e * 8 + 2 * (lane & 3);
+          f[ks][e] = h < a.group && d < D ? __ldg(reinterpret_cast<const float2*>(q + d))
+                                          : make_float2(0.f, 0.f);
+          top = fmaxf(top, fmaxf(fabsf(f[ks][e].x), fabsf(f[ks][e].y)));
         }
-#pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            split2<DT>(f[ks][e].x * up, f[ks][e].y * up, qf[mt][ks][2 * e], qf[mt][ks][2 * e + 1],
-                       qf2[DT == 1 ? mt : 0][ks][e]);
-        m[mt] = -INFINITY;
-        l[mt] = 0.f;
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j) o[mt][j][0] = o[mt][j][1] = 0.f;
+      float up = 1.f;
+      unit_scale = a.scale;
+      if (DT == 0) {
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        // exact powers of two; 0, subnormals and infinities are clamped
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 254) - 127 - 13;
+        up = __uint_as_float((uint32_t)(127 - ex) << 23);
+        unit_scale = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
       }
+#pragma unroll
+      for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          split2<DT>(f[ks][e].x * up, f[ks][e].y * up, qf[ks][2 * e], qf[ks][2 * e + 1],
+                     qf2[ks][e]);
+      m = -INFINITY;
+      l = 0.f;
+#pragma unroll
+      for (int j = 0; j < DP / 8; ++j) o[j][0] = o[j][1] = 0.f;
     }
 
     if (a.tma) {
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
 
     if (mask) {
       // scores of 16 tokens
-      float sc[MT][2][2][4];  // even and odd steps: shorter chains
+      float sc[2][2][4];  // even and odd steps: shorter chains
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), pc = (lane >> 3) & 1;
         const uint32_t at = k0 + r * 128 + ((pc ^ (r & 7)) << 4);
@@ -616,54 +620,49 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
           uint32_t b[4];
           ldsm4(b, (at ^ ((ks & 3) << 5)) + (ks >> 2) * kPanel);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              float(&c)[4] = sc[mt][nt][ks & 1];
+              float(&c)[4] = sc[nt][ks & 1];
               if (ks < 2)
-                mma0<DT>(c, qf[mt][ks], b[2 * nt], b[2 * nt + 1]);
+                mma0<DT>(c, qf[ks], b[2 * nt], b[2 * nt + 1]);
               else
-                mma<DT>(c, qf[mt][ks], b[2 * nt], b[2 * nt + 1]);
+                mma<DT>(c, qf[ks], b[2 * nt], b[2 * nt + 1]);
               if (DT == 1) {
-                const uint32_t q2[4] = {0u, qf2[mt][ks][0], 0u, qf2[mt][ks][1]};
+                const uint32_t q2[4] = {0u, qf2[ks][0], 0u, qf2[ks][1]};
                 mma<DT>(c, q2, b[2 * nt], b[2 * nt + 1]);
               }
             }
         }
       }
-      uint32_t pf[MT][4], pf2[MT][2];
-      float corr[MT];
+      uint32_t pf[4], pf2[2];
+      float corr;
+      float s[4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float s[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float(&c)[2][4] = sc[mt][e >> 1];
-          s[e] = (c[0][e & 1] + c[1][e & 1]) + (c[0][2 + (e & 1)] + c[1][2 + (e & 1)]);
-        }
-        const uint32_t mine = mask >> (2 * (lane & 3));  // rows of s: bits 0, 1, 8, 9
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = mask == 0xffffu || (mine >> ((e >> 1) * 8 + (e & 1)) & 1u) ? s[e] * unit_scale[mt]
-                                                                            : -INFINITY;
-        float mx = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-        const float mn = fmaxf(m[mt], mx);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        corr[mt] = ex2(m[mt] - ref);
-        m[mt] = mn;
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2(fmaf(s[e], unit_scale[mt], kShift - ref));
-          if (w[e] == -INFINITY) p[e] = 0.f;
-        }
-        l[mt] = fmaf(l[mt], corr[mt], (p[0] + p[1]) + (p[2] + p[3]));
-        split2<DT>(p[0], p[1], pf[mt][0], pf[mt][1], pf2[mt][0]);
-        split2<DT>(p[2], p[3], pf[mt][2], pf[mt][3], pf2[mt][1]);
+      for (int e = 0; e < 4; ++e) {
+        const float(&c)[2][4] = sc[e >> 1];
+        s[e] = (c[0][e & 1] + c[1][e & 1]) + (c[0][2 + (e & 1)] + c[1][2 + (e & 1)]);
       }
+      const uint32_t mine = mask >> (2 * (lane & 3));  // rows of s: bits 0, 1, 8, 9
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = mask == 0xffffu || (mine >> ((e >> 1) * 8 + (e & 1)) & 1u) ? s[e] * unit_scale
+                                                                          : -INFINITY;
+      float mx = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+      const float mn = fmaxf(m, mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      corr = ex2(m - ref);
+      m = mn;
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[e] = ex2(fmaf(s[e], unit_scale, kShift - ref));
+        if (w[e] == -INFINITY) p[e] = 0.f;
+      }
+      l = fmaf(l, corr, (p[0] + p[1]) + (p[2] + p[3]));
+      split2<DT>(p[0], p[1], pf[0], pf[1], pf2[0]);
+      split2<DT>(p[2], p[3], pf[2], pf[3], pf2[1]);
       // weighted values; each tile's product is rounded once into the fp32 sums
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), pc = lane >> 4;
       const uint32_t at = v0 + r * 128 + ((pc ^ (r & 7)) << 4);
@@ -672,17 +671,15 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
         uint32_t b[4];
         ldsm4t(b, (at ^ ((jj & 3) << 5)) + (jj >> 2) * kPanel);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
           for (int u = 0; u < 2; ++u) {
             float c[4];
-            mma0<DT>(c, pf[mt], b[2 * u], b[2 * u + 1]);
+            mma0<DT>(c, pf, b[2 * u], b[2 * u + 1]);
             if (DT == 1) {
-              const uint32_t p2[4] = {0u, pf2[mt][0], 0u, pf2[mt][1]};
+              const uint32_t p2[4] = {0u, pf2[0], 0u, pf2[1]};
               mma<DT>(c, p2, b[2 * u], b[2 * u + 1]);
             }
-            o[mt][2 * jj + u][0] = fmaf(o[mt][2 * jj + u][0], corr[mt], c[0] + c[2]);
-            o[mt][2 * jj + u][1] = fmaf(o[mt][2 * jj + u][1], corr[mt], c[1] + c[3]);
+            o[2 * jj + u][0] = fmaf(o[2 * jj + u][0], corr, c[0] + c[2]);
+            o[2 * jj + u][1] = fmaf(o[2 * jj + u][1], corr, c[1] + c[3]);
           }
       }
     }
@@ -692,41 +689,38 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
     if (ends || cc.pos + 1 == share1) {
       const bool begins = at >= share0;
       const int h = lane >> 2;
+      const int hq = ht * 8 + h;  // head of the kv head
+      float lt = l;
+      lt += __shfl_xor_sync(~0u, lt, 1);
+      lt += __shfl_xor_sync(~0u, lt, 2);
+      if (begins && ends) {
+        const size_t row = (size_t)cc.slot * a.heads + g * a.group + hq;
+        if (hq < a.group) {
+          const float inv = lt > 0.f ? 1.f / lt : lt == lt ? 0.f : lt;
+          float* y = a.y + row * D + 2 * (lane & 3);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int hr = 8 * mt + h, hq = ht * 8 * MT + hr;  // head of the unit, of the kv head
-        float lt = l[mt];
-        lt += __shfl_xor_sync(~0u, lt, 1);
-        lt += __shfl_xor_sync(~0u, lt, 2);
-        if (begins && ends) {
-          const size_t row = (size_t)cc.slot * a.heads + g * a.group + hq;
-          if (hq < a.group) {
-            const float inv = lt > 0.f ? 1.f / lt : lt == lt ? 0.f : lt;
-            float* y = a.y + row * D + 2 * (lane & 3);
-#pragma unroll
-            for (int j = 0; j < DP / 8; ++j)
-              if (8 * j < D)
-                *reinterpret_cast<float2*>(y + 8 * j) = make_float2(o[mt][j][0] * inv, o[mt][j][1] * inv);
-            if ((lane & 3) == 0 && a.lse) a.lse[row] = (m[mt] + (log2f(lt) - kShift)) * kLn2;
-          }
-        } else {
-          const int k = begins ? 1 : 0;
-          if (k) {  // into the ring, now idle
-            cp_wait<0>();
-            __syncwarp();
-          }
-          if (hq < a.group) {
-            float* data = piece_data(warp, k) + hr * DP + 2 * (lane & 3);
-#pragma unroll
-            for (int j = 0; j < DP / 8; ++j)
-              *reinterpret_cast<float2*>(data + ((j ^ h) << 3)) = make_float2(o[mt][j][0], o[mt][j][1]);
-          }
-          if ((lane & 3) == 0) {
-            s_m[warp][k][hr] = m[mt];
-            s_l[warp][k][hr] = lt;
-          }
-          if (lane == 0) s_piece[warp][k] = Piece{at, cc.slot, g, ht, cc.v.tiles};
+          for (int j = 0; j < DP / 8; ++j)
+            if (8 * j < D)
+              *reinterpret_cast<float2*>(y + 8 * j) = make_float2(o[j][0] * inv, o[j][1] * inv);
+          if ((lane & 3) == 0 && a.lse) a.lse[row] = (m + (log2f(lt) - kShift)) * kLn2;
         }
+      } else {
+        const int k = begins ? 1 : 0;
+        if (k) {  // into the ring, now idle
+          cp_wait<0>();
+          __syncwarp();
+        }
+        if (hq < a.group) {
+          float* data = piece_data(warp, k) + h * DP + 2 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < DP / 8; ++j)
+            *reinterpret_cast<float2*>(data + ((j ^ h) << 3)) = make_float2(o[j][0], o[j][1]);
+        }
+        if ((lane & 3) == 0) {
+          s_m[warp][k][h] = m;
+          s_l[warp][k][h] = lt;
+        }
+        if (lane == 0) s_piece[warp][k] = Piece{at, cc.slot, g, ht, cc.v.tiles};
       }
       fresh = true;
     }
@@ -770,8 +764,8 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
     const Piece& pc = s_piece[w0][k >= 0];
     const bool local = k >= 0 && at + pc.tiles <= block_end;
     crossing |= !local;
-    const int rows = min(8 * MT, a.group - pc.ht * 8 * MT);
-    const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
+    const int rows = min(8, a.group - pc.ht * 8);
+    const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8;
     const int w = lane & (kAttWarps - 1);  // the lane's warp: its statistics
     const bool in = w >= w0 && w < w1;
     for (int hr = turn & (kAttWarps - 1); hr < rows; hr += kAttWarps) {
@@ -798,7 +792,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
         if (local) {
           finish(a, out0 + hr, d, sum, top, lsum, kShift);
         } else {
-          float* pr = a.part + (((size_t)blockIdx.x * 2 + (k >= 0)) * (8 * MT) + hr) * prow;
+          float* pr = a.part + (((size_t)blockIdx.x * 2 + (k >= 0)) * 8 + hr) * prow;
           __stcg(reinterpret_cast<float4*>(pr + d), sum);
           if (d == 0) __stcg(reinterpret_cast<float2*>(pr + D), make_float2(top, lsum));
         }
@@ -839,8 +833,8 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
       if (s_first[x] < 0) continue;
       const int b0 = s_first[x], nb = s_last[x] - b0 + 1;
       const Piece& pc = *s_cross[x];
-      const int rows = min(8 * MT, a.group - pc.ht * 8 * MT), vecs = D >> 2, items = rows * vecs;
-      const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8 * MT;
+      const int rows = min(8, a.group - pc.ht * 8), vecs = D >> 2, items = rows * vecs;
+      const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8;
       // two items of a thread together, four parts at a time: their reads overlap
 #pragma unroll 1
       for (int e = tid; e < items; e += 2 * kAttThreads) {
@@ -866,7 +860,7 @@ __global__ void __launch_bounds__(kAttThreads, DP == 256 ? 1 : 2) attend_kernel(
             for (int i = 0; i < 2; ++i)
               if (j0 + j < nb) {  // the unit's (j0 + j)-th block
                 const float* pr =
-                    a.part + (((size_t)(b0 + j0 + j) * 2 + (j0 + j == 0)) * (8 * MT) + hr[i]) * prow;
+                    a.part + (((size_t)(b0 + j0 + j) * 2 + (j0 + j == 0)) * 8 + hr[i]) * prow;
                 q[i][j] = __ldcg(reinterpret_cast<const float2*>(pr + D));
                 v[i][j] = __ldcg(reinterpret_cast<const float4*>(pr + d[i]));
               }
@@ -1009,13 +1003,13 @@ static unsigned long long wait_limit() {
   return limit;
 }
 
-template <int DT, int DP, int MT>
+template <int DT, int DP>
 pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
   DevInfo di;
   pi_status st = dev_info(&di);
   if (st != PI_OK) return st;
-  constexpr int smem = att_smem<DP, MT>();
-  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, MT>), smem);
+  constexpr int smem = att_smem<DT, DP>();
+  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP>), smem);
   if (st != PI_OK) return st;
   // Two blocks per SM (one at 256 dims), or fewer where the longest slots that
   // the tables and the window allow cannot use them.
@@ -1023,10 +1017,10 @@ pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream s
   if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
   const long long tiles = (long long)a.slots * a.kv_heads * a.tiles * (seen / 16 + 3 + kUnitCost);
   const long long useful = tiles / (kAttWarps * kMinTiles) + 1;
-  long long grid = di.sms * (DP == 256 ? 1 : 2);
+  long long grid = di.sms * att_blocks<DT, DP>();
   if (grid > kAttendGrid) grid = kAttendGrid;
   if (grid > useful) grid = useful;
-  return launch(attend_kernel<DT, DP, MT>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
+  return launch(attend_kernel<DT, DP>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
                 map);
 }
 
@@ -1073,7 +1067,6 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   a.status = dev_status;
   a.arrived = reinterpret_cast<int*>(static_cast<char*>(ws) + w.arrived);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
-  a.wpart = reinterpret_cast<float*>(static_cast<char*>(ws) + w.wpart);
   a.slots = slots;
   a.heads = heads;
   a.kv_heads = C.kv_heads;
@@ -1093,16 +1086,15 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   a.tma = C.page_tokens % 16 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
           make_rows_map(&map, a.pool, rows, C, panels);
   if (a.tma && C.head_dim % 64 == 0) a.tma = 2;
-  const bool two = att_two_tiles(C.head_dim, a.group);
-  a.tiles = (a.group + (two ? 15 : 7)) / (two ? 16 : 8);
+  a.tiles = (a.group + 7) / 8;
   if (C.dtype == PI_F16) {
-    if (C.head_dim <= 64) return two ? launch_attend<0, 64, 2>(a, map, stream) : launch_attend<0, 64, 1>(a, map, stream);
-    if (C.head_dim <= 128) return two ? launch_attend<0, 128, 2>(a, map, stream) : launch_attend<0, 128, 1>(a, map, stream);
-    return launch_attend<0, 256, 1>(a, map, stream);
+    if (C.head_dim <= 64) return launch_attend<0, 64>(a, map, stream);
+    if (C.head_dim <= 128) return launch_attend<0, 128>(a, map, stream);
+    return launch_attend<0, 256>(a, map, stream);
   }
-  if (C.head_dim <= 64) return two ? launch_attend<1, 64, 2>(a, map, stream) : launch_attend<1, 64, 1>(a, map, stream);
-  if (C.head_dim <= 128) return two ? launch_attend<1, 128, 2>(a, map, stream) : launch_attend<1, 128, 1>(a, map, stream);
-  return launch_attend<1, 256, 1>(a, map, stream);
+  if (C.head_dim <= 64) return launch_attend<1, 64>(a, map, stream);
+  if (C.head_dim <= 128) return launch_attend<1, 128>(a, map, stream);
+  return launch_attend<1, 256>(a, map, stream);
 }
 
 pi_status pi_cache_append(const pi_cache_desc* cache, int32_t layer, int32_t slots,

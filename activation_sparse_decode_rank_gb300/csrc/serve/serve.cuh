@@ -106,17 +106,13 @@ inline pi_status ensure_smem(const void* fn, int bytes) {
   return PI_OK;
 }
 
-constexpr int kAttendGrid = 512;  // most thread blocks of the attention
-
-// Two tiles of eight query heads per unit where the group has them and a
-// head's accumulators leave the registers for it.
-inline bool att_two_tiles(int head_dim, int group) { return group > 8 && head_dim <= 128; }
+constexpr int kAttendGrid = 1024;  // most thread blocks of the attention
 
 // Byte offsets of the regions of a cache workspace.  `arrived` is zero
 // between calls and has one place and size for every cache, so that a
 // workspace may serve calls of several shapes; the rest is scratch.
 struct CacheWs {
-  size_t arrived, part, wpart, blocks, owner, rank, first, before, src, sums, total;
+  size_t arrived, part, blocks, owner, rank, first, before, src, sums, total;
 };
 
 constexpr int kScanPages = 1024;  // pages of one block of the page scans
@@ -132,9 +128,7 @@ inline CacheWs cache_ws(const pi_cache_desc& C, int slots, int heads) {
   (void)slots;
   w.arrived = take(4 * kAttendGrid);
   const size_t scratch = off;
-  const int rows = heads ? (att_two_tiles(C.head_dim, heads / C.kv_heads) ? 16 : 8) : 0;
-  w.part = take((size_t)kAttendGrid * 2 * rows * (C.head_dim + 4) * 4);
-  w.wpart = take(rows == 16 ? (size_t)kAttendGrid * 4 * 16 * (C.head_dim <= 64 ? 64 : 128) * 4 : 0);
+  w.part = take(heads ? (size_t)kAttendGrid * 2 * 8 * (C.head_dim + 4) * 4 : 0);
   const size_t end = off;
   off = scratch;  // the page calls use the same bytes
   w.blocks = take(4 * (((size_t)C.pages + kScanPages - 1) / kScanPages + 1));
