@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   // The warp's share of the line.  Lane t sums the slots [t k, t k + k).
   long long total, share0, share1;
   int grid;
-  Line line;
+  Line line{};
   Cursor cc;  // the tile being computed
   {
     auto unit_len = [](int tiles) { return tiles ? tiles + kUnitCost : 0; };
