@@ -9,15 +9,15 @@
 // drops out.  Each thread's M follows its running maximum.
 //
 // Alternatives without a second pass.  Threads own disjoint sets of elements,
-// so at least k elements are >= tau, the k-th largest of the maxima of fours
-// of threads, and all of the k largest are.  Each thread leaves the maxima of its batches
+// so at least k elements are >= tau, the k-th largest of the maxima of 64
+// sets of threads, and all of the k largest are.  Each thread leaves the maxima of its batches
 // (which the sums need anyway) in shared memory, so that only the batches
 // that reach tau, some k of them, are read again; their elements >= tau are
 // ranked by a unique key (value, then lowest index).  Where ties make more of
 // either than the block has room for, the whole part is read again: slower,
 // as exact, by sorted lists of 32 keys in the lanes of a warp.  Few keys are
 // ordered by counting, each thread, the keys larger than its own: one pass
-// of broadcast reads instead of a chain of exchanges (256 keys at most).
+// of broadcast reads instead of a chain of exchanges (128 keys at most).
 //
 // Bound: HBM bandwidth (each logit read once); for 16-bit logits the pass
 // issues some 5 instructions per logit, not far from the machine's rate at
@@ -43,9 +43,13 @@ struct ScoreArgs {
   int rows, vocab, topk, parts;
 };
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreBlocks = 4;        // per SM
+// Threads of a block.  256 for rows that are few beside the SMs.  From
+// kManyRows rows per SM on 128 with twice the blocks: while one block selects
+// its alternatives, seven others read (4096 x 128256 bf16, 20 alternatives:
+// 185 us against 192; x 32000 fp16: 57 against 69; but 600 rows of 128256, one
+// wave of 256-thread blocks, 36 against 32).
+constexpr int kManyRows = 10;
+constexpr int kScoreThreads = 1024;    // resident threads per SM
 constexpr int kScoreParts = 2048;      // most parts of rows in flight
 constexpr int kBatch = 4;              // 16-byte vectors of a thread's batch
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -100,11 +104,11 @@ __device__ __forceinline__ K merge32(K a, K b) {
   return merge_down(a > r ? a : r);
 }
 // The warps' lists into one, left in warp 0.
-template <typename K>
+template <int WARPS, typename K>
 __device__ __forceinline__ K block_merge(K v, u64 (*sh)[32]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int half = kScoreWarps / 2; half > 0; half >>= 1) {
+  for (int half = WARPS / 2; half > 0; half >>= 1) {
     if (warp >= half && warp < 2 * half) sh[warp][lane] = v;
     __syncthreads();
     if (warp < half) v = merge32(v, (K)sh[warp + half][lane]);
@@ -222,20 +226,21 @@ struct Count {
 };
 
 constexpr int kGroups = 16;  // groups of batches whose maxima a thread leaves
-constexpr int kPicks = 256;  // groups, then elements, that reach tau
+constexpr int kPicks = 128;  // groups, then elements, that reach tau
 
 // One block per (row, part).
-template <int DT>
-__global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(const ScoreArgs a) {
+template <int DT, int T>
+__global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const ScoreArgs a) {
   using V = Vec<DT>;
-  constexpr int VN = V::n, T = kScoreThreads;
+  constexpr int VN = V::n, WARPS = T / 32;
+  constexpr int kSets = 64, kSet = T / kSets;  // sets of threads whose maxima bound the k-th
   constexpr int kSize = DT == 2 ? 4 : 2;
-  __shared__ u64 sh_keys[kScoreWarps][32];
-  __shared__ float sh_sums[kScoreWarps][3];
+  __shared__ u64 sh_keys[WARPS][32];
+  __shared__ float sh_sums[WARPS][3];
   __shared__ float sh_top[kGroups][T];
   __shared__ uint32_t sh_group[kPicks];
   __shared__ u64 sh_pick[kPicks];
-  __shared__ __align__(16) uint32_t sh_four[T / 4];
+  __shared__ __align__(16) uint32_t sh_set[kSets];
   __shared__ uint32_t sh_tau;
   __shared__ u64 sh_list[32];
   __shared__ int sh_groups, sh_picks, sh_last;
@@ -374,26 +379,26 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) sh_sums[warp][0] = top;
-  if (a.topk > 0) {  // maxima of fours of threads, as keys (0: only NaN, or nothing)
+  if (a.topk > 0) {  // maxima of sets of threads, as keys (0: only NaN, or nothing)
     uint32_t k = some ? value_key(sum.m) : 0u;
-    k = max(k, __shfl_xor_sync(~0u, k, 1));
-    k = max(k, __shfl_xor_sync(~0u, k, 2));
-    if ((lane & 3) == 0) sh_four[tid >> 2] = k;
+#pragma unroll
+    for (int o = 1; o < kSet; o <<= 1) k = max(k, __shfl_xor_sync(~0u, k, o));
+    if (tid % kSet == 0) sh_set[tid / kSet] = k;
   }
   __syncthreads();
-  if (a.topk > 0 && tid < T / 4) {  // the one with topk - 1 ahead of it
-    const uint32_t k = sh_four[tid];
+  if (a.topk > 0 && tid < kSets) {  // the one with topk - 1 ahead of it
+    const uint32_t k = sh_set[tid];
     int ahead = 0;
 #pragma unroll 4
-    for (int i = 0; i < T / 4; i += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(sh_four + i);
+    for (int i = 0; i < kSets; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(sh_set + i);
       ahead += (o.x > k || (o.x == k && i < tid)) + (o.y > k || (o.y == k && i + 1 < tid)) +
                (o.z > k || (o.z == k && i + 2 < tid)) + (o.w > k || (o.w == k && i + 3 < tid));
     }
     if (ahead == a.topk - 1) sh_tau = k;
   }
 #pragma unroll
-  for (int w = 0; w < kScoreWarps; ++w) top = fmaxf(top, sh_sums[w][0]);
+  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sh_sums[w][0]);
   {
     const Sums up = raised(sum, top);
     const float s = warp_sum(up.s), t = warp_sum(up.t);
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
           enter(in ? rank_key(x, (j0 + lane) * VN + e - shift) : 0);
         }
       }
-      list = block_merge(list, sh_keys);
+      list = block_merge<WARPS>(list, sh_keys);
       if (warp == 0 && cut_first) {
         const int i = lane - shift;
         enter(lane < VN && i >= 0 && i < a.vocab ? rank_key(logit_at<DT>(base, i), i) : 0);
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
   if (warp == 0) {
     sum = Sums{top, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kScoreWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       sum.s += sh_sums[w][1];
       sum.t += sh_sums[w][2];
     }
@@ -534,9 +539,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
     }
     if (a.topk > 0) {
       list = 0;
-      for (int p = warp; p < a.parts; p += kScoreWarps)
+      for (int p = warp; p < a.parts; p += WARPS)
         list = merge32(list, __ldcg(a.pkeys + (row * a.parts + p) * 32 + lane));
-      list = block_merge(list, sh_keys);
+      list = block_merge<WARPS>(list, sh_keys);
     }
   }
 
@@ -569,12 +574,20 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks) score_kernel(cons
 
 // Parts of a row: enough blocks to fill the GPU, each with a batch at least.
 static int score_parts(int rows, int vocab, int dtype, int sms) {
-  const int slots = sms * kScoreBlocks;
+  const int slots = sms * (kScoreThreads / 256);
   int parts = rows < slots ? slots / rows : 1;
-  const int batches = vocab / (kScoreThreads * kBatch * (dtype == PI_F32 ? 4 : 8));
+  const int batches = vocab / (256 * kBatch * (dtype == PI_F32 ? 4 : 8));
   if (parts > batches) parts = batches;
   if (parts > kScoreParts / rows) parts = kScoreParts / rows;
   return parts > 1 ? parts : 1;
+}
+
+template <int T>
+static pi_status launch_score(const ScoreArgs& a, int dtype, pi_stream stream) {
+  return launch(dtype == PI_F16    ? score_kernel<0, T>
+                : dtype == PI_BF16 ? score_kernel<1, T>
+                                   : score_kernel<2, T>,
+                dim3((unsigned)a.rows, (unsigned)a.parts), T, 0, stream, a);
 }
 
 }  // namespace pis
@@ -614,8 +627,8 @@ pi_status pi_token_logprobs(const void* logits, int32_t dtype, int32_t rows, int
               reinterpret_cast<float*>(w + kScoreParts * 4),
               reinterpret_cast<u64*>(w + kScoreParts * (4 + 16)),
               rows, vocab, topk, score_parts(rows, vocab, dtype, di.sms)};
-  return launch(dtype == PI_F16 ? score_kernel<0> : dtype == PI_BF16 ? score_kernel<1> : score_kernel<2>,
-                dim3((unsigned)rows, (unsigned)a.parts), kScoreThreads, 0, stream, a);
+  return rows >= kManyRows * di.sms ? launch_score<128>(a, dtype, stream)
+                                    : launch_score<256>(a, dtype, stream);
 }
 
 }  // extern "C"

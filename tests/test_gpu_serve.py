@@ -624,6 +624,32 @@ def test_scores_of_ties_sorted_rows_and_banned_tokens(dtype, rows):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("vocab,pad,topk", [(701, 0, 20), (5003, 5, 32), (33_000, 0, 7)])
+def test_scores_of_many_rows(dtype, vocab, pad, topk):
+    # more rows than the GPU holds blocks: random, rising, tied and banned rows
+    # in turn; every 37th is compared
+    R, g = 2100, np.random.default_rng(vocab)
+    x = g.standard_normal((R, vocab)).astype(np.float32) * 3
+    x[1::5] = np.arange(vocab) / 64.0
+    x[2::5] = np.round(x[2::5])
+    x[3::5, g.random(vocab) < 0.98] = -np.inf
+    tok = g.integers(0, vocab, R)
+    (lp, ent, idx, top), st = run_score(x, dtype, tok.tolist(), topk, pad)
+    assert st == 0
+    e = 2.0 ** -20 + vocab * U
+    for r in range(0, R, 37):
+        x16 = torch.from_numpy(x[r]).to(TD[dtype]).double().numpy()
+        wl, we, wi, wt = plain.score_row(x16, int(tok[r]), topk)
+        f = x16[np.isfinite(x16)]
+        tol = 2 * e + 8 * U * (f.max() - f.min() + 20)
+        assert idx[r].astype(int).tolist() == wi, r
+        assert lp[r] == wl or abs(lp[r] - wl) <= tol
+        assert abs(ent[r] - we) <= 4 * e * (1 + math.log(vocab)) + 4 * U * (f.max() - f.min())
+        for a, b in zip(top[r], wt):
+            assert a == b or abs(a - b) <= tol
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_scores_of_odd_rows(dtype):
     V = 3001
     g = np.random.default_rng(6)
