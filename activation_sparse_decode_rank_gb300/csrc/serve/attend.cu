@@ -67,6 +67,10 @@ constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int kUnitCost = 2;  // a unit's start and end, in tiles
 constexpr int kMinTiles = 4;  // a warp's least share, in tiles
+// Units of at most this length (2 is the unit's cost), and no more of them
+// than blocks, have a block each: nothing is joined across blocks, which
+// takes the time of some eight tiles of a warp.
+constexpr int kApartTiles = 48;
 
 // Thread blocks per SM, and stages of a warp's ring, by measurement.  More
 // warps hide a tile's chain of instructions, more stages its loads; bf16 tiles
@@ -348,7 +352,9 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   Line line{};
   Cursor cc;  // the tile being computed
   {
-    auto unit_len = [](int tiles) { return tiles ? tiles + kUnitCost : 0; };
+    int most = 0;  // the longest unit
+    bool apart = false;
+    auto unit_len = [&](int tiles) { return tiles ? apart ? most : tiles + kUnitCost : 0; };
     auto scan = [&](long long v) {  // sums up to and with this lane
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -364,15 +370,23 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       const int n = unit_len(seen_of(a, s).tiles);
       mine += n;
       used += n > 0;
+      most = max(most, n);
     }
-    const long long upto = scan(mine);
-    total = __shfl_sync(~0u, upto, 31) * units;
+    most = (int)__reduce_max_sync(~0u, (uint32_t)most);
+    const int per = (int)__reduce_add_sync(~0u, (uint32_t)used) * units;  // units in use
     grid = gridDim.x;
-    if (total < (long long)grid * kAttWarps * kMinTiles) {
+    if (most <= kApartTiles && per <= grid) {
+      // a block per unit, its tiles shared evenly by the block's warps
+      apart = true;
+      mine = (long long)used * most;
+      grid = per;
+    }
+    long long upto = scan(mine);
+    total = __shfl_sync(~0u, upto, 31) * units;
+    if (!apart && total < (long long)grid * kAttWarps * kMinTiles) {
       // few tiles: if it can be, a multiple of the units, so that equal units
       // begin at a block's start and need no join across blocks
       grid = ((int)total + kAttWarps * kMinTiles - 1) / (kAttWarps * kMinTiles);
-      const int per = (int)__reduce_add_sync(~0u, used) * units;
       if (per > 0 && per <= (int)gridDim.x) {
         const int up = (grid + per - 1) / per * per;
         if (up <= (int)gridDim.x) grid = up;
@@ -384,7 +398,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
     if ((int)blockIdx.x < grid) {
       line.set(total, grid);
       const long long from = line.start(blockIdx.x), n = line.start(blockIdx.x + 1) - from;
-      share0 = from + (warp * n) / kAttWarps;
+      share0 = apart ? from : from + (warp * n) / kAttWarps;
       share1 = from + ((warp + 1) * n) / kAttWarps;
       // its first slot, and where that begins
       long long at = (upto - mine) * units;
@@ -407,6 +421,13 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       cc.ht = unit - cc.g * a.tiles;
       cc.tile = max(0, r - kUnitCost);
       cc.pos = share0 + max(0, kUnitCost - r);
+      if (apart) {  // warps past the last tile have none
+        const int t = cc.v.tiles, each = t / kAttWarps, more = t % kAttWarps;
+        share1 = line.start(blockIdx.x + 1) - t;
+        cc.tile = warp * each + min(warp, more);
+        cc.pos = share0 = share1 + cc.tile;
+        share1 += (warp + 1) * each + min(warp + 1, more);
+      }
     }
   }
   Cursor lc = cc;  // the tile being loaded
@@ -1015,8 +1036,9 @@ pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream s
   // the tables and the window allow cannot use them.
   long long seen = (long long)a.max_pages * a.page_tokens;
   if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
-  const long long tiles = (long long)a.slots * a.kv_heads * a.tiles * (seen / 16 + 3 + kUnitCost);
-  const long long useful = tiles / (kAttWarps * kMinTiles) + 1;
+  const long long units = (long long)a.slots * a.kv_heads * a.tiles;
+  const long long shares = units * (seen / 16 + 3 + kUnitCost) / (kAttWarps * kMinTiles) + 1;
+  const long long useful = shares > units ? shares : units;
   long long grid = di.sms * att_blocks<DT, DP>();
   if (grid > kAttendGrid) grid = kAttendGrid;
   if (grid > useful) grid = useful;

@@ -40,33 +40,44 @@ SIGNATURES = {
 }
 
 
-_L = None
+# These operators run for a few microseconds, so the binding keeps its own part
+# short: entry points and torch's stream lookup are found once, and arguments
+# that are tensors are taken without a call per argument.
+_entry = {}
+_torch = None
+_raw_stream = None
 
 
 def _pkg():
-    """The loaded libpi.so (looked up once)."""
-    global _L
-    if _L is None:
-        from . import lib
-        _L = lib()
-    return _L
+    from . import lib
+    return lib()
+
+
+def _fn(name):
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(_pkg(), name)
+    return f
 
 
 def _ptr(t):
+    """Device pointer of a tensor (or an int address, or None)."""
     if t is None:
         return None
-    return t if isinstance(t, int) else t.data_ptr()
+    return t if type(t) is int else t.data_ptr()
 
 
 def _current_stream():
-    """Handle of torch's current stream.  These operators run for a few
-    microseconds, and making torch's stream object alone takes three, so the
-    handle is taken without one where torch offers that."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    """Handle of torch's current stream; without making a stream object (which
+    takes three microseconds) where torch offers that."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch = torch
+    if _raw_stream is None:
+        return _torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_torch.cuda.current_device())
 
 
 def _stream(s):
@@ -85,11 +96,11 @@ def make_cache_desc(layers: int, pages: int, kv_heads: int, head_dim: int, page_
 
 
 def pi_cache_workspace_size(cache, slots: int, heads: int) -> int:
-    return _pkg().pi_cache_workspace_size(ctypes.byref(cache), slots, heads)
+    return _fn("pi_cache_workspace_size")(ctypes.byref(cache), slots, heads)
 
 
 def pi_logprob_workspace_size(rows: int, vocab: int, topk: int) -> int:
-    return _pkg().pi_logprob_workspace_size(rows, vocab, topk)
+    return _fn("pi_logprob_workspace_size")(rows, vocab, topk)
 
 
 def _zeros(nbytes, where, device):
@@ -114,7 +125,7 @@ def logprob_workspace(rows: int, vocab: int, topk: int, device="cuda"):
 def pi_paged_attention(cache, layer, slots, heads, max_pages, q, k_new, v_new, table, len, pool,
                        scale, window, sinks, y, lse, dev_status, ws, ws_bytes=None,
                        stream=None) -> int:
-    return _pkg().pi_paged_attention(
+    return _fn("pi_paged_attention")(
         ctypes.byref(cache), layer, slots, heads, max_pages, _ptr(q), _ptr(k_new), _ptr(v_new),
         _ptr(table), _ptr(len), _ptr(pool), scale, window, sinks, _ptr(y), _ptr(lse),
         _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
@@ -122,14 +133,14 @@ def pi_paged_attention(cache, layer, slots, heads, max_pages, q, k_new, v_new, t
 
 def pi_cache_append(cache, layer, slots, max_pages, tokens, slot, pos, k, v, table, pool,
                     dev_status, stream=None) -> int:
-    return _pkg().pi_cache_append(
+    return _fn("pi_cache_append")(
         ctypes.byref(cache), layer, slots, max_pages, tokens, _ptr(slot), _ptr(pos), _ptr(k),
         _ptr(v), _ptr(table), _ptr(pool), _ptr(dev_status), _stream(stream))
 
 
 def pi_cache_fork(cache, slots, max_pages, parent, grow, held, table_in, len_in, table, len, ref,
                   pool, pairs, counts, dev_status, ws, ws_bytes=None, stream=None) -> int:
-    return _pkg().pi_cache_fork(
+    return _fn("pi_cache_fork")(
         ctypes.byref(cache), slots, max_pages, _ptr(parent), _ptr(grow), _ptr(held),
         _ptr(table_in), _ptr(len_in), _ptr(table), _ptr(len), _ptr(ref), _ptr(pool), _ptr(pairs),
         _ptr(counts), _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
@@ -137,21 +148,21 @@ def pi_cache_fork(cache, slots, max_pages, parent, grow, held, table_in, len_in,
 
 def pi_cache_compact(cache, slots, max_pages, held, table_in, len, table, ref, map, pool, pairs,
                      counts, dev_status, ws, ws_bytes=None, stream=None) -> int:
-    return _pkg().pi_cache_compact(
+    return _fn("pi_cache_compact")(
         ctypes.byref(cache), slots, max_pages, _ptr(held), _ptr(table_in), _ptr(len), _ptr(table),
         _ptr(ref), _ptr(map), _ptr(pool), _ptr(pairs), _ptr(counts), _ptr(dev_status), _ptr(ws),
         _ws_bytes(ws, ws_bytes), _stream(stream))
 
 
 def pi_cache_copy(cache, pairs, count, cap, pool, dev_status, stream=None) -> int:
-    return _pkg().pi_cache_copy(ctypes.byref(cache), _ptr(pairs), _ptr(count), cap, _ptr(pool),
+    return _fn("pi_cache_copy")(ctypes.byref(cache), _ptr(pairs), _ptr(count), cap, _ptr(pool),
                                 _ptr(dev_status), _stream(stream))
 
 
 def pi_token_logprobs(logits, dtype, rows, vocab, stride, tokens, topk, logprob, entropy, top_idx,
                       top_logprob, dev_status, ws, ws_bytes=None, stream=None) -> int:
     """dtype: "f16", "bf16", "f32" or the C enum's value."""
-    return _pkg().pi_token_logprobs(
+    return _fn("pi_token_logprobs")(
         _ptr(logits), _DTYPES.get(dtype, dtype), rows, vocab, stride, _ptr(tokens), topk,
         _ptr(logprob), _ptr(entropy), _ptr(top_idx), _ptr(top_logprob), _ptr(dev_status), _ptr(ws),
         _ws_bytes(ws, ws_bytes), _stream(stream))
