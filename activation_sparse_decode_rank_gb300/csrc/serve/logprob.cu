@@ -233,7 +233,7 @@ template <int DT, int T>
 __global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const ScoreArgs a) {
   using V = Vec<DT>;
   constexpr int VN = V::n, WARPS = T / 32;
-  constexpr int kSets = 64, kSet = T / kSets;  // sets of threads whose maxima bound the k-th
+  constexpr int kSets = 64;  // sets of threads whose maxima bound the k-th
   constexpr int kSize = DT == 2 ? 4 : 2;
   __shared__ u64 sh_keys[WARPS][32];
   __shared__ float sh_sums[WARPS][3];
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const Score
   __shared__ uint32_t sh_group[kPicks];
   __shared__ u64 sh_pick[kPicks];
   __shared__ __align__(16) uint32_t sh_set[kSets];
+  __shared__ uint32_t sh_max[T];
   __shared__ uint32_t sh_tau;
   __shared__ u64 sh_list[32];
   __shared__ int sh_groups, sh_picks, sh_last;
@@ -379,16 +380,15 @@ __global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const Score
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) sh_sums[warp][0] = top;
-  if (a.topk > 0) {  // maxima of sets of threads, as keys (0: only NaN, or nothing)
-    uint32_t k = some ? value_key(sum.m) : 0u;
-#pragma unroll
-    for (int o = 1; o < kSet; o <<= 1) k = max(k, __shfl_xor_sync(~0u, k, o));
-    if (tid % kSet == 0) sh_set[tid / kSet] = k;
-  }
+  if (a.topk > 0) sh_max[tid] = some ? value_key(sum.m) : 0u;  // 0: only NaN, or nothing
   __syncthreads();
-  if (a.topk > 0 && tid < kSets) {  // the one with topk - 1 ahead of it
-    const uint32_t k = sh_set[tid];
-    int ahead = 0;
+  if (a.topk > 0 && tid < kSets) {  // set s: the threads s, s + 64, ...
+    uint32_t k = sh_max[tid];
+#pragma unroll
+    for (int o = kSets; o < T; o += kSets) k = max(k, sh_max[tid + o]);
+    sh_set[tid] = k;
+    asm volatile("bar.sync 1, %0;" ::"n"(kSets) : "memory");  // the first two warps
+    int ahead = 0;  // the one with topk - 1 ahead of it
 #pragma unroll 4
     for (int i = 0; i < kSets; i += 4) {
       const uint4 o = *reinterpret_cast<const uint4*>(sh_set + i);
@@ -408,6 +408,14 @@ __global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const Score
     }
   }
 
+  auto order = [&](const u64* keys, int n) {  // the first 32 of n <= T keys into sh_list
+    if (tid >= n) return;
+    const u64 k = keys[tid];
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) ahead += keys[i] > k;
+    if (ahead < 32) sh_list[ahead] = k;
+  };
   u64 list = 0;  // warp 0: the 32 largest keys (only the first topk count)
   if (a.topk > 0) {
     __syncthreads();
@@ -459,13 +467,7 @@ __global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const Score
       const int picks = sh_picks;
       all |= picks > kPicks;
       if (!all) {
-        if (tid < picks) {
-          const u64 k = sh_pick[tid];
-          int ahead = 0;
-#pragma unroll 4
-          for (int i = 0; i < picks; ++i) ahead += sh_pick[i] > k;
-          if (ahead < 32) sh_list[ahead] = k;
-        }
+        order(sh_pick, picks);
         __syncthreads();
         if (warp == 0) list = lane < picks ? sh_list[lane] : 0;
       }
