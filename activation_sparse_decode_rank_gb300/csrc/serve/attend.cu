@@ -40,13 +40,13 @@ namespace pis {
 // the order of the sums is fixed).
 //
 // Data flow.  A warp streams its tiles through its own ring of stages, without
-// any block-wide barrier until the end.  Where pages hold multiples of 16
-// tokens a tile lies in one page: one lane orders its K and V as TMA boxes of
-// 16 rows x 128 bytes, swizzled, that arrive on the stage's mbarrier (rows of
-// a box outside the visible set are cleared before use).  Other page sizes,
-// head dimensions below 64 and pools of 2^31 rows or more gather row pieces
-// with cp.async into the same layout.  Head dimensions below 64, 128 or 256
-// are padded with zeros in shared memory only.
+// any block-wide barrier until the end.  Where pages hold multiples of 16 (8)
+// tokens, a tile (half a tile) lies in one page: one lane orders its K and V
+// as TMA boxes of 16 (8) rows, 128-byte swizzle, that arrive on the stage's
+// mbarrier (values of rows outside the visible set are cleared before use).
+// Other page sizes, head dimensions below 64 and pools of 2^31 rows or more
+// gather row pieces with cp.async into the same layout.  Head dimensions below
+// 64, 128 or 256 are padded with zeros in shared memory only.
 struct AttendArgs {
   const float *q, *k_new, *v_new;
   const int *table, *len;
@@ -58,7 +58,7 @@ struct AttendArgs {
   int slots, heads, kv_heads, group, head_dim, page_tokens, pages, max_pages, window, sinks;
   int tiles;      // head tiles per kv head: ceil(group / 8)
   int page_shift; // log2(page_tokens), or -1
-  int tma;        // tiles come as TMA boxes: 1 a panel, 2 a whole tile each
+  int tma;        // tiles come as TMA boxes: 1 of a panel, 2 of all panels
   float scale;    // scale log2(e)
   unsigned long long limit_ns;  // of a wait for a tile
 };
@@ -80,11 +80,11 @@ constexpr int kApartTiles = 48;
 // 109 us (2 x 2 113).
 template <int DT, int DP>
 __host__ __device__ constexpr int att_blocks() {
-  return DP == 256 ? 1 : DP == 64 ? 3 + DT : 2;
+  return DP == 64 ? 3 + DT : 2;
 }
 template <int DT, int DP>
 __host__ __device__ constexpr int att_stages() {
-  return DP == 64 ? 3 - DT : DP == 128 ? 2 + DT : 2;
+  return DP == 64 ? 3 - DT : DP == 128 ? 2 + DT : 1;
 }
 template <int DT, int DP>
 __host__ __device__ constexpr int att_smem() {
@@ -136,16 +136,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, unsigned
   }
   return true;
 }
-// 16 rows of 64 elements at (x, y) of the pool's rows -> shared memory.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
+// K and V of a panel of 64 elements, from column x, of the rows from y of the
+// pool's rows -> shared memory.
+__device__ __forceinline__ void tma_panel(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(m))
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(0), "r"(smem_u32(m))
       : "memory");
 }
-// The K and the V tile at row y of the pool's rows (panels, then K / V).
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int y, uint64_t* m) {
+// The same of all panels.
+__device__ __forceinline__ void tma_panels(uint32_t dst, const CUtensorMap* map, int y, uint64_t* m) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
       "%3, %2, %2}], [%4];" ::"r"(dst),
@@ -320,11 +321,14 @@ struct Piece {
   int slot, g, ht, tiles;
 };
 
-template <int DT, int DP>
+// BR: rows of a box (16 too where tiles are gathered).
+template <int DT, int DP, int BR>
 __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int S = att_stages<DT, DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
-  constexpr int kPanel = 16 * 128;         // 16 rows of 64 elements: a tile is DP / 64 panels
+  // A stage: [16 / BR boxes][DP / 64 panels][K, V][BR rows][64 elements].
+  constexpr int kValues = BR * 128, kPanel = 2 * kValues, kBox = DP / 64 * kPanel;
+  auto row_at = [](int r) { return r / BR * kBox + r % BR * 128; };
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
   constexpr float kShift = DT == 0 ? 14.f : 0.f;  // weights carry 2^kShift
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -434,15 +438,16 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
 
   const uint32_t ring = smem_u32(smem) + warp * S * 2 * kTile;
   const int pieces = D >> 3;
-  const bool one_page = (P & 15) == 0;  // a tile lies in one page
+  const bool one_page = P % BR == 0;  // a box lies in one page
   const size_t v_off = (size_t)a.kv_heads * P * D;
 
   // The tile that lc points at: visible rows, first token, the row within its
   // page (of lane r's row where a tile may span pages), page number.  Where
-  // it may not, lane i holds the page of the unit's tile page0 + i.
+  // it may not, lane i holds the page of box i of the unit's tiles from page0.
   uint32_t next_rows = 0;
   int next_t = 0, next_row = 0, next_page = 0, pages32 = 0, page0 = 0;
   auto page_index = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / P; };
+  constexpr int kBoxes = 16 / BR;  // of a tile
   auto fetch = [&](bool unit_begins) {
     if (unit_begins) {  // bring the unit's query rows near: they are read when its first tile is
       const int rows = min(8, a.group - lc.ht * 8);
@@ -456,13 +461,21 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
     next_t = lc.rows_of(next_rows);
     const int* row = a.table + (size_t)lc.slot * a.max_pages;
     if (one_page) {
-      next_row = next_t - page_index(next_t) * P;
-      if (unit_begins || lc.tile - page0 == 32) {
+      if (BR == 16) next_row = next_t - page_index(next_t) * P;
+      if (unit_begins || lc.tile - page0 == 32 / kBoxes) {
         page0 = lc.tile;
         Cursor c = lc;
-        c.tile += lane;
+        c.tile += lane / kBoxes;
         pages32 = -2;
-        if (c.tile < c.v.tiles) pages32 = __ldg(row + page_index(c.first_token()));
+        if (c.tile < c.v.tiles) {
+          uint32_t seen = 1;
+          int t = BR == 16 ? c.first_token() : c.rows_of(seen);
+          if (BR == 8) {  // a box may hold nothing visible, and its entry no page
+            t += 8 * (lane & 1);
+            seen = seen >> (8 * (lane & 1)) & 0xffu;
+          }
+          if (seen) pages32 = __ldg(row + page_index(t));
+        }
       }
     } else {
       const int t = next_t + (lane & 15), j = page_index(t);
@@ -473,7 +486,34 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   // Sends that tile into a stage.  Piece pc of row r lies in panel pc / 8 at
   // piece (pc ^ r) & 7 of its row.
   constexpr int kRows = 32 / kPieces;  // rows per instruction of the gather: 4, 2, 1
+  auto order = [&](uint32_t to, int y, uint64_t* bar) {  // a box
+    if (a.tma == 2) {
+      tma_panels(to, &map, y, bar);
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < DP / 64; ++c) tma_panel(to + c * kPanel, &map, 64 * c, y, bar);
+    }
+  };
   auto issue = [&](int stage) {
+    const uint32_t k0 = ring + stage * 2 * kTile;
+    uint64_t* bar = &s_bar[warp][stage];
+    if constexpr (BR == 8) {
+      const int i = 2 * (lc.tile - page0);
+      const int p[2] = {__shfl_sync(~0u, pages32, i), __shfl_sync(~0u, pages32, i + 1)};
+      const bool ok[2] = {(unsigned)p[0] < (unsigned)a.pages, (unsigned)p[1] < (unsigned)a.pages};
+      if ((!ok[0] && p[0] != -2) || (!ok[1] && p[1] != -2)) set_status(a.status, PI_ERR_INDEX);
+      if (lane == 0) {
+        s_mask[warp][stage] = next_rows & ((ok[0] ? 0xffu : 0u) | (ok[1] ? 0xff00u : 0u));
+        mbar_expect(bar, (ok[0] + ok[1]) * kBox);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (ok[h]) {
+            const int t = next_t + 8 * h;
+            order(k0 + h * kBox, (p[h] * 2 * a.kv_heads + lc.g) * P + t - page_index(t) * P, bar);
+          }
+      }
+      return;
+    }
     if (one_page) next_page = __shfl_sync(~0u, pages32, lc.tile - page0);
     const bool ok = (unsigned)next_page < (unsigned)a.pages;
     if (!ok && next_page != -2) set_status(a.status, PI_ERR_INDEX);
@@ -484,20 +524,10 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       rows &= __ballot_sync(~0u, ok);
     if (lane == 0) s_mask[warp][stage] = rows;
     const long long row = ok ? ((long long)next_page * 2 * a.kv_heads + lc.g) * P + next_row : 0;
-    const uint32_t k0 = ring + stage * 2 * kTile;
     if (a.tma) {
       if (lane == 0) {
-        uint64_t* bar = &s_bar[warp][stage];
-        mbar_expect(bar, rows ? 2 * kTile : 0);
-        if (rows && a.tma == 2) {
-          tma_tile(k0, &map, (int)row, bar);
-        } else if (rows) {
-#pragma unroll 1
-          for (int c = 0; c < DP / 64; ++c) {
-            tma_box(k0 + c * kPanel, &map, 64 * c, (int)row, bar);
-            tma_box(k0 + kTile + c * kPanel, &map, 64 * c, (int)row + a.kv_heads * P, bar);
-          }
-        }
+        mbar_expect(bar, rows ? kBox : 0);
+        if (rows) order(k0, (int)row, bar);
       }
       return;
     }
@@ -512,9 +542,9 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       if (pc < pieces) {
         const bool take = rows >> r & 1u;
         const uint16_t* p = a.pool + (take ? (size_t)src * D + 8 * pc : 0);
-        const uint32_t to = k0 + (pc >> 3) * kPanel + r * 128 + (((pc ^ r) & 7) << 4);
+        const uint32_t to = k0 + (pc >> 3) * kPanel + row_at(r) + (((pc ^ r) & 7) << 4);
         cp16(to, p, take ? 16 : 0);
-        cp16(to + kTile, p + (take ? v_off : 0), take ? 16 : 0);
+        cp16(to + kValues, p + (take ? v_off : 0), take ? 16 : 0);
       }
     }
     cp_commit();
@@ -595,14 +625,14 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
     }
     __syncwarp();
 
-    const uint32_t k0 = ring + stage * 2 * kTile, v0 = k0 + kTile;
+    const uint32_t k0 = ring + stage * 2 * kTile, v0 = k0 + kValues;
     const uint32_t mask = s_mask[warp][stage];
     if (a.tma && mask != 0xffffu && mask != 0) {
       // values of rows that are not visible: 0 x NaN is not 0
       for (int e = lane; e < 16 * kPieces; e += 32)
         if (!(mask >> (e >> 3 & 15) & 1u))
-          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + kTile + (e >> 7) * kPanel +
-                                    (e & 127) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + (e >> 7) * kPanel + kValues +
+                                    row_at(e >> 3 & 15) + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
       fence_async();
       __syncwarp();
     }
@@ -621,8 +651,8 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
           const float4 x = __ldg(src), y = __ldg(src + 1);
           const uint4 w = make_uint4(pack_bits<DT>(x.x, x.y), pack_bits<DT>(x.z, x.w),
                                      pack_bits<DT>(y.x, y.y), pack_bits<DT>(y.z, y.w));
-          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + kind * kTile +
-                                    (pc >> 3) * kPanel + r * 128 + (((pc ^ r) & 7) << 4)) = w;
+          *reinterpret_cast<uint4*>(smem + (warp * S + stage) * 2 * kTile + kind * kValues +
+                                    (pc >> 3) * kPanel + row_at(r) + (((pc ^ r) & 7) << 4)) = w;
           if (ht == 0) *reinterpret_cast<uint4*>(dst + kind * v_off + 8 * pc) = w;
         }
         fence_async();
@@ -635,7 +665,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       float sc[2][2][4];  // even and odd steps: shorter chains
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), pc = (lane >> 3) & 1;
-        const uint32_t at = k0 + r * 128 + ((pc ^ (r & 7)) << 4);
+        const uint32_t at = k0 + row_at(r) + ((pc ^ (r & 7)) << 4);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
           uint32_t b[4];
@@ -686,7 +716,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       split2<DT>(p[2], p[3], pf[2], pf[3], pf2[1]);
       // weighted values; each tile's product is rounded once into the fp32 sums
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), pc = lane >> 4;
-      const uint32_t at = v0 + r * 128 + ((pc ^ (r & 7)) << 4);
+      const uint32_t at = v0 + row_at(r) + ((pc ^ (r & 7)) << 4);
 #pragma unroll
       for (int jj = 0; jj < DP / 16; ++jj) {
         uint32_t b[4];
@@ -984,17 +1014,17 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
 }
 
 // Map over a layer's rows (K and V rows of every page and kv head), 128-byte
-// swizzle.  Head dimensions that are multiples of 64: {64 elements, rows,
-// panels, K / V}, one box for a whole tile (one request instead of two per
-// panel: a lane's request takes some 100 cycles to issue).  Others: boxes of
-// 16 rows x 64 elements with zeros past the row's end.  False where the driver
-// offers no such map.
+// swizzle, box_rows rows of K and of V per box.  Head dimensions that are
+// multiples of 64: {64 elements, rows, K / V, panels}, a box of all panels (a
+// lane's request takes some 100 cycles to issue).  Others: {row, rows, K / V},
+// a box per panel, zeros past the row's end.  False where the driver offers no
+// such map.
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 static bool make_rows_map(CUtensorMap* m, void* base, long long rows, const pi_cache_desc& C,
-                          int panels) {
+                          int panels, int box_rows) {
   static const EncodeFn encode = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -1005,11 +1035,12 @@ static bool make_rows_map(CUtensorMap* m, void* base, long long rows, const pi_c
   if (!encode) return false;
   const cuuint64_t row = (cuuint64_t)C.head_dim * 2, half = (cuuint64_t)C.kv_heads * C.page_tokens;
   const bool whole = C.head_dim % 64 == 0;
-  const cuuint64_t dims[4] = {whole ? 64u : (cuuint64_t)C.head_dim, (cuuint64_t)rows - (whole ? half : 0),
-                              (cuuint64_t)C.head_dim / 64, 2u};
-  const cuuint64_t strides[3] = {row, 128u, half * row};
-  const cuuint32_t box[4] = {64u, 16u, (cuuint32_t)panels, 2u}, steps[4] = {1u, 1u, 1u, 1u};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, whole ? 4 : 2, base, dims, strides, box, steps,
+  const cuuint64_t dims[4] = {whole ? 64u : (cuuint64_t)C.head_dim, (cuuint64_t)rows - half, 2u,
+                              (cuuint64_t)C.head_dim / 64};
+  const cuuint64_t strides[3] = {row, half * row, 128u};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 2u, (cuuint32_t)panels},
+                   steps[4] = {1u, 1u, 1u, 1u};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, whole ? 4 : 3, base, dims, strides, box, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1024,13 +1055,13 @@ static unsigned long long wait_limit() {
   return limit;
 }
 
-template <int DT, int DP>
-pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
+template <int DT, int DP, int BR>
+pi_status launch_boxes(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
   DevInfo di;
   pi_status st = dev_info(&di);
   if (st != PI_OK) return st;
   constexpr int smem = att_smem<DT, DP>();
-  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP>), smem);
+  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, BR>), smem);
   if (st != PI_OK) return st;
   // Two blocks per SM (one at 256 dims), or fewer where the longest slots that
   // the tables and the window allow cannot use them.
@@ -1042,8 +1073,14 @@ pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream s
   long long grid = di.sms * att_blocks<DT, DP>();
   if (grid > kAttendGrid) grid = kAttendGrid;
   if (grid > useful) grid = useful;
-  return launch(attend_kernel<DT, DP>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
+  return launch(attend_kernel<DT, DP, BR>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
                 map);
+}
+
+template <int DT, int DP>
+pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
+  return a.tma && a.page_tokens % 16 ? launch_boxes<DT, DP, 8>(a, map, stream)
+                                     : launch_boxes<DT, DP, 16>(a, map, stream);
 }
 
 }  // namespace pis
@@ -1105,8 +1142,8 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   CUtensorMap map = {};
   a.limit_ns = wait_limit();
   const int panels = C.head_dim <= 64 ? 1 : C.head_dim <= 128 ? 2 : 4;
-  a.tma = C.page_tokens % 16 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
-          make_rows_map(&map, a.pool, rows, C, panels);
+  a.tma = C.page_tokens % 8 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
+          make_rows_map(&map, a.pool, rows, C, panels, C.page_tokens % 16 ? 8 : 16);
   if (a.tma && C.head_dim % 64 == 0) a.tma = 2;
   a.tiles = (a.group + 7) / 8;
   if (C.dtype == PI_F16) {

@@ -144,6 +144,7 @@ SHAPES = [  # heads, kv_heads, head_dim, page
     (4, 4, 64, 16), (8, 1, 128, 16), (6, 2, 80, 24), (32, 2, 128, 32), (5, 5, 96, 7),
     (3, 1, 256, 128), (12, 1, 8, 1), (40, 2, 72, 16), (14, 2, 200, 8), (2, 1, 136, 16),
     (4, 2, 96, 48), (18, 2, 112, 64), (64, 4, 256, 16), (33, 1, 64, 32), (4, 2, 40, 16),
+    (8, 8, 128, 24), (4, 4, 64, 8), (4, 1, 256, 40), (2, 2, 192, 8),
 ]
 LENS = [0, 1, 15, 16, 17, 33, 64, 100, 257]
 
@@ -163,8 +164,9 @@ def test_attention_matches_64_bits(dtype, shape, append):
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (33, 3), (100, 40), (300, 9),
                                           (50, 2000000000), (2147483647, 2147483647)])
 @pytest.mark.parametrize("append", [False, True])
-def test_attention_window_and_first_tokens(dtype, window, sinks, append):
-    c = Cache(dtype, 8, 2, 64, 16, [0, 1, 16, 34, 99, 100, 101, 333], window, sinks, append)
+@pytest.mark.parametrize("page", [16, 24, 7])
+def test_attention_window_and_first_tokens(dtype, window, sinks, append, page):
+    c = Cache(dtype, 8, 2, 64, page, [0, 1, 16, 34, 99, 100, 101, 333], window, sinks, append)
     c.check(*c.run())
     assert int(c.status[0]) == 0
 
@@ -228,12 +230,13 @@ def test_attention_reads_its_layer(layer):
             assert torch.isnan(c.pool[other]).all()
 
 
-def test_attention_reports_bad_pages_and_lengths():
-    c = Cache("f16", 8, 2, 64, 16, [100, 60, 45])
+@pytest.mark.parametrize("P", [16, 8, 5])
+def test_attention_reports_bad_pages_and_lengths(P):
+    c = Cache("f16", 8, 2, 64, P, [100, 60, 45])
     tab = c.np_table.copy()
-    tab[0, 2], tab[0, 6], tab[2, 0] = c.pages, -1, 2 ** 30
-    y, lse = c.run(table=i32(tab), length=i32([100, c.mp * 16 + 1, 45]))
-    hidden = {0: set(range(32, 48)) | set(range(96, 100)), 2: set(range(16))}
+    tab[0, 2], tab[0, 99 // P], tab[2, 0] = c.pages, -1, 2 ** 30
+    y, lse = c.run(table=i32(tab), length=i32([100, c.mp * P + 1, 45]))
+    hidden = {0: set(range(2 * P, 3 * P)) | set(range(99 // P * P, 100)), 2: set(range(P))}
     c.check(y, lse, hidden, [100, 0, 45])
     assert int(c.status[0]) == pi.PI_ERR_INDEX
     # the workspace is ready for a good call
