@@ -67,8 +67,9 @@ size_t pi_cache_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_
  *     a_t = scale q[s][h] . K[t][g]
  *     y[s][h] = sum_V exp(a_t) V[t][g] / sum_V exp(a_t),
  *     lse[s][h] = log sum_V exp(a_t).
- * An empty slot (n = 0) gives y = 0 and lse = -infinity.  Rows of a page that
- * are not visible are not used whatever they hold (NaN and infinities too).
+ * An empty slot (n = 0), and scores that are all -infinity, give y = 0 and
+ * lse = -infinity.  Rows of a page that are not visible are not used whatever
+ * they hold (NaN and infinities too).
  *   q [slots][heads][head_dim] fp32; y the same shape, fp32; lse NULL or
  *   [slots][heads] fp32; heads a multiple of kv_heads, at most 1024.
  *   k_new, v_new: NULL (the new token is in the cache already), or both
@@ -80,7 +81,11 @@ size_t pi_cache_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_
  * weights as sums of 16-bit parts that together keep at least 22 bits; sums
  * and softmax statistics are fp32.  A length outside [0, max_pages
  * page_tokens] counts as 0 and a page number outside [0, pages) hides its
- * tokens; both write PI_ERR_INDEX to *dev_status. */
+ * tokens; both write PI_ERR_INDEX to *dev_status.  A wait for a tile's copy
+ * that runs out (1 s, or PI_WAIT_LIMIT_NS) writes PI_ERR_TIMEOUT; y is then not
+ * meaningful and ws must be zero-filled again.  The split of the work over
+ * the GPU follows the lengths of all slots, so a slot's result may differ in
+ * rounding between batches; for the same lengths it is the same bit for bit. */
 pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots,
                              int32_t heads, int32_t max_pages, const float* q,
                              const float* k_new, const float* v_new, const int32_t* table,
@@ -122,8 +127,9 @@ pi_status pi_cache_append(const pi_cache_desc* cache, int32_t layer, int32_t slo
  *   pairs [slots][2]: (from, to) of each copied page, in slot order;
  *   counts[0] their number, counts[1] the pages with ref > 0.
  * table_in and len_in are read only; table and len must be other buffers.
- * A parent, length or page number out of range is not followed (the slot
- * begins empty; the entry becomes -1) and writes PI_ERR_INDEX. */
+ * A parent, length or page number out of range is not followed and writes
+ * PI_ERR_INDEX: the slot begins empty; a full page's entry becomes -1; a
+ * partly filled page is replaced by a fresh one, contents undefined. */
 pi_status pi_cache_fork(const pi_cache_desc* cache, int32_t slots, int32_t max_pages,
                         const int32_t* parent, const int32_t* grow, const int32_t* held,
                         const int32_t* table_in, const int32_t* len_in, int32_t* table,
