@@ -387,4 +387,5 @@ def pi_shard_reduce(parts, G, batch, d, residual, y, stream=None) -> int:
 from .serve import (  # noqa: E402
     PI_CACHE_MAX_SLOTS, PI_F32, PI_TOPK_MAX, cache_workspace, logprob_workspace, make_cache_desc,
     pi_cache_append, pi_cache_compact, pi_cache_copy, pi_cache_desc, pi_cache_fork,
-    pi_cache_workspace_size, pi_logprob_workspace_size, pi_paged_attention, pi_token_logprobs)
+    pi_cache_workspace_size, pi_logprob_workspace_size, pi_paged_attention,
+    pi_selftest_attention_timeout, pi_token_logprobs)

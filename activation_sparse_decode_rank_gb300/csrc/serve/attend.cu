@@ -321,8 +321,9 @@ struct Piece {
   int slot, g, ht, tiles;
 };
 
-// BR: rows of a box (16 too where tiles are gathered).
-template <int DT, int DP, int BR>
+// BR: rows of a box (16 too where tiles are gathered).  LOSE: the first tile of
+// block 0 is never ordered (the self-test of the wait that runs out).
+template <int DT, int DP, int BR, bool LOSE>
 __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int S = att_stages<DT, DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
@@ -526,6 +527,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
     const long long row = ok ? ((long long)next_page * 2 * a.kv_heads + lc.g) * P + next_row : 0;
     if (a.tma) {
       if (lane == 0) {
+        if (LOSE && blockIdx.x == 0 && warp == 0 && lc.pos == cc.pos) return;  // its first tile
         mbar_expect(bar, rows ? kBox : 0);
         if (rows) order(k0, (int)row, bar);
       }
@@ -1055,13 +1057,13 @@ static unsigned long long wait_limit() {
   return limit;
 }
 
-template <int DT, int DP, int BR>
+template <int DT, int DP, int BR, bool LOSE = false>
 pi_status launch_boxes(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
   DevInfo di;
   pi_status st = dev_info(&di);
   if (st != PI_OK) return st;
   constexpr int smem = att_smem<DT, DP>();
-  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, BR>), smem);
+  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, BR, LOSE>), smem);
   if (st != PI_OK) return st;
   // Two blocks per SM (one at 256 dims), or fewer where the longest slots that
   // the tables and the window allow cannot use them.
@@ -1073,7 +1075,7 @@ pi_status launch_boxes(const AttendArgs& a, const CUtensorMap& map, pi_stream st
   long long grid = di.sms * att_blocks<DT, DP>();
   if (grid > kAttendGrid) grid = kAttendGrid;
   if (grid > useful) grid = useful;
-  return launch(attend_kernel<DT, DP, BR>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
+  return launch(attend_kernel<DT, DP, BR, LOSE>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
                 map);
 }
 
@@ -1087,20 +1089,12 @@ pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream s
 
 using namespace pis;
 
-extern "C" {
-
-size_t pi_cache_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t heads) {
-  if (check_cache(cache) != PI_OK || slots < 1 || slots > PI_CACHE_MAX_SLOTS) return 0;
-  if (heads < 0 || heads > kMaxHeads || heads % cache->kv_heads) return 0;
-  return cache_ws(*cache, slots, heads).total;
-}
-
-pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots,
-                             int32_t heads, int32_t max_pages, const float* q,
-                             const float* k_new, const float* v_new, const int32_t* table,
-                             const int32_t* len, void* pool, float scale, int32_t window,
-                             int32_t sinks, float* y, float* lse, int32_t* dev_status, void* ws,
-                             size_t ws_bytes, pi_stream stream) {
+static pi_status attention(const pi_cache_desc* cache, int32_t layer, int32_t slots,
+                           int32_t heads, int32_t max_pages, const float* q,
+                           const float* k_new, const float* v_new, const int32_t* table,
+                           const int32_t* len, void* pool, float scale, int32_t window,
+                           int32_t sinks, float* y, float* lse, int32_t* dev_status, void* ws,
+                           size_t ws_bytes, pi_stream stream, unsigned long long lose_ns) {
   pi_status st = check_cache(cache);
   if (st != PI_OK) return st;
   const pi_cache_desc& C = *cache;
@@ -1146,6 +1140,11 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
           make_rows_map(&map, a.pool, rows, C, panels, C.page_tokens % 16 ? 8 : 16);
   if (a.tma && C.head_dim % 64 == 0) a.tma = 2;
   a.tiles = (a.group + 7) / 8;
+  if (lose_ns) {
+    if (C.dtype != PI_F16 || C.head_dim != 64 || a.tma != 2 || C.page_tokens % 16) return PI_ERR_SHAPE;
+    a.limit_ns = lose_ns;
+    return launch_boxes<0, 64, 16, true>(a, map, stream);
+  }
   if (C.dtype == PI_F16) {
     if (C.head_dim <= 64) return launch_attend<0, 64>(a, map, stream);
     if (C.head_dim <= 128) return launch_attend<0, 128>(a, map, stream);
@@ -1154,6 +1153,34 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
   if (C.head_dim <= 64) return launch_attend<1, 64>(a, map, stream);
   if (C.head_dim <= 128) return launch_attend<1, 128>(a, map, stream);
   return launch_attend<1, 256>(a, map, stream);
+}
+
+extern "C" {
+
+size_t pi_cache_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t heads) {
+  if (check_cache(cache) != PI_OK || slots < 1 || slots > PI_CACHE_MAX_SLOTS) return 0;
+  if (heads < 0 || heads > kMaxHeads || heads % cache->kv_heads) return 0;
+  return cache_ws(*cache, slots, heads).total;
+}
+
+pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots,
+                             int32_t heads, int32_t max_pages, const float* q,
+                             const float* k_new, const float* v_new, const int32_t* table,
+                             const int32_t* len, void* pool, float scale, int32_t window,
+                             int32_t sinks, float* y, float* lse, int32_t* dev_status, void* ws,
+                             size_t ws_bytes, pi_stream stream) {
+  return attention(cache, layer, slots, heads, max_pages, q, k_new, v_new, table, len, pool, scale,
+                   window, sinks, y, lse, dev_status, ws, ws_bytes, stream, 0);
+}
+
+pi_status pi_selftest_attention_timeout(const pi_cache_desc* cache, int32_t slots, int32_t heads,
+                                        int32_t max_pages, const float* q, const int32_t* table,
+                                        const int32_t* len, void* pool, float* y,
+                                        int32_t* dev_status, void* ws, size_t ws_bytes,
+                                        int64_t limit_ns, pi_stream stream) {
+  if (limit_ns < 1000 || limit_ns > 5000000000LL) return PI_ERR_SHAPE;
+  return attention(cache, 0, slots, heads, max_pages, q, nullptr, nullptr, table, len, pool, 1.f, 0, 0,
+                   y, nullptr, dev_status, ws, ws_bytes, stream, (unsigned long long)limit_ns);
 }
 
 pi_status pi_cache_append(const pi_cache_desc* cache, int32_t layer, int32_t slots,

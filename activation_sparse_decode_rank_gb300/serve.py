@@ -27,6 +27,8 @@ SIGNATURES = {
     "pi_cache_workspace_size": (_SZ, [_CACHE, _I32, _I32]),
     "pi_paged_attention": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P,
                                           ctypes.c_float, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "pi_selftest_attention_timeout": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _P, _P, _P, _P, _P,
+                                                     _P, _P, _SZ, _I64, _P]),
     "pi_cache_append": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P,
                                        _P]),
     "pi_cache_fork": (ctypes.c_int, [_CACHE, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
@@ -129,6 +131,13 @@ def pi_paged_attention(cache, layer, slots, heads, max_pages, q, k_new, v_new, t
         ctypes.byref(cache), layer, slots, heads, max_pages, _ptr(q), _ptr(k_new), _ptr(v_new),
         _ptr(table), _ptr(len), _ptr(pool), scale, window, sinks, _ptr(y), _ptr(lse),
         _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+
+
+def pi_selftest_attention_timeout(cache, slots, heads, max_pages, q, table, len, pool, y, dev_status,
+                                  ws, limit_ns, ws_bytes=None, stream=None) -> int:
+    return _fn("pi_selftest_attention_timeout")(
+        ctypes.byref(cache), slots, heads, max_pages, _ptr(q), _ptr(table), _ptr(len), _ptr(pool),
+        _ptr(y), _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), limit_ns, _stream(stream))
 
 
 def pi_cache_append(cache, layer, slots, max_pages, tokens, slot, pos, k, v, table, pool,

@@ -93,6 +93,20 @@ pi_status pi_paged_attention(const pi_cache_desc* cache, int32_t layer, int32_t 
                              int32_t sinks, float* y, float* lse, int32_t* dev_status, void* ws,
                              size_t ws_bytes, pi_stream stream);
 
+/* Diagnostic of the attention's failure path: pi_paged_attention (scale 1, no
+ * window, no new rows) on a PI_F16 cache with head_dim 64 and page_tokens a
+ * multiple of 16, except that the copy of block 0's first tile is never
+ * ordered, so the wait for it runs out after limit_ns nanoseconds (1e3 ..
+ * 5e9).  The warp then lets the copies under way land (2 s at most, which the
+ * missing one takes) and leaves, and PI_ERR_TIMEOUT lands in *dev_status; y is
+ * not meaningful and ws must be zero-filled again.  Slot 0 must not be empty.
+ * Returns PI_OK when the launch was issued. */
+pi_status pi_selftest_attention_timeout(const pi_cache_desc* cache, int32_t slots, int32_t heads,
+                                        int32_t max_pages, const float* q, const int32_t* table,
+                                        const int32_t* len, void* pool, float* y,
+                                        int32_t* dev_status, void* ws, size_t ws_bytes,
+                                        int64_t limit_ns, pi_stream stream);
+
 /* Stores keys and values of `tokens` tokens (prompts, or one step): token i
  * of k, v [tokens][kv_heads][head_dim] fp32 goes, rounded to the cache's
  * type, to position pos[i] of slot slot[i] in `layer`.  slot[i] = -1 skips

@@ -268,6 +268,94 @@ def test_attention_past_32_bit_offsets():
     c.check_stored()
 
 
+def test_attention_past_31_bit_rows():
+    # 2.15e9 rows: gathered with 64-bit offsets (34 GB, only its last pages touched)
+    c = Cache("f16", 256, 256, 8, 256, [300, 5], pages=16_400)
+    c.check(*c.run())
+
+
+def test_attention_wait_times_out_and_returns():
+    # a flag that nothing sets: the copy of the first tile is never ordered
+    import time
+    c = Cache("f16", 4, 4, 64, 16, [200, 100])
+    y = torch.zeros((2, 4, 64), device=DEV)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    pi.check(pi.pi_selftest_attention_timeout(c.desc, 2, 4, c.mp, c.qd, c.table, c.len, c.pool, y,
+                                              c.status, c.ws, 2_000_000))
+    torch.cuda.synchronize()
+    assert int(c.status[0]) == pi.PI_ERR_TIMEOUT
+    assert time.perf_counter() - t0 < 6.0  # the limit, and the 2 s that copies get to land
+    c.status.zero_()
+    c.ws.zero_()
+    c.check(*c.run())
+    assert int(c.status[0]) == 0
+
+
+def test_all_operators_in_one_graph():
+    # captured on a side stream, replayed on changed inputs: as direct calls
+    S, H, kv, D, P, mp, V, k = 4, 8, 2, 64, 16, 6, 3000, 5
+    pages = 40
+    g = np.random.default_rng(8)
+    desc = pi.make_cache_desc(1, pages, kv, D, P, "bf16")
+    ws, lws = pi.cache_workspace(desc, S, H, DEV), pi.logprob_workspace(S, V, k, DEV)
+
+    def buffers(seed):
+        r = np.random.default_rng(seed)
+        t = np.full((S, mp), -1)
+        length = r.integers(20, 64, S)
+        order = iter(r.permutation(pages))
+        for s in range(S):
+            for j in range(-(-int(length[s]) // P)):
+                t[s, j] = next(order)
+        f = lambda *sh: torch.from_numpy(r.standard_normal(sh).astype(np.float32)).to(DEV)  # noqa: E731
+        return dict(table=i32(t), len=i32(length), parent=i32(r.integers(0, S, S)),
+                    q=f(S, H, D), k=f(S, kv, D), v=f(S, kv, D), x=f(S, V) * 3,
+                    pool=f(1, pages, 2, kv, P, D).bfloat16(), slot=i32(range(S)), pos=i32([0] * S),
+                    tok=i32(r.integers(0, V, S)))
+
+    one = i32([1] * S)
+    o = dict(t2=i32(np.zeros((S, mp))), l2=i32([0] * S), ref=i32([0] * pages),
+             pairs=i32(np.zeros((pages, 2))), counts=i32([0] * 4), map=i32([0] * pages),
+             y=torch.zeros((S, H, D), device=DEV), lse=torch.zeros((S, H), device=DEV),
+             lp=torch.zeros(S, device=DEV), ent=torch.zeros(S, device=DEV),
+             idx=i32(np.zeros((S, k))), top=torch.zeros((S, k), device=DEV), st=new_status())
+
+    def step(b):
+        pi.check(pi.pi_cache_append(desc, 0, S, mp, S, b["slot"], b["pos"], b["v"], b["k"],
+                                    b["table"], b["pool"], o["st"]))
+        pi.check(pi.pi_cache_fork(desc, S, mp, b["parent"], one, None, b["table"], b["len"], o["t2"],
+                                  o["l2"], o["ref"], b["pool"], o["pairs"], o["counts"], o["st"], ws))
+        pi.check(pi.pi_paged_attention(desc, 0, S, H, mp, b["q"], b["k"], b["v"], o["t2"], o["l2"],
+                                       b["pool"], 0.125, 30, 2, o["y"], o["lse"], o["st"], ws))
+        pi.check(pi.pi_cache_compact(desc, S, mp, None, o["t2"], o["l2"], o["t2"], o["ref"], o["map"],
+                                     b["pool"], o["pairs"], o["counts"], o["st"], ws))
+        pi.check(pi.pi_token_logprobs(b["x"], "f32", S, V, V, b["tok"], k, o["lp"], o["ent"],
+                                      o["idx"], o["top"], o["st"], lws))
+
+    live = buffers(1)
+    step(live)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(live)
+    for seed in (2, 3):
+        b = buffers(seed)
+        for name, t in b.items():
+            live[name].copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in o.items()}
+        step(b)
+        torch.cuda.synchronize()
+        assert int(o["st"][0]) == 0
+        for n, t in o.items():
+            if n == "pairs":
+                t, got[n] = t[: int(o["counts"][0])], got[n][: int(o["counts"][0])]
+            assert torch.equal(t, got[n]), n
+        assert torch.equal(b["pool"], live["pool"])
+
+
 def test_attention_on_another_stream_and_in_a_graph():
     c = Cache("f16", 8, 2, 64, 16, [200, 0, 31])
     want, _ = c.run()

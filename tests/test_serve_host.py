@@ -24,7 +24,7 @@ def test_exports_and_bindings():
     src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "pi_serve.h")).read(),
                  flags=re.S)
     names = sorted(set(re.findall(r"\b(pi_[a-z_]+)\s*\(", src)))
-    assert len(names) == 8
+    assert len(names) == 9
     for n in names:
         assert hasattr(pi.lib(), n) and n in pi.SIGNATURES and callable(getattr(pi, n))
 
@@ -89,6 +89,16 @@ def test_attention_refusals():
     assert pi.pi_paged_attention(c, 0, 4, 8, 10, P, None, None, P, P, P, 1.0, 0, 0, P, None, P, P,
                                  pi.pi_cache_workspace_size(c, 4, 8) - 1,
                                  stream=0) == pi.PI_ERR_WORKSPACE
+
+
+def test_attention_selftest_refusals():
+    def f(c, limit, wsb=None):
+        size = pi.pi_cache_workspace_size(c, 4, 8) if wsb is None else wsb
+        return pi.pi_selftest_attention_timeout(c, 4, 8, 10, P, P, P, P, P, P, P, limit, size, stream=0)
+    assert f(cache(), 10) == pi.PI_ERR_SHAPE and f(cache(), 6 * 10 ** 9) == pi.PI_ERR_SHAPE
+    assert f(cache(), 10 ** 6, 0) == pi.PI_ERR_WORKSPACE
+    for c in (cache(dtype="bf16"), cache(head_dim=128), cache(page_tokens=8)):
+        assert f(c, 10 ** 6) == pi.PI_ERR_SHAPE
 
 
 def append(c=None, **kw):
