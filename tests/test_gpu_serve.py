@@ -180,6 +180,18 @@ def test_attention_long_and_ragged(shape, lens):
         c.check(*c.run())
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,window,sinks", [((32, 32, 96, 8), 0, 0), ((64, 32, 128, 16), 0, 0), ((40, 40, 64, 5), 30, 3)])
+def test_attention_many_short_units(dtype, shape, window, sinks):
+    # more units than blocks, no more than warps, none longer than 64 tokens
+    g = np.random.default_rng(6)
+    lens = g.integers(1, 64 if not window else 2000, 24).tolist()
+    lens[0], lens[7], lens[23] = 0, 1, 63
+    c = Cache(dtype, *shape, lens, window, sinks, append=True)
+    c.check(*c.run())
+    c.check_stored()
+
+
 def test_attention_many_slots():
     g = np.random.default_rng(4)
     c = Cache("f16", 4, 2, 64, 16, g.integers(0, 40, 1024).tolist())
