@@ -37,8 +37,8 @@ namespace pis {
 // kWholeTiles).  A unit inside one warp's share is written from that
 // warp's registers.  A unit that spans warps leaves partial results, joined
 // once at the end: within a thread block through shared memory, across
-// thread blocks by the last of them to arrive, in block order (no waiting;
-// the order of the sums is fixed).
+// thread blocks by the last of them to arrive, in block order, in groups first
+// where they are many (no waiting; the order of the sums is fixed).
 //
 // Data flow.  A warp streams its tiles through its own ring of stages, without
 // any block-wide barrier until the end.  Where pages hold multiples of 16 (8)
@@ -61,7 +61,7 @@ struct AttendArgs {
   uint16_t* pool;  // the layer's pages
   float *y, *lse;
   int* status;
-  int* arrived;   // [kAttendGrid] arrivals at the units that begin in a block
+  int* arrived;   // [2][kAttendGrid] arrivals at the units that begin in a block, at groups
   float* part;    // [grid][2][heads of a unit][head_dim + 4]: o, m, l of units split over blocks
   int slots, heads, kv_heads, group, head_dim, page_tokens, pages, max_pages, window, sinks;
   int tiles;      // head tiles per kv head: ceil(group / 8)
@@ -84,6 +84,12 @@ constexpr int kApartTiles = 48;
 // us, split like longer ones 12.3; 64 slots x 8 kv heads of 128, 60 tokens:
 // 11.1 and 14.6.  At 128 tokens the split is ahead, 12.1 to 13.7.
 constexpr int kWholeTiles = 6;
+
+// Most blocks of a unit whose parts one block joins directly.  More join in two
+// steps, groups of about sqrt(n) blocks and then the groups.  One slot, 32/8
+// heads of 64, 16384 tokens, bf16: 19.2 us, in one step 33.9; 64/8 heads of
+// 128, 8192 tokens, fp16: 18.5 and 26.0.  8 to 16 here measure the same.
+constexpr int kFlatJoin = 10;
 
 // Thread blocks per SM, and stages of a warp's ring, by measurement.  More
 // warps hide a tile's chain of instructions, more stages its loads; bf16 tiles
@@ -880,8 +886,22 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       }
     }
   }
-  __shared__ int s_first[2], s_last[2];
-  __shared__ const Piece* s_cross[2];
+  // The parts to join: n of them, of blocks base, base + stride, ...
+  struct Join {
+    const Piece* pc;
+    int b0, nb, each, groups;  // the unit's blocks; those of a group; groups (0: none)
+    int base, stride, n;
+  };
+  __shared__ Join s_join[2];
+  // Releases the block's parts, which the barrier ordered before it, and
+  // acquires the other blocks'.  True for the last of `of`.
+  auto arrive = [](int* counter, int of) {
+    int n;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+    if (n != of - 1) return false;
+    *counter = 0;
+    return true;
+  };
   if (tid < 2) {  // 0: the unit that came in, 1: the one that goes on
     const Piece* pc = &s_piece[0][0];
     if (tid) {
@@ -889,78 +909,119 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       for (int w = kAttWarps - 2; w >= 0 && pc->at < 0; --w) pc = &s_piece[w][1];
       if (pc->at + pc->tiles <= block_end) pc = &s_piece[0][0];
     }
-    const bool any = pc->at >= 0 && (pc == &s_piece[0][0]) == (tid == 0);
-    s_cross[tid] = pc;
-    s_first[tid] = any ? line.block_of(pc->at) : -1;
-    s_last[tid] = any ? line.block_of(pc->at + pc->tiles - 1) : -1;
+    Join& jn = s_join[tid];
+    jn.pc = pc;
+    jn.nb = 0;
+    if (pc->at >= 0 && (pc == &s_piece[0][0]) == (tid == 0)) {
+      jn.b0 = line.block_of(pc->at);
+      jn.nb = line.block_of(pc->at + pc->tiles - 1) - jn.b0 + 1;
+    }
   }
   if (__syncthreads_or(crossing)) {
-    if (tid < 2 && s_first[tid] >= 0) {
-      // releases the block's parts, which the barrier ordered before it, and
-      // acquires the other blocks'
-      int n;
-      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
-                   : "=r"(n)
-                   : "l"(a.arrived + s_first[tid])
-                   : "memory");
-      if (n == s_last[tid] - s_first[tid])
-        a.arrived[s_first[tid]] = 0;
-      else
-        s_first[tid] = -1;
+    if (tid < 2 && s_join[tid].nb) {
+      Join& jn = s_join[tid];
+      const int nb = jn.nb;
+      jn.stride = 1;
+      if (nb <= kFlatJoin) {
+        jn.groups = 0;
+        jn.base = jn.b0;
+        jn.n = arrive(a.arrived + jn.b0, nb) ? nb : 0;
+      } else {
+        // Groups of about sqrt(nb), none of one block: so a counter at each
+        // group's second block is no other unit's.
+        const int each = (int)ceilf(sqrtf((float)nb));
+        int groups = (nb + each - 1) / each;
+        groups -= nb - (groups - 1) * each == 1;
+        const int i = min(((int)blockIdx.x - jn.b0) / each, groups - 1);
+        const int size = i == groups - 1 ? nb - i * each : each;
+        jn.each = each;
+        jn.groups = groups;
+        jn.base = jn.b0 + i * each;
+        jn.n = arrive(a.arrived + kAttendGrid + jn.base + 1, size) ? size : 0;
+      }
     }
     __syncthreads();
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
-      if (s_first[x] < 0) continue;
-      const int b0 = s_first[x], nb = s_last[x] - b0 + 1;
-      const Piece& pc = *s_cross[x];
+      if (s_join[x].nb == 0) continue;
+      const Join& jn = s_join[x];
+      const Piece& pc = *jn.pc;
       const int rows = min(8, a.group - pc.ht * 8), vecs = D >> 2, items = rows * vecs;
       const size_t out0 = (size_t)pc.slot * a.heads + pc.g * a.group + pc.ht * 8;
-      // two items of a thread together, four parts at a time: their reads overlap
+      // Where block b left its part; a group its own, in the second place of
+      // its first block, or in that of the unit's second block: both blocks
+      // lie within the unit, so no other unit's part is there.
+      auto part_of = [&](int b, bool group) {
+        const int begins = b == jn.b0;
+        return a.part + (size_t)(group ? 2 * (b + begins) + 1 : 2 * b + begins) * (8 * prow);
+      };
 #pragma unroll 1
-      for (int e = tid; e < items; e += 2 * kAttThreads) {
-        float4 sum[2];
-        float top[2], lsum[2];
-        int hr[2], d[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = min(e + i * kAttThreads, items - 1);
-          hr[i] = at / vecs;
-          d[i] = 4 * (at - hr[i] * vecs);
-          sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          top[i] = -INFINITY;
-          lsum[i] = 0.f;
-        }
+      while (jn.n) {
+        const int n = jn.n, base = jn.base, stride = jn.stride;
+        const bool last = jn.groups == 0;
+        // two items of a thread together, four parts at a time: their reads overlap
 #pragma unroll 1
-        for (int j0 = 0; j0 < nb; j0 += 4) {
-          float4 v[2][4];
-          float2 q[2][4];
+        for (int e = tid; e < items; e += 2 * kAttThreads) {
+          float4 sum[2];
+          float top[2], lsum[2];
+          int hr[2], d[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int i = 0; i < 2; ++i) {
+            const int at = min(e + i * kAttThreads, items - 1);
+            hr[i] = at / vecs;
+            d[i] = 4 * (at - hr[i] * vecs);
+            sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            top[i] = -INFINITY;
+            lsum[i] = 0.f;
+          }
+#pragma unroll 1
+          for (int j0 = 0; j0 < n; j0 += 4) {
+            float4 v[2][4];
+            float2 q[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (j0 + j < nb) {  // the unit's (j0 + j)-th block
-                const float* pr =
-                    a.part + (((size_t)(b0 + j0 + j) * 2 + (j0 + j == 0)) * 8 + hr[i]) * prow;
-                q[i][j] = __ldcg(reinterpret_cast<const float2*>(pr + D));
-                v[i][j] = __ldcg(reinterpret_cast<const float4*>(pr + d[i]));
-              }
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+              for (int i = 0; i < 2; ++i)
+                if (j0 + j < n) {  // the (j0 + j)-th part
+                  const float* pr = part_of(base + (j0 + j) * stride, stride > 1) + hr[i] * prow;
+                  q[i][j] = __ldcg(reinterpret_cast<const float2*>(pr + D));
+                  v[i][j] = __ldcg(reinterpret_cast<const float4*>(pr + d[i]));
+                }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (j0 + j < nb) {
-                const float up = fmaxf(top[i], q[i][j].x), ref = up == -INFINITY ? 0.f : up;
-                const float was = ex2(top[i] - ref), is = ex2(q[i][j].x - ref);
-                sum[i] = make_float4(sum[i].x * was, sum[i].y * was, sum[i].z * was, sum[i].w * was);
-                add_scaled(sum[i], v[i][j], is);
-                lsum[i] = fmaf(lsum[i], was, q[i][j].y * is);
-                top[i] = up;
-              }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (j0 + j < n) {
+                  const float up = fmaxf(top[i], q[i][j].x), ref = up == -INFINITY ? 0.f : up;
+                  const float was = ex2(top[i] - ref), is = ex2(q[i][j].x - ref);
+                  sum[i] = make_float4(sum[i].x * was, sum[i].y * was, sum[i].z * was, sum[i].w * was);
+                  add_scaled(sum[i], v[i][j], is);
+                  lsum[i] = fmaf(lsum[i], was, q[i][j].y * is);
+                  top[i] = up;
+                }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (e + i * kAttThreads >= items) break;
+            if (last) {
+              finish(a, out0 + hr[i], d[i], sum[i], top[i], lsum[i], kShift);
+            } else {
+              float* to = part_of(base, true) + hr[i] * prow;
+              __stcg(reinterpret_cast<float4*>(to + d[i]), sum[i]);
+              if (d[i] == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(top[i], lsum[i]));
+            }
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (e + i * kAttThreads < items) finish(a, out0 + hr[i], d[i], sum[i], top[i], lsum[i], kShift);
+        if (last) break;
+        __syncthreads();
+        if (tid == 0) {
+          Join& next = s_join[x];
+          next.n = arrive(a.arrived + next.b0, next.groups) ? next.groups : 0;
+          next.base = next.b0;
+          next.stride = next.each;
+          next.groups = 0;
+        }
+        __syncthreads();
       }
     }
   }

@@ -126,7 +126,7 @@ inline CacheWs cache_ws(const pi_cache_desc& C, int slots, int heads) {
     return o;
   };
   (void)slots;
-  w.arrived = take(4 * kAttendGrid);
+  w.arrived = take(8 * kAttendGrid);
   const size_t scratch = off;
   w.part = take(heads ? (size_t)kAttendGrid * 2 * 8 * (C.head_dim + 4) * 4 : 0);
   const size_t end = off;

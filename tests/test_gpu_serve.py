@@ -181,6 +181,33 @@ def test_attention_long_and_ragged(shape, lens):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", [(16, 1, 128, 16), (20, 2, 128, 24), (32, 2, 80, 8), (48, 2, 64, 8),
+                                   (71, 1, 64, 16), (128, 8, 64, 16), (24, 2, 96, 7), (18, 2, 32, 16)])
+def test_attention_many_heads_per_kv_head(dtype, shape):
+    # more than eight query heads per kv head: short, long (joined across
+    # blocks) and windowed
+    for lens, window, sinks in ((LENS, 0, 0), ([2900, 1, 0, 803, 16], 0, 0), ([2000, 40, 133], 90, 5)):
+        c = Cache(dtype, *shape, lens, window, sinks, append=True)
+        c.check(*c.run())
+        c.check_stored()
+        assert int(c.status[0]) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,lens", [((8, 1, 128, 16), [20011]), ((16, 1, 64, 32), [9000, 0, 3]),
+                                        ((4, 2, 256, 8), [1, 7003]), ((3, 3, 96, 7), [5000, 4100]),
+                                        ((12, 1, 128, 24), [2500, 11000, 640]), ((2, 2, 8, 16), [12000])])
+def test_attention_units_of_many_blocks(dtype, shape, lens):
+    # joined in two steps; the counters are left as they were found
+    c = Cache(dtype, *shape, lens, seed=9)
+    y, lse = c.run()
+    c.check(y, lse)
+    for _ in range(3):
+        y1, l1 = c.run()
+        assert torch.equal(y, y1) and torch.equal(lse, l1)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("shape,window,sinks", [((32, 32, 96, 8), 0, 0), ((64, 32, 128, 16), 0, 0), ((40, 40, 64, 5), 30, 3)])
 def test_attention_many_short_units(dtype, shape, window, sinks):
     # more units than blocks, no more than warps, none longer than 64 tokens
