@@ -341,9 +341,10 @@ struct Piece {
   int slot, g, ht, tiles;
 };
 
-// BR: rows of a box (16 too where tiles are gathered).  LOSE: the first tile of
+// DP: elements of a staged row, DK of them used by the products.  BR: rows of
+// a box (16 too where tiles are gathered).  LOSE: the first tile of
 // block 0 is never ordered (the self-test of the wait that runs out).
-template <int DT, int DP, int BR, bool LOSE>
+template <int DT, int DP, int DK, int BR, bool LOSE>
 __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int S = att_stages<DT, DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
@@ -592,8 +593,8 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
   __syncwarp();
   if (lc.pos < share1) fetch(true);
 
-  uint32_t qf[DP / 16][4], qf2[DP / 16][2];
-  float o[DP / 8][2], m, l, unit_scale;
+  uint32_t qf[DK / 16][4], qf2[DK / 16][2];
+  float o[DK / 8][2], m, l, unit_scale;
   bool fresh = true;
   int ahead = 0, load_stage = 0, stage = 0;
   uint32_t parity = 0;
@@ -617,10 +618,10 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       fresh = false;
       const int h = ht * 8 + (lane >> 2);
       const float* q = a.q + ((size_t)cc.slot * a.heads + g * a.group + min(h, a.group - 1)) * D;
-      float2 f[DP / 16][2];
+      float2 f[DK / 16][2];
       float top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks)
+      for (int ks = 0; ks < DK / 16; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int d = ks * 16 + e * 8 + 2 * (lane & 3);
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
         unit_scale = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
       }
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks)
+      for (int ks = 0; ks < DK / 16; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           split2<DT>(f[ks][e].x * up, f[ks][e].y * up, qf[ks][2 * e], qf[ks][2 * e + 1],
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       m = -INFINITY;
       l = 0.f;
 #pragma unroll
-      for (int j = 0; j < DP / 8; ++j) o[j][0] = o[j][1] = 0.f;
+      for (int j = 0; j < DK / 8; ++j) o[j][0] = o[j][1] = 0.f;
     }
 
     if (a.tma) {
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
         const int r = (lane & 7) + ((lane >> 4) << 3), pc = (lane >> 3) & 1;
         const uint32_t at = k0 + row_at(r) + ((pc ^ (r & 7)) << 4);
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
+        for (int ks = 0; ks < DK / 16; ++ks) {
           uint32_t b[4];
           ldsm4(b, (at ^ ((ks & 3) << 5)) + (ks >> 2) * kPanel);
 #pragma unroll
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), pc = lane >> 4;
       const uint32_t at = v0 + row_at(r) + ((pc ^ (r & 7)) << 4);
 #pragma unroll
-      for (int jj = 0; jj < DP / 16; ++jj) {
+      for (int jj = 0; jj < DK / 16; ++jj) {
         uint32_t b[4];
         ldsm4t(b, (at ^ ((jj & 3) << 5)) + (jj >> 2) * kPanel);
 #pragma unroll
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
           const float inv = lt > 0.f ? 1.f / lt : lt == lt ? 0.f : lt;
           float* y = a.y + row * D + 2 * (lane & 3);
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j)
+          for (int j = 0; j < DK / 8; ++j)
             if (8 * j < D)
               *reinterpret_cast<float2*>(y + 8 * j) = make_float2(o[j][0] * inv, o[j][1] * inv);
           if ((lane & 3) == 0 && a.lse) a.lse[row] = (m + (log2f(lt) - kShift)) * kLn2;
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kern
         if (hq < a.group) {
           float* data = piece_data(warp, k) + h * DP + 2 * (lane & 3);
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j)
+          for (int j = 0; j < DK / 8; ++j)
             *reinterpret_cast<float2*>(data + ((j ^ h) << 3)) = make_float2(o[j][0], o[j][1]);
         }
         if ((lane & 3) == 0) {
@@ -1146,13 +1147,13 @@ static unsigned long long wait_limit() {
   return limit;
 }
 
-template <int DT, int DP, int BR, bool LOSE = false>
+template <int DT, int DP, int DK, int BR, bool LOSE = false>
 pi_status launch_boxes(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
   DevInfo di;
   pi_status st = dev_info(&di);
   if (st != PI_OK) return st;
   constexpr int smem = att_smem<DT, DP>();
-  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, BR, LOSE>), smem);
+  st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, DK, BR, LOSE>), smem);
   if (st != PI_OK) return st;
   // Two blocks per SM (one at 256 dims), or fewer where the longest slots that
   // the tables and the window allow cannot use them.
@@ -1164,14 +1165,29 @@ pi_status launch_boxes(const AttendArgs& a, const CUtensorMap& map, pi_stream st
   long long grid = di.sms * att_blocks<DT, DP>();
   if (grid > kAttendGrid) grid = kAttendGrid;
   if (grid > useful) grid = useful;
-  return launch(attend_kernel<DT, DP, BR, LOSE>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
+  return launch(attend_kernel<DT, DP, DK, BR, LOSE>, dim3((unsigned)grid), kAttThreads, smem, stream, a,
                 map);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int DK = DP>
 pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
-  return a.tma && a.page_tokens % 16 ? launch_boxes<DT, DP, 8>(a, map, stream)
-                                     : launch_boxes<DT, DP, 16>(a, map, stream);
+  return a.tma && a.page_tokens % 16 ? launch_boxes<DT, DP, DK, 8>(a, map, stream)
+                                     : launch_boxes<DT, DP, DK, 16>(a, map, stream);
+}
+
+// Shared memory holds whole panels of 64 elements; the products stop at the
+// next of 80, 96 and 192, which is most of a tile's time where it is
+// instructions.  32 heads, 16 slots to 4096 tokens: heads of 80 64 us in fp16
+// and 73 in bf16 (as 128: 70, 87), of 96 67 and 76 (70, 87); 16 heads of 192
+// 67 and 75 (as 256: 71, 88).
+template <int DT>
+pi_status launch_dims(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
+  if (a.head_dim <= 64) return launch_attend<DT, 64>(a, map, stream);
+  if (a.head_dim <= 80) return launch_attend<DT, 128, 80>(a, map, stream);
+  if (a.head_dim <= 96) return launch_attend<DT, 128, 96>(a, map, stream);
+  if (a.head_dim <= 128) return launch_attend<DT, 128>(a, map, stream);
+  if (a.head_dim <= 192) return launch_attend<DT, 256, 192>(a, map, stream);
+  return launch_attend<DT, 256>(a, map, stream);
 }
 
 }  // namespace pis
@@ -1232,16 +1248,9 @@ static pi_status attention(const pi_cache_desc* cache, int32_t layer, int32_t sl
   if (lose_ns) {
     if (C.dtype != PI_F16 || C.head_dim != 64 || a.tma != 2 || C.page_tokens % 16) return PI_ERR_SHAPE;
     a.limit_ns = lose_ns;
-    return launch_boxes<0, 64, 16, true>(a, map, stream);
+    return launch_boxes<0, 64, 64, 16, true>(a, map, stream);
   }
-  if (C.dtype == PI_F16) {
-    if (C.head_dim <= 64) return launch_attend<0, 64>(a, map, stream);
-    if (C.head_dim <= 128) return launch_attend<0, 128>(a, map, stream);
-    return launch_attend<0, 256>(a, map, stream);
-  }
-  if (C.head_dim <= 64) return launch_attend<1, 64>(a, map, stream);
-  if (C.head_dim <= 128) return launch_attend<1, 128>(a, map, stream);
-  return launch_attend<1, 256>(a, map, stream);
+  return C.dtype == PI_F16 ? launch_dims<0>(a, map, stream) : launch_dims<1>(a, map, stream);
 }
 
 extern "C" {
