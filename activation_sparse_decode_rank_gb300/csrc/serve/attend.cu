@@ -50,8 +50,8 @@ namespace pis {
 // 64, 128 or 256 are padded with zeros in shared memory only.
 //
 // Measured, bytes of the rows seen against a copy's 6.8 TB/s.  32 slots x 40
-// heads of 128, lengths to 2048, fp16: 107 us, 92 %.  8 slots, 64/8 heads of
-// 128, lengths to 131072, bf16: 302 us, 96 %.  24 slots, 32/8 heads of 128, a
+// heads of 128, lengths to 2048, fp16: 108 us, 91 %.  8 slots, 64/8 heads of
+// 128, lengths to 131072, bf16: 300 us, 97 %.  24 slots, 32/8 heads of 128, a
 // window of 1000: 28 us, 49 %, of which 5 to the first tile and 5 in joins.
 // One slot, 16 heads of 64, 200 tokens: 8 us, all latency; an empty launch in
 // its place takes 0.8, one that ends after finding its share 3.
@@ -345,7 +345,8 @@ struct Piece {
 // a box (16 too where tiles are gathered).  LOSE: the first tile of
 // block 0 is never ordered (the self-test of the wait that runs out).
 template <int DT, int DP, int DK, int BR, bool LOSE>
-__global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>()) attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
+    attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int S = att_stages<DT, DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
   // A stage: [16 / BR boxes][DP / 64 panels][K, V][BR rows][64 elements].
@@ -1155,8 +1156,8 @@ pi_status launch_boxes(const AttendArgs& a, const CUtensorMap& map, pi_stream st
   constexpr int smem = att_smem<DT, DP>();
   st = ensure_smem(reinterpret_cast<const void*>(attend_kernel<DT, DP, DK, BR, LOSE>), smem);
   if (st != PI_OK) return st;
-  // Two blocks per SM (one at 256 dims), or fewer where the longest slots that
-  // the tables and the window allow cannot use them.
+  // All blocks that are resident together, or fewer where the longest slots
+  // that the tables and the window allow cannot use them.
   long long seen = (long long)a.max_pages * a.page_tokens;
   if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
   const long long units = (long long)a.slots * a.kv_heads * a.tiles;

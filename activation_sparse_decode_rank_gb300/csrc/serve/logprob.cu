@@ -25,7 +25,7 @@
 // instruction).  Few rows: a row is split over several blocks, and the last
 // of them to arrive joins the parts.
 //
-// Measured: 4096 x 128256 bf16 with 20 alternatives 182 us, 85 % of a copy's
+// Measured: 4096 x 128256 bf16 with 20 alternatives 184 us, 84 % of a copy's
 // 6.8 TB/s (some 20 of it the selection); 7 x 50273 fp32 with 8 alternatives
 // 8.5 us, a chain of reads, selection and join.
 #include "serve.cuh"
