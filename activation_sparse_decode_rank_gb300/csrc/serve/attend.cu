@@ -484,6 +484,11 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
   uint32_t next_rows = 0;
   int next_t = 0, next_row = 0, next_page = 0, pages32 = 0, page0 = 0;
   auto page_index = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / P; };
+  // -2 stands for no visible row, so an entry that is no page number reads as -1.
+  auto page_number = [&](const int* entry) {
+    const int p = __ldg(entry);
+    return (unsigned)p < (unsigned)a.pages ? p : -1;
+  };
   constexpr int kBoxes = 16 / BR;  // of a tile
   auto fetch = [&](bool unit_begins) {
     if (unit_begins) {  // bring the unit's query rows near: they are read when its first tile is
@@ -511,13 +516,13 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
             t += 8 * (lane & 1);
             seen = seen >> (8 * (lane & 1)) & 0xffu;
           }
-          if (seen) pages32 = __ldg(row + page_index(t));
+          if (seen) pages32 = page_number(row + page_index(t));
         }
       }
     } else {
       const int t = next_t + (lane & 15), j = page_index(t);
       next_row = t - j * P;
-      next_page = next_rows >> (lane & 15) & 1u ? __ldg(row + j) : -2;
+      next_page = next_rows >> (lane & 15) & 1u ? page_number(row + j) : -2;
     }
   };
   // Sends that tile into a stage.  Piece pc of row r lies in panel pc / 8 at
