@@ -27,7 +27,8 @@ namespace pis {
 // weights p = exp2(.) of the second product are split the same way.  bf16
 // parts hold 8 bits each, so that type takes a second instruction with the
 // third part.  fp16's narrow exponent range is met by exact powers of two:
-// q is scaled to [2^13, 2^14) per head, p by 2^14.
+// q is scaled to [2^13, 2^14) per head, and p's reference is the maximum less
+// 14, so that the largest p is 2^14.
 //
 // Work split.  The tiles of all (slot, kv head, head tile) units, each unit
 // preceded by kUnitCost positions that stand for its fixed cost, form one
@@ -328,11 +329,11 @@ __device__ __forceinline__ void add_scaled(float4& sum, const float4& x, float f
 
 // Four elements of an output row from its joined parts (no visible token: 0).
 __device__ __forceinline__ void finish(const AttendArgs& a, size_t row, int d, const float4& sum,
-                                       float top, float lsum, float shift) {
+                                       float top, float lsum) {
   const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
   *reinterpret_cast<float4*>(a.y + row * a.head_dim + d) =
       make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-  if (d == 0 && a.lse) a.lse[row] = (top + (log2f(lsum) - shift)) * kLn2;
+  if (d == 0 && a.lse) a.lse[row] = (top + log2f(lsum)) * kLn2;
 }
 
 // A warp's part of a unit that it shares with other warps.
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
   constexpr int kValues = BR * 128, kPanel = 2 * kValues, kBox = DP / 64 * kPanel;
   auto row_at = [](int r) { return r / BR * kBox + r % BR * 128; };
   constexpr int kPieces = DP / 8;          // 16-byte pieces of a staged row
-  constexpr float kShift = DT == 0 ? 14.f : 0.f;  // weights carry 2^kShift
+  constexpr float kShift = 14.f;  // fp16: weights are relative to a maximum less kShift
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_mask[kAttWarps][S];
   __shared__ __align__(8) uint64_t s_bar[kAttWarps][S];
@@ -744,16 +745,16 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       float mx = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+      // From the rounded scores, and rounded up: exponents are at most kShift
+      // however large the scores are.
+      if (DT == 0) mx = __fsub_ru(mx, kShift);
       const float mn = fmaxf(m, mx);
       const float ref = mn == -INFINITY ? 0.f : mn;
       corr = ex2(m - ref);
       m = mn;
       float p[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[e] = ex2(fmaf(s[e], unit_scale, kShift - ref));
-        if (w[e] == -INFINITY) p[e] = 0.f;
-      }
+      for (int e = 0; e < 4; ++e) p[e] = ex2(w[e] - ref);
       l = fmaf(l, corr, (p[0] + p[1]) + (p[2] + p[3]));
       split2<DT>(p[0], p[1], pf[0], pf[1], pf2[0]);
       split2<DT>(p[2], p[3], pf[2], pf[3], pf2[1]);
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
           for (int j = 0; j < DK / 8; ++j)
             if (8 * j < D)
               *reinterpret_cast<float2*>(y + 8 * j) = make_float2(o[j][0] * inv, o[j][1] * inv);
-          if ((lane & 3) == 0 && a.lse) a.lse[row] = (m + (log2f(lt) - kShift)) * kLn2;
+          if ((lane & 3) == 0 && a.lse) a.lse[row] = (m + log2f(lt)) * kLn2;
         }
       } else {
         const int k = begins ? 1 : 0;
@@ -884,7 +885,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
         for (int i = 0; i < kAttWarps; ++i)
           if (i >= w0 && i < w1) add_scaled(sum, v[i], fw[i]);
         if (local) {
-          finish(a, out0 + hr, d, sum, top, lsum, kShift);
+          finish(a, out0 + hr, d, sum, top, lsum);
         } else {
           float* pr = a.part + (((size_t)blockIdx.x * 2 + (k >= 0)) * 8 + hr) * prow;
           __stcg(reinterpret_cast<float4*>(pr + d), sum);
@@ -1011,7 +1012,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
           for (int i = 0; i < 2; ++i) {
             if (e + i * kAttThreads >= items) break;
             if (last) {
-              finish(a, out0 + hr[i], d[i], sum[i], top[i], lsum[i], kShift);
+              finish(a, out0 + hr[i], d[i], sum[i], top[i], lsum[i]);
             } else {
               float* to = part_of(base, true) + hr[i] * prow;
               __stcg(reinterpret_cast<float4*>(to + d[i]), sum[i]);
