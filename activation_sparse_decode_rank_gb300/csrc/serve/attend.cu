@@ -485,11 +485,6 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
   uint32_t next_rows = 0;
   int next_t = 0, next_row = 0, next_page = 0, pages32 = 0, page0 = 0;
   auto page_index = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / P; };
-  // -2 stands for no visible row, so an entry that is no page number reads as -1.
-  auto page_number = [&](const int* entry) {
-    const int p = __ldg(entry);
-    return (unsigned)p < (unsigned)a.pages ? p : -1;
-  };
   constexpr int kBoxes = 16 / BR;  // of a tile
   auto fetch = [&](bool unit_begins) {
     if (unit_begins) {  // bring the unit's query rows near: they are read when its first tile is
@@ -509,7 +504,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
         page0 = lc.tile;
         Cursor c = lc;
         c.tile += lane / kBoxes;
-        pages32 = -2;
+        pages32 = -1;
         if (c.tile < c.v.tiles) {
           uint32_t seen = 1;
           int t = BR == 16 ? c.first_token() : c.rows_of(seen);
@@ -517,13 +512,13 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
             t += 8 * (lane & 1);
             seen = seen >> (8 * (lane & 1)) & 0xffu;
           }
-          if (seen) pages32 = page_number(row + page_index(t));
+          if (seen) pages32 = __ldg(row + page_index(t));
         }
       }
     } else {
       const int t = next_t + (lane & 15), j = page_index(t);
       next_row = t - j * P;
-      next_page = next_rows >> (lane & 15) & 1u ? page_number(row + j) : -2;
+      next_page = next_rows >> (lane & 15) & 1u ? __ldg(row + j) : -1;
     }
   };
   // Sends that tile into a stage.  Piece pc of row r lies in panel pc / 8 at
@@ -544,7 +539,8 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       const int i = 2 * (lc.tile - page0);
       const int p[2] = {__shfl_sync(~0u, pages32, i), __shfl_sync(~0u, pages32, i + 1)};
       const bool ok[2] = {(unsigned)p[0] < (unsigned)a.pages, (unsigned)p[1] < (unsigned)a.pages};
-      if ((!ok[0] && p[0] != -2) || (!ok[1] && p[1] != -2)) set_status(a.status, PI_ERR_INDEX);
+      if ((!ok[0] && (next_rows & 0xffu)) || (!ok[1] && (next_rows & 0xff00u)))
+        set_status(a.status, PI_ERR_INDEX);
       if (lane == 0) {
         s_mask[warp][stage] = next_rows & ((ok[0] ? 0xffu : 0u) | (ok[1] ? 0xff00u : 0u));
         mbar_expect(bar, (ok[0] + ok[1]) * kBox);
@@ -559,7 +555,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
     }
     if (one_page) next_page = __shfl_sync(~0u, pages32, lc.tile - page0);
     const bool ok = (unsigned)next_page < (unsigned)a.pages;
-    if (!ok && next_page != -2) set_status(a.status, PI_ERR_INDEX);
+    if (!ok && (one_page || (next_rows >> (lane & 15) & 1u))) set_status(a.status, PI_ERR_INDEX);
     uint32_t rows = next_rows;  // rows to read: visible, and in a page
     if (one_page)
       rows = ok ? rows : 0;
