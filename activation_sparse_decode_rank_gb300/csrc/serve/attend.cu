@@ -26,9 +26,9 @@ namespace pis {
 // the 22-bit product, and each lane finds both in its own registers.  The
 // weights p = exp2(.) of the second product are split the same way.  bf16
 // parts hold 8 bits each, so that type takes a second instruction with the
-// third part.  fp16's narrow exponent range is met by exact powers of two:
-// q is scaled to [2^13, 2^14) per head, and p's reference is the maximum less
-// 14, so that the largest p is 2^14.
+// third part (q's in halves, so that no row of it is 0).  fp16's narrow
+// exponent range is met by exact powers of two: q is scaled to [2^13, 2^14) per
+// head, and p's reference is the maximum less 14, so that the largest p is 2^14.
 //
 // Work split.  The tiles of all (slot, kv head, head tile) units, each unit
 // preceded by kUnitCost positions that stand for its fixed cost, form one
@@ -245,6 +245,42 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     x -= from_bits<DT>((uint16_t)lo);
     y -= from_bits<DT>((uint16_t)(lo >> 16));
     lo2 = pack_bits<DT>(x, y);
+  }
+}
+
+// Both rounded toward zero.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_rz(float x, float y) {
+  uint32_t r;
+  if (DT == 0) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+// The larger of |x| and least, with the sign of s.
+__device__ __forceinline__ float at_least(float x, float least, float s) {
+  return copysignf(fmaxf(fabsf(x), least), s);
+}
+// Two elements of q as parts: hi + lo (fp16, q scaled), hi + lo + 2 half (bf16).
+// The parts of an element have its sign and are not 0 unless it is, so that
+// an infinite key's product is infinite and of one sign in all of them: that
+// moves q by less than 2^-37 of its head's largest element (fp16), 2^-28 of
+// the element (bf16).
+template <int DT>
+__device__ __forceinline__ void split_q(float x, float y, uint32_t& hi, uint32_t& lo, uint32_t& half) {
+  if (DT == 0) {
+    if (fabsf(x) < 0x1p-24f && x != 0.f) x = copysignf(0x1p-24f, x);
+    if (fabsf(y) < 0x1p-24f && y != 0.f) y = copysignf(0x1p-24f, y);
+  }
+  const float lx = DT == 0 ? 0x1p-24f : fabsf(x) * 0x1p-30f, ly = DT == 0 ? 0x1p-24f : fabsf(y) * 0x1p-30f;
+  hi = pack_rz<DT>(x, y);
+  float rx = x - from_bits<DT>((uint16_t)hi), ry = y - from_bits<DT>((uint16_t)(hi >> 16));
+  if (DT == 0) {
+    lo = pack_bits<DT>(at_least(rx, lx, x), at_least(ry, ly, y));
+  } else {
+    lo = pack_rz<DT>(at_least(rx, lx, x), at_least(ry, ly, y));
+    rx -= from_bits<DT>((uint16_t)lo);
+    ry -= from_bits<DT>((uint16_t)(lo >> 16));
+    half = pack_bits<DT>(0.5f * at_least(rx, lx, x), 0.5f * at_least(ry, ly, y));
   }
 }
 
@@ -646,8 +682,8 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       for (int ks = 0; ks < DK / 16; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          split2<DT>(f[ks][e].x * up, f[ks][e].y * up, qf[ks][2 * e], qf[ks][2 * e + 1],
-                     qf2[ks][e]);
+          split_q<DT>(f[ks][e].x * up, f[ks][e].y * up, qf[ks][2 * e], qf[ks][2 * e + 1],
+                      qf2[ks][e]);
       m = -INFINITY;
       l = 0.f;
 #pragma unroll
@@ -718,7 +754,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
               else
                 mma<DT>(c, qf[ks], b[2 * nt], b[2 * nt + 1]);
               if (DT == 1) {
-                const uint32_t q2[4] = {0u, qf2[ks][0], 0u, qf2[ks][1]};
+                const uint32_t q2[4] = {qf2[ks][0], qf2[ks][0], qf2[ks][1], qf2[ks][1]};
                 mma<DT>(c, q2, b[2 * nt], b[2 * nt + 1]);
               }
             }

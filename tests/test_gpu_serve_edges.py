@@ -65,3 +65,158 @@ def test_attention_of_large_finite_scores(dtype, sign, qscale, shape, lens):
             assert np.abs(y[s, h] - want).max() <= 2.0 ** -20 * np.abs(want).max(), (s, h)
             assert abs(lse[s, h] - a[top]) <= da + 8 * U * abs(a[top]), (s, h)
     assert seen >= len(lens) * c.heads // 2
+
+
+# ------------------------------------------------------------------ infinities
+def plain_special(q, k, v, n, scale, window, sinks):
+    """One slot and kv head as in servehelp.attention, with infinite and NaN
+    operands: products and sums follow IEEE rules (0 x infinity is NaN).  A NaN
+    or +infinity score makes y and lse NaN; a score of -infinity has weight 0; a
+    finite score's weight is positive, however small."""
+    G, D = q.shape
+    t = [i for i in range(n) if window == 0 or i >= n - window or i < sinks]
+    y, lse, mag = np.zeros((G, D)), np.full(G, -np.inf), np.zeros(G)
+    if not t:
+        return y, lse, mag
+    k, v = k[t], v[t]
+    with np.errstate(all="ignore"):
+        a = scale * (q[:, None, :] * k[None]).sum(-1)
+        for g in range(G):
+            if np.isnan(a[g]).any() or np.isposinf(a[g]).any():
+                y[g], lse[g] = np.nan, np.nan
+                continue
+            f = np.isfinite(a[g])
+            w = np.zeros(len(t))
+            if f.any():
+                m = a[g][f].max()
+                w[f] = np.exp(a[g][f] - m)
+                lse[g] = m + np.log(w.sum())
+                mag[g] = (np.abs(q[g]) @ np.abs(k[f]).T).max()
+            finite = np.isfinite(v)
+            y[g] = w @ np.where(finite, v, 0.0) / (w.sum() or 1.0)
+            for d in np.flatnonzero(~finite.all(0)):
+                odd = np.flatnonzero(~finite[:, d])
+                signs = {float(v[i, d]) if f[i] else math.nan for i in odd}
+                y[g, d] = signs.pop() if len(signs) == 1 else math.nan
+    return y, lse, mag
+
+
+def poke(c, kind, s, t, h, d, value):
+    """Sets element d of the key (0) or value (1) of token t of slot s."""
+    new = (c.knew, c.vnew)[kind] if c.append and t == c.lens[s] - 1 else None
+    if new is not None:
+        new[s, h, d] = value
+    else:
+        c.pool[c.layer, int(c.np_table[s, t // c.P]), kind, h, t % c.P, d] = value
+    c.rows[kind, s, t, h, d] = float(torch.tensor(value).to(TD[c.dtype]))
+
+
+def check_special(c, y, lse):
+    torch.cuda.synchronize()
+    y, lse = y.double().cpu().numpy(), lse.double().cpu().numpy()
+    G, odd = c.heads // c.kv, 0
+    for s, n in enumerate(c.lens):
+        for h in range(c.kv):
+            r = slice(h * G, (h + 1) * G)
+            yo, lo, mag = plain_special(c.q[s, r].astype(np.float64), c.rows[0, s, :, h],
+                                        c.rows[1, s, :, h], n, c.scale, c.window, c.sinks)
+            e = (abs(c.scale) * mag * (2.0 ** -21 + c.D * U) + 2.0 ** -20 + n * U)[:, None]
+            vis = c.rows[1, s, :max(n, 1), h]
+            vmax = np.abs(vis[np.isfinite(vis)]).max()
+            for got, want, tol in ((y[s, r], yo, 3 * e * vmax),
+                                   (lse[s, r], lo, 2 * e[:, 0] + 4 * U * np.abs(lo))):
+                f = np.isfinite(want)
+                odd += (~f).sum()
+                assert (np.isnan(got) == np.isnan(want)).all(), (s, h)
+                assert (got[np.isinf(want)] == want[np.isinf(want)]).all(), (s, h)
+                assert (np.abs(got[f] - want[f]) <= np.broadcast_to(tol, want.shape)[f]).all(), (s, h)
+    assert odd > 0 and int(c.status[0]) == 0
+
+
+INF = float("inf")
+SPECIAL_SHAPES = [((8, 2, 64, 16), [1, 16, 90, 333]), ((12, 1, 128, 8), [2, 700]),
+                  ((3, 3, 80, 24), [33, 500]), ((6, 2, 256, 16), [5, 300]),
+                  ((4, 1, 40, 7), [19, 64]), ((8, 1, 128, 32), [9000])]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("q", [-1.0, 1.0, -1.2345678])
+@pytest.mark.parametrize("append", [False, True])
+def test_attention_of_one_token_with_an_infinite_key(dtype, q, append):
+    for shape in ((4, 2, 64, 16), (4, 4, 128, 8), (9, 1, 200, 5)):
+        c = Cache(dtype, *shape, [1], append=append)
+        c.q[:] = q
+        c.qd.fill_(q)
+        for h in range(c.kv):
+            poke(c, 0, 0, 0, h, 7, INF)
+        y, lse = c.run()
+        check_special(c, y, lse)
+        if q < 0:
+            assert (y[0] == 0).all() and torch.isneginf(lse[0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,lens", SPECIAL_SHAPES)
+@pytest.mark.parametrize("append", [False, True])
+@pytest.mark.parametrize("exact_q", [False, True])
+def test_attention_of_infinite_keys(dtype, shape, lens, append, exact_q):
+    # heads of both signs: scores of -infinity and of +infinity, one or several
+    # per slot; queries with and without low parts
+    g = np.random.default_rng(sum(shape))
+    for several in (1, 5):
+        c = Cache(dtype, *shape, lens, append=append)
+        if exact_q:
+            c.q = np.round(c.q * 4).astype(np.float32) / 4
+            c.q[c.q == 0] = 0.25
+            c.qd.copy_(torch.from_numpy(c.q))
+        d = int(g.integers(0, c.D))
+        for s, n in enumerate(lens):
+            for t in {n - 1, *g.integers(0, n, several).tolist()}:
+                for h in range(c.kv):
+                    poke(c, 0, s, t, h, d, INF)
+        check_special(c, *c.run())
+        assert not append or c.check_stored() is None
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,lens", SPECIAL_SHAPES)
+def test_attention_of_scores_that_are_all_minus_infinity(dtype, shape, lens):
+    c = Cache(dtype, *shape, lens)
+    c.q = -np.abs(c.q) - np.float32(1e-30)  # one of them tiny beside the others
+    c.q[..., 3] = -1e-25
+    c.qd.copy_(torch.from_numpy(c.q))
+    for s, n in enumerate(lens):
+        for t in range(n):
+            for h in range(c.kv):
+                poke(c, 0, s, t, h, 3, INF)
+    y, lse = c.run()
+    check_special(c, y, lse)
+    S = len(lens)
+    assert (y[:S] == 0).all() and torch.isneginf(lse[:S]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attention_of_nan_keys_mixed_signs_and_infinite_queries(dtype):
+    # -infinity - infinity and 0 x infinity are NaN, for the heads they concern
+    c = Cache(dtype, 8, 2, 64, 16, [50, 70, 90, 40])
+    poke(c, 0, 0, 20, 0, 5, float("nan"))
+    poke(c, 0, 1, 33, 1, 5, INF)
+    poke(c, 0, 1, 33, 1, 6, -INF)
+    c.q[1, 4, 5], c.q[1, 4, 6] = -2.0, 3.0   # both products -infinity
+    c.q[1, 5, 5], c.q[1, 5, 6] = -2.0, 0.0   # 0 x infinity
+    c.q[2, 3, 9] = -INF                       # keys of both signs: NaN
+    c.q[3, 0, 9] = -INF
+    for t in range(40):
+        poke(c, 0, 3, t, 0, 9, 0.5 + t / 64)  # all scores -infinity
+    c.qd.copy_(torch.from_numpy(c.q))
+    check_special(c, *c.run())
+
+
+def test_attention_of_new_rows_beyond_the_half_type():
+    # 1e6 is rounded to infinity when it is stored
+    c = Cache("f16", 4, 4, 64, 16, [40, 17], append=True)
+    for h in range(4):
+        poke(c, 0, 0, 39, h, h, 1e6)
+        poke(c, 0, 1, 16, h, h, -1e6)
+    check_special(c, *c.run())
+    c.check_stored()
