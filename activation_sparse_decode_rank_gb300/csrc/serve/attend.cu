@@ -575,10 +575,10 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       const int i = 2 * (lc.tile - page0);
       const int p[2] = {__shfl_sync(~0u, pages32, i), __shfl_sync(~0u, pages32, i + 1)};
       const bool ok[2] = {(unsigned)p[0] < (unsigned)a.pages, (unsigned)p[1] < (unsigned)a.pages};
-      if ((!ok[0] && (next_rows & 0xffu)) || (!ok[1] && (next_rows & 0xff00u)))
-        set_status(a.status, PI_ERR_INDEX);
       if (lane == 0) {
-        s_mask[warp][stage] = next_rows & ((ok[0] ? 0xffu : 0u) | (ok[1] ? 0xff00u : 0u));
+        const uint32_t rows = next_rows & ((ok[0] ? 0xffu : 0u) | (ok[1] ? 0xff00u : 0u));
+        if (rows != next_rows) set_status(a.status, PI_ERR_INDEX);
+        s_mask[warp][stage] = rows;
         mbar_expect(bar, (ok[0] + ok[1]) * kBox);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -591,13 +591,15 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
     }
     if (one_page) next_page = __shfl_sync(~0u, pages32, lc.tile - page0);
     const bool ok = (unsigned)next_page < (unsigned)a.pages;
-    if (!ok && (one_page || (next_rows >> (lane & 15) & 1u))) set_status(a.status, PI_ERR_INDEX);
     uint32_t rows = next_rows;  // rows to read: visible, and in a page
     if (one_page)
       rows = ok ? rows : 0;
     else
       rows &= __ballot_sync(~0u, ok);
-    if (lane == 0) s_mask[warp][stage] = rows;
+    if (lane == 0) {
+      if (rows != next_rows) set_status(a.status, PI_ERR_INDEX);
+      s_mask[warp][stage] = rows;
+    }
     const long long row = ok ? ((long long)next_page * 2 * a.kv_heads + lc.g) * P + next_row : 0;
     if (a.tma) {
       if (lane == 0) {
