@@ -372,10 +372,148 @@ __device__ __forceinline__ void finish(const AttendArgs& a, size_t row, int d, c
   if (d == 0 && a.lse) a.lse[row] = (top + log2f(lsum)) * kLn2;
 }
 
+// Weight of a part beside the larger maximum: not 0, so that an infinite sum
+// stays what it is (2^-126 of a finite one changes nothing).
+__device__ __forceinline__ float part_weight(float below) { return fmaxf(ex2(below), 0x1p-126f); }
+
+// Infinite values.  One meets weights' parts that are 0 or negative, and NaN is
+// left of its column's sum.  Where that happened in a warp's share, a pass of
+// its own over the share tells +-infinity from NaN: the loop over the tiles
+// stays free of tests.  Heads whose scores hold NaN or +infinity stay NaN.
+template <int DT>
+struct Unit {  // (slot, kv head, head tile)
+  const AttendArgs& a;
+  int slot, g, ht, rows;
+  Seen v;
+  const float* q;
+  __device__ Unit(const AttendArgs& a, int slot, int g, int ht)
+      : a(a), slot(slot), g(g), ht(ht), rows(min(8, a.group - ht * 8)), v(seen_of(a, slot)),
+        q(a.q + ((size_t)slot * a.heads + g * a.group + ht * 8) * a.head_dim) {}
+  // The visible tokens [first, end) of tile i; returns the tile's first position.
+  __device__ int rows_of(int i, int& first, int& end) const {
+    const bool sink = i < v.first_tiles;
+    const int t = (sink ? i : (v.tail >> 4) + i - v.first_tiles) << 4;
+    first = sink ? 0 : max(0, v.tail - t);
+    end = min(16, (sink ? v.first : v.n) - t);
+    return t;
+  }
+  // Key of a token in the pool; null where its page is out of range.
+  __device__ const uint16_t* key_of(int t) const {
+    const int page = __ldg(a.table + (size_t)slot * a.max_pages + t / a.page_tokens);
+    if ((unsigned)page >= (unsigned)a.pages) return nullptr;
+    return a.pool + (((size_t)page * 2 * a.kv_heads + g) * a.page_tokens + t % a.page_tokens) * a.head_dim;
+  }
+  __device__ bool is_new(int t) const { return a.k_new && t == v.n - 1; }
+  // Element d of a token's key or value, a new one as it is stored.
+  __device__ float element(bool value, int t, const uint16_t* key, int d) const {
+    if (is_new(t))
+      return from_bits<DT>(to_bits<DT>(__ldg((value ? a.v_new : a.k_new) +
+                                             ((size_t)slot * a.kv_heads + g) * a.head_dim + d)));
+    return from_bits<DT>(__ldg(key + (value ? (size_t)a.kv_heads * a.page_tokens * a.head_dim : 0) + d));
+  }
+  __device__ bool finite_key(int t, const uint16_t* key) const {
+    bool ok = !is_new(t);  // a new one is not looked at: its score is computed
+    constexpr uint32_t kTop = DT == 0 ? 0x7c00u : 0x7f80u;
+    for (int e = 0; e < a.head_dim && ok; e += 8) {
+      const uint4 k = __ldg(reinterpret_cast<const uint4*>(key + e));
+      for (uint32_t w : {k.x, k.y, k.z, k.w}) ok = ok && (w & kTop) != kTop && (w >> 16 & kTop) != kTop;
+    }
+    return ok;
+  }
+  __device__ float score(int h, int t, const uint16_t* key) const {
+    float s = 0.f;
+    for (int e = 0; e < a.head_dim; ++e)
+      s = fmaf(__ldg(q + h * a.head_dim + e), element(false, t, key, e), s);
+    return s * a.scale;
+  }
+};
+
+// A part: the tiles [i0, i1) of a unit; head h's element d is at
+// to[h stride + d], or swizzled as the warps' parts are.
+template <int DT>
+__device__ __forceinline__ void part_infinities(const Unit<DT>& u, int i0, int i1, float* to, int stride,
+                                                bool swizzled) {
+  const int lane = threadIdx.x & 31, D = u.a.head_dim;
+  auto at = [&](int h, int d) { return to + h * stride + (swizzled ? ((d >> 3 ^ h) << 3) + (d & 7) : d); };
+  uint32_t odd_q = 0, closed = 0;  // heads, as bits: with a query that is not finite; that stay
+  for (int h = 0; h < u.rows; ++h)
+    for (int e = lane; e < D; e += 32)
+      if (!(fabsf(__ldg(u.q + h * D + e)) < INFINITY)) odd_q |= 1u << h;
+  odd_q = __reduce_or_sync(~0u, odd_q);
+  for (int i = i0 + (lane >> 4); i < i1; i += 2) {  // half a warp per tile
+    int r0, r1;
+    const int t = u.rows_of(i, r0, r1) + (lane & 15);
+    if ((lane & 15) < r0 || (lane & 15) >= r1) continue;
+    const uint16_t* key = u.key_of(t);
+    if (!key) continue;
+    const uint32_t look = u.finite_key(t, key) ? odd_q : ~0u;
+    for (int h = 0; h < u.rows; ++h)
+      if (look >> h & 1u && !(u.score(h, t, key) < INFINITY)) closed |= 1u << h;
+  }
+  closed = __reduce_or_sync(~0u, closed);
+  for (int d = lane; d < D; d += 32) {
+    uint32_t open = 0, pos = 0, neg = 0, nan = 0;
+    for (int h = 0; h < u.rows; ++h)
+      if (*at(h, d) != *at(h, d)) open |= 1u << h;
+    open &= ~closed;
+    for (int i = open ? i0 : i1; i < i1; ++i) {
+      int r0, r1;
+      const int t0 = u.rows_of(i, r0, r1);
+      for (int t = t0 + r0; t < t0 + r1; ++t) {
+        const uint16_t* key = u.key_of(t);
+        if (!key) continue;
+        const float x = u.element(true, t, key, d);
+        if (fabsf(x) < INFINITY) continue;
+        uint32_t none = 0;  // heads whose score is -infinity: 0 x infinity
+        const uint32_t look = open & (u.finite_key(t, key) ? odd_q : ~0u);
+        for (int h = 0; h < u.rows; ++h)
+          if (look >> h & 1u && u.score(h, t, key) == -INFINITY) none |= 1u << h;
+        nan |= x != x ? open : none;
+        (x > 0.f ? pos : neg) |= open & ~none;
+      }
+    }
+    nan |= pos & neg;
+    for (int h = 0; h < u.rows; ++h)
+      if ((open & ~nan & (pos | neg)) >> h & 1u) *at(h, d) = pos >> h & 1u ? INFINITY : -INFINITY;
+  }
+}
+
+// Where a warp's share begins, and whether one of its sums is NaN.
+struct Start {
+  long long pos;
+  int slot, unit, tile, odd;
+};
+// Goes through a warp's share: the pieces are its parts of units shared with
+// other warps, that which came in and that which goes on.
+template <int DT>
+__device__ __noinline__ void infinite_values(const AttendArgs& a, const Start& from, long long share0,
+                                             long long share1, int even, float* piece0, float* piece1,
+                                             int stride) {
+  const int g = from.unit / a.tiles, D = a.head_dim;
+  Cursor c{from.pos, from.slot, g, from.unit - g * a.tiles, from.tile, seen_of(a, from.slot)};
+  for (; c.pos < share1; c.advance(a, even)) {
+    const int left = c.v.tiles - c.tile, n = share1 - c.pos < left ? (int)(share1 - c.pos) : left;
+    const bool begins = c.pos - c.tile >= share0, whole = begins && n == left;
+    part_infinities(Unit<DT>(a, c.slot, c.g, c.ht), c.tile, c.tile + n,
+                    whole ? a.y + ((size_t)c.slot * a.heads + c.g * a.group + c.ht * 8) * D
+                          : begins ? piece1 : piece0,
+                    whole ? D : stride, !whole);
+    c.tile += n - 1;
+    c.pos += n - 1;
+  }
+}
+
 // A warp's part of a unit that it shares with other warps.
 struct Piece {
   long long at;  // line position of the unit's first tile, -1: none
   int slot, g, ht, tiles;
+};
+
+// The parts to join: n of them, of blocks base, base + stride, ...
+struct Join {
+  const Piece* pc;
+  int b0, nb, each, groups;  // the unit's blocks; those of a group; groups (0: none)
+  int base, stride, n;
 };
 
 // DP: elements of a staged row, DK of them used by the products.  BR: rows of
@@ -383,7 +521,7 @@ struct Piece {
 // block 0 is never ordered (the self-test of the wait that runs out).
 template <int DT, int DP, int DK, int BR, bool LOSE>
 __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
-    attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map) {
+    attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int S = att_stages<DT, DP>();
   constexpr int kTile = 16 * DP * 2;       // bytes of a tile of K (or V)
   // A stage: [16 / BR boxes][DP / 64 panels][K, V][BR rows][64 elements].
@@ -397,6 +535,12 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
   __shared__ float s_m[kAttWarps][2][8], s_l[kAttWarps][2][8];
   __shared__ Piece s_piece[kAttWarps][2];
   __shared__ int s_even;
+  // Where the warps' shares begin, until they are done; then the joins.  The
+  // static memory stays within 1 KB: more of it costs a block per SM.
+  __shared__ union {
+    Start start[kAttWarps];
+    Join join[2];
+  } s_both;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = a.head_dim, P = a.page_tokens;
   const int units = a.kv_heads * a.tiles;
@@ -509,6 +653,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
     }
   }
   Cursor lc = cc;  // the tile being loaded
+  if (lane == 0) s_both.start[warp] = Start{cc.pos, cc.slot, cc.g * a.tiles + cc.ht, cc.tile, 0};
 
   const uint32_t ring = smem_u32(smem) + warp * S * 2 * kTile;
   const int pieces = D >> 3;
@@ -831,7 +976,9 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
           for (int j = 0; j < DK / 8; ++j)
             if (8 * j < D)
               *reinterpret_cast<float2*>(y + 8 * j) = make_float2(o[j][0] * inv, o[j][1] * inv);
-          if ((lane & 3) == 0 && a.lse) a.lse[row] = (m + log2f(lt)) * kLn2;
+          if ((lane & 3) == 0) {
+            if (a.lse) a.lse[row] = (m + log2f(lt)) * kLn2;
+          }
         }
       } else {
         const int k = begins ? 1 : 0;
@@ -851,6 +998,10 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
         }
         if (lane == 0) s_piece[warp][k] = Piece{at, cc.slot, g, ht, cc.v.tiles};
       }
+      float any = 0.f;
+#pragma unroll
+      for (int j = 0; j < DK / 8; ++j) any += o[j][0] + o[j][1];
+      if (any != any) s_both.start[warp].odd = 1;
       fresh = true;
     }
     cc.advance(a, s_even);
@@ -868,6 +1019,11 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       parity ^= 1;
     }
   }
+
+  // Infinite values: once more through the share's parts.
+  __syncwarp();
+  if (s_both.start[warp].odd && !late)
+    infinite_values<DT>(a, s_both.start[warp], share0, share1, s_even, piece_data(warp, 0), piece_data(warp, 1), DP);
 
   // Units shared by warps.  A unit's warps within the block: the one that
   // begins it (piece 1) or the block's first (piece 0), then the followers'
@@ -901,7 +1057,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       const float mw = in ? s_m[w][w == k][hr] : -INFINITY, lw = in ? s_l[w][w == k][hr] : 0.f;
       float top = fmaxf(mw, __shfl_xor_sync(~0u, mw, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      const float f = ex2(mw - (top == -INFINITY ? 0.f : top));
+      const float f = part_weight(mw - (top == -INFINITY ? 0.f : top));
       float lsum = lw * f;
       lsum += __shfl_xor_sync(~0u, lsum, 1);
       lsum += __shfl_xor_sync(~0u, lsum, 2);
@@ -928,13 +1084,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       }
     }
   }
-  // The parts to join: n of them, of blocks base, base + stride, ...
-  struct Join {
-    const Piece* pc;
-    int b0, nb, each, groups;  // the unit's blocks; those of a group; groups (0: none)
-    int base, stride, n;
-  };
-  __shared__ Join s_join[2];
+  Join(&s_join)[2] = s_both.join;
   // Releases the block's parts, which the barrier ordered before it, and
   // acquires the other blocks'.  True for the last of `of`.
   auto arrive = [](int* counter, int of) {
@@ -1035,7 +1185,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
               for (int i = 0; i < 2; ++i)
                 if (j0 + j < n) {
                   const float up = fmaxf(top[i], q[i][j].x), ref = up == -INFINITY ? 0.f : up;
-                  const float was = ex2(top[i] - ref), is = ex2(q[i][j].x - ref);
+                  const float was = part_weight(top[i] - ref), is = part_weight(q[i][j].x - ref);
                   sum[i] = make_float4(sum[i].x * was, sum[i].y * was, sum[i].z * was, sum[i].w * was);
                   add_scaled(sum[i], v[i][j], is);
                   lsum[i] = fmaf(lsum[i], was, q[i][j].y * is);

@@ -69,7 +69,13 @@ size_t pi_cache_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_
  *     lse[s][h] = log sum_V exp(a_t).
  * An empty slot (n = 0), and scores that are all -infinity, give y = 0 and
  * lse = -infinity.  Rows of a page that are not visible are not used whatever
- * they hold (NaN and infinities too).
+ * they hold (NaN and infinities too).  Infinite operands of visible rows count
+ * as the formulas say: an infinite key's score is +-infinity (NaN where
+ * products of both signs or 0 x infinity meet), and a score of -infinity
+ * weighs nothing; a score of NaN or +infinity makes the head's y and lse NaN.
+ * An infinite value makes its element of y infinite, however small the weight
+ * (NaN where both signs meet, or where a value that is not finite has the
+ * weight 0 of a score of -infinity).
  *   q [slots][heads][head_dim] fp32; y the same shape, fp32; lse NULL or
  *   [slots][heads] fp32; heads a multiple of kv_heads, at most 1024.
  *   k_new, v_new: NULL (the new token is in the cache already), or both

@@ -220,3 +220,65 @@ def test_attention_of_new_rows_beyond_the_half_type():
         poke(c, 0, 1, 16, h, h, -1e6)
     check_special(c, *c.run())
     c.check_stored()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,lens", SPECIAL_SHAPES)
+@pytest.mark.parametrize("append", [False, True])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (31, 4)])
+def test_attention_of_infinite_values(dtype, shape, lens, append, window, sinks):
+    # a column with one sign, one with both, one with NaN, one of the first
+    # token's, one of the last's; hidden rows hold them too
+    g = np.random.default_rng(sum(shape) + append)
+    c = Cache(dtype, *shape, lens, window, sinks, append=append)
+    for s, n in enumerate(lens):
+        seen = [t for t in range(n) if not window or t >= n - window or t < sinks]
+        for h in range(c.kv):
+            pick = lambda: int(g.choice(seen))  # noqa: E731
+            for t in {pick(), pick(), pick()}:
+                poke(c, 1, s, t, h, 1, -INF)
+            poke(c, 1, s, pick(), h, 8, INF)
+            poke(c, 1, s, pick(), h, 8, -INF)
+            poke(c, 1, s, pick(), h, 17, float("nan"))
+            poke(c, 1, s, pick(), h, 17, INF)
+            poke(c, 1, s, 0, h, c.D - 1, INF) if 0 in seen else None
+            poke(c, 1, s, n - 1, h, c.D - 2, -INF)
+            if len(seen) < n:
+                poke(c, 1, s, seen[-1] - window, h, 20, INF)
+    check_special(c, *c.run())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attention_of_infinite_values_of_any_weight(dtype):
+    # weights from 1 down to far below fp32's smallest, in a unit that several
+    # blocks share; a score of -infinity has no weight to multiply
+    n = 6000
+    for lens in ([n], [300, 40]):
+        c = Cache(dtype, 4, 1, 128, 16, lens, qscale=0.0)
+        for s in range(len(lens)):
+            c.q[s, :, 0] = (0.01, 1.0, 4.0, -4.0)
+            for i, t in enumerate(np.linspace(0, lens[s] - 1, 12).astype(int)):
+                poke(c, 0, s, int(t), 0, 0, -100.0 * i)
+                poke(c, 1, s, int(t), 0, 3 * i, INF if i % 2 else -INF)
+            poke(c, 0, s, lens[s] - 3, 0, 5, INF)   # scores 0 x infinity: NaN but for head 2
+        c.q[:, 2, 5] = -1.0
+        c.qd.copy_(torch.from_numpy(c.q))
+        for s in range(len(lens)):
+            poke(c, 1, s, lens[s] - 3, 0, 70, INF)
+        check_special(c, *c.run())
+        # ... and without it
+        for s in range(len(lens)):
+            poke(c, 0, s, lens[s] - 3, 0, 5, 0.0)
+        check_special(c, *c.run())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attention_of_infinite_keys_and_values(dtype):
+    c = Cache(dtype, 16, 1, 64, 16, [200, 3000])
+    for s, t in ((0, 7), (0, 100), (1, 10), (1, 2500)):
+        poke(c, 0, s, t, 0, 4, INF if t != 100 else -INF)
+        poke(c, 1, s, t + 1, 0, 9, INF)
+        poke(c, 1, s, t, 0, 10, -INF)
+    c.q[0, :8, 4] = 0.25
+    c.qd.copy_(torch.from_numpy(c.q))
+    check_special(c, *c.run())
