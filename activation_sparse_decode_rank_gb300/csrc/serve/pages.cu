@@ -89,24 +89,24 @@ __device__ __forceinline__ int used_pages(const PageArgs& a, int s) {
 }
 
 // Sum over the block, and the sum of the threads before this one.  T threads.
-template <int T>
-__device__ __forceinline__ int block_scan(int v, int* total) {
-  __shared__ int sh[T / 32 + 1];
+template <int T, typename V>
+__device__ __forceinline__ V block_scan(V v, V* total) {
+  __shared__ V sh[T / 32 + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int upto = v;
+  V upto = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int w = __shfl_up_sync(~0u, upto, o);
+    const V w = __shfl_up_sync(~0u, upto, o);
     if (lane >= o) upto += w;
   }
   __syncthreads();
   if (lane == 31) sh[warp] = upto;
   __syncthreads();
   if (warp == 0) {
-    int w = lane < T / 32 ? sh[lane] : 0;
+    V w = lane < T / 32 ? sh[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(~0u, w, o);
+      const V x = __shfl_up_sync(~0u, w, o);
       if (lane >= o) w += x;
     }
     __syncwarp();
@@ -232,11 +232,13 @@ __device__ void settle(const PageArgs& a, int nb) {
     }
     need = max(0, pages_of(want, a.page_tokens) - first);
   }
-  int need_sum, pair_sum;
-  const int before = block_scan<T>(need, &need_sum);
-  const int got = max(0, min(need, sum - before));
+  // 1024 slots may want more pages than 2^31; `sum` of them at most are there
+  long long need_sum;
+  int pair_sum;
+  const int before = (int)min(block_scan<T>((long long)need, &need_sum), (long long)sum);
+  const int got = min(need, sum - before);
   const bool copied = from >= 0 && got > 0;
-  const int pair = block_scan<T>(copied, &pair_sum);
+  const int pair = block_scan<T>((int)copied, &pair_sum);
   if (s < a.slots) {
     a.first[s] = first;
     a.before[s] = before;
@@ -245,9 +247,10 @@ __device__ void settle(const PageArgs& a, int nb) {
     a.len[s] = got < need ? min(want, (first + got) * a.page_tokens) : want;
   }
   if (threadIdx.x == 0) {
-    a.sums[kSumNeed] = min(need_sum, sum);
+    const int taken = (int)min(need_sum, (long long)sum);
+    a.sums[kSumNeed] = taken;
     a.counts[0] = pair_sum;
-    a.counts[1] = a.pages - sum + min(need_sum, sum);
+    a.counts[1] = a.pages - sum + taken;
     if (need_sum > sum) set_status(a.status, PI_ERR_CAPACITY);
   }
 }
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kScanPages) place_kernel(const PageArgs a) {
   const int p = blockIdx.x * kScanPages + threadIdx.x;
   const bool in = p < a.pages && counts<FORK, false>(a, p);
   int total;
-  at += block_scan<kScanPages>(in, &total);
+  at += block_scan<kScanPages>((int)in, &total);
   if (FORK) {
     if (!in || at >= need) return;
     const int s = slot_of(before, a.slots, at), j = at - before[s];
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(1024) small_kernel(const PageArgs a) {
     const int before = block_scan<T>(need, &need_sum);
     const int got = max(0, min(need, sum - before));
     const bool copied = last >= 0 && got > 0;
-    const int pair = block_scan<T>(copied, &pair_sum);
+    const int pair = block_scan<T>((int)copied, &pair_sum);
     if (tid < a.slots) {
       sh_whole[tid] = first;
       sh_before[tid] = before;

@@ -282,3 +282,23 @@ def test_attention_of_infinite_keys_and_values(dtype):
     c.q[0, :8, 4] = 0.25
     c.qd.copy_(torch.from_numpy(c.q))
     check_special(c, *c.run())
+
+
+# ------------------------------------------------------------------ page counts past 2^31
+def test_fork_wants_more_pages_than_32_bits_count():
+    # 1024 slots that each want 2^21 pages of one token (2^31 in all, tables of
+    # 8 GB), 1000 pages to be had: the first slot takes them
+    S, mp, pages = 1024, 1 << 21, 1000
+    desc = pi.make_cache_desc(1, pages, 1, 8, 1, "f16")
+    tables = [torch.empty((S, mp), dtype=torch.int32, device=DEV) for _ in range(2)]
+    length, ref, pairs = i32([7] * S), i32([7] * pages), i32([[7, 7]] * S)
+    counts, st, ws = i32([7] * 4), new_status(), pi.cache_workspace(desc, S, 0, DEV)
+    pi.check(pi.pi_cache_fork(desc, S, mp, i32([-1] * S), i32([mp] * S), None, tables[0], i32([0] * S),
+                              tables[1], length, ref, None, pairs, counts, st, ws))
+    torch.cuda.synchronize()
+    assert int(st[0]) == pi.PI_ERR_CAPACITY
+    assert length.tolist() == [pages] + [0] * (S - 1) and ref.tolist() == [1] * pages
+    assert counts.tolist() == [0, pages, 7, 7]
+    assert tables[1][0, :pages].tolist() == list(range(pages))
+    tables[1][0, :pages] = -1
+    assert int(tables[1].max()) == -1 and int(tables[1].min()) == -1
