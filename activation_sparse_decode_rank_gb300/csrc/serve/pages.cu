@@ -130,7 +130,7 @@ __device__ __forceinline__ void clear_pass(const PageArgs& a, int first, int ste
 // Entries [first, end) of slot s, four at a time where rows are aligned to
 // that.  Fork: full pages are shared, the lowest slot bids for each partly
 // filled one, and the slot's full pages, partly filled page and wanted length
-// are noted.
+// are noted.  A row may end at 2^31 - 1: loops count from `first`.
 template <bool FORK>
 __device__ __forceinline__ void count_pass(const PageArgs& a, int s, int first, int end) {
   if (FORK) {
@@ -153,21 +153,24 @@ __device__ __forceinline__ void count_pass(const PageArgs& a, int s, int first, 
       return p;
     };
     if ((a.max_pages & 3) == 0) {
-      for (int j = first + 4 * threadIdx.x; j < end; j += 4 * kPageThreads) {
+      for (int i = 4 * threadIdx.x; i < end - first; i += 4 * kPageThreads) {
+        const int j = first + i;
         int4 p = make_int4(-1, -1, -1, -1);
         if (j < whole) p = __ldg(reinterpret_cast<const int4*>(src + j));
         p = make_int4(take(j, p.x), take(j + 1, p.y), take(j + 2, p.z), take(j + 3, p.w));
         *reinterpret_cast<int4*>(dst + j) = p;
       }
     } else {
-      for (int j = first + threadIdx.x; j < end; j += kPageThreads)
+      for (int i = threadIdx.x; i < end - first; i += kPageThreads) {
+        const int j = first + i;
         dst[j] = take(j, j < whole ? __ldg(src + j) : -1);
+      }
     }
   } else {
     const int used = used_pages(a, s);
     const int* src = a.table_in + (size_t)s * a.max_pages;
-    for (int j = first + threadIdx.x; j < min(end, used); j += kPageThreads) {
-      const int p = checked_page(src[j], a.pages, a.status);
+    for (int i = threadIdx.x; i < min(end, used) - first; i += kPageThreads) {
+      const int p = checked_page(src[first + i], a.pages, a.status);
       if (p >= 0) atomicAdd(a.owner + p, 1);
     }
   }

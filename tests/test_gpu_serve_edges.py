@@ -302,3 +302,28 @@ def test_fork_wants_more_pages_than_32_bits_count():
     assert tables[1][0, :pages].tolist() == list(range(pages))
     tables[1][0, :pages] = -1
     assert int(tables[1].max()) == -1 and int(tables[1].min()) == -1
+
+
+@pytest.mark.parametrize("mp", [2 ** 31 - 1, 2 ** 31 - 4])
+def test_tables_that_end_at_the_largest_index(mp):
+    # one slot, pages of one token, a row of 8 GB read one entry or four at a time
+    pages = 9
+    desc = pi.make_cache_desc(1, pages, 1, 8, 1, "f16")
+    tables = [torch.empty((1, mp), dtype=torch.int32, device=DEV) for _ in range(2)]
+    tables[0][0, :3] = i32([8, 2, 5])
+    length, ref, where, pairs = i32([0]), i32([7] * pages), i32([7] * pages), i32([[7, 7]] * pages)
+    counts, st, ws = i32([7] * 4), new_status(), pi.cache_workspace(desc, 1, 0, DEV)
+    pi.check(pi.pi_cache_fork(desc, 1, mp, i32([0]), i32([2]), None, tables[0], i32([3]), tables[1], length,
+                              ref, None, pairs, counts, st, ws))
+    torch.cuda.synchronize()
+    del tables[0]
+    t = tables[0]
+    assert int(st[0]) == 0 and length.tolist() == [5] and counts.tolist() == [0, 5, 7, 7]
+    assert t[0, :5].tolist() == [8, 2, 5, 0, 1] and ref.tolist() == [1, 1, 1, 0, 0, 1, 0, 0, 1]
+    pi.check(pi.pi_cache_compact(desc, 1, mp, None, t, length, t, ref, where, None, pairs, counts, st, ws))
+    torch.cuda.synchronize()
+    assert int(st[0]) == 0 and counts.tolist()[:2] == [2, 5]
+    assert t[0, :5].tolist() == [4, 2, 3, 0, 1] and ref.tolist() == [1, 1, 1, 1, 1, 0, 0, 0, 0]
+    t[0, :5] = -1
+    for part in t[0].split(1 << 28):
+        assert int(part.max()) == -1 and int(part.min()) == -1
