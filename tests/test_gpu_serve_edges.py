@@ -327,3 +327,176 @@ def test_tables_that_end_at_the_largest_index(mp):
     t[0, :5] = -1
     for part in t[0].split(1 << 28):
         assert int(part.max()) == -1 and int(part.min()) == -1
+
+
+# ------------------------------------------------------------------ sums that are split
+def indicate(c):
+    """Values that are 1 in one element and 0 in the others, the element chosen
+    by the token's tile of 16: y is then each class's share of the weights."""
+    for s, n in enumerate(c.lens):
+        t = np.arange(n)
+        v = (t[:, None] // 16 % c.D == np.arange(c.D)[None, :]).astype(np.float64)
+        c.rows[1, s, :n] = v[:, None, :]
+        for j in range(-(-n // c.P)):
+            t0, t1 = j * c.P, min(n, (j + 1) * c.P)
+            blk = torch.from_numpy(v[t0:t1]).to(TD[c.dtype]).to(DEV)
+            c.pool[c.layer, int(c.np_table[s, j]), 1, :, :t1 - t0] = blk[None]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,lens", [
+    ((8, 1, 128, 64), [20011]), ((16, 1, 64, 32), [9000, 0, 3]), ((4, 2, 256, 8), [1, 7003]),
+    ((3, 3, 96, 7), [5000, 4100]), ((12, 1, 128, 24), [2500, 11000, 640]),
+    ((40, 40, 128, 16), [700, 1300, 61]), ((8, 8, 64, 16), [333] * 30), ((6, 2, 40, 16), [1000, 257])])
+def test_attention_loses_and_doubles_no_part(dtype, shape, lens):
+    # All terms are positive, so an element of y has a relative error: the
+    # weights' e = |da| + 2^-20 in numerator and denominator, 2^-22 of the
+    # weights' parts, 2^-19 for the 16 products of a tile, and U for each sum of
+    # tiles, warps and parts that it passes (under 2^10 of them at these sizes:
+    # a warp's tiles, 4 warps, groups, parts).  A tile that is lost or counted
+    # twice moves its element by one over the tiles of its class: a 40th at least.
+    c = Cache(dtype, *shape, lens, qscale=0.05)
+    indicate(c)
+    y, lse = c.run()
+    torch.cuda.synchronize()
+    y, lse = y.double().cpu().numpy(), lse.double().cpu().numpy()
+    G = c.heads // c.kv
+    for s, n in enumerate(lens):
+        for h in range(c.heads):
+            if n == 0:
+                assert (y[s, h] == 0).all()
+                continue
+            q, k = c.q[s, h].astype(np.float64), c.rows[0, s, :n, h // G]
+            a = c.scale * (k @ q)
+            p = np.exp(a - a.max())
+            want = p @ c.rows[1, s, :n, h // G] / p.sum()
+            da = c.scale * (np.abs(k) @ np.abs(q)).max() * (2.0 ** -21 + c.D * U)
+            tol = 2 * (da + 2.0 ** -20 + 2.0 ** -22 + 2.0 ** -19 + 2 ** 10 * U)
+            assert tol < 1 / 1000
+            assert (np.abs(y[s, h] - want) <= tol * want).all(), (s, h)
+            z = a.max() + math.log(p.sum())
+            assert abs(lse[s, h] - z) <= tol + 4 * U * abs(z), (s, h)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab,topk", [(1, 50273, 8), (2, 200001, 32), (7, 50273, 0), (1, 131072, 1),
+                                             (300, 33000, 4), (1700, 9001, 3)])
+def test_scores_lose_and_double_no_part(dtype, rows, vocab, topk):
+    # A sum passes 32 terms of a thread's batch, at most vocab / 4096 batches (128
+    # threads a row, 32 elements a batch), 5 + 8 warp sums and 64 parts: under 256
+    # roundings, so its relative error is e = 2^-20 + 2^8 U.  The entropy's
+    # t / s has terms of one sign but for the largest's, of mean |d| under the
+    # entropy's own size: |d entropy| <= 2 e (1 + log n) + 4 U R.  Every part's
+    # share of either sum is a 64th or more: logits rise and fall slowly over
+    # the row, so that no part is like another.
+    g = np.random.default_rng(vocab)
+    x = g.standard_normal((rows, vocab)) + 2 * np.sin(np.arange(vocab) * (7.0 / vocab))
+    tok = g.integers(0, vocab, rows)
+    xd = torch.from_numpy(x).to(TD[dtype]).to(DEV)
+    x = xd.double().cpu().numpy()
+    lp, ent = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    idx, top = i32(np.zeros((rows, max(1, topk)))), torch.empty((rows, max(1, topk)), device=DEV)
+    st = new_status()
+    pi.check(pi.pi_token_logprobs(xd, dtype, rows, vocab, vocab, i32(tok), topk, lp, ent, idx, top, st,
+                                  pi.logprob_workspace(rows, vocab, topk, DEV)))
+    torch.cuda.synchronize()
+    m = x.max(1, keepdims=True)
+    z = m + np.log(np.exp(x - m).sum(1, keepdims=True))
+    p = np.exp(x - z)
+    want_ent, want_lp = -(p * (x - z)).sum(1), x[np.arange(rows), tok] - z[:, 0]
+    e, R = 2.0 ** -20 + 2.0 ** 8 * U, float(x.max() - x.min())
+    got_ent, got_lp = ent.double().cpu().numpy(), lp.double().cpu().numpy()
+    assert (np.abs(got_ent - want_ent) <= 2 * e * (1 + math.log(vocab)) + 4 * U * R).all()
+    assert (np.abs(got_lp - want_lp) <= 2 * e + 4 * U * (np.abs(want_lp) + R)).all()
+    assert int(st[0]) == 0
+
+
+# ------------------------------------------------------------------ scales, workspaces, threads
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.125, -3.0, 1e-30])
+def test_attention_scales(dtype, scale):
+    c = Cache(dtype, 8, 2, 64, 16, [0, 1, 40, 300, 1000])
+    c.scale = scale
+    y, lse = c.run()
+    torch.cuda.synchronize()
+    y, lse = y.double().cpu().numpy(), lse.double().cpu().numpy()
+    for s, n in enumerate(c.lens):
+        for h in range(c.heads if n else 0):
+            q, k = c.q[s, h].astype(np.float64), c.rows[0, s, :n, h // 4]
+            a = scale * (k @ q)
+            p = np.exp(a - a.max())
+            want, z = p @ c.rows[1, s, :n, h // 4] / p.sum(), a.max() + math.log(p.sum())
+            e = abs(scale) * (np.abs(k) @ np.abs(q)).max() * (2.0 ** -21 + c.D * U) + 2.0 ** -20 + n * U
+            assert (np.abs(y[s, h] - want) <= 3 * e * np.abs(c.rows[1, s, :n]).max()).all()
+            assert abs(lse[s, h] - z) <= 2 * e + 4 * U * abs(z)
+
+
+def test_one_workspace_serves_caches_of_several_shapes():
+    # attention joined across blocks, forks and compactions of other pools in
+    # between, on one workspace: each call's results are those on its own
+    a = Cache("f16", 8, 1, 128, 16, [9000, 70])
+    b = Cache("bf16", 12, 3, 256, 8, [3000, 0, 17], seed=2)
+    small, large = (9, 4, 7, 40), (600, 16, 90, 70_001)
+    sizes = [pi.pi_cache_workspace_size(c.desc, len(c.lens), c.heads) for c in (a, b)]
+    for S, P, mp, pages in (small, large):
+        sizes.append(pi.pi_cache_workspace_size(pi.make_cache_desc(1, pages, 1, 8, P, "f16"), S, 0))
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device=DEV)
+    want = [c.run() for c in (a, b)]
+    a.ws = b.ws = ws
+
+    def pages_calls(S, P, mp, pages):
+        desc = pi.make_cache_desc(1, pages, 1, 8, P, "f16")
+        table, length, st = i32(np.full((S, mp), -1)), i32([0] * S), new_status()
+        t2, l2, ref, where = i32(np.full((S, mp), -1)), i32([0] * S), i32([0] * pages), i32([0] * pages)
+        pairs, counts = i32(np.zeros((pages, 2))), i32([0] * 4)
+        need = P * (pages // (2 * S))
+        pi.check(pi.pi_cache_fork(desc, S, mp, i32([-1] * S), i32([need] * S), None, table, length, t2, l2,
+                                  ref, None, pairs, counts, st, ws))
+        assert l2.tolist() == [need] * S and int(counts[1]) == S * (need // P) and int(st[0]) == 0
+        pi.check(pi.pi_cache_compact(desc, S, mp, None, t2, l2, t2, ref, where, None, pairs, counts, st, ws))
+        assert int(counts[1]) == S * (need // P) and int(st[0]) == 0
+
+    for _ in range(2):
+        for c, (y, lse) in zip((a, b), want):
+            y1, l1 = c.run()
+            assert torch.equal(y, y1) and torch.equal(lse, l1)
+            pages_calls(*small)
+            y1, l1 = c.run()
+            assert torch.equal(y, y1) and torch.equal(lse, l1)
+            pages_calls(*large)
+
+
+def test_two_threads_on_two_streams():
+    # each with its own workspace; what one call looks up once is shared
+    import threading
+    torch.cuda.synchronize()
+    work, failed = [], []
+    for i in range(2):
+        c = Cache(("f16", "bf16")[i], 8, 2, (128, 96)[i], 16, [3000, 1, 200], seed=i)
+        x = torch.randn((5, 30011), device=DEV)
+        work.append((c, x, torch.cuda.Stream(), c.run()))
+    torch.cuda.synchronize()
+
+    def go(c, x, stream, want):
+        try:
+            with torch.cuda.stream(stream):
+                ent, top = torch.empty(5, device=DEV), torch.empty((5, 3), device=DEV)
+                idx = torch.empty((5, 3), dtype=torch.int32, device=DEV)
+                st, ws = new_status(), pi.logprob_workspace(5, 30011, 3, DEV)
+                best = torch.topk(x, 3).indices.int()
+                for _ in range(20):
+                    y, lse = c.run()
+                    pi.check(pi.pi_token_logprobs(x, "f32", 5, 30011, 30011, None, 3, None, ent, idx, top,
+                                                  st, ws))
+                    stream.synchronize()
+                    assert torch.equal(y, want[0]) and torch.equal(lse, want[1])
+                    assert torch.equal(idx, best) and int(st[0]) == 0
+        except Exception as e:  # reported by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=go, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
