@@ -885,7 +885,12 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
 
     if (mask) {
       // scores of 16 tokens
-      float sc[2][2][4];  // even and odd steps: shorter chains
+      // [0], [1]: even and odd steps, shorter chains (bf16 of 64 dims has no
+      // registers for both); [2]: bf16's third part, whose small sums would be cut
+      // beside the large ones (errors of y 0.4e-6 to 0.5e-6, in one sum 0.7e-6 to
+      // 1.2e-6)
+      constexpr int kChains = DT == 1 && DP == 64 ? 1 : 2;
+      float sc[2][3][4];
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), pc = (lane >> 3) & 1;
         const uint32_t at = k0 + row_at(r) + ((pc ^ (r & 7)) << 4);
@@ -895,14 +900,17 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
           ldsm4(b, (at ^ ((ks & 3) << 5)) + (ks >> 2) * kPanel);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              float(&c)[4] = sc[nt][ks & 1];
-              if (ks < 2)
+              float(&c)[4] = sc[nt][ks % kChains];
+              if (ks < kChains)
                 mma0<DT>(c, qf[ks], b[2 * nt], b[2 * nt + 1]);
               else
                 mma<DT>(c, qf[ks], b[2 * nt], b[2 * nt + 1]);
               if (DT == 1) {
                 const uint32_t q2[4] = {qf2[ks][0], qf2[ks][0], qf2[ks][1], qf2[ks][1]};
-                mma<DT>(c, q2, b[2 * nt], b[2 * nt + 1]);
+                if (ks == 0)
+                  mma0<DT>(sc[nt][2], q2, b[2 * nt], b[2 * nt + 1]);
+                else
+                  mma<DT>(sc[nt][2], q2, b[2 * nt], b[2 * nt + 1]);
               }
             }
         }
@@ -912,8 +920,10 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
       float s[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float(&c)[2][4] = sc[e >> 1];
-        s[e] = (c[0][e & 1] + c[1][e & 1]) + (c[0][2 + (e & 1)] + c[1][2 + (e & 1)]);
+        const float(&c)[3][4] = sc[e >> 1];
+        constexpr int k2 = kChains == 2 ? 1 : 2;
+        s[e] = (c[0][e & 1] + c[k2][e & 1]) + (c[0][2 + (e & 1)] + c[k2][2 + (e & 1)]);
+        if (DT == 1 && kChains == 2) s[e] += c[2][e & 1] + c[2][2 + (e & 1)];
       }
       const uint32_t mine = mask >> (2 * (lane & 3));  // rows of s: bits 0, 1, 8, 9
       float w[4];
