@@ -111,6 +111,13 @@ __host__ __device__ constexpr int att_smem() {
   return kAttWarps * att_stages<DT, DP>() * 16 * DP * 4 + kAttWarps * 8 * DP * 4;
 }
 
+// Where warp w leaves its first (k = 0) and its last part: the latter in its ring.
+template <int DT, int DP>
+__device__ __forceinline__ float* piece_data(unsigned char* smem, int w, int k) {
+  constexpr int kRing = att_stages<DT, DP>() * 16 * DP * 4;
+  return reinterpret_cast<float*>(smem + (k ? w * kRing : kAttWarps * kRing + w * 8 * DP * 4));
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
@@ -414,6 +421,7 @@ struct Unit {  // (slot, kv head, head tile)
   __device__ bool finite_key(int t, const uint16_t* key) const {
     bool ok = !is_new(t);  // a new one is not looked at: its score is computed
     constexpr uint32_t kTop = DT == 0 ? 0x7c00u : 0x7f80u;
+#pragma unroll 1
     for (int e = 0; e < a.head_dim && ok; e += 8) {
       const uint4 k = __ldg(reinterpret_cast<const uint4*>(key + e));
       for (uint32_t w : {k.x, k.y, k.z, k.w}) ok = ok && (w & kTop) != kTop && (w >> 16 & kTop) != kTop;
@@ -422,6 +430,7 @@ struct Unit {  // (slot, kv head, head tile)
   }
   __device__ float score(int h, int t, const uint16_t* key) const {
     float s = 0.f;
+#pragma unroll 1
     for (int e = 0; e < a.head_dim; ++e)
       s = fmaf(__ldg(q + h * a.head_dim + e), element(false, t, key, e), s);
     return s * a.scale;
@@ -429,52 +438,71 @@ struct Unit {  // (slot, kv head, head tile)
 };
 
 // A part: the tiles [i0, i1) of a unit; head h's element d is at
-// to[h stride + d], or swizzled as the warps' parts are.
+// to[h stride + d], or swizzled as the warps' parts are.  l: the heads' sums of
+// weights (NaN where a score is NaN or +infinity); null: found from the keys.
 template <int DT>
 __device__ __forceinline__ void part_infinities(const Unit<DT>& u, int i0, int i1, float* to, int stride,
-                                                bool swizzled) {
+                                                bool swizzled, const float* l) {
   const int lane = threadIdx.x & 31, D = u.a.head_dim;
   auto at = [&](int h, int d) { return to + h * stride + (swizzled ? ((d >> 3 ^ h) << 3) + (d & 7) : d); };
+  auto each_token = [&](auto f) {  // the lanes' tokens: half a warp per tile
+#pragma unroll 1
+    for (int i = i0 + (lane >> 4); i < i1; i += 2) {
+      int r0, r1;
+      const int t = u.rows_of(i, r0, r1) + (lane & 15);
+      if ((lane & 15) < r0 || (lane & 15) >= r1) continue;
+      if (const uint16_t* key = u.key_of(t)) f(t, key);
+    }
+    __syncwarp();
+  };
   uint32_t odd_q = 0, closed = 0;  // heads, as bits: with a query that is not finite; that stay
-  for (int h = 0; h < u.rows; ++h)
+#pragma unroll 1
+  for (int h = 0; h < u.rows; ++h) {
+#pragma unroll 1
     for (int e = lane; e < D; e += 32)
       if (!(fabsf(__ldg(u.q + h * D + e)) < INFINITY)) odd_q |= 1u << h;
-  odd_q = __reduce_or_sync(~0u, odd_q);
-  for (int i = i0 + (lane >> 4); i < i1; i += 2) {  // half a warp per tile
-    int r0, r1;
-    const int t = u.rows_of(i, r0, r1) + (lane & 15);
-    if ((lane & 15) < r0 || (lane & 15) >= r1) continue;
-    const uint16_t* key = u.key_of(t);
-    if (!key) continue;
-    const uint32_t look = u.finite_key(t, key) ? odd_q : ~0u;
-    for (int h = 0; h < u.rows; ++h)
-      if (look >> h & 1u && !(u.score(h, t, key) < INFINITY)) closed |= 1u << h;
+    if (l && l[h] != l[h]) closed |= 1u << h;
   }
-  closed = __reduce_or_sync(~0u, closed);
-  for (int d = lane; d < D; d += 32) {
-    uint32_t open = 0, pos = 0, neg = 0, nan = 0;
-    for (int h = 0; h < u.rows; ++h)
-      if (*at(h, d) != *at(h, d)) open |= 1u << h;
-    open &= ~closed;
-    for (int i = open ? i0 : i1; i < i1; ++i) {
-      int r0, r1;
-      const int t0 = u.rows_of(i, r0, r1);
-      for (int t = t0 + r0; t < t0 + r1; ++t) {
-        const uint16_t* key = u.key_of(t);
-        if (!key) continue;
+  odd_q = __reduce_or_sync(~0u, odd_q);
+  // heads of `of` whose score of the token may not be finite
+  auto doubtful = [&](int t, const uint16_t* key, uint32_t of) {
+    return of & (u.finite_key(t, key) ? odd_q : ~0u);
+  };
+  if (!l) {
+    each_token([&](int t, const uint16_t* key) {
+      const uint32_t look = doubtful(t, key, ~closed);
+#pragma unroll 1
+      for (int h = 0; h < u.rows; ++h)
+        if (look >> h & 1u && !(u.score(h, t, key) < INFINITY)) closed |= 1u << h;
+    });
+    closed = __reduce_or_sync(~0u, closed);
+  }
+  for (int d0 = 0; d0 < D; d0 += 32) {
+    uint32_t nans = 0;  // of column d0 + lane
+#pragma unroll 1
+    for (int h = 0; h < u.rows && d0 + lane < D; ++h)
+      if (*at(h, d0 + lane) != *at(h, d0 + lane)) nans |= 1u << h;
+    nans &= ~closed;
+    for (uint32_t columns = __ballot_sync(~0u, nans != 0); columns; columns &= columns - 1) {
+      const int from = __ffs(columns) - 1, d = d0 + from;
+      const uint32_t open = __shfl_sync(~0u, nans, from);
+      uint32_t pos = 0, neg = 0, nan = 0;
+      each_token([&](int t, const uint16_t* key) {
         const float x = u.element(true, t, key, d);
-        if (fabsf(x) < INFINITY) continue;
+        if (fabsf(x) < INFINITY) return;
         uint32_t none = 0;  // heads whose score is -infinity: 0 x infinity
-        const uint32_t look = open & (u.finite_key(t, key) ? odd_q : ~0u);
+        const uint32_t look = doubtful(t, key, open);
+#pragma unroll 1
         for (int h = 0; h < u.rows; ++h)
           if (look >> h & 1u && u.score(h, t, key) == -INFINITY) none |= 1u << h;
         nan |= x != x ? open : none;
         (x > 0.f ? pos : neg) |= open & ~none;
-      }
+      });
+      pos = __reduce_or_sync(~0u, pos);
+      neg = __reduce_or_sync(~0u, neg);
+      nan = __reduce_or_sync(~0u, nan) | (pos & neg);
+      if ((open & ~nan & (pos | neg)) >> lane & 1u) *at(lane, d) = pos >> lane & 1u ? INFINITY : -INFINITY;
     }
-    nan |= pos & neg;
-    for (int h = 0; h < u.rows; ++h)
-      if ((open & ~nan & (pos | neg)) >> h & 1u) *at(h, d) = pos >> h & 1u ? INFINITY : -INFINITY;
   }
 }
 
@@ -483,12 +511,11 @@ struct Start {
   long long pos;
   int slot, unit, tile, odd;
 };
-// Goes through a warp's share: the pieces are its parts of units shared with
-// other warps, that which came in and that which goes on.
-template <int DT>
-__device__ __noinline__ void infinite_values(const AttendArgs& a, const Start& from, long long share0,
-                                             long long share1, int even, float* piece0, float* piece1,
-                                             int stride) {
+// Goes through a warp's share.  l: [2][8], of its parts of units shared with
+// other warps.
+template <int DT, int DP>
+__device__ __forceinline__ void infinite_values(const AttendArgs& a, const Start& from, long long share0,
+                                             long long share1, int even, unsigned char* smem, const float* l) {
   const int g = from.unit / a.tiles, D = a.head_dim;
   Cursor c{from.pos, from.slot, g, from.unit - g * a.tiles, from.tile, seen_of(a, from.slot)};
   for (; c.pos < share1; c.advance(a, even)) {
@@ -496,8 +523,8 @@ __device__ __noinline__ void infinite_values(const AttendArgs& a, const Start& f
     const bool begins = c.pos - c.tile >= share0, whole = begins && n == left;
     part_infinities(Unit<DT>(a, c.slot, c.g, c.ht), c.tile, c.tile + n,
                     whole ? a.y + ((size_t)c.slot * a.heads + c.g * a.group + c.ht * 8) * D
-                          : begins ? piece1 : piece0,
-                    whole ? D : stride, !whole);
+                          : piece_data<DT, DP>(smem, threadIdx.x >> 5, begins),
+                    whole ? D : DP, !whole, whole ? nullptr : l + 8 * begins);
     c.tile += n - 1;
     c.pos += n - 1;
   }
@@ -544,11 +571,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = a.head_dim, P = a.page_tokens;
   const int units = a.kv_heads * a.tiles;
-  // where a warp leaves its first and its last part
-  auto piece_data = [&](int w, int k) -> float* {
-    if (k) return reinterpret_cast<float*>(smem + w * S * 2 * kTile);
-    return reinterpret_cast<float*>(smem + kAttWarps * S * 2 * kTile) + w * 8 * DP;
-  };
+  auto piece_data = [&](int w, int k) { return pis::piece_data<DT, DP>(smem, w, k); };
   if (lane < 2) s_piece[warp][lane].at = -1;
   if (lane < S) mbar_init(&s_bar[warp][lane], 1);
   fence_mbar_init();
@@ -1033,7 +1056,7 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
   // Infinite values: once more through the share's parts.
   __syncwarp();
   if (s_both.start[warp].odd && !late)
-    infinite_values<DT>(a, s_both.start[warp], share0, share1, s_even, piece_data(warp, 0), piece_data(warp, 1), DP);
+    infinite_values<DT, DP>(a, s_both.start[warp], share0, share1, s_even, smem, s_l[warp][0]);
 
   // Units shared by warps.  A unit's warps within the block: the one that
   // begins it (piece 1) or the block's first (piece 0), then the followers'
