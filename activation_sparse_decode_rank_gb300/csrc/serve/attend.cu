@@ -51,10 +51,10 @@ namespace pis {
 // 64, 128 or 256 are padded with zeros in shared memory only.
 //
 // Measured, bytes of the rows seen against a copy's 6.8 TB/s.  32 slots x 40
-// heads of 128, lengths to 2048, fp16: 108 us, 91 %.  8 slots, 64/8 heads of
-// 128, lengths to 131072, bf16: 300 us, 97 %.  24 slots, 32/8 heads of 128, a
-// window of 1000: 28 us, 49 %, of which 5 to the first tile and 5 in joins.
-// One slot, 16 heads of 64, 200 tokens: 8 us, all latency; an empty launch in
+// heads of 128, lengths to 2048, fp16: 109 us, 91 %.  8 slots, 64/8 heads of
+// 128, lengths to 131072, bf16: 302 us, 97 %.  24 slots, 32/8 heads of 128, a
+// window of 1000: 28.4 us, 49 %, of which 5 to the first tile and 5 in joins.
+// One slot, 16 heads of 64, 200 tokens: 8.3 us, all latency; an empty launch in
 // its place takes 0.8, one that ends after finding its share 3.
 struct AttendArgs {
   const float *q, *k_new, *v_new;
@@ -81,23 +81,25 @@ constexpr int kMinTiles = 4;  // a warp's least share, in tiles
 // takes the time of some eight tiles of a warp.
 constexpr int kApartTiles = 48;
 // Units of at most this length, and no more of them than warps, have a warp
-// each: nothing is joined at all.  22 slots x 32 heads of 96, 64 tokens: 10.0
-// us, split like longer ones 12.3; 64 slots x 8 kv heads of 128, 60 tokens:
-// 11.1 and 14.6.  At 128 tokens the split is ahead, 12.1 to 13.7.
+// each: nothing is joined at all.  22 slots x 32 heads of 96, 64 tokens: fp16
+// 9.8 us, split like longer ones 12.4, bf16 10.4 and 12.9; 64 slots x 8 kv heads
+// of 128, 60 tokens: 10.1 and 14.2, 11.2 and 15.1.  At 128 tokens the split is
+// ahead by a tenth.
 constexpr int kWholeTiles = 6;
 
 // Most blocks of a unit whose parts one block joins directly.  More join in two
 // steps, groups of about sqrt(n) blocks and then the groups.  One slot, 32/8
-// heads of 64, 16384 tokens, bf16: 19.2 us, in one step 33.9; 64/8 heads of
-// 128, 8192 tokens, fp16: 18.5 and 26.0.  8 to 16 here measure the same.
+// heads of 64, 16384 tokens, bf16: 22.1 us, in one step 43.0; 64/8 heads of
+// 128, 8192 tokens, fp16: 21.1 and 31.6.  8 to 16 here measure the same.
 constexpr int kFlatJoin = 10;
 
 // Thread blocks per SM, and stages of a warp's ring, by measurement.  More
 // warps hide a tile's chain of instructions, more stages its loads; bf16 tiles
 // take half as many instructions again.  32 slots to 4096 tokens, 32 heads of
-// 64: fp16 3 x 3 87 us (2 x 6 116), bf16 4 x 2 96 us (3 x 3 102, 2 x 6 128).
-// 32 slots to 2048, 40 heads of 128: fp16 2 x 2 107 us (2 x 3 114), bf16 2 x 3
-// 109 us (2 x 2 113).
+// 64: fp16 3 x 3 89.5 us (2 x 6 120), bf16 4 x 2 98 us (3 x 3 102, 2 x 6 130).
+// 32 slots to 2048, 40 heads of 128: fp16 2 x 2 109 us (2 x 3 115.5), bf16 2 x 3
+// 109.5 us (2 x 2 111).  bf16 of 256 dims spills 270 to 340 bytes at 255
+// registers, of 64 dims 30 to 60 at 128.
 template <int DT, int DP>
 __host__ __device__ constexpr int att_blocks() {
   return DP == 64 ? 3 + DT : 2;
@@ -386,7 +388,9 @@ __device__ __forceinline__ float part_weight(float below) { return fmaxf(ex2(bel
 // Infinite values.  One meets weights' parts that are 0 or negative, and NaN is
 // left of its column's sum.  Where that happened in a warp's share, a pass of
 // its own over the share tells +-infinity from NaN: the loop over the tiles
-// stays free of tests.  Heads whose scores hold NaN or +infinity stay NaN.
+// stays free of tests.  Heads whose scores hold NaN or +infinity stay NaN.  One
+// infinite channel in every value of a layer: 346 us for 32 slots x 40 heads
+// of 128 where finite ones take 109, 850 us for 8 slots to 131072 tokens (302).
 template <int DT>
 struct Unit {  // (slot, kv head, head tile)
   const AttendArgs& a;
@@ -1266,8 +1270,9 @@ __global__ void __launch_bounds__(kAttThreads, att_blocks<DT, DP>())
 // (token, K or V, kv head, piece): all its reads are under way before the
 // first store.  Bound: HBM bandwidth (fp32 rows in, 16-bit rows out).  N = 4
 // for prompts (12001 tokens of 32 heads of 128: 97 us, 90 % of the measured
-// copy rate; N = 1: 104.7), 1 where N = 4 would leave SMs without a block (32
-// tokens of 40 heads: 2.4 us against 3.2).
+// copy rate; N = 1: 104.7; 8 bytes spill at 64 registers), 1 where N = 4 would
+// leave SMs without a block (32 tokens of 40 heads, in a graph: 1.7 us against
+// 3.1).
 
 struct AppendArgs {
   const float *k, *v;
@@ -1401,9 +1406,9 @@ pi_status launch_attend(const AttendArgs& a, const CUtensorMap& map, pi_stream s
 
 // Shared memory holds whole panels of 64 elements; the products stop at the
 // next of 80, 96 and 192, which is most of a tile's time where it is
-// instructions.  32 heads, 16 slots to 4096 tokens: heads of 80 64 us in fp16
-// and 73 in bf16 (as 128: 70, 87), of 96 67 and 76 (70, 87); 16 heads of 192
-// 67 and 75 (as 256: 71, 88).
+// instructions.  32 heads, 16 slots to 4096 tokens: heads of 80 67 us in fp16
+// and 74 in bf16 (as 128: 75, 84), of 96 70 and 77 (75, 84); 16 heads of 192
+// 69 and 77 (as 256: 73, 92).
 template <int DT>
 pi_status launch_dims(const AttendArgs& a, const CUtensorMap& map, pi_stream stream) {
   if (a.head_dim <= 64) return launch_attend<DT, 64>(a, map, stream);

@@ -20,14 +20,16 @@
 // of broadcast reads instead of a chain of exchanges (128 keys at most).
 //
 // Bound: HBM bandwidth (each logit read once); for 16-bit logits the pass
-// issues some 5 instructions per logit, not far from the machine's rate at
-// that bandwidth, hence the packed forms (two FP32 operations per
-// instruction).  Few rows: a row is split over several blocks, and the last
+// issues 9 instructions per logit, selection and start included (two thirds of
+// the issue slots at that bandwidth), hence the packed forms (two FP32
+// operations per instruction).  Few rows: a row is split over several blocks, and the last
 // of them to arrive joins the parts.
 //
-// Measured: 4096 x 128256 bf16 with 20 alternatives 184 us, 84 % of a copy's
-// 6.8 TB/s (some 20 of it the selection); 7 x 50273 fp32 with 8 alternatives
-// 8.5 us, a chain of reads, selection and join.
+// Measured: 4096 x 128256 bf16 with 20 alternatives 182 to 185 us, 84 % of a
+// copy's 6.8 TB/s (some 20 of it the selection); 7 x 50273 fp32 with 8
+// alternatives 8.3 us, a chain of reads, selection and join.  Rows with ties or
+// so few finite logits that the part is read again: 4096 x 32000 fp16 with three
+// allowed tokens 245 us (60 where all, 1 in 100 or 1 in 1000 are allowed).
 #include "serve.cuh"
 
 namespace pis {
@@ -50,7 +52,7 @@ struct ScoreArgs {
 // Threads of a block.  256 for rows that are few beside the SMs.  From
 // kManyRows rows per SM on 128 with twice the blocks: while one block selects
 // its alternatives, seven others read (4096 x 128256 bf16, 20 alternatives:
-// 185 us against 192; x 32000 fp16: 57 against 69; but 600 rows of 128256, one
+// 182 us against 189; x 32000 fp16: 60 against 73; but 600 rows of 128256, one
 // wave of 256-thread blocks, 36 against 32).
 constexpr int kManyRows = 10;
 constexpr int kScoreThreads = 1024;    // resident threads per SM
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(T, kScoreThreads / T) score_kernel(const Score
   const int v1 = (int)((long long)(part + 1) * nvec / a.parts);
   // whole vectors [w0, w1); the elements of the row's first and last, where cut,
   // go to lanes of the warps 0 and 1, which read them before all else (6294 rows
-  // of 23150, fp16: 66 us; read by one thread each at the end 80)
+  // of 23150, fp16, one alternative: 66 us; read by one thread each at the end 80)
   const bool cut_first = v0 == 0 && shift;
   const int w0 = cut_first ? 1 : v0;
   const bool cut_last = v1 == nvec && (a.vocab + shift) % VN && nvec - 1 >= w0;

@@ -183,8 +183,9 @@ pi_status pi_cache_copy(const pi_cache_desc* cache, const int32_t* pairs, const 
 size_t pi_logprob_workspace_size(int32_t rows, int32_t vocab, int32_t topk);
 
 /* Scores tokens from logits x [rows] of `vocab` values, row r at
- * logits + r stride (elements; stride >= vocab, no alignment needed beyond
- * the buffer's), dtype PI_F16, PI_BF16 or PI_F32.  With z = log sum exp(x):
+ * logits + r stride (elements; stride >= vocab; rows may begin anywhere, the
+ * pointers passed are 16-byte aligned like all: a shifted view such as
+ * tokens[1:] is copied first), dtype PI_F16, PI_BF16 or PI_F32.  With z = log sum exp(x):
  *     logprob[r] = x[tokens[r]] - z      (0 where tokens[r] = -1)
  *     entropy[r] = z - sum_i p_i x_i,  p_i = exp(x_i - z)  (p_i = 0: nothing)
  *     top_idx[r][j], top_logprob[r][j]: the topk largest logits in descending
