@@ -272,8 +272,8 @@ __device__ __forceinline__ float at_least(float x, float least, float s) {
 // Two elements of q as parts: hi + lo (fp16, q scaled), hi + lo + 2 half (bf16).
 // The parts of an element have its sign and are not 0 unless it is, so that
 // an infinite key's product is infinite and of one sign in all of them: that
-// moves q by less than 2^-37 of its head's largest element (fp16), 2^-28 of
-// the element (bf16).
+// moves q by less than 2^-36 of its head's largest element (fp16), 2^-28 of
+// the element (bf16; below 2^-96 its parts may still be 0).
 template <int DT>
 __device__ __forceinline__ void split_q(float x, float y, uint32_t& hi, uint32_t& lo, uint32_t& half) {
   if (DT == 0) {

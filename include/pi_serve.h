@@ -71,8 +71,9 @@ size_t pi_cache_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_
  * lse = -infinity.  Rows of a page that are not visible are not used whatever
  * they hold (NaN and infinities too).  Infinite operands of visible rows count
  * as the formulas say: an infinite key's score is +-infinity (NaN where
- * products of both signs or 0 x infinity meet), and a score of -infinity
- * weighs nothing; a score of NaN or +infinity makes the head's y and lse NaN.
+ * products of both signs or 0 x infinity meet; beside it, elements of q below
+ * 2^-96 may count as 0 in PI_BF16), and a score of -infinity weighs nothing; a
+ * score of NaN or +infinity makes the head's y and lse NaN.
  * An infinite value makes its element of y infinite, however small the weight
  * (NaN where both signs meet, or where a value that is not finite has the
  * weight 0 of a score of -infinity).
