@@ -36,13 +36,14 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
 
 # Translation units: the FFN library and the serving operators (csrc/serve),
 # compiled side by side and linked into one libpi.so.
-_UNITS = ["pi_abi.cu", "serve/attend.cu", "serve/pages.cu", "serve/logprob.cu"]
+_UNITS = ["pi_abi.cu", "serve/attend.cu", "serve/pages.cu", "serve/logprob.cu",
+          "serve/tree.cu", "serve/sample.cu"]
 
 
 def _sources():
     srcs = [os.path.join(d, f) for d in (_CSRC, os.path.join(_CSRC, "serve"))
             for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))]
-    return srcs + [os.path.join(_INCLUDE, "pi.h"), os.path.join(_INCLUDE, "pi_serve.h")]
+    return srcs + [os.path.join(_INCLUDE, h) for h in ("pi.h", "pi_serve.h", "pi_draft.h")]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -143,7 +144,7 @@ SIGNATURES = {
     "pi_shard_layer": (ctypes.c_int, [_DESC, _W, _I32, _I32, _W, _P]),
     "pi_shard_reduce": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _P]),
 }
-# ... and of include/pi_serve.h, bound in serve.py.
+# ... and of include/pi_serve.h and include/pi_draft.h, bound in serve.py.
 SIGNATURES.update(serve.SIGNATURES)
 
 
@@ -385,7 +386,8 @@ def pi_shard_reduce(parts, G, batch, d, residual, y, stream=None) -> int:
 
 
 from .serve import (  # noqa: E402
-    PI_CACHE_MAX_SLOTS, PI_F32, PI_TOPK_MAX, cache_workspace, logprob_workspace, make_cache_desc,
-    pi_cache_append, pi_cache_compact, pi_cache_copy, pi_cache_desc, pi_cache_fork,
-    pi_cache_workspace_size, pi_logprob_workspace_size, pi_paged_attention,
-    pi_selftest_attention_timeout, pi_token_logprobs)
+    PI_CACHE_MAX_SLOTS, PI_F32, PI_TOPK_MAX, PI_TREE_MAX, cache_workspace, logprob_workspace,
+    make_cache_desc, pi_cache_append, pi_cache_compact, pi_cache_copy, pi_cache_desc, pi_cache_fork,
+    pi_cache_workspace_size, pi_logprob_workspace_size, pi_paged_attention, pi_sample_workspace_size,
+    pi_selftest_attention_timeout, pi_token_logprobs, pi_token_sample, pi_tree_accept,
+    pi_tree_attention, pi_tree_workspace_size, sample_workspace, tree_workspace)

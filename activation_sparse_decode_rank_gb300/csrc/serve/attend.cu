@@ -1,9 +1,5 @@
 // attend.cu — attention of one new token per slot over a paged cache, and
 // the stores of new keys and values (include/pi_serve.h).
-#include <cuda.h>
-
-#include <cstdlib>
-
 #include "serve.cuh"
 
 namespace pis {
@@ -120,51 +116,6 @@ __device__ __forceinline__ float* piece_data(unsigned char* smem, int w, int k) 
   return reinterpret_cast<float*>(smem + (k ? w * kRing : kAttWarps * kRing + w * 8 * DP * 4));
 }
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-// mbarriers (one arrival each: the lane that orders a tile) and TMA boxes.
-__device__ __forceinline__ void mbar_init(uint64_t* m, unsigned count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(m)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void fence_mbar_init() {
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-// Orders this thread's writes to shared memory before later TMA writes there.
-__device__ __forceinline__ void fence_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint64_t* m, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint64_t* m, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(m)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Waits for the phase of that parity, for limit_ns at most; the warp agrees.
-__device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, unsigned long long limit_ns) {
-  bool ok = mbar_try(m, parity);
-  if (!__all_sync(~0u, ok)) {
-    const unsigned long long t0 = now_ns();
-    while (!__all_sync(~0u, ok = ok || mbar_try(m, parity)))
-      if (__any_sync(~0u, now_ns() - t0 > limit_ns)) return false;
-  }
-  return true;
-}
 // K and V of a panel of 64 elements, from column x, of the rows from y of the
 // pool's rows -> shared memory.
 __device__ __forceinline__ void tma_panel(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
@@ -237,12 +188,6 @@ __device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // Two values as packed 16-bit parts: hi + lo (fp16), hi + lo + lo2 (bf16).
 template <int DT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
@@ -363,8 +308,6 @@ struct Line {
   }
 };
 
-constexpr float kLn2 = 0.6931471805599453f;
-
 __device__ __forceinline__ void add_scaled(float4& sum, const float4& x, float f) {
   sum.x = fmaf(x.x, f, sum.x);
   sum.y = fmaf(x.y, f, sum.y);
@@ -380,10 +323,6 @@ __device__ __forceinline__ void finish(const AttendArgs& a, size_t row, int d, c
       make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
   if (d == 0 && a.lse) a.lse[row] = (top + log2f(lsum)) * kLn2;
 }
-
-// Weight of a part beside the larger maximum: not 0, so that an infinite sum
-// stays what it is (2^-126 of a finite one changes nothing).
-__device__ __forceinline__ float part_weight(float below) { return fmaxf(ex2(below), 0x1p-126f); }
 
 // Infinite values.  One meets weights' parts that are 0 or negative, and NaN is
 // left of its column's sum.  Where that happened in a warp's share, a pass of
@@ -1340,19 +1279,9 @@ __global__ void __launch_bounds__(256, 4) append_kernel(const AppendArgs a) {
 // lane's request takes some 100 cycles to issue).  Others: {row, rows, K / V},
 // a box per panel, zeros past the row's end.  False where the driver offers no
 // such map.
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 static bool make_rows_map(CUtensorMap* m, void* base, long long rows, const pi_cache_desc& C,
                           int panels, int box_rows) {
-  static const EncodeFn encode = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    const cudaError_t e =
-        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
-  }();
+  const EncodeFn encode = tensor_map_encoder();
   if (!encode) return false;
   const cuuint64_t row = (cuuint64_t)C.head_dim * 2, half = (cuuint64_t)C.kv_heads * C.page_tokens;
   const bool whole = C.head_dim % 64 == 0;
@@ -1364,16 +1293,6 @@ static bool make_rows_map(CUtensorMap* m, void* base, long long rows, const pi_c
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, whole ? 4 : 3, base, dims, strides, box, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Limit of a wait: 1 s, or PI_WAIT_LIMIT_NS as for the FFN kernels.
-static unsigned long long wait_limit() {
-  static const unsigned long long limit = [] {
-    const char* e = std::getenv("PI_WAIT_LIMIT_NS");
-    const unsigned long long v = e ? std::strtoull(e, nullptr, 10) : 0;
-    return v >= 1000ull && v <= 10000000000ull ? v : 1000000000ull;
-  }();
-  return limit;
 }
 
 template <int DT, int DP, int DK, int BR, bool LOSE = false>

@@ -58,7 +58,7 @@ constexpr int kManyRows = 10;
 constexpr int kScoreThreads = 1024;    // resident threads per SM
 constexpr int kScoreParts = 2048;      // most parts of rows in flight
 constexpr int kBatch = 4;              // 16-byte vectors of a thread's batch
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <int DT>
 __device__ __forceinline__ float logit_at(const void* p, long long i) {
@@ -138,11 +138,6 @@ __device__ __forceinline__ float floor_nan(float d) {
 }
 __device__ __forceinline__ float distance(float x, float ref) {
   return huge(ref) ? (x - ref) * kLog2e : fmaf(x, kLog2e, -__fmul_rn(ref, kLog2e));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 // The same sums relative to top >= a.m.
 __device__ __forceinline__ Sums raised(const Sums& a, float top) {

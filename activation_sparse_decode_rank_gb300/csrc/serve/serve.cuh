@@ -1,17 +1,20 @@
-// serve.cuh — what the serving operators (declared in include/pi_serve.h)
-// share: argument checks, workspace layout, launches, small device helpers.
+// serve.cuh — what the serving operators (declared in include/pi_serve.h and
+// include/pi_draft.h) share: argument checks, workspace layout, launches, small
+// device helpers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstdlib>
 #include <mutex>
 #include <unordered_map>
 #include <utility>
 
-#include "../../../include/pi_serve.h"
+#include "../../../include/pi_draft.h"
 
 namespace pis {
 
@@ -106,6 +109,32 @@ inline pi_status ensure_smem(const void* fn, int bytes) {
   return PI_OK;
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// The driver's encoder of tensor maps; null where it has none.
+inline EncodeFn tensor_map_encoder() {
+  static const EncodeFn encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
+  }();
+  return encode;
+}
+
+// Limit of a wait: 1 s, or PI_WAIT_LIMIT_NS as for the FFN kernels.
+inline unsigned long long wait_limit() {
+  static const unsigned long long limit = [] {
+    const char* e = std::getenv("PI_WAIT_LIMIT_NS");
+    const unsigned long long v = e ? std::strtoull(e, nullptr, 10) : 0;
+    return v >= 1000ull && v <= 10000000000ull ? v : 1000000000ull;
+  }();
+  return limit;
+}
+
 constexpr int kAttendGrid = 1024;  // most thread blocks of the attention
 
 // Byte offsets of the regions of a cache workspace.  `arrived` is zero
@@ -175,6 +204,63 @@ template <int DT>
 __device__ __forceinline__ uint32_t pack_bits(float a, float b) {
   return (uint32_t)to_bits<DT>(a) | ((uint32_t)to_bits<DT>(b) << 16);
 }
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+// mbarriers.
+__device__ __forceinline__ void mbar_init(uint64_t* m, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(m)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void fence_mbar_init() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Orders this thread's writes to shared memory before later TMA writes there.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* m, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* m, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(m)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase of that parity, for limit_ns at most; the warp agrees.
+__device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, unsigned long long limit_ns) {
+  bool ok = mbar_try(m, parity);
+  if (!__all_sync(~0u, ok)) {
+    const unsigned long long t0 = now_ns();
+    while (!__all_sync(~0u, ok = ok || mbar_try(m, parity)))
+      if (__any_sync(~0u, now_ns() - t0 > limit_ns)) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Weight of a part beside the larger maximum: not 0, so that an infinite sum
+// stays what it is (2^-126 of a finite one changes nothing).
+__device__ __forceinline__ float part_weight(float below) { return fmaxf(ex2(below), 0x1p-126f); }
 
 // a / b for a >= 0, b > 0: in 32 bits where a allows it.
 __device__ __forceinline__ long long quotient(long long a, int b) {

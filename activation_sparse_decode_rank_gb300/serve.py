@@ -1,4 +1,5 @@
-"""ctypes binding of the serving operators (C ABI in include/pi_serve.h).
+"""ctypes binding of the serving operators (C ABI in include/pi_serve.h and
+include/pi_draft.h).
 
 As in the package's other bindings, each ``pi_*`` function has the name and
 argument order of its C entry point and only marshals arguments; tensors stay
@@ -12,6 +13,7 @@ import ctypes
 PI_F32 = 2
 PI_CACHE_MAX_SLOTS = 1024
 PI_TOPK_MAX = 32
+PI_TREE_MAX = 64
 _DTYPES = {"f16": 0, "bf16": 1, "f32": PI_F32}
 
 
@@ -39,6 +41,15 @@ SIGNATURES = {
     "pi_logprob_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "pi_token_logprobs": (ctypes.c_int, [_P, _I32, _I32, _I32, _I64, _P, _I32, _P, _P, _P, _P, _P,
                                          _P, _SZ, _P]),
+    "pi_tree_workspace_size": (_SZ, [_CACHE, _I32, _I32, _I32]),
+    "pi_tree_attention": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P,
+                                         _P, _P, ctypes.c_float, _I32, _I32, _P, _P, _P, _P, _SZ,
+                                         _P]),
+    "pi_tree_accept": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                      _P, _P, _P]),
+    "pi_sample_workspace_size": (_SZ, [_I32, _I32]),
+    "pi_token_sample": (ctypes.c_int, [_P, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                       _SZ, _P]),
 }
 
 
@@ -105,6 +116,14 @@ def pi_logprob_workspace_size(rows: int, vocab: int, topk: int) -> int:
     return _fn("pi_logprob_workspace_size")(rows, vocab, topk)
 
 
+def pi_tree_workspace_size(cache, slots: int, heads: int, drafts: int) -> int:
+    return _fn("pi_tree_workspace_size")(ctypes.byref(cache), slots, heads, drafts)
+
+
+def pi_sample_workspace_size(rows: int, vocab: int) -> int:
+    return _fn("pi_sample_workspace_size")(rows, vocab)
+
+
 def _zeros(nbytes, where, device):
     import torch
 
@@ -122,6 +141,16 @@ def cache_workspace(cache, slots: int, heads: int = 0, device="cuda"):
 def logprob_workspace(rows: int, vocab: int, topk: int, device="cuda"):
     """A zero-filled workspace of pi_logprob_workspace_size(rows, vocab, topk) bytes."""
     return _zeros(pi_logprob_workspace_size(rows, vocab, topk), "pi_logprob_workspace_size", device)
+
+
+def tree_workspace(cache, slots: int, heads: int, drafts: int, device="cuda"):
+    """A zero-filled workspace of pi_tree_workspace_size(cache, slots, heads, drafts) bytes."""
+    return _zeros(pi_tree_workspace_size(cache, slots, heads, drafts), "pi_tree_workspace_size", device)
+
+
+def sample_workspace(rows: int, vocab: int, device="cuda"):
+    """A zero-filled workspace of pi_sample_workspace_size(rows, vocab) bytes."""
+    return _zeros(pi_sample_workspace_size(rows, vocab), "pi_sample_workspace_size", device)
 
 
 def pi_paged_attention(cache, layer, slots, heads, max_pages, q, k_new, v_new, table, len, pool,
@@ -174,4 +203,30 @@ def pi_token_logprobs(logits, dtype, rows, vocab, stride, tokens, topk, logprob,
     return _fn("pi_token_logprobs")(
         _ptr(logits), _DTYPES.get(dtype, dtype), rows, vocab, stride, _ptr(tokens), topk,
         _ptr(logprob), _ptr(entropy), _ptr(top_idx), _ptr(top_logprob), _ptr(dev_status), _ptr(ws),
+        _ws_bytes(ws, ws_bytes), _stream(stream))
+
+
+def pi_tree_attention(cache, layer, slots, heads, max_pages, drafts, parent, count, q, k_new, v_new,
+                      table, len, pool, scale, window, sinks, y, lse, dev_status, ws, ws_bytes=None,
+                      stream=None) -> int:
+    return _fn("pi_tree_attention")(
+        ctypes.byref(cache), layer, slots, heads, max_pages, drafts, _ptr(parent), _ptr(count),
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(table), _ptr(len), _ptr(pool), scale, window, sinks,
+        _ptr(y), _ptr(lse), _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+
+
+def pi_tree_accept(cache, slots, max_pages, drafts, parent, count, tokens, choice, table, len, pool,
+                   len_out, path, accepted, next, dev_status, stream=None) -> int:
+    return _fn("pi_tree_accept")(
+        ctypes.byref(cache), slots, max_pages, drafts, _ptr(parent), _ptr(count), _ptr(tokens),
+        _ptr(choice), _ptr(table), _ptr(len), _ptr(pool), _ptr(len_out), _ptr(path), _ptr(accepted),
+        _ptr(next), _ptr(dev_status), _stream(stream))
+
+
+def pi_token_sample(logits, dtype, rows, vocab, stride, temperature, top_k, top_p, min_p, u, token,
+                    logprob, dev_status, ws, ws_bytes=None, stream=None) -> int:
+    """dtype: "f16", "bf16", "f32" or the C enum's value."""
+    return _fn("pi_token_sample")(
+        _ptr(logits), _DTYPES.get(dtype, dtype), rows, vocab, stride, _ptr(temperature), _ptr(top_k),
+        _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(logprob), _ptr(dev_status), _ptr(ws),
         _ws_bytes(ws, ws_bytes), _stream(stream))
