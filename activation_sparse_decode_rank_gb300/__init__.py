@@ -37,7 +37,7 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
 # Translation units: the FFN library and the serving operators (csrc/serve),
 # compiled side by side and linked into one libpi.so.
 _UNITS = ["pi_abi.cu", "serve/attend.cu", "serve/pages.cu", "serve/logprob.cu",
-          "serve/tree.cu", "serve/sample.cu"]
+          "serve/tree.cu", "serve/accept.cu", "serve/sample.cu"]
 
 
 def _sources():

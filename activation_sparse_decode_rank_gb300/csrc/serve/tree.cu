@@ -1,5 +1,6 @@
-// tree.cu — attention of drafted tokens over a paged cache, and the drafts
-// that stay in it (include/pi_draft.h).
+// tree.cu — attention of drafted tokens over a paged cache (include/pi_draft.h).
+#include <type_traits>
+
 #include "serve.cuh"
 
 namespace pis {
@@ -28,6 +29,7 @@ __device__ __forceinline__ TreeSlot tree_slot(const TreeArgs& a, int slot) {
   v.count = ok ? c : 0;
   v.base = ok ? n - c : 0;
   v.tail = a.window > 0 ? max(0, v.base + 1 - a.window) : 0;
+  if (a.sinks >= v.tail) v.tail = 0;  // nothing in between
   v.first = min(v.tail, a.sinks);
   return v;
 }
@@ -173,157 +175,1049 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
   }
 }
 
-// One warp per query row, in fp32.
-template <int DT>
-__global__ void __launch_bounds__(128) tree_rows_kernel(const __grid_constant__ TreeArgs a) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31, D = a.head_dim;
-  const long long rows = (long long)a.slots * a.drafts * a.heads;
-  for (long long row = blockIdx.x * 4ll + (threadIdx.x >> 5); row < rows; row += gridDim.x * 4ll) {
-    const int slot = (int)(row / (a.drafts * a.heads)), i = (int)(row / a.heads) % a.drafts, h = (int)(row % a.heads);
-    const int g = h / a.group;
-    const TreeSlot v = tree_slot(a, slot);
-    if (lane == 0 && i == 0 && h == 0 && tree_slot_bad(a, slot)) set_status(a.status, PI_ERR_INDEX);
-    if (i >= v.count) continue;
-    const unsigned long long path = a.parent
-        ? tree_path(a, i, [&](int j) { return __ldg(a.parent + (size_t)slot * a.drafts + j); })
-        : (2ull << i) - 1;
-    if (a.k_new && h % a.group == 0) {
-      const int t = v.base + i, j = t / a.page_tokens;
-      const int page = checked_page(__ldg(a.table + (size_t)slot * a.max_pages + j), a.pages, a.status);
-      const size_t from = (((size_t)slot * a.drafts + i) * a.kv_heads + g) * D;
-      if (page >= 0)
-        for (int e = lane; e < D; e += 32) {
-          uint16_t* to = a.pool + (((size_t)page * 2 * a.kv_heads + g) * a.page_tokens + t - j * a.page_tokens) * D + e;
-          *to = to_bits<DT>(__ldg(a.k_new + from + e));
-          to[(size_t)a.kv_heads * a.page_tokens * D] = to_bits<DT>(__ldg(a.v_new + from + e));
-        }
-    }
-    const float* q = a.q + row * D;
-    RowSums r = {-INFINITY, 0.f, {}};
-    const int lo = a.window > 0 ? v.base + __popcll(path) - a.window : 0;
-    row_add_cached<DT>(a, slot, g, q, 0, v.first, lo, r);
-    row_add_cached<DT>(a, slot, g, q, v.tail, v.base, lo, r);
-    row_add_drafts<DT>(a, slot, v, g, q, tree_seen(a, v.base, path), r);
-    const float inv = r.l > 0.f ? 1.f / r.l : r.l == r.l ? 0.f : r.l;
-    if (8 * lane < D) {
-      float4* to = reinterpret_cast<float4*>(a.y + row * D + 8 * lane);
-      to[0] = make_float4(r.o[0] * inv, r.o[1] * inv, r.o[2] * inv, r.o[3] * inv);
-      to[1] = make_float4(r.o[4] * inv, r.o[5] * inv, r.o[6] * inv, r.o[7] * inv);
-    }
-    if (lane == 0 && a.lse) a.lse[row] = (r.m + log2f(r.l)) * kLn2;
-  }
+// ------------------------------------------------------------------ tensor cores
+//
+// The query rows of a kv head, drafts x heads of its group, are the 128 rows of
+// the fifth-generation tensor cores' tile: S = Q K^T (M = 128 rows, N = tokens),
+// O += P V, both accumulated in tensor memory.
+//
+// A unit is (slot, kv head, MR query rows, up to 128 columns of V).  It goes
+// through tiles of TN tokens: the drafts' own, then those of the cache.  The
+// units' tiles, each unit preceded by kUnitCost positions for its fixed cost,
+// form one line of which every block takes an equal contiguous share; a unit
+// that several blocks share is joined by a second kernel.
+//
+// Precision.  q and the weights p are fp32 and enter as sums of 16-bit parts (two
+// in fp16, with q scaled by a power of two per row and p by 2^14; three in bf16),
+// low parts first.  A tile's O is read back and added to fp32 registers with a
+// rounded add: the tensor cores' own sums would drift over a long cache.
+//
+// Roles of a block's 12 warps.  0-3: load Q, softmax; row = thread.  4-7: add the
+// tiles' O, one row per thread, and write.  8: issues the MMAs.  9-11: fill K and
+// V: whole boxes of BR tokens by TMA, everything else (drafts, the ends of what is
+// seen, odd page sizes) by hand, with zeros for values nobody sees.
+//
+// Operands that are not finite.  Rows whose sums come out NaN or infinite are
+// gone through again in fp32, token by token, by the warp that would write them.
+template <int DT, int DP>
+struct TreeTile {
+  static constexpr int TN = DP == 256 ? 64 : 128;  // tokens of a tile
+  static constexpr int MR = DP == 256 ? 64 : 128;  // query rows of a unit
+  static constexpr int DV = DP < 128 ? DP : 128;   // columns of V of a unit
+  static constexpr int NP = DT == 0 ? 2 : 3;       // parts of q and p
+  static constexpr int S = DP == 64 ? 4 : DP == 256 && DT == 0 ? 3 : 2;  // stages
+  static constexpr int NO = DT == 1 && DP == 128 ? 1 : 2;  // O tiles in tensor memory
+  static constexpr int NA = NO + 2;
+  static constexpr int kQ = MR * DP * 2, kK = TN * DP * 2, kV = TN * DV * 2;  // bytes
+  static constexpr int kStages = NP * kQ, kMisc = kStages + S * (kK + kV);
+  // tensor-memory columns: two S tiles, whose place the first parts of P take; the
+  // third parts of P; O
+  static constexpr int kThird = 2 * TN, kO = kThird + (DT == 1 ? TN : 0);
+  static_assert(kO + NO * DV <= 512, "tensor memory");
+};
+constexpr int kTreeThreads = 384;
+constexpr int kTreeGrid = 192;   // most blocks
+constexpr int kTreeCost = 1;     // a unit's fixed cost, in tiles
+constexpr int kTreeWhole = 6;    // units of at most this many tiles are not split
+constexpr int kTreeShare = 3;    // least share of a block
+
+// NA: rescaling factors in flight; the sums may be that many tiles behind
+template <int NA>
+struct TreeShared {
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[2], pfull[2], ofull[2], oempty[2];
+  uint64_t qfull, lfull, lempty, fin;
+  uint32_t taddr;
+  int bad;
+  uint32_t hide[8][4];   // tokens of a tile whose page is out of range
+  float l[128], m[128];  // a segment's sums and reference
+  union {
+    float alpha[NA][128];
+    struct {
+      long long sum[12], len[12];
+      int most[12];
+      long long at;
+      int slot, unit;
+    } scan;
+  };
+};
+template <int NA>
+struct TreeSharedScale : TreeShared<NA> {
+  float qs[2][128];  // rows' 2^-e of q (fp16)
+};
+template <int DT, int NA>
+using TreeSharedOf = std::conditional_t<DT == 0, TreeSharedScale<NA>, TreeShared<NA>>;
+template <int DT, int DP>
+__host__ __device__ constexpr int tree_smem() {
+  return TreeTile<DT, DP>::kMisc + (int)sizeof(TreeSharedOf<DT, TreeTile<DT, DP>::NA>);
 }
 
-// ------------------------------------------------------------------ acceptance
-//
-// The root is taken; from a draft that is taken, the first child whose token is
-// the one chosen there.  A block walks the path of one slot by itself: of the
-// drafts that fit, the lowest child of the current one is a ballot away.
-// Confirmed drafts move up behind one another: step j's row goes to place j
-// <= its own, so a thread that copies its piece of the rows in the path's order,
-// reading a batch before writing it, overwrites no row that is still needed.
-// Bound: the moved rows' bytes.
-struct AcceptArgs {
-  const int *parent, *count, *tokens, *choice, *table, *len;
-  uint16_t* pool;
-  int *len_out, *path, *accepted, *next, *status;
-  int slots, drafts, max_pages, layers, kv_heads, head_dim, page_tokens, pages;
-  int blocks;  // per slot
+struct TreeSpan {  // a unit that begins in a block and ends in a later one
+  int slot, unit, last, some;
+};
+struct TreeWork {
+  TreeArgs a;
+  TreeSpan* span;  // [grid]
+  float* part;     // [grid][2][MR][DV + 4]
+  int halves;      // units of V's columns
+  int tma, box;    // tiles come as TMA boxes; their rows
+  unsigned long long limit_ns;
+  int lose;        // self-test: block 0's first box is never ordered
 };
 
-constexpr int kAcceptThreads = 256;
+__device__ __forceinline__ void mbar_arrive(uint64_t* m) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
+}
+__device__ __forceinline__ void tree_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(m))
+      : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: sbo = the distance of
+// 8-row groups.  MN-major: lbo = the distance of 64-element groups along M or N, sbo
+// = that of 8-row groups along K.
+__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;  // descriptor version of this family
+  d |= (uint64_t)2 << 61;  // 128-byte swizzle
+  return d;
+}
+// Instruction descriptor of kind::f16: D fp32, A and B of DT, M = 128, N = n.
+template <int DT>
+__device__ __forceinline__ uint32_t tree_idesc(int n, bool b_nmajor) {
+  return (1u << 4) | ((uint32_t)DT << 7) | ((uint32_t)DT << 10) | (b_nmajor ? 1u << 16 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* m) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(m))
+               : "memory");
+}
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_ld32(float* v, uint32_t t) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tm_ld16(float* v, uint32_t t) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+}
+__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
-__global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptArgs a) {
+// A unit and its tiles.
+struct TreeUnit {
+  int slot, unit;  // number within the slot: (g, rt, half)
+  TreeSlot v;
+  int g, row0, rows, half;  // query rows [row0, row0 + rows) of the kv head
+  int start, firsts, tiles; // first token of the window's tiles; tiles of the first tokens; all
+};
+template <int TN>
+__device__ __forceinline__ int tree_tiles(const TreeSlot& v) {
+  return 1 + (v.first + TN - 1) / TN + (v.base > v.tail ? (v.base - (v.tail & ~15) + TN - 1) / TN : 0);
+}
+__device__ __forceinline__ int tree_units(const TreeWork& w, const TreeSlot& v, int mr) {
+  return v.count ? w.a.kv_heads * ((v.count * w.a.group + mr - 1) / mr) * w.halves : 0;
+}
+// Goes through a block's share: segments [tile0, tile1) of units.
+template <int TN, int MR>
+struct TreeWalk {
+  const TreeWork& w;
+  TreeUnit u;
+  long long at, end;  // of the unit on the line; of the share
+  long long from;     // where the share begins
+  bool whole;
+  int units;          // of the slot
+  int tile0, tile1;
+  __device__ __forceinline__ TreeWalk(const TreeWork& w, int slot, int unit, long long at, long long from,
+                                      long long end, bool whole)
+      : w(w), at(at), end(end), from(from), whole(whole) {
+    u.slot = slot;
+    u.unit = unit;
+    if (at < end) open();
+  }
+  __device__ __forceinline__ void open() {
+    u.v = tree_slot(w.a, u.slot);
+    units = tree_units(w, u.v, MR);
+    u.start = u.v.tail & ~15;
+    u.firsts = (u.v.first + TN - 1) / TN;
+    u.tiles = tree_tiles<TN>(u.v);
+    fit();
+  }
+  __device__ __forceinline__ void fit() {
+    const int rts = units / (w.a.kv_heads * w.halves), per = rts * w.halves;
+    u.g = u.unit / per;
+    const int r = u.unit - u.g * per, rt = r / w.halves;
+    u.half = r - rt * w.halves;
+    u.row0 = rt * MR;
+    u.rows = min(MR, u.v.count * w.a.group - u.row0);
+    if (whole) {
+      tile0 = 0;
+      tile1 = u.tiles;
+    } else {
+      const long long a0 = from - at - kTreeCost, a1 = end - at - kTreeCost;
+      tile0 = a0 > 0 ? (int)a0 : 0;
+      tile1 = a1 < u.tiles ? (int)a1 : u.tiles;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ bool any() const { return tile1 > tile0; }
+  __device__ __forceinline__ bool begins() const { return tile0 == 0; }
+  __device__ __forceinline__ bool ends() const { return tile1 == u.tiles; }
+  __device__ __forceinline__ void next() {
+    at += whole ? 1 : u.tiles + kTreeCost;
+    if (at >= end) return;
+    if (++u.unit < units) {
+      fit();
+      return;
+    }
+    u.unit = 0;
+    do ++u.slot;
+    while (u.slot < w.a.slots && tree_slot(w.a, u.slot).count == 0);
+    if (u.slot >= w.a.slots) {
+      at = end;
+      return;
+    }
+    open();
+  }
+  // Tile i >= 1 holds the tokens from t0 on, of which [lo, hi) are seen by some draft.
+  __device__ __forceinline__ int cached(int i, int& lo, int& hi) const {
+    const bool first = i <= u.firsts;
+    const int t0 = first ? (i - 1) * TN : u.start + (i - 1 - u.firsts) * TN;
+    lo = first ? 0 : u.v.tail;
+    hi = first ? u.v.first : u.v.base;
+    return t0;
+  }
+  // Its columns in the products.
+  __device__ __forceinline__ int columns(int i) const {
+    if (i == 0) return (u.v.count + 15) & ~15;
+    int lo, hi;
+    const int t0 = cached(i, lo, hi);
+    return min(TN, (hi - t0 + 15) & ~15);
+  }
+};
+
+// A part's line position to block, and back (as in the attention of one token).
+struct TreeLine {
+  long long each;
+  int more;
+  __device__ __forceinline__ void set(long long total, int blocks) {
+    each = quotient(total, blocks);
+    more = (int)(total - each * blocks);
+  }
+  __device__ __forceinline__ long long start(int b) const { return b * each + min(b, more); }
+  __device__ __forceinline__ int block_of(long long pos) const {
+    const long long head = more * (each + 1);
+    return pos >= head ? more + (int)((pos - head) / each) : (int)(pos / (each + 1));
+  }
+};
+
+// A row's draft, and what it sees.
+struct TreeRow {
+  int draft, lo;  // lo: least visible cached token but for the first `sinks`
+  unsigned long long seen;
+  const float* q;
+  size_t out;     // row of y
+};
+template <typename F>
+__device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, const TreeUnit& u, int r, F parent) {
+  TreeRow x;
+  const int R = u.row0 + r;
+  x.draft = R / a.group;
+  const unsigned long long path =
+      a.parent ? tree_path(a, x.draft, parent) : (2ull << x.draft) - 1;
+  x.lo = a.window > 0 ? u.v.base + __popcll(path) - a.window : 0;
+  x.seen = tree_seen(a, u.v.base, path);
+  x.out = ((size_t)u.slot * a.drafts + x.draft) * a.heads + u.g * a.group + R - x.draft * a.group;
+  x.q = a.q + x.out * a.head_dim;
+  return x;
+}
+
+// The segment [tile0, tile1) of row r once more, in fp32; the warp's lanes hold the
+// columns 8 lane .. of it.
+template <int DT, int TN, int MR>
+__device__ __noinline__ RowSums tree_again(const TreeWork& w, const TreeUnit& u, int tile0, int tile1, int r) {
+  const TreeArgs& a = w.a;
+  const TreeRow x = tree_row(a, u, r, [&](int j) { return __ldg(a.parent + (size_t)u.slot * a.drafts + j); });
+  RowSums s = {-INFINITY, 0.f, {}};
+  const int f0 = max(tile0, 1) - 1, f1 = min(tile1 - 1, u.firsts);
+  if (f0 < f1) row_add_cached<DT>(a, u.slot, u.g, x.q, f0 * TN, min(u.v.first, f1 * TN), x.lo, s);
+  const int w0 = max(tile0 - 1 - u.firsts, 0), w1 = tile1 - 1 - u.firsts;
+  if (w0 < w1)
+    row_add_cached<DT>(a, u.slot, u.g, x.q, max(u.v.tail, u.start + w0 * TN), min(u.v.base, u.start + w1 * TN), x.lo, s);
+  if (tile0 == 0) row_add_drafts<DT>(a, u.slot, u.v, u.g, x.q, x.seen, s);
+  return s;
+}
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_kernel(const __grid_constant__ TreeWork w, const __grid_constant__ CUtensorMap map) {
+  using C = TreeTile<DT, DP>;
+  constexpr int TN = C::TN, MR = C::MR, DV = C::DV, NP = C::NP, S = C::S, NO = C::NO;
+  constexpr int kPanelK = TN * 128, kPanelQ = MR * 128;  // bytes of 64 columns
+  constexpr int NA = C::NA;
+  using Shared = TreeSharedOf<DT, NA>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem + C::kMisc);
+  const TreeArgs& a = w.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int D = a.head_dim, P = a.page_tokens;
   pdl_enter();
-  __shared__ int s_path[64], s_n;
-  __shared__ long long s_row[64];  // first of the row's elements in a layer, of K and kv head 0
-  const int slot = blockIdx.x / a.blocks, part = blockIdx.x - slot * a.blocks;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int P = a.page_tokens, most = a.max_pages * P;
-  const int n = __ldg(a.len + slot), c = a.count ? __ldg(a.count + slot) : a.drafts;
-  const bool ok = n >= 0 && n <= most && c >= 0 && c <= a.drafts && c <= n;
-  const int count = ok ? c : 0, base = n - c;
-  if (tid < 32) {
-    bool bad = !ok;
-    int par[2], tok[2], want[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = lane + 32 * k;
-      const size_t at = (size_t)slot * a.drafts + i;
-      const bool in = i < count;
-      par[k] = in ? a.parent ? __ldg(a.parent + at) : i - 1 : -1;
-      tok[k] = in ? __ldg(a.tokens + at) : 0;
-      want[k] = in ? __ldg(a.choice + at) : -1;
-      if (in && (par[k] < -1 || par[k] >= i)) {
-        bad = true;
-        par[k] = -1;
-      }
+
+  // ---- the block's share of the line
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.kfull[i], 3);
+      mbar_init(&sh.vfull[i], 3);
+      mbar_init(&sh.kempty[i], 1);
+      mbar_init(&sh.vempty[i], 1);
     }
-    int at = 0, steps = 0, chosen = -1;
-    while (steps < count) {
-      if (lane == 0) s_path[steps] = at;
-      ++steps;
-      const int w0 = __shfl_sync(~0u, want[0], at & 31), w1 = __shfl_sync(~0u, want[1], at & 31);
-      chosen = at < 32 ? w0 : w1;
-      const unsigned f0 = __ballot_sync(~0u, chosen >= 0 && lane < count && par[0] == at && tok[0] == chosen);
-      const unsigned f1 = __ballot_sync(~0u, chosen >= 0 && lane + 32 < count && par[1] == at && tok[1] == chosen);
-      if (!(f0 | f1)) break;
-      at = f0 ? __ffs(f0) - 1 : 31 + __ffs(f1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.pfull[i], 4);
+      mbar_init(&sh.ofull[i], 1);
+      mbar_init(&sh.oempty[i], 4);
     }
-    __syncwarp();
-    if (part == 0) {
-      if (bad) set_status(a.status, PI_ERR_INDEX);
-      for (int i = lane; i < a.drafts; i += 32)
-        a.path[(size_t)slot * a.drafts + i] = i < steps ? s_path[i] : -1;
-      if (lane == 0) {
-        a.len_out[slot] = ok ? base + steps : 0;
-        a.accepted[slot] = steps;
-        a.next[slot] = chosen;
-      }
-    }
-    if (lane == 0) s_n = steps;
+    mbar_init(&sh.qfull, 4);
+    mbar_init(&sh.lfull, 4);
+    mbar_init(&sh.lempty, 4);
+    mbar_init(&sh.fin, 1);
+    fence_mbar_init();
+    sh.bad = 0;
   }
-  __syncthreads();
-  if (!a.pool) return;
-  (void)P;
-  // rows that stay where they are come first on the path
-  const int steps = s_n;
-  int first = 0;
-  while (first < steps && s_path[first] == first) ++first;
-  if (first == steps) return;
-  const size_t half = (size_t)a.kv_heads * P * a.head_dim;
-  auto row_of = [&](int t) -> long long {
-    const int j = t / P;
-    const int page = checked_page(__ldg(a.table + (size_t)slot * a.max_pages + j), a.pages, a.status);
-    return page < 0 ? -1 : (long long)page * 2 * (long long)half + (long long)(t - j * P) * a.head_dim;
+  long long share0, share1, unit_at;
+  int first_slot, first_unit, grid;
+  bool whole;
+  TreeLine line;
+  {
+    auto& sc = sh.scan;
+    const int k = (a.slots + kTreeThreads - 1) / kTreeThreads, s0 = tid * k, s1 = min(a.slots, s0 + k);
+    long long units = 0, tiles = 0;
+    int most = 0;
+    for (int s = s0; s < s1; ++s) {
+      const TreeSlot v = tree_slot(a, s);
+      if (blockIdx.x == 0 && tree_slot_bad(a, s)) set_status(a.status, PI_ERR_INDEX);
+      const int n = tree_units(w, v, MR), t = tree_tiles<TN>(v);
+      units += n;
+      tiles += (long long)n * (t + kTreeCost);
+      if (n) most = max(most, t);
+    }
+    auto sum_up = [&](long long v) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += x;
+      }
+      return v;
+    };
+    const long long upto_u = sum_up(units), upto_t = sum_up(tiles);
+    most = (int)__reduce_max_sync(~0u, (uint32_t)most);
+    if (lane == 31) {
+      sc.sum[warp] = upto_u;
+      sc.len[warp] = upto_t;
+    }
+    if (lane == 0) sc.most[warp] = most;
+    __syncthreads();
+    long long all_u = 0, all_t = 0, low_u = 0, low_t = 0;
+    most = 0;
+    for (int i = 0; i < kTreeThreads / 32; ++i) {
+      if (i == warp) low_u = all_u, low_t = all_t;
+      all_u += sc.sum[i];
+      all_t += sc.len[i];
+      most = max(most, sc.most[i]);
+    }
+    whole = most <= kTreeWhole;
+    const long long total = whole ? all_u : all_t;
+    grid = gridDim.x;
+    const long long useful = whole ? all_u : max(1ll, all_t / kTreeShare);
+    if (useful < grid) grid = max(1, (int)useful);
+    line.set(total, grid);
+    share0 = share1 = 0;
+    if ((int)blockIdx.x < grid) {
+      share0 = line.start(blockIdx.x);
+      share1 = line.start(blockIdx.x + 1);
+    }
+    // the thread whose slots hold the share's start
+    long long at = whole ? low_u + upto_u - units : low_t + upto_t - tiles;
+    if (share0 >= at && share0 < at + (whole ? units : tiles) && share0 < share1) {
+      for (int s = s0; s < s1; ++s) {
+        const TreeSlot v = tree_slot(a, s);
+        const int n = tree_units(w, v, MR), len = whole ? 1 : tree_tiles<TN>(v) + kTreeCost;
+        if (share0 < at + (long long)n * len) {
+          sc.slot = s;
+          sc.unit = (int)((share0 - at) / len);
+          sc.at = at + (long long)sc.unit * len;
+          break;
+        }
+        at += (long long)n * len;
+      }
+    }
+    __syncthreads();
+    const bool some = share0 < share1;
+    first_slot = some ? sc.slot : 0;
+    first_unit = some ? sc.unit : 0;
+    unit_at = some ? sc.at : 0;
+    if (warp == 8) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.taddr)));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+  }
+  const uint32_t tmem = sh.taddr;
+  TreeWalk<TN, MR> walk(w, first_slot, first_unit, unit_at, share0, share1, whole);
+  const int kd = (D + 15) >> 4;  // steps of 16 along a row
+  int t = 0;                     // tiles so far
+  bool ok = true;
+  auto gave_up = [&] {
+    set_status(a.status, PI_ERR_TIMEOUT);
+    *(volatile int*)&sh.bad = 1;
+    ok = false;
   };
-  __shared__ long long s_to[64];
-  for (int j = first + tid; j < steps; j += kAcceptThreads) {
-    s_row[j] = row_of(base + s_path[j]);
-    s_to[j] = row_of(base + j);
+#define TREE_WAIT(bar, parity)                            \
+  if (!mbar_wait(bar, (uint32_t)(parity), w.limit_ns)) { \
+    gave_up();                                            \
+    break;                                                \
   }
-  __syncthreads();
-  const int pieces = a.head_dim >> 3;
-  const long long layer = (long long)a.pages * 2 * half, total = 2ll * a.layers * a.kv_heads * pieces;
-  for (long long e = (long long)part * kAcceptThreads + tid; e < total; e += (long long)a.blocks * kAcceptThreads) {
-    const long long r = e / pieces;
-    const int piece = (int)(e - r * pieces), g = (int)(r % a.kv_heads);
-    const long long kv = r / a.kv_heads;  // 2 layer + (K, V)
-    uint16_t* at = a.pool + (kv >> 1) * layer + (kv & 1) * half + (size_t)g * P * a.head_dim + 8 * piece;
-    constexpr int B = 8;
-    for (int j0 = first; j0 < steps; j0 += B) {
-      uint4 x[B];
+
+  if (warp < 4) {
+    // ---- Q, softmax
+    const float flip = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
+    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
+    constexpr float kShift = DT == 0 ? 14.f : 0.f;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    const int row = tid;
+    int seg = 0;
+    for (; walk.more() && ok; walk.next()) {
+      if (!walk.any()) continue;
+      const TreeUnit& u = walk.u;
+      // rows warp, warp + 4, ...: split into parts
+      constexpr int E = DP / 32, B = 4;
+#pragma unroll 1
+      for (int r0 = warp; r0 < u.rows; r0 += 4 * B) {
+        float x[B][E];
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (j0 + j < steps && s_row[j0 + j] >= 0) x[j] = *reinterpret_cast<const uint4*>(at + s_row[j0 + j]);
+        for (int b = 0; b < B; ++b) {
+          const int r = r0 + 4 * b;
+          const int R = u.row0 + r, i = R / a.group;
+          const float* q = a.q + (((size_t)u.slot * a.drafts + i) * a.heads + u.g * a.group + R - i * a.group) * D + E * lane;
+          if (r < u.rows && E * lane < D) {
+            if constexpr (E == 2) {
+              const float2 f = __ldg(reinterpret_cast<const float2*>(q));
+              x[b][0] = f.x, x[b][1] = f.y;
+            } else {
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (j0 + j < steps && s_row[j0 + j] >= 0 && s_to[j0 + j] >= 0)
-          *reinterpret_cast<uint4*>(at + s_to[j0 + j]) = x[j];
+              for (int e = 0; e < E; e += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(q + e));
+                x[b][e] = f.x, x[b][e + 1] = f.y, x[b][e + 2] = f.z, x[b][e + 3] = f.w;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[b][e] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int r = r0 + 4 * b;
+          if (r >= u.rows) break;
+          if constexpr (DT == 0) {
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[b][e]));
+            top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
+            int ex = 140 - (int)(__float_as_uint(top) >> 23);  // the largest into [2^13, 2^14)
+            if (!(top > 0.f && top < INFINITY)) ex = 0;
+            ex = max(-100, min(100, ex));
+            const float f = __uint_as_float((uint32_t)(ex + 127) << 23);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[b][e] *= f;
+            if (lane == 0) sh.qs[seg & 1][r] = __uint_as_float((uint32_t)(127 - ex) << 23);
+          }
+          uint32_t part[NP][E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            float y = x[b][2 * e] * flip, z = x[b][2 * e + 1] * flip;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              part[p][e] = pack_bits<DT>(y, z);
+              y -= from_bits<DT>((uint16_t)part[p][e]);
+              z -= from_bits<DT>((uint16_t)(part[p][e] >> 16));
+            }
+          }
+          const int c = E * lane;
+          unsigned char* to = smem + (c >> 6) * kPanelQ + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + 2 * (c & 7);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to + p * C::kQ) = part[p][0];
+            else if constexpr (E == 4) *reinterpret_cast<uint2*>(to + p * C::kQ) = make_uint2(part[p][0], part[p][1]);
+            else *reinterpret_cast<uint4*>(to + p * C::kQ) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+          }
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.qfull);
+      // the row's own draft
+      const bool live = 32 * warp < u.rows;
+      int pa = -1, pb = -1;
+      if (live && a.parent) {
+        if (lane < u.v.count) pa = __ldg(a.parent + (size_t)u.slot * a.drafts + lane);
+        if (lane + 32 < u.v.count) pb = __ldg(a.parent + (size_t)u.slot * a.drafts + lane + 32);
+      }
+      int lo = 0;
+      unsigned long long seen = 0;
+      if (live) {
+        const int draft = (u.row0 + min(row, u.rows - 1)) / a.group;
+        unsigned long long path = (2ull << draft) - 1;
+        if (a.parent) {  // all lanes together: the parents are in their registers
+          path = 0;
+          int j = draft;
+          while (__any_sync(~0u, j >= 0)) {
+            const int x0 = __shfl_sync(~0u, pa, j & 31), x1 = __shfl_sync(~0u, pb, j & 31);
+            if (j >= 0) {
+              path |= 1ull << j;
+              int p = j < 32 ? x0 : x1;
+              if (p < -1 || p >= j) {
+                set_status(a.status, PI_ERR_INDEX);
+                p = -1;
+              }
+              j = p;
+            }
+          }
+        }
+        lo = a.window > 0 ? u.v.base + __popcll(path) - a.window : 0;
+        seen = tree_seen(a, u.v.base, path);
+      }
+      TREE_WAIT(&sh.qfull, seg & 1);
+      float scl = scale;
+      if constexpr (DT == 0) scl = live && row < u.rows ? scale * sh.qs[seg & 1][row] : scale;
+      const int sinks = u.v.tail > 0 ? 0 : a.sinks;
+      float m = -INFINITY, ref = -INFINITY, l = 0.f;
+      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
+        const int buf = t & 1;
+        TREE_WAIT(&sh.sfull[buf], (t >> 1) & 1);
+        if (live) {
+          tm_fence_after();
+          const uint32_t src = lanes + (uint32_t)(buf * TN);
+          const int cols = walk.columns(i);
+          float v[TN];
+#pragma unroll
+          for (int k = 0; k < TN / 32; ++k)
+            if (32 * k < cols) tm_ld32(v + 32 * k, src + 32 * k);
+          // the columns that the row sees, as bits
+          uint32_t mask[TN / 32], all = ~0u;
+          if (i == 0) {
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k) mask[k] = k < 2 ? (uint32_t)(seen >> (32 * k)) : 0u;
+          } else {
+            int any_lo, hi;
+            const int t0 = walk.cached(i, any_lo, hi);
+            const int from = (i <= u.firsts ? 0 : lo) - t0, n = hi - t0, sink = sinks - t0;
+            auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k)
+              mask[k] = below(n - 32 * k) & (~below(from - 32 * k) | below(sink - 32 * k));
+          }
+#pragma unroll
+          for (int k = 0; k < TN / 32; ++k) {
+            mask[k] &= ~sh.hide[t & 7][k];
+            all &= mask[k];
+          }
+          tm_wait_ld();
+          if (!__all_sync(~0u, all == ~0u)) {
+#pragma unroll
+            for (int c = 0; c < TN; ++c) v[c] = mask[c >> 5] >> (c & 31) & 1u ? v[c] : -INFINITY;
+          }
+          float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int c = 4; c < TN; ++c) top[c & 3] = fmaxf(top[c & 3], v[c]);
+          const float up = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scl);
+          // weights are relative to the maximum less kShift, which rounding must not take
+          // far from it
+          const float at = up == -INFINITY ? 0.f : up;
+          float next = at - kShift;
+          if (!(at - next <= kShift + 1.f)) next = at;
+          const float alpha = m == -INFINITY ? 0.f : ex2(ref - next);
+          m = up;
+          ref = next;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < TN / 32; ++k) {
+            if (32 * k >= cols) continue;
+            uint32_t part[NP][16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float y = ex2(__fmul_rn(v[32 * k + 2 * c], scl) - next);
+              float z = ex2(__fmul_rn(v[32 * k + 2 * c + 1], scl) - next);
+              sum[c & 1] += y;
+              sum[2 + (c & 1)] += z;
+#pragma unroll
+              for (int p = 0; p < NP; ++p) {
+                part[p][c] = pack_bits<DT>(y, z);
+                y -= from_bits<DT>((uint16_t)part[p][c]);
+                z -= from_bits<DT>((uint16_t)(part[p][c] >> 16));
+              }
+            }
+            tm_st16(src + 16 * k, part[0]);
+            tm_st16(src + TN / 2 + 16 * k, part[1]);
+            if constexpr (NP == 3) tm_st16(lanes + C::kThird + buf * (TN / 2) + 16 * k, part[2]);
+          }
+          l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+          sh.alpha[t % NA][row] = alpha;
+          tm_wait_st();
+          tm_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pfull[buf]);
+      }
+      if (!ok) break;
+      if (seg > 0) TREE_WAIT(&sh.lempty, (seg - 1) & 1);
+      sh.l[row] = l;
+      sh.m[row] = ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.lfull);
+      ++seg;
     }
+  } else if (warp < 8) {
+    // ---- O
+    const int row = tid - 128;
+    const uint32_t lanes = tmem + ((uint32_t)(row & ~31) << 16) + C::kO;
+    int seg = 0;
+    TreeSpan span{0, 0, 0, 0};
+    for (; walk.more() && ok; walk.next()) {
+      if (!walk.any()) continue;
+      const TreeUnit& u = walk.u;
+      const bool live = (row & ~31) < u.rows;
+      const int dh = min(DV, D - u.half * 128);  // the unit's columns
+      float o[DV];
+#pragma unroll
+      for (int c = 0; c < DV; ++c) o[c] = 0.f;
+      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
+        const int buf = t % NO;
+        TREE_WAIT(&sh.ofull[buf], (t / NO) & 1);
+        if (live) {
+          tm_fence_after();
+          const float alpha = sh.alpha[t % NA][row];
+#pragma unroll
+          for (int c0 = 0; c0 < DV; c0 += 16) {
+            float x[16];
+            tm_ld16(x, lanes + buf * DV + c0);
+            tm_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c0 + c] = fmaf(o[c0 + c], alpha, x[c]);
+          }
+          tm_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.oempty[buf]);
+      }
+      if (!ok) break;
+      TREE_WAIT(&sh.lfull, seg & 1);
+      const float l = sh.l[row], m = sh.m[row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.lempty);
+      ++seg;
+      const bool begins = walk.begins(), ends = walk.ends();
+      if (begins && !ends) span = TreeSpan{u.slot, u.unit, line.block_of(walk.at + kTreeCost + u.tiles - 1), 1};
+      if (!live) continue;
+      bool again = false;
+      if (row < u.rows) {
+        again = !(fabsf(l) < INFINITY);
+#pragma unroll
+        for (int c = 0; c < DV; ++c) again |= c < dh && !(fabsf(o[c]) < INFINITY);
+      }
+      const int R = u.row0 + row, draft = R / a.group;
+      const size_t out = ((size_t)u.slot * a.drafts + draft) * a.heads + u.g * a.group + R - draft * a.group;
+      float* part = w.part + ((size_t)(2 * blockIdx.x + begins) * MR + row) * (DV + 4);
+      if (row < u.rows && !again) {
+        if (begins && ends) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          float4* to = reinterpret_cast<float4*>(a.y + out * D + u.half * 128);
+#pragma unroll
+          for (int c = 0; c < DV; c += 4)
+            if (c < dh) to[c / 4] = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
+          if (a.lse && u.half == 0) a.lse[out] = (m + log2f(l)) * kLn2;
+        } else {
+#pragma unroll
+          for (int c = 0; c < DV; c += 4)
+            __stcg(reinterpret_cast<float4*>(part + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+          __stcg(reinterpret_cast<float2*>(part + DV), make_float2(m, l));
+        }
+      }
+      for (uint32_t left = __ballot_sync(~0u, again); left; left &= left - 1) {
+        const int r = (row & ~31) + __ffs(left) - 1;
+        const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, r);
+        const float inv = s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
+        const int Rr = u.row0 + r, dr = Rr / a.group, c = 8 * lane - 128 * u.half;
+        const size_t to_row = ((size_t)u.slot * a.drafts + dr) * a.heads + u.g * a.group + Rr - dr * a.group;
+        float* pr = w.part + ((size_t)(2 * blockIdx.x + begins) * MR + r) * (DV + 4);
+        const bool direct = begins && ends;
+        const float f = direct ? inv : 1.f;
+        if (c >= 0 && c < dh) {
+          float4* to = reinterpret_cast<float4*>(direct ? a.y + to_row * D + 8 * lane : pr + c);
+          __stcg(to, make_float4(s.o[0] * f, s.o[1] * f, s.o[2] * f, s.o[3] * f));
+          __stcg(to + 1, make_float4(s.o[4] * f, s.o[5] * f, s.o[6] * f, s.o[7] * f));
+        }
+        if (lane == 0) {
+          if (!direct) __stcg(reinterpret_cast<float2*>(pr + DV), make_float2(s.m, s.l));
+          else if (a.lse && u.half == 0) a.lse[to_row] = (s.m + log2f(s.l)) * kLn2;
+        }
+      }
+    }
+    if (row == 0) w.span[blockIdx.x] = span;
+  } else if (warp == 8) {
+    // ---- MMAs
+    int seg = 0, cols_before = 0, nv_before = 0;
+    auto pv = [&](int p, int cols, int nv) {  // tile p's O
+      const int buf = p & 1, st = p % S, ob = p % NO;
+      if (!mbar_wait(&sh.vfull[st], (uint32_t)((p / S) & 1), w.limit_ns) ||
+          !mbar_wait(&sh.pfull[buf], (uint32_t)((p >> 1) & 1), w.limit_ns) ||
+          (p >= NO && !mbar_wait(&sh.oempty[ob], (uint32_t)(((p / NO) - 1) & 1), w.limit_ns))) {
+        gave_up();
+        return;
+      }
+      tm_fence_after();
+      if (lane == 0) {
+        const uint32_t vst = smem_u32(smem + C::kStages + st * (C::kK + C::kV) + C::kK);
+        const uint32_t idesc = tree_idesc<DT>(nv, true);
+        const uint32_t d = tmem + C::kO + ob * DV;
+        bool add = false;
+#pragma unroll
+        for (int part = NP - 1; part >= 0; --part) {
+          const uint32_t pa = part == 2 ? tmem + C::kThird + buf * (TN / 2) : tmem + buf * TN + part * (TN / 2);
+          for (int ks = 0; ks < cols / 16; ++ks) {
+            mma_ts(d, pa + 8 * ks, tree_desc(vst + 2048 * ks, kPanelK), idesc, add);
+            add = true;
+          }
+        }
+        mma_commit(&sh.vempty[st]);
+        mma_commit(&sh.ofull[ob]);
+      }
+      __syncwarp();
+    };
+    for (; walk.more() && ok; walk.next()) {
+      if (!walk.any()) continue;
+      const int nv = (min(DV, D - walk.u.half * 128) + 15) & ~15;
+      for (int i = walk.tile0; i < walk.tile1 && ok; ++i, ++t) {
+        const int st = t % S, buf = t & 1, cols = walk.columns(i);
+        if (i == walk.tile0) {
+          if (t > 0) pv(t - 1, cols_before, nv_before);
+          if (!ok) break;
+          TREE_WAIT(&sh.qfull, seg & 1);
+        }
+        TREE_WAIT(&sh.kfull[st], (t / S) & 1);
+        tm_fence_after();
+        if (lane == 0) {
+          const uint32_t qs = smem_u32(smem), ks = smem_u32(smem + C::kStages + st * (C::kK + C::kV));
+          const uint32_t idesc = tree_idesc<DT>(cols, false);
+          bool add = false;
+#pragma unroll
+          for (int part = NP - 1; part >= 0; --part)
+            for (int k = 0; k < kd; ++k) {
+              mma_ss(tmem + buf * TN, tree_desc(qs + part * C::kQ + (k >> 2) * kPanelQ + (k & 3) * 32, 16),
+                     tree_desc(ks + (k >> 2) * kPanelK + (k & 3) * 32, 16), idesc, add);
+              add = true;
+            }
+          mma_commit(&sh.kempty[st]);
+          mma_commit(&sh.sfull[buf]);
+        }
+        __syncwarp();
+        if (i > walk.tile0) pv(t - 1, cols_before, nv_before);
+        cols_before = cols;
+        nv_before = nv;
+      }
+      ++seg;
+    }
+    if (ok && t > 0) pv(t - 1, cols_before, nv_before);
+  } else {
+    // ---- K and V
+    const int pw = warp - 9, pt = tid - 288;  // of 3 warps, 96 threads
+    for (; walk.more() && ok; walk.next()) {
+      if (!walk.any()) continue;
+      const TreeUnit& u = walk.u;
+      const int dh = min(DV, D - u.half * 128), d0 = u.half * 128;
+      const int pk = (D + 63) >> 6, pv = (dh + 63) >> 6;       // panels
+      const int ck = 2 * kd, cv = ((dh + 15) & ~15) >> 3;      // 16-byte pieces of a row
+      const size_t half = (size_t)a.kv_heads * P * D;          // K to V in a page
+      auto key_of = [&](int tok) -> const uint16_t* {          // null: page out of range
+        const int j = tok / P;
+        const int page = checked_page(__ldg(a.table + (size_t)u.slot * a.max_pages + j), a.pages, a.status);
+        return page < 0 ? nullptr : a.pool + (((size_t)page * 2 * a.kv_heads + u.g) * P + tok - j * P) * D;
+      };
+      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
+        const int st = t % S, cols = walk.columns(i);
+        unsigned char* const ks = smem + C::kStages + st * (C::kK + C::kV);
+        unsigned char* const vs = ks + C::kK;
+        auto place = [&](unsigned char* base, int r, int c) {  // piece c of row r
+          return reinterpret_cast<uint4*>(base + (c >> 3) * kPanelK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        };
+        // rows [r0, r1) of K or V by hand: load(row, first element) gives a piece
+        auto fill = [&](unsigned char* base, int r0, int r1, int pieces, auto load) {
+          const int n = (r1 - r0) * pieces;
+          for (int e0 = pt; e0 < n; e0 += 96 * 4) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = e0 + 96 * k, r = e / pieces;
+              if (e < n) x[k] = load(r0 + r, 8 * (e - r * pieces));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = e0 + 96 * k, r = e / pieces;
+              if (e < n) *place(base, r0 + r, e - r * pieces) = x[k];
+            }
+          }
+        };
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint32_t kpar = (uint32_t)(((t / S) - 1) & 1);
+        int t0 = 0, lo = 0, hi = 0, page = 0;
+        bool boxes = false;
+        const int nbox = cols / w.box;
+        if (i > 0) {
+          t0 = walk.cached(i, lo, hi);
+          if (w.tma) {
+            const int b0 = t0 + lane * w.box;
+            bool good = true;
+            if (lane < nbox && b0 + w.box > lo && b0 < hi) {
+              page = __ldg(a.table + (size_t)u.slot * a.max_pages + b0 / P);
+              good = (unsigned)page < (unsigned)a.pages;
+            }
+            boxes = __all_sync(~0u, good);
+          }
+        }
+        if (t >= S) TREE_WAIT(&sh.kempty[st], kpar);
+        if (i == 0) {
+          // the drafts: rounded to the cache's type where they are new, and stored
+          const bool keep = a.k_new && u.row0 == 0;
+          auto draft = [&](const float* from, bool value, int r, int e) {
+            if (r >= u.v.count || e >= (value ? dh : D)) return zero;
+            if (value) e += d0;
+            if (!a.k_new) {
+              const uint16_t* key = key_of(u.v.base + r);
+              return key ? *reinterpret_cast<const uint4*>(key + (value ? half : 0) + e) : zero;
+            }
+            const float4* f = reinterpret_cast<const float4*>(
+                from + (((size_t)u.slot * a.drafts + r) * a.kv_heads + u.g) * D + e);
+            const float4 x = __ldg(f), y = __ldg(f + 1);
+            const uint4 b = make_uint4(pack_bits<DT>(x.x, x.y), pack_bits<DT>(x.z, x.w), pack_bits<DT>(y.x, y.y),
+                                       pack_bits<DT>(y.z, y.w));
+            if (keep && (value || u.half == 0)) {
+              const uint16_t* key = key_of(u.v.base + r);
+              if (key) *reinterpret_cast<uint4*>(const_cast<uint16_t*>(key) + (value ? half : 0) + e) = b;
+            }
+            return b;
+          };
+          fill(ks, 0, cols, ck, [&](int r, int e) { return draft(a.k_new, false, r, e); });
+          if (pw == 0) {
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k) {
+              const int r = 32 * k + lane;
+              const uint32_t h = __ballot_sync(~0u, !a.k_new && r < u.v.count && !key_of(u.v.base + r));
+              if (lane == 0) sh.hide[t & 7][k] = h;
+            }
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kfull[st]);
+          if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
+          fill(vs, 0, cols, cv, [&](int r, int e) { return draft(a.v_new, true, r, e); });
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.vfull[st]);
+          continue;
+        }
+        auto cached_piece = [&](bool value, int r, int e) {
+          const int tok = t0 + r;
+          if (tok < lo || tok >= hi || e >= (value ? dh : D)) return zero;
+          const uint16_t* key = key_of(tok);
+          return key ? *reinterpret_cast<const uint4*>(key + (value ? half + d0 : 0) + e) : zero;
+        };
+        if (!boxes) {
+          fill(ks, 0, cols, ck, [&](int r, int e) { return cached_piece(false, r, e); });
+          if (pw == 0) {
+#pragma unroll
+            for (int k = 0; k < TN / 32; ++k) {
+              const int tok = t0 + 32 * k + lane;
+              const uint32_t h = __ballot_sync(~0u, 32 * k + lane < cols && tok >= lo && tok < hi && !key_of(tok));
+              if (lane == 0) sh.hide[t & 7][k] = h;
+            }
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kfull[st]);
+          if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
+          fill(vs, 0, cols, cv, [&](int r, int e) { return cached_piece(true, r, e); });
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.vfull[st]);
+          continue;
+        }
+        // TMA: box b's K where anything of it is seen, its V where all of it is; the V
+        // rows of the other boxes by hand
+        if (pw == 0 && lane < TN / 32) sh.hide[t & 7][lane] = 0;
+        auto order = [&](bool value, int panels, unsigned char* base, uint64_t* bar) {
+          const int e = pw + 3 * lane, b = min(e / panels, 31), p = e - b * panels;
+          const int pg = __shfl_sync(~0u, page, b), b0 = t0 + b * w.box;
+          const bool mine = e < nbox * panels &&
+                            (value ? b0 >= lo && b0 + w.box <= hi : b0 + w.box > lo && b0 < hi);
+          const int n = __popc(__ballot_sync(~0u, mine));
+          const bool lost = w.lose && blockIdx.x == 0 && t == 1 && !value;
+          __syncwarp();
+          if (lane == 0) mbar_expect(bar, (uint32_t)(n * w.box * 128));
+          __syncwarp();
+          if (mine && !(lost && e == 0)) {
+            const long long y = (((long long)pg * 2 + value) * a.kv_heads + u.g) * P + b0 % P;
+            tree_box(smem_u32(base + p * kPanelK + b * w.box * 128), &map, (value ? d0 : 0) + 64 * p, (int)y, bar);
+          }
+        };
+        order(false, pk, ks, &sh.kfull[st]);
+        if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
+        for (int b = 0; b < nbox; ++b) {
+          const int b0 = t0 + b * w.box;
+          if (b0 >= lo && b0 + w.box <= hi) continue;
+          fill(vs, b * w.box, (b + 1) * w.box, cv, [&](int r, int e) { return cached_piece(true, r, e); });
+        }
+        fence_async();
+        order(true, pv, vs, &sh.vfull[st]);
+      }
+    }
+  }
+#undef TREE_WAIT
+  tm_fence_before();
+  __syncthreads();
+  if (sh.bad) {  // copies and MMAs under way come to their end (2 s at most)
+    if (warp == 9)
+      for (int i = 0; i < S && i < t; ++i) {
+        const int k = i + ((t - 1 - i) / S) * S;
+        mbar_wait(&sh.kfull[i], (uint32_t)((k / S) & 1), 500000000ull);
+        mbar_wait(&sh.vfull[i], (uint32_t)((k / S) & 1), 500000000ull);
+      }
+    if (warp == 8) {
+      if (lane == 0) mma_commit(&sh.fin);
+      mbar_wait(&sh.fin, 0, 2000000000ull);
+    }
+    __syncthreads();
+  }
+  if (warp == 8) {
+    tm_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
 }
+
+// Joins the parts of the units that several blocks share: a warp per row.
+template <int DT, int DP>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeWork w) {
+  using C = TreeTile<DT, DP>;
+  constexpr int MR = C::MR, DV = C::DV;
+  pdl_enter();
+  const TreeArgs& a = w.a;
+  const TreeSpan sp = w.span[blockIdx.x];
+  if (!sp.some) return;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  TreeWalk<C::TN, MR> walk(w, sp.slot, sp.unit, 0, 0, 1, true);
+  const TreeUnit& u = walk.u;
+  if (r >= u.rows) return;
+  const int n = sp.last - blockIdx.x + 1, dh = min(DV, a.head_dim - u.half * 128);
+  float top = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const float* pr = w.part + ((size_t)(2 * (blockIdx.x + j) + (j == 0)) * MR + r) * (DV + 4);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(pr + DV));
+    const float4 x = 4 * lane < DV ? __ldcg(reinterpret_cast<const float4*>(pr + 4 * lane)) : o;
+    // a part of nothing that is seen has the sum 0
+    const float up = ml.y == 0.f ? top : fmaxf(top, ml.x), ref = up == -INFINITY ? 0.f : up;
+    const float was = part_weight(top - ref), is = ml.y == 0.f ? 0.f : part_weight(ml.x - ref);
+    o.x = fmaf(x.x, is, o.x * was);
+    o.y = fmaf(x.y, is, o.y * was);
+    o.z = fmaf(x.z, is, o.z * was);
+    o.w = fmaf(x.w, is, o.w * was);
+    l = fmaf(ml.y, is, l * was);
+    top = up;
+  }
+  const int R = u.row0 + r, draft = R / a.group;
+  const size_t out = ((size_t)u.slot * a.drafts + draft) * a.heads + u.g * a.group + R - draft * a.group;
+  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+  if (4 * lane < dh)
+    *reinterpret_cast<float4*>(a.y + out * a.head_dim + u.half * 128 + 4 * lane) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (lane == 0 && a.lse && u.half == 0) a.lse[out] = (top + log2f(l)) * kLn2;
+}
+
+template <int DT, int DP>
+static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const DevInfo& di, pi_stream stream) {
+  using C = TreeTile<DT, DP>;
+  constexpr int smem = tree_smem<DT, DP>();
+  static_assert(smem <= 232448, "shared memory");
+  pi_status st = ensure_smem(reinterpret_cast<const void*>(tree_kernel<DT, DP>), smem);
+  if (st != PI_OK) return st;
+  // all blocks that are resident together, or fewer where the longest slots that the
+  // tables and the window allow cannot use them
+  const TreeArgs& a = w.a;
+  long long seen = (long long)a.max_pages * a.page_tokens;
+  if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
+  const long long units = (long long)a.slots * a.kv_heads * ((a.drafts * a.group + C::MR - 1) / C::MR) * w.halves;
+  const long long most = seen / C::TN + 4;  // tiles of a unit
+  const bool whole = most <= kTreeWhole;
+  const long long useful = whole ? units : units * (most + kTreeCost);
+  long long grid = di.sms < kTreeGrid ? di.sms : kTreeGrid;
+  if (grid > useful) grid = useful;
+  st = launch(tree_kernel<DT, DP>, dim3((unsigned)grid), kTreeThreads, smem, stream, w, map);
+  if (st != PI_OK || whole || grid < 2) return st;
+  const int rows = a.drafts * a.group < C::MR ? a.drafts * a.group : C::MR;
+  return launch(tree_join_kernel<DT, DP>, dim3((unsigned)(grid - 1), (unsigned)((rows + 7) / 8)), 256, 0, stream, w);
+}
+
+// Map over a layer's rows (K and V rows of every page and kv head): boxes of 64
+// elements of `box` rows, 128-byte swizzle, zeros past a row's end.
+static bool tree_map(CUtensorMap* m, void* base, long long rows, int head_dim, int box) {
+  const EncodeFn encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)head_dim * 2};
+  const cuuint32_t boxes[2] = {64u, (cuuint32_t)box}, steps[2] = {1u, 1u};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, boxes, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kTreeSpans = (kTreeGrid * sizeof(TreeSpan) + kAlign - 1) / kAlign * kAlign;
 
 }  // namespace pis
 
@@ -334,7 +1228,8 @@ extern "C" {
 size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t heads, int32_t drafts) {
   if (check_cache(cache) != PI_OK || slots < 1 || slots > PI_CACHE_MAX_SLOTS) return 0;
   if (heads < 1 || heads > kMaxHeads || heads % cache->kv_heads || drafts < 1 || drafts > PI_TREE_MAX) return 0;
-  return kAlign;
+  const int dv = cache->head_dim <= 64 ? 64 : 128;
+  return kTreeSpans + (size_t)kTreeGrid * 2 * (cache->head_dim > 128 ? 64 : 128) * (dv + 4) * 4;
 }
 
 pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots, int32_t heads,
@@ -352,6 +1247,7 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   if (drafts < 1 || drafts > PI_TREE_MAX || window < 0 || sinks < 0) return PI_ERR_SHAPE;
   if (!q || !table || !len || !pool || !y || !dev_status || !ws || !k_new != !v_new) return PI_ERR_NULL;
   if (!all_aligned(parent, count, q, k_new, v_new, table, len, pool, y, lse, dev_status, ws)) return PI_ERR_ALIGN;
+  const int lose = 0;
   if (ws_bytes < pi_tree_workspace_size(cache, slots, heads, drafts)) return PI_ERR_WORKSPACE;
   TreeArgs a{};
   a.q = q;
@@ -377,42 +1273,25 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   a.window = window;
   a.sinks = sinks;
   a.scale = scale * 1.4426950408889634f;
-  const long long rows = (long long)slots * drafts * heads, blocks = (rows + 3) / 4;
-  return launch(C.dtype == PI_F16 ? tree_rows_kernel<0> : tree_rows_kernel<1>,
-                dim3((unsigned)(blocks < 65536 ? blocks : 65536)), 128, 0, stream, a);
-}
-
-pi_status pi_tree_accept(const pi_cache_desc* cache, int32_t slots, int32_t max_pages, int32_t drafts,
-                         const int32_t* parent, const int32_t* count, const int32_t* tokens,
-                         const int32_t* choice, const int32_t* table, const int32_t* len, void* pool,
-                         int32_t* len_out, int32_t* path, int32_t* accepted, int32_t* next,
-                         int32_t* dev_status, pi_stream stream) {
-  pi_status st = check_cache(cache);
-  if (st != PI_OK) return st;
-  const pi_cache_desc& C = *cache;
-  st = check_slots(C, slots, max_pages);
-  if (st != PI_OK) return st;
-  if (drafts < 1 || drafts > PI_TREE_MAX) return PI_ERR_SHAPE;
-  if (!tokens || !choice || !table || !len || !len_out || !path || !accepted || !next || !dev_status)
-    return PI_ERR_NULL;
-  if (!all_aligned(parent, count, tokens, choice, table, len, pool, len_out, path, accepted, next, dev_status))
-    return PI_ERR_ALIGN;
-  // every block of a slot reads what these hold
-  for (const void* out : {(const void*)len_out, (const void*)path, (const void*)accepted, (const void*)next})
-    for (const void* in : {(const void*)parent, (const void*)count, (const void*)tokens, (const void*)choice,
-                           (const void*)table, (const void*)len})
-      if (out == in) return PI_ERR_SHAPE;
-  AcceptArgs a{parent, count, tokens, choice, table, len, static_cast<uint16_t*>(pool), len_out, path, accepted,
-               next, dev_status, slots, drafts, max_pages, C.layers, C.kv_heads, C.head_dim, C.page_tokens,
-               C.pages, 1};
+  TreeWork w{};
+  w.a = a;
+  w.span = static_cast<TreeSpan*>(ws);
+  w.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTreeSpans);
+  w.halves = C.head_dim > 128 ? 2 : 1;
+  w.limit_ns = wait_limit();
+  w.lose = lose;
+  const long long rows = (long long)C.pages * 2 * C.kv_heads * C.page_tokens;
+  CUtensorMap map = {};
+  w.box = C.page_tokens % 16 ? 8 : 16;
+  w.tma = C.page_tokens % 8 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
+          tree_map(&map, a.pool, rows, C.head_dim, w.box);
   DevInfo di;
   st = dev_info(&di);
   if (st != PI_OK) return st;
-  // enough blocks to fill the GPU, while each thread has a piece of the rows
-  const long long work = pool ? (2ll * C.layers * C.kv_heads * (C.head_dim / 8) + kAcceptThreads - 1) / kAcceptThreads : 1;
-  const long long fill = (8ll * di.sms + slots - 1) / slots;
-  a.blocks = (int)(work < fill ? work : fill);
-  return launch(tree_accept_kernel, dim3((unsigned)(a.blocks * slots)), kAcceptThreads, 0, stream, a);
+  const bool f16 = C.dtype == PI_F16;
+  if (C.head_dim <= 64) return f16 ? launch_tree<0, 64>(w, map, di, stream) : launch_tree<1, 64>(w, map, di, stream);
+  if (C.head_dim <= 128) return f16 ? launch_tree<0, 128>(w, map, di, stream) : launch_tree<1, 128>(w, map, di, stream);
+  return f16 ? launch_tree<0, 256>(w, map, di, stream) : launch_tree<1, 256>(w, map, di, stream);
 }
 
 }  // extern "C"
