@@ -34,8 +34,6 @@
 
 namespace pis {
 
-typedef unsigned long long u64;
-
 struct ScoreArgs {
   const void* logits;
   long long stride;
@@ -152,28 +150,6 @@ __device__ __forceinline__ void add_one(Sums& a, float ref, float x) {
   const float d = floor_nan(distance(x, ref)), e = ex2(d);
   a.s += e;
   a.t = fmaf(e, d, a.t);
-}
-
-// Two fp32 values in one register pair.
-__device__ __forceinline__ u64 pair(float x, float y) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 halves(u64 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 template <int DT>

@@ -27,7 +27,6 @@
 namespace pis {
 
 namespace cg = cooperative_groups;
-typedef unsigned long long u64;
 
 struct SampleArgs {
   const void* logits;

@@ -262,6 +262,35 @@ constexpr float kLn2 = 0.6931471805599453f;
 // stays what it is (2^-126 of a finite one changes nothing).
 __device__ __forceinline__ float part_weight(float below) { return fmaxf(ex2(below), 0x1p-126f); }
 
+typedef unsigned long long u64;
+
+// Two fp32 values in one register pair.
+__device__ __forceinline__ u64 pair(float x, float y) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 halves(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // a / b for a >= 0, b > 0: in 32 bits where a allows it.
 __device__ __forceinline__ long long quotient(long long a, int b) {
   return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);

@@ -192,10 +192,12 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 // low parts first.  A tile's O is read back and added to fp32 registers with a
 // rounded add: the tensor cores' own sums would drift over a long cache.
 //
-// Roles of a block's 12 warps.  0-3: load Q, softmax; row = thread.  4-7: add the
-// tiles' O, one row per thread, and write.  8: issues the MMAs.  9-11: fill K and
-// V: whole boxes of BR tokens by TMA, everything else (drafts, the ends of what is
-// seen, odd page sizes) by hand, with zeros for values nobody sees.
+// Roles of a block's 12 warps.  0-7: load Q, softmax, and add up O; a thread has
+// half a row, warps w and w + 4 the same rows, which share their maximum.  8:
+// issues the MMAs: S of the next tile, then O of the last, so that the products run
+// while the warps 0-7 are at the tile in between.  9-11: fill K and V: whole boxes of
+// tokens by TMA, everything else (drafts, the ends of what is seen, odd page sizes)
+// by hand, with zeros for values nobody sees.
 //
 // Operands that are not finite.  Rows whose sums come out NaN or infinite are
 // gone through again in fp32, token by token, by the warp that would write them.
@@ -207,7 +209,6 @@ struct TreeTile {
   static constexpr int NP = DT == 0 ? 2 : 3;       // parts of q and p
   static constexpr int S = DP == 64 ? 4 : DP == 256 && DT == 0 ? 3 : 2;  // stages
   static constexpr int NO = DT == 1 && DP == 128 ? 1 : 2;  // O tiles in tensor memory
-  static constexpr int NA = NO + 2;
   static constexpr int kQ = MR * DP * 2, kK = TN * DP * 2, kV = TN * DV * 2;  // bytes
   static constexpr int kStages = NP * kQ, kMisc = kStages + S * (kK + kV);
   // tensor-memory columns: two S tiles, whose place the first parts of P take; the
@@ -220,18 +221,16 @@ constexpr int kTreeGrid = 192;   // most blocks
 constexpr int kTreeCost = 1;     // a unit's fixed cost, in tiles
 constexpr int kTreeWhole = 6;    // units of at most this many tiles are not split
 constexpr int kTreeShare = 3;    // least share of a block
+constexpr int kTreeHide = 8;     // more than the tiles between the filling of K and the softmax
 
-// NA: rescaling factors in flight; the sums may be that many tiles behind
-template <int NA>
 struct TreeShared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[2], pfull[2], ofull[2], oempty[2];
-  uint64_t qfull, lfull, lempty, fin;
+  uint64_t pair[4], qfull, fin;
   uint32_t taddr;
   int bad;
-  uint32_t hide[8][4];   // tokens of a tile whose page is out of range
-  float l[128], m[128];  // a segment's sums and reference
+  uint32_t hide[kTreeHide][4];  // tokens of a tile whose page is out of range
   union {
-    float alpha[NA][128];
+    float top[2][2][128];  // rows' maxima, of a tile's two halves; at a segment's end their sums
     struct {
       long long sum[12], len[12];
       int most[12];
@@ -240,15 +239,14 @@ struct TreeShared {
     } scan;
   };
 };
-template <int NA>
-struct TreeSharedScale : TreeShared<NA> {
+struct TreeSharedScale : TreeShared {
   float qs[2][128];  // rows' 2^-e of q (fp16)
 };
-template <int DT, int NA>
-using TreeSharedOf = std::conditional_t<DT == 0, TreeSharedScale<NA>, TreeShared<NA>>;
+template <int DT>
+using TreeSharedOf = std::conditional_t<DT == 0, TreeSharedScale, TreeShared>;
 template <int DT, int DP>
 __host__ __device__ constexpr int tree_smem() {
-  return TreeTile<DT, DP>::kMisc + (int)sizeof(TreeSharedOf<DT, TreeTile<DT, DP>::NA>);
+  return TreeTile<DT, DP>::kMisc + (int)sizeof(TreeSharedOf<DT>);
 }
 
 struct TreeSpan {  // a unit that begins in a block and ends in a later one
@@ -259,7 +257,10 @@ struct TreeWork {
   TreeSpan* span;  // [grid]
   float* part;     // [grid][2][MR][DV + 4]
   int halves;      // units of V's columns
-  int tma, box;    // tiles come as TMA boxes; their rows
+  int tma;         // tiles come as TMA boxes
+  int box, edge;   // rows of a box: in tiles that are seen whole, in others
+  int align;       // tokens that a window's first tile begins at a multiple of
+  int page_shift;  // log2(page_tokens), or -1
   unsigned long long limit_ns;
   int lose;        // self-test: block 0's first box is never ordered
 };
@@ -291,6 +292,14 @@ __device__ __forceinline__ uint32_t tree_idesc(int n, bool b_nmajor) {
   return (1u << 4) | ((uint32_t)DT << 7) | ((uint32_t)DT << 10) | (b_nmajor ? 1u << 16 : 0u) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+// True in one lane of the warp, the same one every time.
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -311,7 +320,13 @@ __device__ __forceinline__ void mma_commit(uint64_t* m) {
 }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The values of the loads before it may be used behind it.
+template <int N>
+__device__ __forceinline__ void tm_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_ld32(float* v, uint32_t t) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -332,14 +347,28 @@ __device__ __forceinline__ void tm_ld16(float* v, uint32_t t) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t));
 }
-__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
+// Two fp32 values rounded to 16 bits in one instruction (two conversions take four
+// times as long as the packed one), and what that left.
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float x, float y) {
+  uint32_t r;
+  if (DT == 0) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ u64 left2(u64 v, uint32_t r) {
+  float2 h;
+  if (DT == 0) h = __half22float2(*reinterpret_cast<const __half2*>(&r));
+  else h = make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  return fma2(pair(h.x, h.y), pair(-1.f, -1.f), v);
+}
 // A unit and its tiles.
 struct TreeUnit {
   int slot, unit;  // number within the slot: (g, rt, half)
@@ -348,8 +377,8 @@ struct TreeUnit {
   int start, firsts, tiles; // first token of the window's tiles; tiles of the first tokens; all
 };
 template <int TN>
-__device__ __forceinline__ int tree_tiles(const TreeSlot& v) {
-  return 1 + (v.first + TN - 1) / TN + (v.base > v.tail ? (v.base - (v.tail & ~15) + TN - 1) / TN : 0);
+__device__ __forceinline__ int tree_tiles(const TreeWork& w, const TreeSlot& v) {
+  return 1 + (v.first + TN - 1) / TN + (v.base > v.tail ? (v.base - (v.tail & -w.align) + TN - 1) / TN : 0);
 }
 __device__ __forceinline__ int tree_units(const TreeWork& w, const TreeSlot& v, int mr) {
   return v.count ? w.a.kv_heads * ((v.count * w.a.group + mr - 1) / mr) * w.halves : 0;
@@ -359,14 +388,12 @@ template <int TN, int MR>
 struct TreeWalk {
   const TreeWork& w;
   TreeUnit u;
-  long long at, end;  // of the unit on the line; of the share
-  long long from;     // where the share begins
+  long long at, end;  // from the share's begin: of the unit on the line, of the share's end
   bool whole;
   int units;          // of the slot
   int tile0, tile1;
-  __device__ __forceinline__ TreeWalk(const TreeWork& w, int slot, int unit, long long at, long long from,
-                                      long long end, bool whole)
-      : w(w), at(at), end(end), from(from), whole(whole) {
+  __device__ __forceinline__ TreeWalk(const TreeWork& w, int slot, int unit, long long at, long long end, bool whole)
+      : w(w), at(at), end(end), whole(whole) {
     u.slot = slot;
     u.unit = unit;
     if (at < end) open();
@@ -374,9 +401,9 @@ struct TreeWalk {
   __device__ __forceinline__ void open() {
     u.v = tree_slot(w.a, u.slot);
     units = tree_units(w, u.v, MR);
-    u.start = u.v.tail & ~15;
+    u.start = u.v.tail & -w.align;
     u.firsts = (u.v.first + TN - 1) / TN;
-    u.tiles = tree_tiles<TN>(u.v);
+    u.tiles = tree_tiles<TN>(w, u.v);
     fit();
   }
   __device__ __forceinline__ void fit() {
@@ -390,8 +417,8 @@ struct TreeWalk {
       tile0 = 0;
       tile1 = u.tiles;
     } else {
-      const long long a0 = from - at - kTreeCost, a1 = end - at - kTreeCost;
-      tile0 = a0 > 0 ? (int)a0 : 0;
+      const long long a1 = end - at - kTreeCost;
+      tile0 = at < -kTreeCost ? (int)(-at - kTreeCost) : 0;
       tile1 = a1 < u.tiles ? (int)a1 : u.tiles;
     }
   }
@@ -471,7 +498,7 @@ __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, const TreeUnit& u
 // The segment [tile0, tile1) of row r once more, in fp32; the warp's lanes hold the
 // columns 8 lane .. of it.
 template <int DT, int TN, int MR>
-__device__ __noinline__ RowSums tree_again(const TreeWork& w, const TreeUnit& u, int tile0, int tile1, int r) {
+__device__ __forceinline__ RowSums tree_again(const TreeWork& w, const TreeUnit& u, int tile0, int tile1, int r) {
   const TreeArgs& a = w.a;
   const TreeRow x = tree_row(a, u, r, [&](int j) { return __ldg(a.parent + (size_t)u.slot * a.drafts + j); });
   RowSums s = {-INFINITY, 0.f, {}};
@@ -486,12 +513,12 @@ __device__ __noinline__ RowSums tree_again(const TreeWork& w, const TreeUnit& u,
 
 template <int DT, int DP>
 __global__ void __launch_bounds__(kTreeThreads, 1)
-    tree_kernel(const __grid_constant__ TreeWork w, const __grid_constant__ CUtensorMap map) {
+    tree_kernel(const __grid_constant__ TreeWork w, const __grid_constant__ CUtensorMap map,
+                const __grid_constant__ CUtensorMap edge_map) {
   using C = TreeTile<DT, DP>;
   constexpr int TN = C::TN, MR = C::MR, DV = C::DV, NP = C::NP, S = C::S, NO = C::NO;
   constexpr int kPanelK = TN * 128, kPanelQ = MR * 128;  // bytes of 64 columns
-  constexpr int NA = C::NA;
-  using Shared = TreeSharedOf<DT, NA>;
+  using Shared = TreeSharedOf<DT>;
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kMisc);
   const TreeArgs& a = w.a;
@@ -509,13 +536,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pfull[i], 4);
+      mbar_init(&sh.pfull[i], 8);
       mbar_init(&sh.ofull[i], 1);
-      mbar_init(&sh.oempty[i], 4);
+      mbar_init(&sh.oempty[i], 8);
     }
-    mbar_init(&sh.qfull, 4);
-    mbar_init(&sh.lfull, 4);
-    mbar_init(&sh.lempty, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
+    mbar_init(&sh.qfull, 8);
     mbar_init(&sh.fin, 1);
     fence_mbar_init();
     sh.bad = 0;
@@ -532,7 +558,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int s = s0; s < s1; ++s) {
       const TreeSlot v = tree_slot(a, s);
       if (blockIdx.x == 0 && tree_slot_bad(a, s)) set_status(a.status, PI_ERR_INDEX);
-      const int n = tree_units(w, v, MR), t = tree_tiles<TN>(v);
+      const int n = tree_units(w, v, MR), t = tree_tiles<TN>(w, v);
       units += n;
       tiles += (long long)n * (t + kTreeCost);
       if (n) most = max(most, t);
@@ -577,7 +603,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (share0 >= at && share0 < at + (whole ? units : tiles) && share0 < share1) {
       for (int s = s0; s < s1; ++s) {
         const TreeSlot v = tree_slot(a, s);
-        const int n = tree_units(w, v, MR), len = whole ? 1 : tree_tiles<TN>(v) + kTreeCost;
+        const int n = tree_units(w, v, MR), len = whole ? 1 : tree_tiles<TN>(w, v) + kTreeCost;
         if (share0 < at + (long long)n * len) {
           sc.slot = s;
           sc.unit = (int)((share0 - at) / len);
@@ -601,7 +627,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tm_fence_after();
   }
   const uint32_t tmem = sh.taddr;
-  TreeWalk<TN, MR> walk(w, first_slot, first_unit, unit_at, share0, share1, whole);
+  TreeWalk<TN, MR> walk(w, first_slot, first_unit, unit_at - share0, share1 - share0, whole);
   const int kd = (D + 15) >> 4;  // steps of 16 along a row
   int t = 0;                     // tiles so far
   bool ok = true;
@@ -616,25 +642,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     break;                                                \
   }
 
-  if (warp < 4) {
-    // ---- Q, softmax
+  if (warp < 8) {
+    // ---- Q, softmax, O
+    constexpr int HC = TN / 2, HO = DV / 2;  // a half's columns of S, of O
+    const int h = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
     const float flip = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
     const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
     constexpr float kShift = DT == 0 ? 14.f : 0.f;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-    const int row = tid;
-    int seg = 0;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
+    int seg = 0, met = 0;
+    // The other half's value of the row; false where the wait ran out.
+    auto meet = [&](float& mine, float& theirs) {
+      sh.top[met & 1][h][row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pair[wq]);
+      if (!mbar_wait(&sh.pair[wq], (uint32_t)(met & 1), w.limit_ns)) return false;
+      theirs = sh.top[met & 1][1 - h][row];
+      ++met;
+      return true;
+    };
+    TreeSpan span{0, 0, 0, 0};
     for (; walk.more() && ok; walk.next()) {
       if (!walk.any()) continue;
       const TreeUnit& u = walk.u;
-      // rows warp, warp + 4, ...: split into parts
-      constexpr int E = DP / 32, B = 4;
+      // rows warp, warp + 8, ...: split into parts
+      constexpr int E = DP / 32, B = DP == 256 ? 2 : 4;
 #pragma unroll 1
-      for (int r0 = warp; r0 < u.rows; r0 += 4 * B) {
+      for (int r0 = warp; r0 < u.rows; r0 += 8 * B) {
         float x[B][E];
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-          const int r = r0 + 4 * b;
+          const int r = r0 + 8 * b;
           const int R = u.row0 + r, i = R / a.group;
           const float* q = a.q + (((size_t)u.slot * a.drafts + i) * a.heads + u.g * a.group + R - i * a.group) * D + E * lane;
           if (r < u.rows && E * lane < D) {
@@ -655,7 +693,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-          const int r = r0 + 4 * b;
+          const int r = r0 + 8 * b;
           if (r >= u.rows) break;
           if constexpr (DT == 0) {
             float top = 0.f;
@@ -695,7 +733,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.qfull);
       // the row's own draft
-      const bool live = 32 * warp < u.rows;
+      const bool live = 32 * wq < u.rows;
       int pa = -1, pb = -1;
       if (live && a.parent) {
         if (lane < u.v.count) pa = __ldg(a.parent + (size_t)u.slot * a.drafts + lane);
@@ -728,161 +766,159 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       TREE_WAIT(&sh.qfull, seg & 1);
       float scl = scale;
       if constexpr (DT == 0) scl = live && row < u.rows ? scale * sh.qs[seg & 1][row] : scale;
-      const int sinks = u.v.tail > 0 ? 0 : a.sinks;
-      float m = -INFINITY, ref = -INFINITY, l = 0.f;
-      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
-        const int buf = t & 1;
-        TREE_WAIT(&sh.sfull[buf], (t >> 1) & 1);
-        if (live) {
-          tm_fence_after();
-          const uint32_t src = lanes + (uint32_t)(buf * TN);
-          const int cols = walk.columns(i);
-          float v[TN];
-#pragma unroll
-          for (int k = 0; k < TN / 32; ++k)
-            if (32 * k < cols) tm_ld32(v + 32 * k, src + 32 * k);
-          // the columns that the row sees, as bits
-          uint32_t mask[TN / 32], all = ~0u;
-          if (i == 0) {
-#pragma unroll
-            for (int k = 0; k < TN / 32; ++k) mask[k] = k < 2 ? (uint32_t)(seen >> (32 * k)) : 0u;
-          } else {
-            int any_lo, hi;
-            const int t0 = walk.cached(i, any_lo, hi);
-            const int from = (i <= u.firsts ? 0 : lo) - t0, n = hi - t0, sink = sinks - t0;
-            auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
-#pragma unroll
-            for (int k = 0; k < TN / 32; ++k)
-              mask[k] = below(n - 32 * k) & (~below(from - 32 * k) | below(sink - 32 * k));
-          }
-#pragma unroll
-          for (int k = 0; k < TN / 32; ++k) {
-            mask[k] &= ~sh.hide[t & 7][k];
-            all &= mask[k];
-          }
-          tm_wait_ld();
-          if (!__all_sync(~0u, all == ~0u)) {
-#pragma unroll
-            for (int c = 0; c < TN; ++c) v[c] = mask[c >> 5] >> (c & 31) & 1u ? v[c] : -INFINITY;
-          }
-          float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int c = 4; c < TN; ++c) top[c & 3] = fmaxf(top[c & 3], v[c]);
-          const float up = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scl);
-          // weights are relative to the maximum less kShift, which rounding must not take
-          // far from it
-          const float at = up == -INFINITY ? 0.f : up;
-          float next = at - kShift;
-          if (!(at - next <= kShift + 1.f)) next = at;
-          const float alpha = m == -INFINITY ? 0.f : ex2(ref - next);
-          m = up;
-          ref = next;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < TN / 32; ++k) {
-            if (32 * k >= cols) continue;
-            uint32_t part[NP][16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float y = ex2(__fmul_rn(v[32 * k + 2 * c], scl) - next);
-              float z = ex2(__fmul_rn(v[32 * k + 2 * c + 1], scl) - next);
-              sum[c & 1] += y;
-              sum[2 + (c & 1)] += z;
-#pragma unroll
-              for (int p = 0; p < NP; ++p) {
-                part[p][c] = pack_bits<DT>(y, z);
-                y -= from_bits<DT>((uint16_t)part[p][c]);
-                z -= from_bits<DT>((uint16_t)(part[p][c] >> 16));
-              }
-            }
-            tm_st16(src + 16 * k, part[0]);
-            tm_st16(src + TN / 2 + 16 * k, part[1]);
-            if constexpr (NP == 3) tm_st16(lanes + C::kThird + buf * (TN / 2) + 16 * k, part[2]);
-          }
-          l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-          sh.alpha[t % NA][row] = alpha;
-          tm_wait_st();
-          tm_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pfull[buf]);
-      }
-      if (!ok) break;
-      if (seg > 0) TREE_WAIT(&sh.lempty, (seg - 1) & 1);
-      sh.l[row] = l;
-      sh.m[row] = ref;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.lfull);
       ++seg;
-    }
-  } else if (warp < 8) {
-    // ---- O
-    const int row = tid - 128;
-    const uint32_t lanes = tmem + ((uint32_t)(row & ~31) << 16) + C::kO;
-    int seg = 0;
-    TreeSpan span{0, 0, 0, 0};
-    for (; walk.more() && ok; walk.next()) {
-      if (!walk.any()) continue;
-      const TreeUnit& u = walk.u;
-      const bool live = (row & ~31) < u.rows;
-      const int dh = min(DV, D - u.half * 128);  // the unit's columns
-      float o[DV];
+      const int sinks = u.v.tail > 0 ? 0 : a.sinks;
+      float m = -INFINITY, ref = -INFINITY, l = 0.f, alpha = 0.f;
+      u64 o2[HO / 2];
 #pragma unroll
-      for (int c = 0; c < DV; ++c) o[c] = 0.f;
-      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
-        const int buf = t % NO;
-        TREE_WAIT(&sh.ofull[buf], (t / NO) & 1);
+      for (int c = 0; c < HO / 2; ++c) o2[c] = 0;
+      auto add_o = [&](int p, float factor) {  // tile p's O; false where the wait ran out
+        const int buf = p % NO;
+        if (!mbar_wait(&sh.ofull[buf], (uint32_t)((p / NO) & 1), w.limit_ns)) return false;
         if (live) {
           tm_fence_after();
-          const float alpha = sh.alpha[t % NA][row];
+          const u64 f2 = pair(factor, factor);
 #pragma unroll
-          for (int c0 = 0; c0 < DV; c0 += 16) {
-            float x[16];
-            tm_ld16(x, lanes + buf * DV + c0);
-            tm_wait_ld();
+          for (int c0 = 0; c0 < HO; c0 += 32) {
+            float x[32];
+            tm_ld32(x, lanes + C::kO + buf * DV + h * HO + c0);
+            tm_wait_ld<32>(x);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c0 + c] = fmaf(o[c0 + c], alpha, x[c]);
+            for (int c = 0; c < 16; ++c) o2[c0 / 2 + c] = fma2(o2[c0 / 2 + c], f2, pair(x[2 * c], x[2 * c + 1]));
           }
           tm_fence_before();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.oempty[buf]);
+        return true;
+      };
+      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
+        const int buf = t & 1;
+        TREE_WAIT(&sh.sfull[buf], (t >> 1) & 1);
+        const float before = alpha;
+        if (live) {
+          tm_fence_after();
+          const uint32_t src = lanes + (uint32_t)(buf * TN);
+          float v[HC];
+#pragma unroll
+          for (int k = 0; k < HC / 32; ++k) tm_ld32(v + 32 * k, src + h * HC + 32 * k);
+          // the columns that the row does not see
+          int any_lo = 0, hi = 0, t0 = 0;
+          if (i > 0) t0 = walk.cached(i, any_lo, hi);
+          const int from = i <= u.firsts ? 0 : lo;
+          bool all = i > 0 && t0 >= from && t0 + TN <= hi;
+#pragma unroll
+          for (int k = 0; k < HC / 32; ++k) all &= !sh.hide[t % kTreeHide][h * (HC / 32) + k];
+          tm_wait_ld<HC>(v);
+          if (!__all_sync(~0u, all)) {
+            auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
+#pragma unroll
+            for (int k = 0; k < HC / 32; ++k) {
+              const int word = h * (HC / 32) + k, at = t0 + 32 * word;
+              uint32_t mask = i > 0 ? below(hi - at) & (~below(from - at) | below(sinks - at))
+                                    : word < 2 ? (uint32_t)(seen >> (32 * word)) : 0u;
+              mask &= ~sh.hide[t % kTreeHide][word];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[32 * k + c] = mask >> c & 1u ? v[32 * k + c] : -INFINITY;
+            }
+          }
+          float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int c = 4; c < HC; ++c) top[c & 3] = fmaxf(top[c & 3], v[c]);
+          float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), theirs = 0.f;
+          if (!meet(mine, theirs)) {
+            gave_up();
+            break;
+          }
+          const float up = fmaxf(m, fmaxf(mine, theirs) * scl);
+          // weights are relative to the maximum less kShift, which rounding must not take
+          // far from it
+          const float at = up == -INFINITY ? 0.f : up;
+          float next = at - kShift;
+          if (!(at - next <= kShift + 1.f)) next = at;
+          alpha = m == -INFINITY ? 0.f : ex2(ref - next);
+          m = up;
+          ref = next;
+          const u64 scl2 = pair(scl, scl), next2 = pair(-next, -next);
+          u64 sum[2] = {0, 0};
+          const uint32_t dst = src + h * (HC / 2);
+#pragma unroll
+          for (int k = 0; k < HC / 16; ++k) {
+            uint32_t part[NP][8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float2 d = halves(add2(mul2(pair(v[16 * k + 2 * c], v[16 * k + 2 * c + 1]), scl2), next2));
+              u64 p = pair(ex2(d.x), ex2(d.y));
+              sum[c & 1] = add2(sum[c & 1], p);
+#pragma unroll
+              for (int i = 0; i < NP; ++i) {
+                const float2 f = halves(p);
+                part[i][c] = round2<DT>(f.x, f.y);
+                if (i + 1 < NP) p = left2<DT>(p, part[i][c]);
+              }
+            }
+            tm_st8(dst + 8 * k, part[0]);
+            tm_st8(dst + TN / 2 + 8 * k, part[1]);
+            if constexpr (NP == 3) tm_st8(lanes + C::kThird + buf * (TN / 2) + h * (HC / 2) + 8 * k, part[2]);
+          }
+          const float2 both = halves(add2(sum[0], sum[1]));
+          l = fmaf(l, alpha, both.x + both.y);
+          tm_wait_st();
+          tm_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pfull[buf]);
+        if (i > walk.tile0 && !add_o(t - 1, before)) {
+          gave_up();
+          break;
+        }
       }
       if (!ok) break;
-      TREE_WAIT(&sh.lfull, seg & 1);
-      const float l = sh.l[row], m = sh.m[row];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.lempty);
-      ++seg;
-      const bool begins = walk.begins(), ends = walk.ends();
-      if (begins && !ends) span = TreeSpan{u.slot, u.unit, line.block_of(walk.at + kTreeCost + u.tiles - 1), 1};
-      if (!live) continue;
-      bool again = false;
-      if (row < u.rows) {
-        again = !(fabsf(l) < INFINITY);
-#pragma unroll
-        for (int c = 0; c < DV; ++c) again |= c < dh && !(fabsf(o[c]) < INFINITY);
+      if (!add_o(t - 1, alpha)) {
+        gave_up();
+        break;
       }
+      const bool begins = walk.begins(), ends = walk.ends();
+      if (begins && !ends) span = TreeSpan{u.slot, u.unit, line.block_of(share0 + walk.at + kTreeCost + u.tiles - 1), 1};
+      if (!live) continue;
+      const int dh = min(DV, D - u.half * 128) - h * HO;  // the half's columns of the unit's
+      float o[HO];
+      bool odd = false;
+#pragma unroll
+      for (int c = 0; c < HO / 2; ++c) {
+        const float2 f = halves(o2[c]);
+        o[2 * c] = f.x;
+        o[2 * c + 1] = f.y;
+        odd |= 2 * c < dh && !(fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY);
+      }
+      float theirs = 0.f;
+      if (odd) l = NAN;  // for the other half too
+      if (!meet(l, theirs)) {
+        gave_up();
+        break;
+      }
+      l = h ? theirs + l : l + theirs;
+      const bool again = row < u.rows && !(l < INFINITY);
       const int R = u.row0 + row, draft = R / a.group;
       const size_t out = ((size_t)u.slot * a.drafts + draft) * a.heads + u.g * a.group + R - draft * a.group;
       float* part = w.part + ((size_t)(2 * blockIdx.x + begins) * MR + row) * (DV + 4);
       if (row < u.rows && !again) {
         if (begins && ends) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
-          float4* to = reinterpret_cast<float4*>(a.y + out * D + u.half * 128);
+          float4* to = reinterpret_cast<float4*>(a.y + out * D + u.half * 128 + h * HO);
 #pragma unroll
-          for (int c = 0; c < DV; c += 4)
+          for (int c = 0; c < HO; c += 4)
             if (c < dh) to[c / 4] = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
-          if (a.lse && u.half == 0) a.lse[out] = (m + log2f(l)) * kLn2;
+          if (a.lse && u.half == 0 && h == 0) a.lse[out] = (ref + log2f(l)) * kLn2;
         } else {
 #pragma unroll
-          for (int c = 0; c < DV; c += 4)
-            __stcg(reinterpret_cast<float4*>(part + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
-          __stcg(reinterpret_cast<float2*>(part + DV), make_float2(m, l));
+          for (int c = 0; c < HO; c += 4)
+            __stcg(reinterpret_cast<float4*>(part + h * HO + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+          if (h == 0) __stcg(reinterpret_cast<float2*>(part + DV), make_float2(ref, l));
         }
       }
       for (uint32_t left = __ballot_sync(~0u, again); left; left &= left - 1) {
-        const int r = (row & ~31) + __ffs(left) - 1;
+        const int r = 32 * wq + __ffs(left) - 1;
         const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, r);
         const float inv = s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
         const int Rr = u.row0 + r, dr = Rr / a.group, c = 8 * lane - 128 * u.half;
@@ -890,18 +926,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         float* pr = w.part + ((size_t)(2 * blockIdx.x + begins) * MR + r) * (DV + 4);
         const bool direct = begins && ends;
         const float f = direct ? inv : 1.f;
-        if (c >= 0 && c < dh) {
+        if (c >= h * HO && c < h * HO + HO && c < h * HO + dh) {
           float4* to = reinterpret_cast<float4*>(direct ? a.y + to_row * D + 8 * lane : pr + c);
           __stcg(to, make_float4(s.o[0] * f, s.o[1] * f, s.o[2] * f, s.o[3] * f));
           __stcg(to + 1, make_float4(s.o[4] * f, s.o[5] * f, s.o[6] * f, s.o[7] * f));
         }
-        if (lane == 0) {
+        if (lane == 0 && h == 0) {
           if (!direct) __stcg(reinterpret_cast<float2*>(pr + DV), make_float2(s.m, s.l));
           else if (a.lse && u.half == 0) a.lse[to_row] = (s.m + log2f(s.l)) * kLn2;
         }
       }
     }
-    if (row == 0) w.span[blockIdx.x] = span;
+    if (tid == 0) w.span[blockIdx.x] = span;
   } else if (warp == 8) {
     // ---- MMAs
     int seg = 0, cols_before = 0, nv_before = 0;
@@ -914,18 +950,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         return;
       }
       tm_fence_after();
-      if (lane == 0) {
-        const uint32_t vst = smem_u32(smem + C::kStages + st * (C::kK + C::kV) + C::kK);
+      if (elected()) {
+        const uint64_t vd = tree_desc(smem_u32(smem + C::kStages + st * (C::kK + C::kV) + C::kK), kPanelK);
         const uint32_t idesc = tree_idesc<DT>(nv, true);
         const uint32_t d = tmem + C::kO + ob * DV;
         bool add = false;
 #pragma unroll
         for (int part = NP - 1; part >= 0; --part) {
           const uint32_t pa = part == 2 ? tmem + C::kThird + buf * (TN / 2) : tmem + buf * TN + part * (TN / 2);
-          for (int ks = 0; ks < cols / 16; ++ks) {
-            mma_ts(d, pa + 8 * ks, tree_desc(vst + 2048 * ks, kPanelK), idesc, add);
-            add = true;
-          }
+#pragma unroll
+          for (int ks = 0; ks < TN / 16; ++ks)
+            if (16 * ks < cols) {
+              mma_ts(d, pa + 8 * ks, vd + (2048 >> 4) * ks, idesc, add);
+              add = true;
+            }
         }
         mma_commit(&sh.vempty[st]);
         mma_commit(&sh.ofull[ob]);
@@ -944,17 +982,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         TREE_WAIT(&sh.kfull[st], (t / S) & 1);
         tm_fence_after();
-        if (lane == 0) {
-          const uint32_t qs = smem_u32(smem), ks = smem_u32(smem + C::kStages + st * (C::kK + C::kV));
+        if (elected()) {
+          const uint64_t qd = tree_desc(smem_u32(smem), 16);
+          const uint64_t kdesc = tree_desc(smem_u32(smem + C::kStages + st * (C::kK + C::kV)), 16);
           const uint32_t idesc = tree_idesc<DT>(cols, false);
           bool add = false;
 #pragma unroll
           for (int part = NP - 1; part >= 0; --part)
-            for (int k = 0; k < kd; ++k) {
-              mma_ss(tmem + buf * TN, tree_desc(qs + part * C::kQ + (k >> 2) * kPanelQ + (k & 3) * 32, 16),
-                     tree_desc(ks + (k >> 2) * kPanelK + (k & 3) * 32, 16), idesc, add);
-              add = true;
-            }
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+              if (k < kd) {
+                mma_ss(tmem + buf * TN, qd + ((part * C::kQ + (k >> 2) * kPanelQ + (k & 3) * 32) >> 4),
+                       kdesc + (((k >> 2) * kPanelK + (k & 3) * 32) >> 4), idesc, add);
+                add = true;
+              }
           mma_commit(&sh.kempty[st]);
           mma_commit(&sh.sfull[buf]);
         }
@@ -976,145 +1017,137 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int pk = (D + 63) >> 6, pv = (dh + 63) >> 6;       // panels
       const int ck = 2 * kd, cv = ((dh + 15) & ~15) >> 3;      // 16-byte pieces of a row
       const size_t half = (size_t)a.kv_heads * P * D;          // K to V in a page
+      auto index_of = [&](int tok) { return w.page_shift >= 0 ? tok >> w.page_shift : tok / P; };
       auto key_of = [&](int tok) -> const uint16_t* {          // null: page out of range
-        const int j = tok / P;
+        const int j = index_of(tok);
         const int page = checked_page(__ldg(a.table + (size_t)u.slot * a.max_pages + j), a.pages, a.status);
         return page < 0 ? nullptr : a.pool + (((size_t)page * 2 * a.kv_heads + u.g) * P + tok - j * P) * D;
       };
+      // Lane b's box of a tile: whether it is seen, its page and its row of the pool; read
+      // a tile ahead.
+      struct Boxes {
+        int t0, lo, hi, box, page, row;
+        bool whole, some;
+      };
+      auto boxes_of = [&](int i) {
+        Boxes x{u.v.base, u.v.base, u.v.base + u.v.count, 0, 0, 0, false, false};  // the drafts
+        if (i == 0 || i >= walk.tile1) return x;
+        x.t0 = walk.cached(i, x.lo, x.hi);
+        if (!w.tma) return x;
+        x.whole = x.t0 >= x.lo && x.t0 + TN <= x.hi;
+        x.box = x.whole ? w.box : w.edge;
+        const int b0 = x.t0 + lane * x.box;
+        x.some = lane * x.box < TN && b0 + x.box > x.lo && b0 < x.hi;
+        if (x.some) {
+          const int j = index_of(b0);
+          x.page = __ldg(a.table + (size_t)u.slot * a.max_pages + j);
+          x.row = b0 - j * P;
+        }
+        return x;
+      };
+      Boxes ahead = boxes_of(walk.tile0);
       for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
-        const int st = t % S, cols = walk.columns(i);
+        const int st = t % S;
         unsigned char* const ks = smem + C::kStages + st * (C::kK + C::kV);
         unsigned char* const vs = ks + C::kK;
-        auto place = [&](unsigned char* base, int r, int c) {  // piece c of row r
-          return reinterpret_cast<uint4*>(base + (c >> 3) * kPanelK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        };
-        // rows [r0, r1) of K or V by hand: load(row, first element) gives a piece
-        auto fill = [&](unsigned char* base, int r0, int r1, int pieces, auto load) {
-          const int n = (r1 - r0) * pieces;
-          for (int e0 = pt; e0 < n; e0 += 96 * 4) {
-            uint4 x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = e0 + 96 * k, r = e / pieces;
-              if (e < n) x[k] = load(r0 + r, 8 * (e - r * pieces));
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = e0 + 96 * k, r = e / pieces;
-              if (e < n) *place(base, r0 + r, e - r * pieces) = x[k];
-            }
-          }
-        };
-        const uint4 zero = make_uint4(0, 0, 0, 0);
         const uint32_t kpar = (uint32_t)(((t / S) - 1) & 1);
-        int t0 = 0, lo = 0, hi = 0, page = 0;
-        bool boxes = false;
-        const int nbox = cols / w.box;
-        if (i > 0) {
-          t0 = walk.cached(i, lo, hi);
-          if (w.tma) {
-            const int b0 = t0 + lane * w.box;
-            bool good = true;
-            if (lane < nbox && b0 + w.box > lo && b0 < hi) {
-              page = __ldg(a.table + (size_t)u.slot * a.max_pages + b0 / P);
-              good = (unsigned)page < (unsigned)a.pages;
-            }
-            boxes = __all_sync(~0u, good);
-          }
-        }
-        if (t >= S) TREE_WAIT(&sh.kempty[st], kpar);
-        if (i == 0) {
-          // the drafts: rounded to the cache's type where they are new, and stored
-          const bool keep = a.k_new && u.row0 == 0;
-          auto draft = [&](const float* from, bool value, int r, int e) {
-            if (r >= u.v.count || e >= (value ? dh : D)) return zero;
-            if (value) e += d0;
-            if (!a.k_new) {
-              const uint16_t* key = key_of(u.v.base + r);
-              return key ? *reinterpret_cast<const uint4*>(key + (value ? half : 0) + e) : zero;
-            }
-            const float4* f = reinterpret_cast<const float4*>(
-                from + (((size_t)u.slot * a.drafts + r) * a.kv_heads + u.g) * D + e);
-            const float4 x = __ldg(f), y = __ldg(f + 1);
-            const uint4 b = make_uint4(pack_bits<DT>(x.x, x.y), pack_bits<DT>(x.z, x.w), pack_bits<DT>(y.x, y.y),
-                                       pack_bits<DT>(y.z, y.w));
-            if (keep && (value || u.half == 0)) {
-              const uint16_t* key = key_of(u.v.base + r);
-              if (key) *reinterpret_cast<uint4*>(const_cast<uint16_t*>(key) + (value ? half : 0) + e) = b;
-            }
-            return b;
-          };
-          fill(ks, 0, cols, ck, [&](int r, int e) { return draft(a.k_new, false, r, e); });
-          if (pw == 0) {
-#pragma unroll
-            for (int k = 0; k < TN / 32; ++k) {
-              const int r = 32 * k + lane;
-              const uint32_t h = __ballot_sync(~0u, !a.k_new && r < u.v.count && !key_of(u.v.base + r));
-              if (lane == 0) sh.hide[t & 7][k] = h;
-            }
-          }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.kfull[st]);
-          if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
-          fill(vs, 0, cols, cv, [&](int r, int e) { return draft(a.v_new, true, r, e); });
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.vfull[st]);
-          continue;
-        }
-        auto cached_piece = [&](bool value, int r, int e) {
+        const Boxes now = ahead;
+        const int t0 = now.t0, lo = now.lo, hi = now.hi;
+        const int cols = i == 0 ? (u.v.count + 15) & ~15 : min(TN, (hi - t0 + 15) & ~15);
+        const bool boxes = now.box && __all_sync(~0u, !now.some || (unsigned)now.page < (unsigned)a.pages);
+        const bool fresh = i == 0 && a.k_new;
+        ahead = boxes_of(i + 1);
+        const int box_row = (now.page * 2 * a.kv_heads + u.g) * P + now.row;  // of K
+        // Rows [r0, r1) of K or V by hand, zeros where nobody sees a row or its page is
+        // out of range.  New drafts are rounded to the cache's type, and stored by the
+        // first unit of their kv head.
+        auto piece = [&](bool value, int r, int e) {
           const int tok = t0 + r;
-          if (tok < lo || tok >= hi || e >= (value ? dh : D)) return zero;
-          const uint16_t* key = key_of(tok);
-          return key ? *reinterpret_cast<const uint4*>(key + (value ? half + d0 : 0) + e) : zero;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (tok < lo || tok >= hi || e >= (value ? dh : D)) return x;
+          if (value) e += d0;
+          const uint16_t* key = nullptr;
+          if (!fresh || (u.row0 == 0 && (value || u.half == 0))) {
+            key = key_of(tok);
+            if (key && value) key += half;
+          }
+          if (fresh) {
+            const float4* f = reinterpret_cast<const float4*>(
+                (value ? a.v_new : a.k_new) + (((size_t)u.slot * a.drafts + r) * a.kv_heads + u.g) * D + e);
+            const float4 y = __ldg(f), z = __ldg(f + 1);
+            x = make_uint4(round2<DT>(y.x, y.y), round2<DT>(y.z, y.w), round2<DT>(z.x, z.y), round2<DT>(z.z, z.w));
+            if (key) *reinterpret_cast<uint4*>(const_cast<uint16_t*>(key) + e) = x;
+          } else if (key) {
+            x = *reinterpret_cast<const uint4*>(key + e);
+          }
+          return x;
         };
-        if (!boxes) {
-          fill(ks, 0, cols, ck, [&](int r, int e) { return cached_piece(false, r, e); });
-          if (pw == 0) {
+        auto fill = [&](bool value, int r0, int r1) {
+          const int pieces = value ? cv : ck, n = (r1 - r0) * pieces;
+          unsigned char* base = value ? vs : ks;
+#pragma unroll 1
+          for (int e0 = pt; e0 < n; e0 += 96 * 2) {
+            uint4 x[2];
+            int r[2], c[2];
 #pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int e = min(e0 + 96 * k, n - 1);
+              r[k] = e / pieces;
+              c[k] = e - r[k] * pieces;
+              r[k] += r0;
+              x[k] = piece(value, r[k], 8 * c[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4*>(base + (c[k] >> 3) * kPanelK + r[k] * 128 + (((c[k] & 7) ^ (r[k] & 7)) << 4)) = x[k];
+          }
+        };
+        if (t >= S) TREE_WAIT(&sh.kempty[st], kpar);
+        if (pw == 0) {
+          if (boxes || fresh) {
+            if (lane < TN / 32) sh.hide[t % kTreeHide][lane] = 0;
+          } else {
+#pragma unroll 1
             for (int k = 0; k < TN / 32; ++k) {
               const int tok = t0 + 32 * k + lane;
-              const uint32_t h = __ballot_sync(~0u, 32 * k + lane < cols && tok >= lo && tok < hi && !key_of(tok));
-              if (lane == 0) sh.hide[t & 7][k] = h;
+              const uint32_t h = __ballot_sync(~0u, tok >= lo && tok < hi && !key_of(tok));
+              if (lane == 0) sh.hide[t % kTreeHide][k] = h;
             }
           }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.kfull[st]);
-          if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
-          fill(vs, 0, cols, cv, [&](int r, int e) { return cached_piece(true, r, e); });
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.vfull[st]);
-          continue;
         }
-        // TMA: box b's K where anything of it is seen, its V where all of it is; the V
-        // rows of the other boxes by hand
-        if (pw == 0 && lane < TN / 32) sh.hide[t & 7][lane] = 0;
+        if (!boxes) fill(false, 0, cols);
+        // TMA: a box's K where anything of it is seen, its V where all of it is; the V rows
+        // of the other boxes by hand
         auto order = [&](bool value, int panels, unsigned char* base, uint64_t* bar) {
-          const int e = pw + 3 * lane, b = min(e / panels, 31), p = e - b * panels;
-          const int pg = __shfl_sync(~0u, page, b), b0 = t0 + b * w.box;
-          const bool mine = e < nbox * panels &&
-                            (value ? b0 >= lo && b0 + w.box <= hi : b0 + w.box > lo && b0 < hi);
+          const int e = pw + 3 * lane, b = panels == 1 ? e : panels == 2 ? e >> 1 : panels == 4 ? e >> 2 : e / panels;
+          const int p = e - b * panels, y = __shfl_sync(~0u, box_row, b & 31) + (value ? a.kv_heads * P : 0);
+          const int r = b * now.box;  // of the tile
+          const bool mine = boxes && r < cols && (now.whole || (value ? t0 + r >= lo && t0 + r + now.box <= hi
+                                                                      : t0 + r + now.box > lo && t0 + r < hi));
           const int n = __popc(__ballot_sync(~0u, mine));
-          const bool lost = w.lose && blockIdx.x == 0 && t == 1 && !value;
+          if (lane == 0) mbar_expect(bar, (uint32_t)(n * now.box * 128));
           __syncwarp();
-          if (lane == 0) mbar_expect(bar, (uint32_t)(n * w.box * 128));
-          __syncwarp();
-          if (mine && !(lost && e == 0)) {
-            const long long y = (((long long)pg * 2 + value) * a.kv_heads + u.g) * P + b0 % P;
-            tree_box(smem_u32(base + p * kPanelK + b * w.box * 128), &map, (value ? d0 : 0) + 64 * p, (int)y, bar);
-          }
+          if (mine && !(w.lose && blockIdx.x == 0 && t == 1 && !value && e == 0))
+            tree_box(smem_u32(base + p * kPanelK + r * 128), now.whole ? &map : &edge_map, (value ? d0 : 0) + 64 * p, y, bar);
         };
+        fence_async();
+        __syncwarp();
         order(false, pk, ks, &sh.kfull[st]);
         if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
-        for (int b = 0; b < nbox; ++b) {
-          const int b0 = t0 + b * w.box;
-          if (b0 >= lo && b0 + w.box <= hi) continue;
-          fill(vs, b * w.box, (b + 1) * w.box, cv, [&](int r, int e) { return cached_piece(true, r, e); });
+        if (!now.whole) {
+#pragma unroll 1
+          for (int r = 0; r < cols;) {
+            const int b0 = t0 + r, n = boxes ? now.box : cols;
+            if (!boxes || b0 < lo || b0 + now.box > hi) fill(true, r, r + n);
+            r += n;
+          }
+          fence_async();
+          __syncwarp();
+        } else if (!boxes) {
+          fill(true, 0, cols);
+          fence_async();
+          __syncwarp();
         }
-        fence_async();
         order(true, pv, vs, &sh.vfull[st]);
       }
     }
@@ -1151,7 +1184,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   const TreeSpan sp = w.span[blockIdx.x];
   if (!sp.some) return;
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  TreeWalk<C::TN, MR> walk(w, sp.slot, sp.unit, 0, 0, 1, true);
+  TreeWalk<C::TN, MR> walk(w, sp.slot, sp.unit, 0, 1, true);
   const TreeUnit& u = walk.u;
   if (r >= u.rows) return;
   const int n = sp.last - blockIdx.x + 1, dh = min(DV, a.head_dim - u.half * 128);
@@ -1182,7 +1215,8 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 }
 
 template <int DT, int DP>
-static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const DevInfo& di, pi_stream stream) {
+static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const CUtensorMap& edge_map, const DevInfo& di,
+                             pi_stream stream) {
   using C = TreeTile<DT, DP>;
   constexpr int smem = tree_smem<DT, DP>();
   static_assert(smem <= 232448, "shared memory");
@@ -1194,12 +1228,13 @@ static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const DevInfo&
   long long seen = (long long)a.max_pages * a.page_tokens;
   if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
   const long long units = (long long)a.slots * a.kv_heads * ((a.drafts * a.group + C::MR - 1) / C::MR) * w.halves;
-  const long long most = seen / C::TN + 4;  // tiles of a unit
+  const long long most = (seen + 63) / C::TN + 4;  // tiles of a unit
   const bool whole = most <= kTreeWhole;
   const long long useful = whole ? units : units * (most + kTreeCost);
   long long grid = di.sms < kTreeGrid ? di.sms : kTreeGrid;
   if (grid > useful) grid = useful;
-  st = launch(tree_kernel<DT, DP>, dim3((unsigned)grid), kTreeThreads, smem, stream, w, map);
+  st = launch(tree_kernel<DT, DP>, dim3((unsigned)grid), kTreeThreads, smem, stream, w, map,
+              edge_map);
   if (st != PI_OK || whole || grid < 2) return st;
   const int rows = a.drafts * a.group < C::MR ? a.drafts * a.group : C::MR;
   return launch(tree_join_kernel<DT, DP>, dim3((unsigned)(grid - 1), (unsigned)((rows + 7) / 8)), 256, 0, stream, w);
@@ -1281,17 +1316,22 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   w.limit_ns = wait_limit();
   w.lose = lose;
   const long long rows = (long long)C.pages * 2 * C.kv_heads * C.page_tokens;
-  CUtensorMap map = {};
-  w.box = C.page_tokens % 16 ? 8 : 16;
-  w.tma = C.page_tokens % 8 == 0 && C.head_dim >= 64 && rows < (1ll << 31) &&
-          tree_map(&map, a.pool, rows, C.head_dim, w.box);
+  CUtensorMap map = {}, edge_map = {};
+  w.box = C.page_tokens & -C.page_tokens;
+  w.box = w.box < 64 ? w.box : 64;
+  w.edge = w.box < 16 ? w.box : 16;
+  w.align = w.box > 16 ? w.box : 16;
+  w.page_shift = C.page_tokens & (C.page_tokens - 1) ? -1 : __builtin_ctz((unsigned)C.page_tokens);
+  w.tma = w.box >= 8 && C.head_dim >= 64 && rows < (1ll << 31) &&
+          tree_map(&map, a.pool, rows, C.head_dim, w.box) &&
+          tree_map(&edge_map, a.pool, rows, C.head_dim, w.edge);
   DevInfo di;
   st = dev_info(&di);
   if (st != PI_OK) return st;
   const bool f16 = C.dtype == PI_F16;
-  if (C.head_dim <= 64) return f16 ? launch_tree<0, 64>(w, map, di, stream) : launch_tree<1, 64>(w, map, di, stream);
-  if (C.head_dim <= 128) return f16 ? launch_tree<0, 128>(w, map, di, stream) : launch_tree<1, 128>(w, map, di, stream);
-  return f16 ? launch_tree<0, 256>(w, map, di, stream) : launch_tree<1, 256>(w, map, di, stream);
+  if (C.head_dim <= 64) return f16 ? launch_tree<0, 64>(w, map, edge_map, di, stream) : launch_tree<1, 64>(w, map, edge_map, di, stream);
+  if (C.head_dim <= 128) return f16 ? launch_tree<0, 128>(w, map, edge_map, di, stream) : launch_tree<1, 128>(w, map, edge_map, di, stream);
+  return f16 ? launch_tree<0, 256>(w, map, edge_map, di, stream) : launch_tree<1, 256>(w, map, edge_map, di, stream);
 }
 
 }  // extern "C"
