@@ -250,6 +250,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, unsigned
   }
   return true;
 }
+// The same for waits that are short as a rule: looks a few times before it lets the
+// hardware suspend the warp.
+__device__ __forceinline__ bool mbar_spin(uint64_t* m, uint32_t parity, unsigned long long limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(m)), "r"(parity)
+        : "memory");
+    if (__all_sync(~0u, ok)) return true;
+  }
+  return mbar_wait(m, parity, limit_ns);
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -211,8 +211,8 @@ struct TreeTile {
   static constexpr int NO = DT == 1 && DP == 128 ? 1 : 2;  // O tiles in tensor memory
   static constexpr int kQ = MR * DP * 2, kK = TN * DP * 2, kV = TN * DV * 2;  // bytes
   static constexpr int kStages = NP * kQ, kMisc = kStages + S * (kK + kV);
-  // tensor-memory columns: two S tiles, whose place the first parts of P take; the
-  // third parts of P; O
+  // tensor-memory columns: two S tiles, 16 columns of which become the first two parts
+  // of P for the same 16 tokens; the third parts of P; O
   static constexpr int kThird = 2 * TN, kO = kThird + (DT == 1 ? TN : 0);
   static_assert(kO + NO * DV <= 512, "tensor memory");
 };
@@ -223,11 +223,28 @@ constexpr int kTreeWhole = 6;    // units of at most this many tiles are not spl
 constexpr int kTreeShare = 3;    // least share of a block
 constexpr int kTreeHide = 8;     // more than the tiles between the filling of K and the softmax
 
+// `total` positions over `blocks` blocks: the first `more` take one more.
+struct TreeLine {
+  long long each;
+  int more;
+  __device__ __forceinline__ void set(long long total, int blocks) {
+    each = quotient(total, blocks);
+    more = (int)(total - each * blocks);
+  }
+  __device__ __forceinline__ long long start(int b) const { return b * each + min(b, more); }
+  __device__ __forceinline__ int block_of(long long pos) const {
+    const long long head = more * (each + 1);
+    return pos >= head ? more + (int)((pos - head) / each) : (int)(pos / (each + 1));
+  }
+};
+
 struct TreeShared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[2], pfull[2], ofull[2], oempty[2];
-  uint64_t pair[4], qfull, fin;
+  uint64_t pair[4], join, qfull, fin;
   uint32_t taddr;
   int bad;
+  TreeLine line;
+  long long share0;
   uint32_t hide[kTreeHide][4];  // tokens of a tile whose page is out of range
   union {
     float top[2][2][128];  // rows' maxima, of a tile's two halves; at a segment's end their sums
@@ -459,21 +476,6 @@ struct TreeWalk {
   }
 };
 
-// A part's line position to block, and back (as in the attention of one token).
-struct TreeLine {
-  long long each;
-  int more;
-  __device__ __forceinline__ void set(long long total, int blocks) {
-    each = quotient(total, blocks);
-    more = (int)(total - each * blocks);
-  }
-  __device__ __forceinline__ long long start(int b) const { return b * each + min(b, more); }
-  __device__ __forceinline__ int block_of(long long pos) const {
-    const long long head = more * (each + 1);
-    return pos >= head ? more + (int)((pos - head) / each) : (int)(pos / (each + 1));
-  }
-};
-
 // A row's draft, and what it sees.
 struct TreeRow {
   int draft, lo;  // lo: least visible cached token but for the first `sinks`
@@ -542,9 +544,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
     mbar_init(&sh.qfull, 8);
+    mbar_init(&sh.join, 8);
     mbar_init(&sh.fin, 1);
     fence_mbar_init();
     sh.bad = 0;
+    w.span[blockIdx.x] = TreeSpan{0, 0, 0, 0};
   }
   long long share0, share1, unit_at;
   int first_slot, first_unit, grid;
@@ -615,6 +619,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     __syncthreads();
     const bool some = share0 < share1;
+    if (tid == 0) {
+      sh.line = line;
+      sh.share0 = share0;
+    }
     first_slot = some ? sc.slot : 0;
     first_unit = some ? sc.unit : 0;
     unit_at = some ? sc.at : 0;
@@ -645,26 +653,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (warp < 8) {
     // ---- Q, softmax, O
     constexpr int HC = TN / 2, HO = DV / 2;  // a half's columns of S, of O
-    const int h = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
+    const int h = warp >> 2, wq = warp & 3, place = 32 * wq + lane;
     const float flip = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
     const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
     constexpr float kShift = DT == 0 ? 14.f : 0.f;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
-    int seg = 0, met = 0;
+    int seg = 0, met = 0, joined = 0;
     // The other half's value of the row; false where the wait ran out.
-    auto meet = [&](float& mine, float& theirs) {
-      sh.top[met & 1][h][row] = mine;
+    auto meet = [&](float mine, float& theirs) {
+      sh.top[met & 1][h][place] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.pair[wq]);
-      if (!mbar_wait(&sh.pair[wq], (uint32_t)(met & 1), w.limit_ns)) return false;
-      theirs = sh.top[met & 1][1 - h][row];
+      if (!mbar_spin(&sh.pair[wq], (uint32_t)(met & 1), w.limit_ns)) return false;
+      theirs = sh.top[met & 1][1 - h][place];
       ++met;
       return true;
     };
-    TreeSpan span{0, 0, 0, 0};
+    auto meet_all = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.join);
+      return mbar_spin(&sh.join, (uint32_t)(joined++ & 1), w.limit_ns);
+    };
     for (; walk.more() && ok; walk.next()) {
       if (!walk.any()) continue;
       const TreeUnit& u = walk.u;
+      // The unit's rows stand in the tile as often as they fit, and each copy takes its
+      // share of a tile's columns: the weights of the others' columns are 0 there, and
+      // the copies' sums are joined at the segment's end.
+      const int blocks = u.rows <= 32 ? 1 : MR == 64 || u.rows <= 64 ? 2 : 4, copies = MR / 32 / blocks;
+      const int copy = wq / blocks, row = 32 * (wq - copy * blocks) + lane;
       // rows warp, warp + 8, ...: split into parts
       constexpr int E = DP / 32, B = DP == 256 ? 2 : 4;
 #pragma unroll 1
@@ -723,9 +740,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           unsigned char* to = smem + (c >> 6) * kPanelQ + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + 2 * (c & 7);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to + p * C::kQ) = part[p][0];
-            else if constexpr (E == 4) *reinterpret_cast<uint2*>(to + p * C::kQ) = make_uint2(part[p][0], part[p][1]);
-            else *reinterpret_cast<uint4*>(to + p * C::kQ) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+#pragma unroll 1
+            for (int j = 0; j < copies; ++j) {
+              unsigned char* at = to + p * C::kQ + j * blocks * (32 * 128);
+              if constexpr (E == 2) *reinterpret_cast<uint32_t*>(at) = part[p][0];
+              else if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = make_uint2(part[p][0], part[p][1]);
+              else *reinterpret_cast<uint4*>(at) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+            }
           }
         }
       }
@@ -733,7 +754,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.qfull);
       // the row's own draft
-      const bool live = 32 * wq < u.rows;
+      const bool live = copy < copies && (row & ~31) < u.rows;
       int pa = -1, pb = -1;
       if (live && a.parent) {
         if (lane < u.v.count) pa = __ldg(a.parent + (size_t)u.slot * a.drafts + lane);
@@ -769,68 +790,55 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       ++seg;
       const int sinks = u.v.tail > 0 ? 0 : a.sinks;
       float m = -INFINITY, ref = -INFINITY, l = 0.f, alpha = 0.f;
+      const int chunks = HC / 16 / copies;                          // of 16 columns
+      const int first = copy * (TN / copies) + h * (HC / copies);  // column
       u64 o2[HO / 2];
 #pragma unroll
       for (int c = 0; c < HO / 2; ++c) o2[c] = 0;
-      auto add_o = [&](int p, float factor) {  // tile p's O; false where the wait ran out
-        const int buf = p % NO;
-        if (!mbar_wait(&sh.ofull[buf], (uint32_t)((p / NO) & 1), w.limit_ns)) return false;
-        if (live) {
-          tm_fence_after();
-          const u64 f2 = pair(factor, factor);
-#pragma unroll
-          for (int c0 = 0; c0 < HO; c0 += 32) {
-            float x[32];
-            tm_ld32(x, lanes + C::kO + buf * DV + h * HO + c0);
-            tm_wait_ld<32>(x);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o2[c0 / 2 + c] = fma2(o2[c0 / 2 + c], f2, pair(x[2 * c], x[2 * c + 1]));
-          }
-          tm_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.oempty[buf]);
-        return true;
-      };
-      for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
+      for (int i = walk.tile0;; ++i, ++t) {  // the softmax of tile i, then the sums with tile i - 1's O
         const int buf = t & 1;
-        TREE_WAIT(&sh.sfull[buf], (t >> 1) & 1);
         const float before = alpha;
-        if (live) {
+        const bool tile = i < walk.tile1;
+        if (tile) TREE_WAIT(&sh.sfull[buf], (t >> 1) & 1);
+        if (live && tile) {
           tm_fence_after();
-          const uint32_t src = lanes + (uint32_t)(buf * TN);
-          float v[HC];
-#pragma unroll
-          for (int k = 0; k < HC / 32; ++k) tm_ld32(v + 32 * k, src + h * HC + 32 * k);
-          // the columns that the row does not see
+          const uint32_t src = lanes + (uint32_t)(buf * TN + first);
+          // the columns that the row does not see, 16 at a time
           int any_lo = 0, hi = 0, t0 = 0;
           if (i > 0) t0 = walk.cached(i, any_lo, hi);
           const int from = i <= u.firsts ? 0 : lo;
           bool all = i > 0 && t0 >= from && t0 + TN <= hi;
 #pragma unroll
-          for (int k = 0; k < HC / 32; ++k) all &= !sh.hide[t % kTreeHide][h * (HC / 32) + k];
-          tm_wait_ld<HC>(v);
-          if (!__all_sync(~0u, all)) {
+          for (int k = 0; k < TN / 32; ++k) all &= !sh.hide[t % kTreeHide][k];
+          all = __all_sync(~0u, all);
+          auto load = [&](int k, float (&v)[16]) {
+            tm_ld16(v, src + 16 * k);
+            tm_wait_ld<16>(v);
+            if (all) return;
             auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
+            const int c0 = first + 16 * k, at = t0 + c0;
+            uint32_t mask = i > 0 ? below(hi - at) & (~below(from - at) | below(sinks - at))
+                                  : c0 < 64 ? (uint32_t)(seen >> c0) : 0u;
+            mask &= ~(sh.hide[t % kTreeHide][c0 >> 5] >> (c0 & 31));
 #pragma unroll
-            for (int k = 0; k < HC / 32; ++k) {
-              const int word = h * (HC / 32) + k, at = t0 + 32 * word;
-              uint32_t mask = i > 0 ? below(hi - at) & (~below(from - at) | below(sinks - at))
-                                    : word < 2 ? (uint32_t)(seen >> (32 * word)) : 0u;
-              mask &= ~sh.hide[t % kTreeHide][word];
+            for (int c = 0; c < 16; ++c) v[c] = mask >> c & 1u ? v[c] : -INFINITY;
+          };
+          float top = -INFINITY, theirs = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < chunks; ++k) {
+            float v[16];
+            load(k, v);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) v[32 * k + c] = mask >> c & 1u ? v[32 * k + c] : -INFINITY;
-            }
+            for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+              for (int c = 0; c < o; ++c) v[c] = fmaxf(v[c], v[c + o]);
+            top = fmaxf(top, v[0]);
           }
-          float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int c = 4; c < HC; ++c) top[c & 3] = fmaxf(top[c & 3], v[c]);
-          float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), theirs = 0.f;
-          if (!meet(mine, theirs)) {
+          if (!meet(top, theirs)) {
             gave_up();
             break;
           }
-          const float up = fmaxf(m, fmaxf(mine, theirs) * scl);
+          const float up = fmaxf(m, fmaxf(top, theirs) * scl);
           // weights are relative to the maximum less kShift, which rounding must not take
           // far from it
           const float at = up == -INFINITY ? 0.f : up;
@@ -840,14 +848,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           m = up;
           ref = next;
           const u64 scl2 = pair(scl, scl), next2 = pair(-next, -next);
+          const uint32_t third = lanes + C::kThird + buf * (TN / 2) + first / 2;
           u64 sum[2] = {0, 0};
-          const uint32_t dst = src + h * (HC / 2);
-#pragma unroll
-          for (int k = 0; k < HC / 16; ++k) {
+#pragma unroll 1
+          for (int k = 0; k < chunks; ++k) {
+            float v[16];
+            load(k, v);
             uint32_t part[NP][8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float2 d = halves(add2(mul2(pair(v[16 * k + 2 * c], v[16 * k + 2 * c + 1]), scl2), next2));
+              const float2 d = halves(add2(mul2(pair(v[2 * c], v[2 * c + 1]), scl2), next2));
               u64 p = pair(ex2(d.x), ex2(d.y));
               sum[c & 1] = add2(sum[c & 1], p);
 #pragma unroll
@@ -857,9 +867,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (i + 1 < NP) p = left2<DT>(p, part[i][c]);
               }
             }
-            tm_st8(dst + 8 * k, part[0]);
-            tm_st8(dst + TN / 2 + 8 * k, part[1]);
-            if constexpr (NP == 3) tm_st8(lanes + C::kThird + buf * (TN / 2) + h * (HC / 2) + 8 * k, part[2]);
+            tm_st8(src + 16 * k, part[0]);
+            tm_st8(src + 16 * k + 8, part[1]);
+            if constexpr (NP == 3) tm_st8(third + 8 * k, part[2]);
+          }
+          if (copies > 1) {  // the other copies' columns, every other 16 by each half
+            const uint32_t zero[8] = {};
+            const uint32_t to = lanes + (uint32_t)(buf * TN);
+#pragma unroll 1
+            for (int k = h; k < TN / 16; k += 2) {
+              if (16 * k >= first - h * 16 * chunks && 16 * k < first - h * 16 * chunks + 32 * chunks) continue;
+              tm_st8(to + 16 * k, zero);
+              tm_st8(to + 16 * k + 8, zero);
+              if constexpr (NP == 3) tm_st8(lanes + C::kThird + buf * (TN / 2) + 8 * k, zero);
+            }
           }
           const float2 both = halves(add2(sum[0], sum[1]));
           l = fmaf(l, alpha, both.x + both.y);
@@ -867,20 +888,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tm_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pfull[buf]);
-        if (i > walk.tile0 && !add_o(t - 1, before)) {
-          gave_up();
-          break;
+        if (lane == 0 && tile) mbar_arrive(&sh.pfull[buf]);
+        if (i > walk.tile0) {
+          const int ob = (t - 1) % NO;
+          if (!mbar_wait(&sh.ofull[ob], (uint32_t)(((t - 1) / NO) & 1), w.limit_ns)) {
+            gave_up();
+            break;
+          }
+          if (live) {
+            tm_fence_after();
+            const u64 f2 = pair(before, before);
+#pragma unroll
+            for (int c0 = 0; c0 < HO; c0 += 16) {
+              float x[16];
+              tm_ld16(x, lanes + C::kO + ob * DV + h * HO + c0);
+              tm_wait_ld<16>(x);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) o2[c0 / 2 + c] = fma2(o2[c0 / 2 + c], f2, pair(x[2 * c], x[2 * c + 1]));
+            }
+            tm_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.oempty[ob]);
         }
+        if (!tile) break;
       }
       if (!ok) break;
-      if (!add_o(t - 1, alpha)) {
-        gave_up();
-        break;
-      }
       const bool begins = walk.begins(), ends = walk.ends();
-      if (begins && !ends) span = TreeSpan{u.slot, u.unit, line.block_of(share0 + walk.at + kTreeCost + u.tiles - 1), 1};
-      if (!live) continue;
+      if (begins && !ends && tid == 0)
+        w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + kTreeCost + u.tiles - 1), 1};
       const int dh = min(DV, D - u.half * 128) - h * HO;  // the half's columns of the unit's
       float o[HO];
       bool odd = false;
@@ -889,15 +925,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const float2 f = halves(o2[c]);
         o[2 * c] = f.x;
         o[2 * c + 1] = f.y;
-        odd |= 2 * c < dh && !(fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY);
       }
-      float theirs = 0.f;
-      if (odd) l = NAN;  // for the other half too
-      if (!meet(l, theirs)) {
-        gave_up();
-        break;
+#pragma unroll
+      for (int c = 0; c < HO; ++c) odd |= c < dh && !(fabsf(o[c]) < INFINITY);
+      if (live) {
+        float theirs = 0.f;
+        if (odd) l = NAN;  // for the other half too
+        if (!meet(l, theirs)) {
+          gave_up();
+          break;
+        }
+        l = h ? theirs + l : l + theirs;
       }
-      l = h ? theirs + l : l + theirs;
+      if (copies > 1) {  // joined in Q's place, whose products are done
+        float* const sums = reinterpret_cast<float*>(smem);
+        auto of = [&](int j) { return sums + ((j - 1) * 32 * blocks + row) * (DV + 3); };
+        if (live && copy > 0) {
+          float* to = of(copy);
+#pragma unroll
+          for (int c = 0; c < HO; ++c) to[h * HO + c] = o[c];
+          if (h == 0) to[DV] = ref, to[DV + 1] = l;
+        }
+        if (!meet_all()) {
+          gave_up();
+          break;
+        }
+        if (live && copy == 0) {
+#pragma unroll 1
+          for (int j = 1; j < copies; ++j) {
+            const float* other = of(j);
+            const float their_ref = other[DV], their_l = other[DV + 1];
+            const float up = their_l == 0.f ? ref : l == 0.f ? their_ref : fmaxf(ref, their_ref);
+            const float mine = l == 0.f ? 0.f : ex2(ref - up), theirs = their_l == 0.f ? 0.f : ex2(their_ref - up);
+#pragma unroll
+            for (int c = 0; c < HO; ++c) o[c] = fmaf(other[h * HO + c], theirs, o[c] * mine);
+            l = fmaf(their_l, theirs, l * mine);
+            ref = up;
+          }
+        }
+        if (!meet_all()) {
+          gave_up();
+          break;
+        }
+      }
+      if (!live || copy) continue;
       const bool again = row < u.rows && !(l < INFINITY);
       const int R = u.row0 + row, draft = R / a.group;
       const size_t out = ((size_t)u.slot * a.drafts + draft) * a.heads + u.g * a.group + R - draft * a.group;
@@ -918,7 +989,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
       for (uint32_t left = __ballot_sync(~0u, again); left; left &= left - 1) {
-        const int r = 32 * wq + __ffs(left) - 1;
+        const int r = (row & ~31) + __ffs(left) - 1;
         const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, r);
         const float inv = s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
         const int Rr = u.row0 + r, dr = Rr / a.group, c = 8 * lane - 128 * u.half;
@@ -937,7 +1008,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
     }
-    if (tid == 0) w.span[blockIdx.x] = span;
   } else if (warp == 8) {
     // ---- MMAs
     int seg = 0, cols_before = 0, nv_before = 0;
@@ -957,11 +1027,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         bool add = false;
 #pragma unroll
         for (int part = NP - 1; part >= 0; --part) {
-          const uint32_t pa = part == 2 ? tmem + C::kThird + buf * (TN / 2) : tmem + buf * TN + part * (TN / 2);
+          const uint32_t pa = part == 2 ? tmem + C::kThird + buf * (TN / 2) : tmem + buf * TN + part * 8;
 #pragma unroll
           for (int ks = 0; ks < TN / 16; ++ks)
             if (16 * ks < cols) {
-              mma_ts(d, pa + 8 * ks, vd + (2048 >> 4) * ks, idesc, add);
+              mma_ts(d, pa + (part == 2 ? 8 : 16) * ks, vd + (2048 >> 4) * ks, idesc, add);
               add = true;
             }
         }
