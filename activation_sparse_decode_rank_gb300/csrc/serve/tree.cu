@@ -201,20 +201,26 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 //
 // Operands that are not finite.  Rows whose sums come out NaN or infinite are
 // gone through again in fp32, token by token, by the warp that would write them.
-template <int DT, int DP>
-struct TreeTile {
+template <int DT, int DP, int MR>
+struct TreeTile {  // MR: query rows of a unit
+  static constexpr bool kFew = MR <= 32;
   static constexpr int TN = DP == 256 ? 64 : 128;  // tokens of a tile
-  static constexpr int MR = DP == 256 ? 64 : 128;  // query rows of a unit
   static constexpr int DV = DP < 128 ? DP : 128;   // columns of V of a unit
   static constexpr int NP = DT == 0 ? 2 : 3;       // parts of q and p
+  static constexpr int NQ = NP * MR;               // few rows: columns of S and O
   static constexpr int S = DP == 64 ? 4 : DP == 256 && DT == 0 ? 3 : 2;  // stages
-  static constexpr int NO = DT == 1 && DP == 128 ? 1 : 2;  // O tiles in tensor memory
-  static constexpr int kQ = MR * DP * 2, kK = TN * DP * 2, kV = TN * DV * 2;  // bytes
-  static constexpr int kStages = NP * kQ, kMisc = kStages + S * (kK + kV);
-  // tensor-memory columns: two S tiles, 16 columns of which become the first two parts
-  // of P for the same 16 tokens; the third parts of P; O
-  static constexpr int kThird = 2 * TN, kO = kThird + (DT == 1 ? TN : 0);
-  static_assert(kO + NO * DV <= 512, "tensor memory");
+  static constexpr int NO = !kFew && DT == 1 && DP == 128 ? 1 : 2;  // O tiles in tensor memory
+  static constexpr int kK = TN * DP * 2, kV = TN * DV * 2;  // bytes of a stage
+  static constexpr int kQ = MR * DP * 2;                    // of a part of Q
+  static constexpr int kP = kFew ? (NQ + 63) / 64 * TN * 128 : 0;  // of P, two of which
+  static constexpr int kStages = (NP * kQ + 1023) / 1024 * 1024, kWeights = kStages + S * (kK + kV),
+                       kMisc = kWeights + 2 * kP;
+  // tensor-memory columns.  Many rows: two S tiles, 16 columns of which become the
+  // first two parts of P for the same 16 tokens; the third parts of P; O.  Few rows: two
+  // S tiles; O.
+  static constexpr int kS = kFew ? NQ : TN, kO1 = kFew ? NQ : DV;  // of a tile
+  static constexpr int kThird = 2 * kS, kO = kThird + (!kFew && DT == 1 ? TN : 0);
+  static_assert(kO + NO * kO1 <= 512, "tensor memory");
 };
 constexpr int kTreeThreads = 384;
 constexpr int kTreeGrid = 192;   // most blocks
@@ -240,7 +246,7 @@ struct TreeLine {
 
 struct TreeShared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[2], pfull[2], ofull[2], oempty[2];
-  uint64_t pair[4], join, qfull, fin;
+  uint64_t pair[4], qfull, fin;
   uint32_t taddr;
   int bad;
   TreeLine line;
@@ -248,6 +254,7 @@ struct TreeShared {
   uint32_t hide[kTreeHide][4];  // tokens of a tile whose page is out of range
   union {
     float top[2][2][128];  // rows' maxima, of a tile's two halves; at a segment's end their sums
+    float few[2][2][4][16];  // few rows: [..][half of the rows][32 tokens][row]
     struct {
       long long sum[12], len[12];
       int most[12];
@@ -259,11 +266,16 @@ struct TreeShared {
 struct TreeSharedScale : TreeShared {
   float qs[2][128];  // rows' 2^-e of q (fp16)
 };
-template <int DT>
-using TreeSharedOf = std::conditional_t<DT == 0, TreeSharedScale, TreeShared>;
-template <int DT, int DP>
+struct TreeSharedFew : TreeShared {  // of a segment's rows
+  float qs[2][32];
+  int lo[2][32];
+  u64 seen[2][32];
+};
+template <int DT, bool FEW>
+using TreeSharedOf = std::conditional_t<FEW, TreeSharedFew, std::conditional_t<DT == 0, TreeSharedScale, TreeShared>>;
+template <int DT, int DP, int MR>
 __host__ __device__ constexpr int tree_smem() {
-  return TreeTile<DT, DP>::kMisc + (int)sizeof(TreeSharedOf<DT>);
+  return TreeTile<DT, DP, MR>::kMisc + (int)sizeof(TreeSharedOf<DT, MR <= 32>);
 }
 
 struct TreeSpan {  // a unit that begins in a block and ends in a later one
@@ -303,10 +315,11 @@ __device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo) {
   d |= (uint64_t)2 << 61;  // 128-byte swizzle
   return d;
 }
-// Instruction descriptor of kind::f16: D fp32, A and B of DT, M = 128, N = n.
+// Instruction descriptor of kind::f16: D fp32, A and B of DT, M = 128, N = n; A and B
+// K-major, or M- and N-major.
 template <int DT>
-__device__ __forceinline__ uint32_t tree_idesc(int n, bool b_nmajor) {
-  return (1u << 4) | ((uint32_t)DT << 7) | ((uint32_t)DT << 10) | (b_nmajor ? 1u << 16 : 0u) |
+__device__ __forceinline__ uint32_t tree_idesc(int n, bool b_nmajor, bool a_mmajor = false) {
+  return (1u << 4) | ((uint32_t)DT << 7) | ((uint32_t)DT << 10) | (a_mmajor ? 1u << 15 : 0u) | (b_nmajor ? 1u << 16 : 0u) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 // True in one lane of the warp, the same one every time.
@@ -356,6 +369,12 @@ __device__ __forceinline__ void tm_ld32(float* v, uint32_t t) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t));
 }
+__device__ __forceinline__ void tm_ld8(float* v, uint32_t t) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
 __device__ __forceinline__ void tm_ld16(float* v, uint32_t t) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -369,7 +388,13 @@ __device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t* r) {
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-
+__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // Two fp32 values rounded to 16 bits in one instruction (two conversions take four
 // times as long as the packed one), and what that left.
 template <int DT>
@@ -513,14 +538,15 @@ __device__ __forceinline__ RowSums tree_again(const TreeWork& w, const TreeUnit&
   return s;
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int MR>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeWork w, const __grid_constant__ CUtensorMap map,
                 const __grid_constant__ CUtensorMap edge_map) {
-  using C = TreeTile<DT, DP>;
-  constexpr int TN = C::TN, MR = C::MR, DV = C::DV, NP = C::NP, S = C::S, NO = C::NO;
-  constexpr int kPanelK = TN * 128, kPanelQ = MR * 128;  // bytes of 64 columns
-  using Shared = TreeSharedOf<DT>;
+  using C = TreeTile<DT, DP, MR>;
+  constexpr bool kFew = C::kFew;
+  constexpr int TN = C::TN, DV = C::DV, NP = C::NP, NQ = C::NQ, S = C::S, NO = C::NO;
+  constexpr int kPanelK = TN * 128, kPanelQ = (kFew ? NQ : MR) * 128;  // bytes of 64 columns
+  using Shared = TreeSharedOf<DT, kFew>;
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kMisc);
   const TreeArgs& a = w.a;
@@ -542,9 +568,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mbar_init(&sh.ofull[i], 1);
       mbar_init(&sh.oempty[i], 8);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], kFew ? 4 : 2);
     mbar_init(&sh.qfull, 8);
-    mbar_init(&sh.join, 8);
     mbar_init(&sh.fin, 1);
     fence_mbar_init();
     sh.bad = 0;
@@ -651,37 +676,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
 
   if (warp < 8) {
+    if constexpr (!kFew) {
     // ---- Q, softmax, O
     constexpr int HC = TN / 2, HO = DV / 2;  // a half's columns of S, of O
-    const int h = warp >> 2, wq = warp & 3, place = 32 * wq + lane;
+    const int h = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
     const float flip = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
     const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
     constexpr float kShift = DT == 0 ? 14.f : 0.f;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
-    int seg = 0, met = 0, joined = 0;
+    int seg = 0, met = 0;
     // The other half's value of the row; false where the wait ran out.
     auto meet = [&](float mine, float& theirs) {
-      sh.top[met & 1][h][place] = mine;
+      sh.top[met & 1][h][row] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.pair[wq]);
       if (!mbar_spin(&sh.pair[wq], (uint32_t)(met & 1), w.limit_ns)) return false;
-      theirs = sh.top[met & 1][1 - h][place];
+      theirs = sh.top[met & 1][1 - h][row];
       ++met;
       return true;
-    };
-    auto meet_all = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.join);
-      return mbar_spin(&sh.join, (uint32_t)(joined++ & 1), w.limit_ns);
     };
     for (; walk.more() && ok; walk.next()) {
       if (!walk.any()) continue;
       const TreeUnit& u = walk.u;
-      // The unit's rows stand in the tile as often as they fit, and each copy takes its
-      // share of a tile's columns: the weights of the others' columns are 0 there, and
-      // the copies' sums are joined at the segment's end.
-      const int blocks = u.rows <= 32 ? 1 : MR == 64 || u.rows <= 64 ? 2 : 4, copies = MR / 32 / blocks;
-      const int copy = wq / blocks, row = 32 * (wq - copy * blocks) + lane;
       // rows warp, warp + 8, ...: split into parts
       constexpr int E = DP / 32, B = DP == 256 ? 2 : 4;
 #pragma unroll 1
@@ -740,13 +756,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           unsigned char* to = smem + (c >> 6) * kPanelQ + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + 2 * (c & 7);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-#pragma unroll 1
-            for (int j = 0; j < copies; ++j) {
-              unsigned char* at = to + p * C::kQ + j * blocks * (32 * 128);
-              if constexpr (E == 2) *reinterpret_cast<uint32_t*>(at) = part[p][0];
-              else if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = make_uint2(part[p][0], part[p][1]);
-              else *reinterpret_cast<uint4*>(at) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-            }
+            if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to + p * C::kQ) = part[p][0];
+            else if constexpr (E == 4) *reinterpret_cast<uint2*>(to + p * C::kQ) = make_uint2(part[p][0], part[p][1]);
+            else *reinterpret_cast<uint4*>(to + p * C::kQ) = make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
           }
         }
       }
@@ -754,7 +766,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.qfull);
       // the row's own draft
-      const bool live = copy < copies && (row & ~31) < u.rows;
+      const bool live = 32 * wq < u.rows;
       int pa = -1, pb = -1;
       if (live && a.parent) {
         if (lane < u.v.count) pa = __ldg(a.parent + (size_t)u.slot * a.drafts + lane);
@@ -790,8 +802,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       ++seg;
       const int sinks = u.v.tail > 0 ? 0 : a.sinks;
       float m = -INFINITY, ref = -INFINITY, l = 0.f, alpha = 0.f;
-      const int chunks = HC / 16 / copies;                          // of 16 columns
-      const int first = copy * (TN / copies) + h * (HC / copies);  // column
+      const int first = h * HC;  // column
       u64 o2[HO / 2];
 #pragma unroll
       for (int c = 0; c < HO / 2; ++c) o2[c] = 0;
@@ -811,10 +822,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
           for (int k = 0; k < TN / 32; ++k) all &= !sh.hide[t % kTreeHide][k];
           all = __all_sync(~0u, all);
-          auto load = [&](int k, float (&v)[16]) {
-            tm_ld16(v, src + 16 * k);
-            tm_wait_ld<16>(v);
-            if (all) return;
+          auto hide = [&](int k, float* v) {  // of the 16 columns k
             auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
             const int c0 = first + 16 * k, at = t0 + c0;
             uint32_t mask = i > 0 ? below(hi - at) & (~below(from - at) | below(sinks - at))
@@ -824,16 +832,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int c = 0; c < 16; ++c) v[c] = mask >> c & 1u ? v[c] : -INFINITY;
           };
           float top = -INFINITY, theirs = 0.f;
-#pragma unroll 1
-          for (int k = 0; k < chunks; ++k) {
-            float v[16];
-            load(k, v);
+          auto top_of = [&](int k) {  // of 32 columns from 16 k on
+            float v[32];
+            tm_ld32(v, src + 16 * k);
+            tm_wait_ld<32>(v);
+            if (!all) {
+              hide(k, v);
+              hide(k + 1, v + 16);
+            }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
+            for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
               for (int c = 0; c < o; ++c) v[c] = fmaxf(v[c], v[c + o]);
             top = fmaxf(top, v[0]);
-          }
+          };
+#pragma unroll 1
+          for (int k = 0; k < HC / 16; k += 2) top_of(k);
           if (!meet(top, theirs)) {
             gave_up();
             break;
@@ -850,38 +864,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const u64 scl2 = pair(scl, scl), next2 = pair(-next, -next);
           const uint32_t third = lanes + C::kThird + buf * (TN / 2) + first / 2;
           u64 sum[2] = {0, 0};
-#pragma unroll 1
-          for (int k = 0; k < chunks; ++k) {
-            float v[16];
-            load(k, v);
-            uint32_t part[NP][8];
+          auto weights_of = [&](int k) {  // of 32 columns from 16 k on
+            float v[32];
+            tm_ld32(v, src + 16 * k);
+            tm_wait_ld<32>(v);
+            if (!all) {
+              hide(k, v);
+              hide(k + 1, v + 16);
+            }
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float2 d = halves(add2(mul2(pair(v[2 * c], v[2 * c + 1]), scl2), next2));
-              u64 p = pair(ex2(d.x), ex2(d.y));
-              sum[c & 1] = add2(sum[c & 1], p);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t part[16], last[8];
 #pragma unroll
-              for (int i = 0; i < NP; ++i) {
-                const float2 f = halves(p);
-                part[i][c] = round2<DT>(f.x, f.y);
-                if (i + 1 < NP) p = left2<DT>(p, part[i][c]);
+              for (int c = 0; c < 8; ++c) {
+                const float2 d = halves(add2(mul2(pair(v[16 * j + 2 * c], v[16 * j + 2 * c + 1]), scl2), next2));
+                u64 p = pair(ex2(d.x), ex2(d.y));
+                sum[c & 1] = add2(sum[c & 1], p);
+                float2 f = halves(p);
+                part[c] = round2<DT>(f.x, f.y);
+                p = left2<DT>(p, part[c]);
+                f = halves(p);
+                part[8 + c] = round2<DT>(f.x, f.y);
+                if constexpr (NP == 3) {
+                  f = halves(left2<DT>(p, part[8 + c]));
+                  last[c] = round2<DT>(f.x, f.y);
+                }
               }
+              tm_st16(src + 16 * (k + j), part);
+              if constexpr (NP == 3) tm_st8(third + 8 * (k + j), last);
             }
-            tm_st8(src + 16 * k, part[0]);
-            tm_st8(src + 16 * k + 8, part[1]);
-            if constexpr (NP == 3) tm_st8(third + 8 * k, part[2]);
-          }
-          if (copies > 1) {  // the other copies' columns, every other 16 by each half
-            const uint32_t zero[8] = {};
-            const uint32_t to = lanes + (uint32_t)(buf * TN);
+          };
 #pragma unroll 1
-            for (int k = h; k < TN / 16; k += 2) {
-              if (16 * k >= first - h * 16 * chunks && 16 * k < first - h * 16 * chunks + 32 * chunks) continue;
-              tm_st8(to + 16 * k, zero);
-              tm_st8(to + 16 * k + 8, zero);
-              if constexpr (NP == 3) tm_st8(lanes + C::kThird + buf * (TN / 2) + 8 * k, zero);
-            }
-          }
+          for (int k = 0; k < HC / 16; k += 2) weights_of(k);
           const float2 both = halves(add2(sum[0], sum[1]));
           l = fmaf(l, alpha, both.x + both.y);
           tm_wait_st();
@@ -898,14 +912,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (live) {
             tm_fence_after();
             const u64 f2 = pair(before, before);
+            float x[HO];
 #pragma unroll
-            for (int c0 = 0; c0 < HO; c0 += 16) {
-              float x[16];
-              tm_ld16(x, lanes + C::kO + ob * DV + h * HO + c0);
-              tm_wait_ld<16>(x);
+            for (int c0 = 0; c0 < HO; c0 += 32) tm_ld32(x + c0, lanes + C::kO + ob * DV + h * HO + c0);
+            tm_wait_ld<HO>(x);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) o2[c0 / 2 + c] = fma2(o2[c0 / 2 + c], f2, pair(x[2 * c], x[2 * c + 1]));
-            }
+            for (int c = 0; c < HO / 2; ++c) o2[c] = fma2(o2[c], f2, pair(x[2 * c], x[2 * c + 1]));
             tm_fence_before();
           }
           __syncwarp();
@@ -937,38 +949,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         l = h ? theirs + l : l + theirs;
       }
-      if (copies > 1) {  // joined in Q's place, whose products are done
-        float* const sums = reinterpret_cast<float*>(smem);
-        auto of = [&](int j) { return sums + ((j - 1) * 32 * blocks + row) * (DV + 3); };
-        if (live && copy > 0) {
-          float* to = of(copy);
-#pragma unroll
-          for (int c = 0; c < HO; ++c) to[h * HO + c] = o[c];
-          if (h == 0) to[DV] = ref, to[DV + 1] = l;
-        }
-        if (!meet_all()) {
-          gave_up();
-          break;
-        }
-        if (live && copy == 0) {
-#pragma unroll 1
-          for (int j = 1; j < copies; ++j) {
-            const float* other = of(j);
-            const float their_ref = other[DV], their_l = other[DV + 1];
-            const float up = their_l == 0.f ? ref : l == 0.f ? their_ref : fmaxf(ref, their_ref);
-            const float mine = l == 0.f ? 0.f : ex2(ref - up), theirs = their_l == 0.f ? 0.f : ex2(their_ref - up);
-#pragma unroll
-            for (int c = 0; c < HO; ++c) o[c] = fmaf(other[h * HO + c], theirs, o[c] * mine);
-            l = fmaf(their_l, theirs, l * mine);
-            ref = up;
-          }
-        }
-        if (!meet_all()) {
-          gave_up();
-          break;
-        }
-      }
-      if (!live || copy) continue;
+      if (!live) continue;
       const bool again = row < u.rows && !(l < INFINITY);
       const int R = u.row0 + row, draft = R / a.group;
       const size_t out = ((size_t)u.slot * a.drafts + draft) * a.heads + u.g * a.group + R - draft * a.group;
@@ -1008,6 +989,282 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
     }
+    } else {
+    // ---- Q, softmax, O of few rows: a thread has a token of S and P, a column of V of O, in
+    // both for half of the rows; lane j keeps the figures of row j of its half
+    constexpr int RH = MR / 2;
+    const int h = warp >> 2, wq = warp & 3, place = 32 * wq + lane, own = lane & (RH - 1);
+    const float flip = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
+    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
+    constexpr float kShift = DT == 0 ? 14.f : 0.f;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16) + h * RH;
+    int seg = 0, met = 0;
+    // The four warps of a half show each other a value per row; false where the wait ran
+    // out.
+    auto meet = [&](float mine, float (&all)[4]) {
+      if (lane < RH) sh.few[met & 1][h][wq][lane] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pair[h]);
+      if (!mbar_spin(&sh.pair[h], (uint32_t)(met & 1), w.limit_ns)) return false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) all[k] = sh.few[met & 1][h][k][own];
+      ++met;
+      return true;
+    };
+    for (; walk.more() && ok; walk.next()) {
+      if (!walk.any()) continue;
+      const TreeUnit& u = walk.u;
+      // rows warp, warp + 8, ...: split into parts
+      constexpr int E = DP / 32, B = MR / 8;
+      float x[B][E];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int r = warp + 8 * b, R = u.row0 + r, i = R / a.group;
+        const float* q = a.q + (((size_t)u.slot * a.drafts + i) * a.heads + u.g * a.group + R - i * a.group) * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[b][e] = 0.f;
+        if (r < u.rows && E * lane < D) {
+          if constexpr (E == 2) {
+            const float2 f = __ldg(reinterpret_cast<const float2*>(q));
+            x[b][0] = f.x, x[b][1] = f.y;
+          } else {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(q));
+            x[b][0] = f.x, x[b][1] = f.y, x[b][E - 2] = f.z, x[b][E - 1] = f.w;
+          }
+        }
+      }
+      if (warp == 7) {  // what the rows see, a lane each
+        int lo = 0;
+        u64 seen = 0;
+        if (lane < u.rows) {
+          const int draft = (u.row0 + lane) / a.group;
+          const u64 path = a.parent
+              ? tree_path(a, draft, [&](int j) { return __ldg(a.parent + (size_t)u.slot * a.drafts + j); })
+              : (2ull << draft) - 1;
+          lo = a.window > 0 ? u.v.base + __popcll(path) - a.window : 0;
+          seen = tree_seen(a, u.v.base, path);
+        }
+        sh.lo[seg & 1][lane] = lo;
+        sh.seen[seg & 1][lane] = seen;
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int r = warp + 8 * b;
+        float back = 1.f;
+        if constexpr (DT == 0) {
+          float top = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[b][e]));
+          top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
+          int ex = 140 - (int)(__float_as_uint(top) >> 23);  // the largest into [2^13, 2^14)
+          if (!(top > 0.f && top < INFINITY)) ex = 0;
+          ex = max(-100, min(100, ex));
+          const float f = __uint_as_float((uint32_t)(ex + 127) << 23);
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[b][e] *= f;
+          back = __uint_as_float((uint32_t)(127 - ex) << 23);
+        }
+        if (lane == 0) sh.qs[seg & 1][r] = back;
+        const int c = E * lane;
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = x[b][e] * flip;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          uint32_t part[E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            part[e] = round2<DT>(y[2 * e], y[2 * e + 1]);
+            y[2 * e] -= from_bits<DT>((uint16_t)part[e]);
+            y[2 * e + 1] -= from_bits<DT>((uint16_t)(part[e] >> 16));
+          }
+          const int n = p * MR + r;
+          unsigned char* to = smem + (c >> 6) * kPanelQ + n * 128 + ((((c >> 3) & 7) ^ (n & 7)) << 4) + 2 * (c & 7);
+          if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to) = part[0];
+          else *reinterpret_cast<uint2*>(to) = make_uint2(part[0], part[E / 2 - 1]);
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.qfull);
+      TREE_WAIT(&sh.qfull, seg & 1);
+      const bool live = h * RH < u.rows;
+      const float scl = scale * sh.qs[seg & 1][h * RH + own];
+      const int* const los = sh.lo[seg & 1] + h * RH;
+      const u64* const seens = sh.seen[seg & 1] + h * RH;
+      const int sinks = u.v.tail > 0 ? 0 : a.sinks;
+      float m = -INFINITY, ref = -INFINITY, alpha = 0.f;
+      float l[RH], o[RH];
+#pragma unroll
+      for (int j = 0; j < RH; ++j) l[j] = o[j] = 0.f;
+      // the sum of a row's parts, lowest first
+      auto load = [&](float (&v)[RH], uint32_t from) {
+        float z[NP][RH];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          if constexpr (RH == 16) tm_ld16(z[p], from + p * MR);
+          else tm_ld8(z[p], from + p * MR);
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) tm_wait_ld<RH>(z[p]);
+#pragma unroll
+        for (int j = 0; j < RH; ++j) v[j] = NP == 3 ? (z[NP - 1][j] + z[1][j]) + z[0][j] : z[1][j] + z[0][j];
+      };
+      for (int i = walk.tile0;; ++i, ++t) {  // the softmax of tile i, then the sums with tile i - 1's O
+        const int buf = t & 1;
+        const float before = alpha;
+        const bool tile = i < walk.tile1;
+        if (tile) TREE_WAIT(&sh.sfull[buf], (t >> 1) & 1);
+        if (live && tile) {
+          tm_fence_after();
+          float v[RH];
+          load(v, lanes + buf * NQ);
+          int any_lo = 0, hi = 0, t0 = 0;
+          if (i > 0) t0 = walk.cached(i, any_lo, hi);
+          const int tok = t0 + place;
+          const bool gone = sh.hide[t % kTreeHide][wq] >> lane & 1u;
+          // a window's tokens from base + 1 on below the deepest row's are not seen by all
+          if (i == 0) {
+#pragma unroll
+            for (int j = 0; j < RH; ++j)
+              v[j] = place < 64 && (seens[j] >> (place & 63) & 1) && !gone ? v[j] : -INFINITY;
+          } else if (i <= u.firsts || a.window == 0) {
+            if (__any_sync(~0u, tok >= hi || gone)) {
+#pragma unroll
+              for (int j = 0; j < RH; ++j) v[j] = tok < hi && !gone ? v[j] : -INFINITY;
+            }
+          } else if (__any_sync(~0u, tok >= hi || gone || tok < u.v.base - a.window + PI_TREE_MAX)) {
+#pragma unroll
+            for (int j = 0; j < RH; ++j)
+              v[j] = tok < hi && !gone && (tok >= los[j] || tok < sinks) ? v[j] : -INFINITY;
+          }
+          // rows' maxima over the warp's tokens: as whole numbers of the same order
+          int top = 0;
+#pragma unroll
+          for (int j = 0; j < RH; ++j) {
+            const int bits = __float_as_int(v[j]);
+            const int most = __reduce_max_sync(~0u, bits ^ (bits >> 31 & 0x7fffffff));
+            top = own == j ? most : top;
+          }
+          float tops[4];
+          if (!meet(__int_as_float(top ^ (top >> 31 & 0x7fffffff)), tops)) {
+            gave_up();
+            break;
+          }
+          const float up = fmaxf(m, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scl);
+          const float at = up == -INFINITY ? 0.f : up;
+          float next = at - kShift;
+          if (!(at - next <= kShift + 1.f)) next = at;
+          alpha = m == -INFINITY ? 0.f : ex2(ref - next);
+          m = up;
+          ref = next;
+          unsigned char* const pt = smem + C::kWeights + buf * C::kP + place * 128;
+          u64 p[RH / 2];
+#pragma unroll
+          for (int j = 0; j < RH; ++j) {
+            const float c = __shfl_sync(~0u, scl, j), n = __shfl_sync(~0u, next, j), f = __shfl_sync(~0u, alpha, j);
+            v[j] = ex2(__fmul_rn(v[j], c) - n);
+            l[j] = fmaf(l[j], f, v[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < RH / 2; ++j) p[j] = pair(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            uint32_t part[RH / 2];
+#pragma unroll
+            for (int j = 0; j < RH / 2; ++j) {
+              const float2 f = halves(p[j]);
+              part[j] = round2<DT>(f.x, f.y);
+              if (k + 1 < NP) p[j] = left2<DT>(p[j], part[j]);
+            }
+            const int n = k * MR + h * RH;
+#pragma unroll
+            for (int j = 0; j < RH / 8; ++j)
+              *reinterpret_cast<uint4*>(pt + ((n + 8 * j) >> 6) * kPanelK + (((((n + 8 * j) >> 3) & 7) ^ (place & 7)) << 4)) =
+                  make_uint4(part[4 * j], part[4 * j + 1], part[4 * j + 2], part[4 * j + 3]);
+          }
+          fence_async();
+          tm_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0 && tile) mbar_arrive(&sh.pfull[buf]);
+        if (i > walk.tile0) {
+          const int ob = (t - 1) % NO;
+          if (!mbar_wait(&sh.ofull[ob], (uint32_t)(((t - 1) / NO) & 1), w.limit_ns)) {
+            gave_up();
+            break;
+          }
+          if (live) {
+            tm_fence_after();
+            float x[RH];
+            load(x, lanes + C::kO + ob * NQ);
+#pragma unroll
+            for (int j = 0; j < RH; ++j) o[j] = fmaf(o[j], __shfl_sync(~0u, before, j), x[j]);
+            tm_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.oempty[ob]);
+        }
+        if (!tile) break;
+      }
+      if (!ok) break;
+      ++seg;
+      const bool begins = walk.begins(), ends = walk.ends(), direct = begins && ends;
+      if (begins && !ends && tid == 0)
+        w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + kTreeCost + u.tiles - 1), 1};
+      if (!live) continue;
+      const int dh = min(DV, D);
+      float mine = 0.f;
+#pragma unroll
+      for (int j = 0; j < RH; ++j) {
+        const float sum = warp_sum(l[j]);
+        const bool odd = __any_sync(~0u, place < dh && !(fabsf(o[j]) < INFINITY));
+        mine = own == j ? odd ? NAN : sum : mine;
+      }
+      float sums[4];
+      if (!meet(mine, sums)) {
+        gave_up();
+        break;
+      }
+      const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      const int r = h * RH + own, R = u.row0 + r, draft = R / a.group;
+      const int out = (u.slot * a.drafts + draft) * a.heads + u.g * a.group + R - draft * a.group;
+      const bool good = r < u.rows && sum < INFINITY, again = r < u.rows && !good;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const uint32_t rows = __ballot_sync(~0u, good);
+      float* const part = w.part + ((size_t)(2 * blockIdx.x + begins) * MR + h * RH) * (DV + 4);
+      if (wq == 0 && lane < RH && good) {
+        if (!direct) __stcg(reinterpret_cast<float2*>(part + lane * (DV + 4) + DV), make_float2(ref, sum));
+        else if (a.lse) a.lse[out] = (ref + log2f(sum)) * kLn2;
+      }
+#pragma unroll
+      for (int j = 0; j < RH; ++j) {
+        const float f = __shfl_sync(~0u, inv, j);
+        const int to = __shfl_sync(~0u, out, j);
+        if (place < dh && rows >> j & 1u) {
+          if (direct) a.y[(size_t)to * D + place] = o[j] * f;
+          else __stcg(part + j * (DV + 4) + place, o[j]);
+        }
+      }
+      // a row in four to each of the half's warps
+      for (uint32_t left = __ballot_sync(~0u, again && lane < RH && (lane & 3) == wq); left; left &= left - 1) {
+        const int j = __ffs(left) - 1;
+        const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, h * RH + j);
+        const float f = !direct ? 1.f : s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
+        const int to_row = __shfl_sync(~0u, out, j);
+        float* pr = part + j * (DV + 4);
+        if (8 * lane < dh) {
+          float4* to = reinterpret_cast<float4*>(direct ? a.y + (size_t)to_row * D + 8 * lane : pr + 8 * lane);
+          __stcg(to, make_float4(s.o[0] * f, s.o[1] * f, s.o[2] * f, s.o[3] * f));
+          __stcg(to + 1, make_float4(s.o[4] * f, s.o[5] * f, s.o[6] * f, s.o[7] * f));
+        }
+        if (lane == 0) {
+          if (!direct) __stcg(reinterpret_cast<float2*>(pr + DV), make_float2(s.m, s.l));
+          else if (a.lse) a.lse[to_row] = (s.m + log2f(s.l)) * kLn2;
+        }
+      }
+    }
+    }
   } else if (warp == 8) {
     // ---- MMAs
     int seg = 0, cols_before = 0, nv_before = 0;
@@ -1021,9 +1278,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       tm_fence_after();
       if (elected()) {
-        const uint64_t vd = tree_desc(smem_u32(smem + C::kStages + st * (C::kK + C::kV) + C::kK), kPanelK);
+        const uint32_t d = tmem + C::kO + ob * C::kO1;
+        const uint32_t vs = smem_u32(smem + C::kStages + st * (C::kK + C::kV) + C::kK);
+        if constexpr (kFew) {  // V^T (rows from DV on are not looked at) by P
+          const uint64_t vd = tree_desc(vs, DV == 128 ? kPanelK : 0);
+          const uint64_t pd = tree_desc(smem_u32(smem + C::kWeights + buf * C::kP), kPanelK);
+          const uint32_t idesc = tree_idesc<DT>(NQ, true, true);
+#pragma unroll
+          for (int ks = 0; ks < TN / 16; ++ks)
+            if (16 * ks < cols) mma_ss(d, vd + (2048 >> 4) * ks, pd + (2048 >> 4) * ks, idesc, ks > 0);
+        } else {
+        const uint64_t vd = tree_desc(vs, kPanelK);
         const uint32_t idesc = tree_idesc<DT>(nv, true);
-        const uint32_t d = tmem + C::kO + ob * DV;
         bool add = false;
 #pragma unroll
         for (int part = NP - 1; part >= 0; --part) {
@@ -1034,6 +1300,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               mma_ts(d, pa + (part == 2 ? 8 : 16) * ks, vd + (2048 >> 4) * ks, idesc, add);
               add = true;
             }
+        }
         }
         mma_commit(&sh.vempty[st]);
         mma_commit(&sh.ofull[ob]);
@@ -1055,6 +1322,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (elected()) {
           const uint64_t qd = tree_desc(smem_u32(smem), 16);
           const uint64_t kdesc = tree_desc(smem_u32(smem + C::kStages + st * (C::kK + C::kV)), 16);
+          if constexpr (kFew) {  // K by Q^T
+            const uint32_t idesc = tree_idesc<DT>(NQ, false);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+              if (k < kd)
+                mma_ss(tmem + buf * NQ, kdesc + (((k >> 2) * kPanelK + (k & 3) * 32) >> 4),
+                       qd + (((k >> 2) * kPanelQ + (k & 3) * 32) >> 4), idesc, k > 0);
+          } else {
           const uint32_t idesc = tree_idesc<DT>(cols, false);
           bool add = false;
 #pragma unroll
@@ -1066,6 +1341,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                        kdesc + (((k >> 2) * kPanelK + (k & 3) * 32) >> 4), idesc, add);
                 add = true;
               }
+          }
           mma_commit(&sh.kempty[st]);
           mma_commit(&sh.sfull[buf]);
         }
@@ -1115,6 +1391,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         return x;
       };
+      // the rows of q are read when the warps 0-7 come to the segment
+      for (int e = pt; e < u.rows * ((D + 31) / 32); e += 96) {
+        const int r = e / ((D + 31) / 32), R = u.row0 + r, d = R / a.group;
+        const float* q = a.q + (((size_t)u.slot * a.drafts + d) * a.heads + u.g * a.group + R - d * a.group) * D +
+                         32 * (e - r * ((D + 31) / 32));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+      }
       Boxes ahead = boxes_of(walk.tile0);
       for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
         const int st = t % S;
@@ -1245,10 +1528,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // Joins the parts of the units that several blocks share: a warp per row.
-template <int DT, int DP>
+template <int DT, int DP, int MR>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeWork w) {
-  using C = TreeTile<DT, DP>;
-  constexpr int MR = C::MR, DV = C::DV;
+  using C = TreeTile<DT, DP, MR>;
+  constexpr int DV = C::DV;
   pdl_enter();
   const TreeArgs& a = w.a;
   const TreeSpan sp = w.span[blockIdx.x];
@@ -1284,30 +1567,45 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   if (lane == 0 && a.lse && u.half == 0) a.lse[out] = (top + log2f(l)) * kLn2;
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int MR>
 static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const CUtensorMap& edge_map, const DevInfo& di,
                              pi_stream stream) {
-  using C = TreeTile<DT, DP>;
-  constexpr int smem = tree_smem<DT, DP>();
+  using C = TreeTile<DT, DP, MR>;
+  constexpr int smem = tree_smem<DT, DP, MR>();
   static_assert(smem <= 232448, "shared memory");
-  pi_status st = ensure_smem(reinterpret_cast<const void*>(tree_kernel<DT, DP>), smem);
+  pi_status st = ensure_smem(reinterpret_cast<const void*>(tree_kernel<DT, DP, MR>), smem);
   if (st != PI_OK) return st;
   // all blocks that are resident together, or fewer where the longest slots that the
   // tables and the window allow cannot use them
   const TreeArgs& a = w.a;
   long long seen = (long long)a.max_pages * a.page_tokens;
   if (a.window > 0 && (long long)a.window + a.sinks < seen) seen = (long long)a.window + a.sinks;
-  const long long units = (long long)a.slots * a.kv_heads * ((a.drafts * a.group + C::MR - 1) / C::MR) * w.halves;
+  const long long units = (long long)a.slots * a.kv_heads * ((a.drafts * a.group + MR - 1) / MR) * w.halves;
   const long long most = (seen + 63) / C::TN + 4;  // tiles of a unit
   const bool whole = most <= kTreeWhole;
   const long long useful = whole ? units : units * (most + kTreeCost);
   long long grid = di.sms < kTreeGrid ? di.sms : kTreeGrid;
   if (grid > useful) grid = useful;
-  st = launch(tree_kernel<DT, DP>, dim3((unsigned)grid), kTreeThreads, smem, stream, w, map,
+  st = launch(tree_kernel<DT, DP, MR>, dim3((unsigned)grid), kTreeThreads, smem, stream, w, map,
               edge_map);
   if (st != PI_OK || whole || grid < 2) return st;
-  const int rows = a.drafts * a.group < C::MR ? a.drafts * a.group : C::MR;
-  return launch(tree_join_kernel<DT, DP>, dim3((unsigned)(grid - 1), (unsigned)((rows + 7) / 8)), 256, 0, stream, w);
+  const int rows = a.drafts * a.group < MR ? a.drafts * a.group : MR;
+  return launch(tree_join_kernel<DT, DP, MR>, dim3((unsigned)(grid - 1), (unsigned)((rows + 7) / 8)), 256, 0, stream, w);
+}
+
+template <int DT>
+static pi_status launch_rows(TreeWork& w, const CUtensorMap& map, const CUtensorMap& edge_map, const DevInfo& di,
+                             pi_stream stream) {
+  const int rows = w.a.drafts * w.a.group;
+  if (w.a.head_dim <= 64)
+    return rows <= 16   ? launch_tree<DT, 64, 16>(w, map, edge_map, di, stream)
+           : rows <= 32 ? launch_tree<DT, 64, 32>(w, map, edge_map, di, stream)
+                        : launch_tree<DT, 64, 128>(w, map, edge_map, di, stream);
+  if (w.a.head_dim <= 128)
+    return rows <= 16   ? launch_tree<DT, 128, 16>(w, map, edge_map, di, stream)
+           : rows <= 32 ? launch_tree<DT, 128, 32>(w, map, edge_map, di, stream)
+                        : launch_tree<DT, 128, 128>(w, map, edge_map, di, stream);
+  return launch_tree<DT, 256, 64>(w, map, edge_map, di, stream);
 }
 
 // Map over a layer's rows (K and V rows of every page and kv head): boxes of 64
@@ -1399,9 +1697,7 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   st = dev_info(&di);
   if (st != PI_OK) return st;
   const bool f16 = C.dtype == PI_F16;
-  if (C.head_dim <= 64) return f16 ? launch_tree<0, 64>(w, map, edge_map, di, stream) : launch_tree<1, 64>(w, map, edge_map, di, stream);
-  if (C.head_dim <= 128) return f16 ? launch_tree<0, 128>(w, map, edge_map, di, stream) : launch_tree<1, 128>(w, map, edge_map, di, stream);
-  return f16 ? launch_tree<0, 256>(w, map, edge_map, di, stream) : launch_tree<1, 256>(w, map, edge_map, di, stream);
+  return f16 ? launch_rows<0>(w, map, edge_map, di, stream) : launch_rows<1>(w, map, edge_map, di, stream);
 }
 
 }  // extern "C"
