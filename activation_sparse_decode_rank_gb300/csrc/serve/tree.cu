@@ -192,11 +192,11 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 // low parts first.  A tile's O is read back and added to fp32 registers with a
 // rounded add: the tensor cores' own sums would drift over a long cache.
 //
-// Roles of a block's 12 warps.  0-7: load Q, softmax, and add up O; a thread has
+// Roles of a block's warps.  0-7: load Q, softmax, and add up O; a thread has
 // half a row, warps w and w + 4 the same rows, which share their maximum.  8:
 // issues the MMAs: S of the next tile, then O of the last, so that the products run
-// while the warps 0-7 are at the tile in between.  9-11: fill K and V: whole boxes of
-// tokens by TMA, everything else (drafts, the ends of what is seen, odd page sizes)
+// while the warps 0-7 are at the tile in between.  From 9 on: fill K, or V: whole boxes
+// of tokens by TMA, everything else (drafts, the ends of what is seen, odd page sizes)
 // by hand, with zeros for values nobody sees.
 //
 // Operands that are not finite.  Rows whose sums come out NaN or infinite are
@@ -204,6 +204,8 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 template <int DT, int DP, int MR>
 struct TreeTile {  // MR: query rows of a unit
   static constexpr bool kFew = MR <= 32;
+  static constexpr int KW = kFew ? 2 : 1, VW = 2;  // warps that fill K, V
+  static constexpr int kThreads = 32 * (9 + KW + VW);
   static constexpr int TN = DP == 256 ? 64 : 128;  // tokens of a tile
   static constexpr int DV = DP < 128 ? DP : 128;   // columns of V of a unit
   static constexpr int NP = DT == 0 ? 2 : 3;       // parts of q and p
@@ -222,7 +224,7 @@ struct TreeTile {  // MR: query rows of a unit
   static constexpr int kThird = 2 * kS, kO = kThird + (!kFew && DT == 1 ? TN : 0);
   static_assert(kO + NO * kO1 <= 512, "tensor memory");
 };
-constexpr int kTreeThreads = 384;
+constexpr int kTreeWarps = 13;   // at most
 constexpr int kTreeGrid = 192;   // most blocks
 constexpr int kTreeCost = 1;     // a unit's fixed cost, in tiles
 constexpr int kTreeWhole = 6;    // units of at most this many tiles are not split
@@ -256,8 +258,8 @@ struct TreeShared {
     float top[2][2][128];  // rows' maxima, of a tile's two halves; at a segment's end their sums
     float few[2][2][4][16];  // few rows: [..][half of the rows][32 tokens][row]
     struct {
-      long long sum[12], len[12];
-      int most[12];
+      long long sum[kTreeWarps], len[kTreeWarps];
+      int most[kTreeWarps];
       long long at;
       int slot, unit;
     } scan;
@@ -539,7 +541,7 @@ __device__ __forceinline__ RowSums tree_again(const TreeWork& w, const TreeUnit&
 }
 
 template <int DT, int DP, int MR>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+__global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     tree_kernel(const __grid_constant__ TreeWork w, const __grid_constant__ CUtensorMap map,
                 const __grid_constant__ CUtensorMap edge_map) {
   using C = TreeTile<DT, DP, MR>;
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // ---- the block's share of the line
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.kfull[i], 3);
-      mbar_init(&sh.vfull[i], 3);
+      mbar_init(&sh.kfull[i], C::KW);
+      mbar_init(&sh.vfull[i], C::VW);
       mbar_init(&sh.kempty[i], 1);
       mbar_init(&sh.vempty[i], 1);
     }
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   TreeLine line;
   {
     auto& sc = sh.scan;
-    const int k = (a.slots + kTreeThreads - 1) / kTreeThreads, s0 = tid * k, s1 = min(a.slots, s0 + k);
+    const int k = (a.slots + C::kThreads - 1) / C::kThreads, s0 = tid * k, s1 = min(a.slots, s0 + k);
     long long units = 0, tiles = 0;
     int most = 0;
     for (int s = s0; s < s1; ++s) {
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncthreads();
     long long all_u = 0, all_t = 0, low_u = 0, low_t = 0;
     most = 0;
-    for (int i = 0; i < kTreeThreads / 32; ++i) {
+    for (int i = 0; i < C::kThreads / 32; ++i) {
       if (i == warp) low_u = all_u, low_t = all_t;
       all_u += sc.sum[i];
       all_t += sc.len[i];
@@ -1354,20 +1356,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     if (ok && t > 0) pv(t - 1, cols_before, nv_before);
   } else {
-    // ---- K and V
-    const int pw = warp - 9, pt = tid - 288;  // of 3 warps, 96 threads
+    // ---- K, or V
+    const bool value = warp >= 9 + C::KW;
+    const int pw = warp - 9 - (value ? C::KW : 0), warps = value ? C::VW : C::KW;  // of the operand's warps
+    uint64_t* const full = value ? sh.vfull : sh.kfull;
+    uint64_t* const empty = value ? sh.vempty : sh.kempty;
+    const size_t half = (size_t)a.kv_heads * P * D;  // K to V in a page
     for (; walk.more() && ok; walk.next()) {
       if (!walk.any()) continue;
       const TreeUnit& u = walk.u;
-      const int dh = min(DV, D - u.half * 128), d0 = u.half * 128;
-      const int pk = (D + 63) >> 6, pv = (dh + 63) >> 6;       // panels
-      const int ck = 2 * kd, cv = ((dh + 15) & ~15) >> 3;      // 16-byte pieces of a row
-      const size_t half = (size_t)a.kv_heads * P * D;          // K to V in a page
+      const int dh = min(DV, D - u.half * 128);                  // the unit's columns of V
+      const int d0 = value ? u.half * 128 : 0, d1 = value ? dh : D;  // the operand's elements of a row
+      const int panels = (d1 + 63) >> 6, pieces = value ? ((dh + 15) & ~15) >> 3 : 2 * kd;  // of 16 bytes
       auto index_of = [&](int tok) { return w.page_shift >= 0 ? tok >> w.page_shift : tok / P; };
-      auto key_of = [&](int tok) -> const uint16_t* {          // null: page out of range
+      auto row_of = [&](int tok) -> const uint16_t* {  // null: page out of range
         const int j = index_of(tok);
         const int page = checked_page(__ldg(a.table + (size_t)u.slot * a.max_pages + j), a.pages, a.status);
-        return page < 0 ? nullptr : a.pool + (((size_t)page * 2 * a.kv_heads + u.g) * P + tok - j * P) * D;
+        return page < 0 ? nullptr
+                        : a.pool + (((size_t)page * 2 * a.kv_heads + u.g) * P + tok - j * P) * D + (value ? half : 0) + d0;
       };
       // Lane b's box of a tile: whether it is seen, its page and its row of the pool; read
       // a tile ahead.
@@ -1392,116 +1398,97 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         return x;
       };
       // the rows of q are read when the warps 0-7 come to the segment
-      for (int e = pt; e < u.rows * ((D + 31) / 32); e += 96) {
-        const int r = e / ((D + 31) / 32), R = u.row0 + r, d = R / a.group;
-        const float* q = a.q + (((size_t)u.slot * a.drafts + d) * a.heads + u.g * a.group + R - d * a.group) * D +
-                         32 * (e - r * ((D + 31) / 32));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-      }
+      if (value)
+        for (int e = 32 * pw + lane; e < u.rows * ((D + 31) / 32); e += 32 * C::VW) {
+          const int r = e / ((D + 31) / 32), R = u.row0 + r, d = R / a.group;
+          const float* q = a.q + (((size_t)u.slot * a.drafts + d) * a.heads + u.g * a.group + R - d * a.group) * D +
+                           32 * (e - r * ((D + 31) / 32));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+        }
+      const int be = pw + warps * lane;  // the lane's box and panel of a tile
+      const int bb = panels == 1 ? be : panels == 2 ? be >> 1 : panels == 4 ? be >> 2 : be / panels, bp = be - bb * panels;
       Boxes ahead = boxes_of(walk.tile0);
       for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
         const int st = t % S;
-        unsigned char* const ks = smem + C::kStages + st * (C::kK + C::kV);
-        unsigned char* const vs = ks + C::kK;
-        const uint32_t kpar = (uint32_t)(((t / S) - 1) & 1);
+        unsigned char* const to = smem + C::kStages + st * (C::kK + C::kV) + (value ? C::kK : 0);
         const Boxes now = ahead;
         const int t0 = now.t0, lo = now.lo, hi = now.hi;
         const int cols = i == 0 ? (u.v.count + 15) & ~15 : min(TN, (hi - t0 + 15) & ~15);
         const bool boxes = now.box && __all_sync(~0u, !now.some || (unsigned)now.page < (unsigned)a.pages);
         const bool fresh = i == 0 && a.k_new;
         ahead = boxes_of(i + 1);
-        const int box_row = (now.page * 2 * a.kv_heads + u.g) * P + now.row;  // of K
-        // Rows [r0, r1) of K or V by hand, zeros where nobody sees a row or its page is
-        // out of range.  New drafts are rounded to the cache's type, and stored by the
-        // first unit of their kv head.
-        auto piece = [&](bool value, int r, int e) {
-          const int tok = t0 + r;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (tok < lo || tok >= hi || e >= (value ? dh : D)) return x;
-          if (value) e += d0;
-          const uint16_t* key = nullptr;
-          if (!fresh || (u.row0 == 0 && (value || u.half == 0))) {
-            key = key_of(tok);
-            if (key && value) key += half;
-          }
-          if (fresh) {
-            const float4* f = reinterpret_cast<const float4*>(
-                (value ? a.v_new : a.k_new) + (((size_t)u.slot * a.drafts + r) * a.kv_heads + u.g) * D + e);
-            const float4 y = __ldg(f), z = __ldg(f + 1);
-            x = make_uint4(round2<DT>(y.x, y.y), round2<DT>(y.z, y.w), round2<DT>(z.x, z.y), round2<DT>(z.z, z.w));
-            if (key) *reinterpret_cast<uint4*>(const_cast<uint16_t*>(key) + e) = x;
-          } else if (key) {
-            x = *reinterpret_cast<const uint4*>(key + e);
-          }
-          return x;
-        };
-        auto fill = [&](bool value, int r0, int r1) {
-          const int pieces = value ? cv : ck, n = (r1 - r0) * pieces;
-          unsigned char* base = value ? vs : ks;
-#pragma unroll 1
-          for (int e0 = pt; e0 < n; e0 += 96 * 2) {
-            uint4 x[2];
-            int r[2], c[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int e = min(e0 + 96 * k, n - 1);
-              r[k] = e / pieces;
-              c[k] = e - r[k] * pieces;
-              r[k] += r0;
-              x[k] = piece(value, r[k], 8 * c[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<uint4*>(base + (c[k] >> 3) * kPanelK + r[k] * 128 + (((c[k] & 7) ^ (r[k] & 7)) << 4)) = x[k];
-          }
-        };
-        if (t >= S) TREE_WAIT(&sh.kempty[st], kpar);
-        if (pw == 0) {
+        const int box_row = __shfl_sync(~0u, (now.page * 2 * a.kv_heads + u.g) * P + now.row, bb & 31) +
+                            (value ? a.kv_heads * P : 0);
+        if (t >= S) TREE_WAIT(empty + st, ((t / S) - 1) & 1);
+        if (!value && pw == 0) {
           if (boxes || fresh) {
             if (lane < TN / 32) sh.hide[t % kTreeHide][lane] = 0;
           } else {
 #pragma unroll 1
             for (int k = 0; k < TN / 32; ++k) {
               const int tok = t0 + 32 * k + lane;
-              const uint32_t h = __ballot_sync(~0u, tok >= lo && tok < hi && !key_of(tok));
+              const uint32_t h = __ballot_sync(~0u, tok >= lo && tok < hi && !row_of(tok));
               if (lane == 0) sh.hide[t % kTreeHide][k] = h;
             }
           }
         }
-        if (!boxes) fill(false, 0, cols);
-        // TMA: a box's K where anything of it is seen, its V where all of it is; the V rows
-        // of the other boxes by hand
-        auto order = [&](bool value, int panels, unsigned char* base, uint64_t* bar) {
-          const int e = pw + 3 * lane, b = panels == 1 ? e : panels == 2 ? e >> 1 : panels == 4 ? e >> 2 : e / panels;
-          const int p = e - b * panels, y = __shfl_sync(~0u, box_row, b & 31) + (value ? a.kv_heads * P : 0);
-          const int r = b * now.box;  // of the tile
-          const bool mine = boxes && r < cols && (now.whole || (value ? t0 + r >= lo && t0 + r + now.box <= hi
-                                                                      : t0 + r + now.box > lo && t0 + r < hi));
-          const int n = __popc(__ballot_sync(~0u, mine));
-          if (lane == 0) mbar_expect(bar, (uint32_t)(n * now.box * 128));
-          __syncwarp();
-          if (mine && !(w.lose && blockIdx.x == 0 && t == 1 && !value && e == 0))
-            tree_box(smem_u32(base + p * kPanelK + r * 128), now.whole ? &map : &edge_map, (value ? d0 : 0) + 64 * p, y, bar);
-        };
-        fence_async();
-        __syncwarp();
-        order(false, pk, ks, &sh.kfull[st]);
-        if (t >= S) TREE_WAIT(&sh.vempty[st], kpar);
-        if (!now.whole) {
+        // Rows by hand, zeros where nobody sees a row or its page is out of range: all
+        // of them, or those of V in boxes that are not seen whole.  New drafts are
+        // rounded to the cache's type, and stored by the first unit of their kv head.
+        if (!boxes || (value && !now.whole)) {
+          auto piece = [&](int r, int e) {
+            const int tok = t0 + r;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (tok < lo || tok >= hi || e >= d1) return x;
+            if (!fresh) {
+              const uint16_t* row = row_of(tok);
+              return row ? *reinterpret_cast<const uint4*>(row + e) : x;
+            }
+            const float4* f = reinterpret_cast<const float4*>(
+                (value ? a.v_new : a.k_new) + (((size_t)u.slot * a.drafts + r) * a.kv_heads + u.g) * D + d0 + e);
+            const float4 y = __ldg(f), z = __ldg(f + 1);
+            return make_uint4(round2<DT>(y.x, y.y), round2<DT>(y.z, y.w), round2<DT>(z.x, z.y), round2<DT>(z.z, z.w));
+          };
+          const bool keep = fresh && u.row0 == 0 && (value || u.half == 0);
 #pragma unroll 1
-          for (int r = 0; r < cols;) {
-            const int b0 = t0 + r, n = boxes ? now.box : cols;
-            if (!boxes || b0 < lo || b0 + now.box > hi) fill(true, r, r + n);
-            r += n;
+          for (int r0 = 0; r0 < cols;) {
+            const int rows = boxes ? now.box : cols, b0 = t0 + r0, n = rows * pieces;
+            if (!boxes || b0 < lo || b0 + rows > hi) {
+#pragma unroll 1
+              for (int e0 = 32 * pw + lane; e0 < n; e0 += 128 * warps) {
+                uint4 x[4];
+                int r[4], c[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int e = min(e0 + 32 * warps * k, n - 1);
+                  r[k] = e / pieces;
+                  c[k] = e - r[k] * pieces;
+                  r[k] += r0;
+                  x[k] = piece(r[k], 8 * c[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  *reinterpret_cast<uint4*>(to + (c[k] >> 3) * kPanelK + r[k] * 128 + (((c[k] & 7) ^ (r[k] & 7)) << 4)) = x[k];
+                  if (keep && t0 + r[k] < hi && 8 * c[k] < d1)
+                    if (const uint16_t* row = row_of(t0 + r[k]))
+                      *reinterpret_cast<uint4*>(const_cast<uint16_t*>(row) + 8 * c[k]) = x[k];
+                }
+              }
+            }
+            r0 += rows;
           }
           fence_async();
-          __syncwarp();
-        } else if (!boxes) {
-          fill(true, 0, cols);
-          fence_async();
-          __syncwarp();
         }
-        order(true, pv, vs, &sh.vfull[st]);
+        __syncwarp();
+        // TMA: a box of K where anything of it is seen, of V where all of it is
+        const int r = bb * now.box;  // of the tile
+        const bool mine = boxes && r < cols && (now.whole || (value ? t0 + r >= lo && t0 + r + now.box <= hi
+                                                                    : t0 + r + now.box > lo && t0 + r < hi));
+        const int n = __popc(__ballot_sync(~0u, mine));
+        if (lane == 0) mbar_expect(full + st, (uint32_t)(n * now.box * 128));
+        __syncwarp();
+        if (mine && !(w.lose && blockIdx.x == 0 && t == 1 && !value && be == 0))
+          tree_box(smem_u32(to + bp * kPanelK + r * 128), now.whole ? &map : &edge_map, d0 + 64 * bp, box_row, full + st);
       }
     }
   }
@@ -1509,11 +1496,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   tm_fence_before();
   __syncthreads();
   if (sh.bad) {  // copies and MMAs under way come to their end (2 s at most)
-    if (warp == 9)
+    if (warp >= 9)
       for (int i = 0; i < S && i < t; ++i) {
         const int k = i + ((t - 1 - i) / S) * S;
-        mbar_wait(&sh.kfull[i], (uint32_t)((k / S) & 1), 500000000ull);
-        mbar_wait(&sh.vfull[i], (uint32_t)((k / S) & 1), 500000000ull);
+        mbar_wait((warp >= 9 + C::KW ? sh.vfull : sh.kfull) + i, (uint32_t)((k / S) & 1), 500000000ull);
       }
     if (warp == 8) {
       if (lane == 0) mma_commit(&sh.fin);
@@ -1586,7 +1572,7 @@ static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const CUtensor
   const long long useful = whole ? units : units * (most + kTreeCost);
   long long grid = di.sms < kTreeGrid ? di.sms : kTreeGrid;
   if (grid > useful) grid = useful;
-  st = launch(tree_kernel<DT, DP, MR>, dim3((unsigned)grid), kTreeThreads, smem, stream, w, map,
+  st = launch(tree_kernel<DT, DP, MR>, dim3((unsigned)grid), C::kThreads, smem, stream, w, map,
               edge_map);
   if (st != PI_OK || whole || grid < 2) return st;
   const int rows = a.drafts * a.group < MR ? a.drafts * a.group : MR;
