@@ -204,19 +204,21 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 template <int DT, int DP, int MR>
 struct TreeTile {  // MR: query rows of a unit
   static constexpr bool kFew = MR <= 32;
-  static constexpr int KW = kFew ? 2 : 1, VW = 2;  // warps that fill K, V
+  static constexpr int KW = MR == 16 ? 2 : 1, VW = 2;  // warps that fill K, V
   static constexpr int kThreads = 32 * (9 + KW + VW);
   static constexpr int TN = DP == 256 ? 64 : 128;  // tokens of a tile
   static constexpr int DV = DP < 128 ? DP : 128;   // columns of V of a unit
   static constexpr int NP = DT == 0 ? 2 : 3;       // parts of q and p
   static constexpr int NQ = NP * MR;               // few rows: columns of S and O
-  static constexpr int S = DP == 64 ? 4 : DP == 256 && DT == 0 ? 3 : 2;  // stages
+  // stages of K, of V
+  static constexpr int SV = DP == 64 ? 4 : DP == 256 && DT == 0 ? 3 : 2,
+                       SK = kFew && DP == 128 && (DT == 0 || MR == 16) ? 3 : SV;
   static constexpr int NO = !kFew && DT == 1 && DP == 128 ? 1 : 2;  // O tiles in tensor memory
   static constexpr int kK = TN * DP * 2, kV = TN * DV * 2;  // bytes of a stage
   static constexpr int kQ = MR * DP * 2;                    // of a part of Q
   static constexpr int kP = kFew ? (NQ + 63) / 64 * TN * 128 : 0;  // of P, two of which
-  static constexpr int kStages = (NP * kQ + 1023) / 1024 * 1024, kWeights = kStages + S * (kK + kV),
-                       kMisc = kWeights + 2 * kP;
+  static constexpr int kStages = (NP * kQ + 1023) / 1024 * 1024, kWeights = kStages + SK * kK + SV * kV,
+                       kMisc = kWeights + 2 * kP, kValues = kStages + SK * kK;
   // tensor-memory columns.  Many rows: two S tiles, 16 columns of which become the
   // first two parts of P for the same 16 tokens; the third parts of P; O.  Few rows: two
   // S tiles; O.
@@ -269,6 +271,7 @@ struct TreeSharedScale : TreeShared {
   float qs[2][128];  // rows' 2^-e of q (fp16)
 };
 struct TreeSharedFew : TreeShared {  // of a segment's rows
+  float4 figures[8][16];  // a warp's rows: factor of the scores, reference, the sums' factors
   float qs[2][32];
   int lo[2][32];
   u64 seen[2][32];
@@ -413,6 +416,25 @@ __device__ __forceinline__ u64 left2(u64 v, uint32_t r) {
   else h = make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
   return fma2(pair(h.x, h.y), pair(-1.f, -1.f), v);
 }
+// The rows' values of all lanes joined, N rows: row i's in the lanes 32 i / N and on.
+// Halves of the rows change places as halves of the lanes do.
+template <int N, typename F>
+__device__ __forceinline__ float warp_rows(float (&v)[N], F join) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = N / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+      v[i] = join(keep, __shfl_xor_sync(~0u, send, off));
+    }
+  }
+#pragma unroll
+  for (int off = 16 / N; off > 0; off >>= 1) v[0] = join(v[0], __shfl_xor_sync(~0u, v[0], off));
+  return v[0];
+}
+
 // A unit and its tiles.
 struct TreeUnit {
   int slot, unit;  // number within the slot: (g, rt, half)
@@ -546,7 +568,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
                 const __grid_constant__ CUtensorMap edge_map) {
   using C = TreeTile<DT, DP, MR>;
   constexpr bool kFew = C::kFew;
-  constexpr int TN = C::TN, DV = C::DV, NP = C::NP, NQ = C::NQ, S = C::S, NO = C::NO;
+  constexpr int TN = C::TN, DV = C::DV, NP = C::NP, NQ = C::NQ, SK = C::SK, SV = C::SV, NO = C::NO;
   constexpr int kPanelK = TN * 128, kPanelQ = (kFew ? NQ : MR) * 128;  // bytes of 64 columns
   using Shared = TreeSharedOf<DT, kFew>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -993,9 +1015,9 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     }
     } else {
     // ---- Q, softmax, O of few rows: a thread has a token of S and P, a column of V of O, in
-    // both for half of the rows; lane j keeps the figures of row j of its half
-    constexpr int RH = MR / 2;
-    const int h = warp >> 2, wq = warp & 3, place = 32 * wq + lane, own = lane & (RH - 1);
+    // both for half of the rows; Q lanes keep the figures of a row of the half
+    constexpr int RH = MR / 2, Q = 32 / RH;
+    const int h = warp >> 2, wq = warp & 3, place = 32 * wq + lane, own = lane / Q;
     const float flip = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
     const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
     constexpr float kShift = DT == 0 ? 14.f : 0.f;
@@ -1004,7 +1026,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     // The four warps of a half show each other a value per row; false where the wait ran
     // out.
     auto meet = [&](float mine, float (&all)[4]) {
-      if (lane < RH) sh.few[met & 1][h][wq][lane] = mine;
+      if (lane % Q == 0) sh.few[met & 1][h][wq][own] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.pair[h]);
       if (!mbar_spin(&sh.pair[h], (uint32_t)(met & 1), w.limit_ns)) return false;
@@ -1140,16 +1162,11 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
             for (int j = 0; j < RH; ++j)
               v[j] = tok < hi && !gone && (tok >= los[j] || tok < sinks) ? v[j] : -INFINITY;
           }
-          // rows' maxima over the warp's tokens: as whole numbers of the same order
-          int top = 0;
-#pragma unroll
-          for (int j = 0; j < RH; ++j) {
-            const int bits = __float_as_int(v[j]);
-            const int most = __reduce_max_sync(~0u, bits ^ (bits >> 31 & 0x7fffffff));
-            top = own == j ? most : top;
-          }
           float tops[4];
-          if (!meet(__int_as_float(top ^ (top >> 31 & 0x7fffffff)), tops)) {
+          float most[RH];
+#pragma unroll
+          for (int j = 0; j < RH; ++j) most[j] = v[j];
+          if (!meet(warp_rows(most, [](float x, float y) { return fmaxf(x, y); }), tops)) {
             gave_up();
             break;
           }
@@ -1162,11 +1179,14 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           ref = next;
           unsigned char* const pt = smem + C::kWeights + buf * C::kP + place * 128;
           u64 p[RH / 2];
+          __syncwarp();
+          if (lane % Q == 0) sh.figures[warp][own] = make_float4(scl, next, alpha, before);
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < RH; ++j) {
-            const float c = __shfl_sync(~0u, scl, j), n = __shfl_sync(~0u, next, j), f = __shfl_sync(~0u, alpha, j);
-            v[j] = ex2(__fmul_rn(v[j], c) - n);
-            l[j] = fmaf(l[j], f, v[j]);
+            const float4 f = sh.figures[warp][j];
+            v[j] = ex2(__fmul_rn(v[j], f.x) - f.y);
+            l[j] = fmaf(l[j], f.z, v[j]);
           }
 #pragma unroll
           for (int j = 0; j < RH / 2; ++j) p[j] = pair(v[2 * j], v[2 * j + 1]);
@@ -1201,7 +1221,10 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
             float x[RH];
             load(x, lanes + C::kO + ob * NQ);
 #pragma unroll
-            for (int j = 0; j < RH; ++j) o[j] = fmaf(o[j], __shfl_sync(~0u, before, j), x[j]);
+            for (int j = 0; j < RH; ++j) {
+              const float4 f = sh.figures[warp][j];
+              o[j] = fmaf(o[j], tile ? f.w : f.z, x[j]);
+            }
             tm_fence_before();
           }
           __syncwarp();
@@ -1216,15 +1239,11 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + kTreeCost + u.tiles - 1), 1};
       if (!live) continue;
       const int dh = min(DV, D);
-      float mine = 0.f;
 #pragma unroll
-      for (int j = 0; j < RH; ++j) {
-        const float sum = warp_sum(l[j]);
-        const bool odd = __any_sync(~0u, place < dh && !(fabsf(o[j]) < INFINITY));
-        mine = own == j ? odd ? NAN : sum : mine;
-      }
+      for (int j = 0; j < RH; ++j)
+        if (place < dh && !(fabsf(o[j]) < INFINITY)) l[j] = NAN;
       float sums[4];
-      if (!meet(mine, sums)) {
+      if (!meet(warp_rows(l, [](float x, float y) { return x + y; }), sums)) {
         gave_up();
         break;
       }
@@ -1235,25 +1254,25 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const uint32_t rows = __ballot_sync(~0u, good);
       float* const part = w.part + ((size_t)(2 * blockIdx.x + begins) * MR + h * RH) * (DV + 4);
-      if (wq == 0 && lane < RH && good) {
-        if (!direct) __stcg(reinterpret_cast<float2*>(part + lane * (DV + 4) + DV), make_float2(ref, sum));
+      if (wq == 0 && lane % Q == 0 && good) {
+        if (!direct) __stcg(reinterpret_cast<float2*>(part + own * (DV + 4) + DV), make_float2(ref, sum));
         else if (a.lse) a.lse[out] = (ref + log2f(sum)) * kLn2;
       }
 #pragma unroll
       for (int j = 0; j < RH; ++j) {
-        const float f = __shfl_sync(~0u, inv, j);
-        const int to = __shfl_sync(~0u, out, j);
-        if (place < dh && rows >> j & 1u) {
+        const float f = __shfl_sync(~0u, inv, j * Q);
+        const int to = __shfl_sync(~0u, out, j * Q);
+        if (place < dh && rows >> (j * Q) & 1u) {
           if (direct) a.y[(size_t)to * D + place] = o[j] * f;
           else __stcg(part + j * (DV + 4) + place, o[j]);
         }
       }
       // a row in four to each of the half's warps
-      for (uint32_t left = __ballot_sync(~0u, again && lane < RH && (lane & 3) == wq); left; left &= left - 1) {
-        const int j = __ffs(left) - 1;
+      for (uint32_t left = __ballot_sync(~0u, again && lane % Q == 0 && (own & 3) == wq); left; left &= left - 1) {
+        const int j = (__ffs(left) - 1) / Q;
         const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, h * RH + j);
         const float f = !direct ? 1.f : s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
-        const int to_row = __shfl_sync(~0u, out, j);
+        const int to_row = __shfl_sync(~0u, out, j * Q);
         float* pr = part + j * (DV + 4);
         if (8 * lane < dh) {
           float4* to = reinterpret_cast<float4*>(direct ? a.y + (size_t)to_row * D + 8 * lane : pr + 8 * lane);
@@ -1271,8 +1290,8 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     // ---- MMAs
     int seg = 0, cols_before = 0, nv_before = 0;
     auto pv = [&](int p, int cols, int nv) {  // tile p's O
-      const int buf = p & 1, st = p % S, ob = p % NO;
-      if (!mbar_wait(&sh.vfull[st], (uint32_t)((p / S) & 1), w.limit_ns) ||
+      const int buf = p & 1, st = p % SV, ob = p % NO;
+      if (!mbar_wait(&sh.vfull[st], (uint32_t)((p / SV) & 1), w.limit_ns) ||
           !mbar_wait(&sh.pfull[buf], (uint32_t)((p >> 1) & 1), w.limit_ns) ||
           (p >= NO && !mbar_wait(&sh.oempty[ob], (uint32_t)(((p / NO) - 1) & 1), w.limit_ns))) {
         gave_up();
@@ -1281,7 +1300,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       tm_fence_after();
       if (elected()) {
         const uint32_t d = tmem + C::kO + ob * C::kO1;
-        const uint32_t vs = smem_u32(smem + C::kStages + st * (C::kK + C::kV) + C::kK);
+        const uint32_t vs = smem_u32(smem + C::kValues + st * C::kV);
         if constexpr (kFew) {  // V^T (rows from DV on are not looked at) by P
           const uint64_t vd = tree_desc(vs, DV == 128 ? kPanelK : 0);
           const uint64_t pd = tree_desc(smem_u32(smem + C::kWeights + buf * C::kP), kPanelK);
@@ -1313,17 +1332,17 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       if (!walk.any()) continue;
       const int nv = (min(DV, D - walk.u.half * 128) + 15) & ~15;
       for (int i = walk.tile0; i < walk.tile1 && ok; ++i, ++t) {
-        const int st = t % S, buf = t & 1, cols = walk.columns(i);
+        const int st = t % SK, buf = t & 1, cols = walk.columns(i);
         if (i == walk.tile0) {
           if (t > 0) pv(t - 1, cols_before, nv_before);
           if (!ok) break;
           TREE_WAIT(&sh.qfull, seg & 1);
         }
-        TREE_WAIT(&sh.kfull[st], (t / S) & 1);
+        TREE_WAIT(&sh.kfull[st], (t / SK) & 1);
         tm_fence_after();
         if (elected()) {
           const uint64_t qd = tree_desc(smem_u32(smem), 16);
-          const uint64_t kdesc = tree_desc(smem_u32(smem + C::kStages + st * (C::kK + C::kV)), 16);
+          const uint64_t kdesc = tree_desc(smem_u32(smem + C::kStages + st * C::kK), 16);
           if constexpr (kFew) {  // K by Q^T
             const uint32_t idesc = tree_idesc<DT>(NQ, false);
 #pragma unroll
@@ -1359,6 +1378,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     // ---- K, or V
     const bool value = warp >= 9 + C::KW;
     const int pw = warp - 9 - (value ? C::KW : 0), warps = value ? C::VW : C::KW;  // of the operand's warps
+    const int stages = value ? SV : SK;
     uint64_t* const full = value ? sh.vfull : sh.kfull;
     uint64_t* const empty = value ? sh.vempty : sh.kempty;
     const size_t half = (size_t)a.kv_heads * P * D;  // K to V in a page
@@ -1409,8 +1429,8 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       const int bb = panels == 1 ? be : panels == 2 ? be >> 1 : panels == 4 ? be >> 2 : be / panels, bp = be - bb * panels;
       Boxes ahead = boxes_of(walk.tile0);
       for (int i = walk.tile0; i < walk.tile1; ++i, ++t) {
-        const int st = t % S;
-        unsigned char* const to = smem + C::kStages + st * (C::kK + C::kV) + (value ? C::kK : 0);
+        const int round = t / stages, st = t - round * stages;
+        unsigned char* const to = smem + (value ? C::kValues + st * C::kV : C::kStages + st * C::kK);
         const Boxes now = ahead;
         const int t0 = now.t0, lo = now.lo, hi = now.hi;
         const int cols = i == 0 ? (u.v.count + 15) & ~15 : min(TN, (hi - t0 + 15) & ~15);
@@ -1419,7 +1439,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         ahead = boxes_of(i + 1);
         const int box_row = __shfl_sync(~0u, (now.page * 2 * a.kv_heads + u.g) * P + now.row, bb & 31) +
                             (value ? a.kv_heads * P : 0);
-        if (t >= S) TREE_WAIT(empty + st, ((t / S) - 1) & 1);
+        if (round > 0) TREE_WAIT(empty + st, (round - 1) & 1);
         if (!value && pw == 0) {
           if (boxes || fresh) {
             if (lane < TN / 32) sh.hide[t % kTreeHide][lane] = 0;
@@ -1496,11 +1516,12 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
   tm_fence_before();
   __syncthreads();
   if (sh.bad) {  // copies and MMAs under way come to their end (2 s at most)
-    if (warp >= 9)
-      for (int i = 0; i < S && i < t; ++i) {
-        const int k = i + ((t - 1 - i) / S) * S;
-        mbar_wait((warp >= 9 + C::KW ? sh.vfull : sh.kfull) + i, (uint32_t)((k / S) & 1), 500000000ull);
-      }
+    if (warp >= 9) {
+      const bool value = warp >= 9 + C::KW;
+      const int stages = value ? SV : SK;
+      for (int i = 0; i < stages && i < t; ++i)
+        mbar_wait((value ? sh.vfull : sh.kfull) + i, (uint32_t)((t - 1 - i) / stages & 1), 500000000ull);
+    }
     if (warp == 8) {
       if (lane == 0) mma_commit(&sh.fin);
       mbar_wait(&sh.fin, 0, 2000000000ull);
