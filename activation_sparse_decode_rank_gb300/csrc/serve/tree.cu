@@ -228,8 +228,10 @@ struct TreeTile {  // MR: query rows of a unit
 };
 constexpr int kTreeWarps = 13;   // at most
 constexpr int kTreeGrid = 192;   // most blocks
-// A unit's fixed cost, in tiles: Q, its drafts' rows, its output.
-__host__ __device__ constexpr int tree_cost(int mr) { return mr <= 32 ? 3 : 8; }
+// A unit's fixed cost, in tiles: Q, its drafts' rows, its output.  With 1 instead, 32
+// slots x 40 heads, 13 drafts, take 238 us (174), 8 slots, 64/8 heads, chains of 64,
+// 1084 us (470): a slot with nothing before its drafts is all fixed cost.
+__host__ __device__ __forceinline__ int tree_cost(int mr, int drafts) { return 4 + (mr <= 32 ? drafts / 8 : drafts / 4); }
 constexpr int kTreeWhole = 6;    // units of at most this many tiles are not split
 constexpr int kTreeShare = 3;    // least share of a block
 constexpr int kTreeHide = 8;     // more than the tiles between the filling of K and the softmax
@@ -484,8 +486,8 @@ struct TreeWalk {
       tile0 = 0;
       tile1 = u.tiles;
     } else {
-      const long long a1 = end - at - tree_cost(MR);
-      tile0 = at < -tree_cost(MR) ? (int)(-at - tree_cost(MR)) : 0;
+      const long long a1 = end - at - tree_cost(MR, u.v.count);
+      tile0 = at < -tree_cost(MR, u.v.count) ? (int)(-at - tree_cost(MR, u.v.count)) : 0;
       tile1 = a1 < u.tiles ? (int)a1 : u.tiles;
     }
   }
@@ -494,7 +496,7 @@ struct TreeWalk {
   __device__ __forceinline__ bool begins() const { return tile0 == 0; }
   __device__ __forceinline__ bool ends() const { return tile1 == u.tiles; }
   __device__ __forceinline__ void next() {
-    at += whole ? 1 : u.tiles + tree_cost(MR);
+    at += whole ? 1 : u.tiles + tree_cost(MR, u.v.count);
     if (at >= end) return;
     if (++u.unit < units) {
       fit();
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       if (blockIdx.x == 0 && tree_slot_bad(a, s)) set_status(a.status, PI_ERR_INDEX);
       const int n = tree_units(w, v, MR), t = tree_tiles<TN>(w, v);
       units += n;
-      tiles += (long long)n * (t + tree_cost(MR));
+      tiles += (long long)n * (t + tree_cost(MR, v.count));
       if (n) most = max(most, t);
     }
     auto sum_up = [&](long long v) {
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     if (share0 >= at && share0 < at + (whole ? units : tiles) && share0 < share1) {
       for (int s = s0; s < s1; ++s) {
         const TreeSlot v = tree_slot(a, s);
-        const int n = tree_units(w, v, MR), len = whole ? 1 : tree_tiles<TN>(w, v) + tree_cost(MR);
+        const int n = tree_units(w, v, MR), len = whole ? 1 : tree_tiles<TN>(w, v) + tree_cost(MR, v.count);
         if (share0 < at + (long long)n * len) {
           sc.slot = s;
           sc.unit = (int)((share0 - at) / len);
@@ -953,7 +955,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       if (!ok) break;
       const bool begins = walk.begins(), ends = walk.ends();
       if (begins && !ends && tid == 0)
-        w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + tree_cost(MR) + u.tiles - 1), 1};
+        w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + tree_cost(MR, u.v.count) + u.tiles - 1), 1};
       const int dh = min(DV, D - u.half * 128) - h * HO;  // the half's columns of the unit's
       float o[HO];
       bool odd = false;
@@ -1237,7 +1239,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       ++seg;
       const bool begins = walk.begins(), ends = walk.ends(), direct = begins && ends;
       if (begins && !ends && tid == 0)
-        w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + tree_cost(MR) + u.tiles - 1), 1};
+        w.span[blockIdx.x] = TreeSpan{u.slot, u.unit, sh.line.block_of(sh.share0 + walk.at + tree_cost(MR, u.v.count) + u.tiles - 1), 1};
       if (!live) continue;
       const int dh = min(DV, D);
 #pragma unroll
@@ -1591,7 +1593,7 @@ static pi_status launch_tree(TreeWork& w, const CUtensorMap& map, const CUtensor
   const long long units = (long long)a.slots * a.kv_heads * ((a.drafts * a.group + MR - 1) / MR) * w.halves;
   const long long most = (seen + 63) / C::TN + 4;  // tiles of a unit
   const bool whole = most <= kTreeWhole;
-  const long long useful = whole ? units : units * (most + tree_cost(MR));
+  const long long useful = whole ? units : units * (most + tree_cost(MR, a.drafts));
   long long grid = di.sms < kTreeGrid ? di.sms : kTreeGrid;
   if (grid > useful) grid = useful;
   st = launch(tree_kernel<DT, DP, MR>, dim3((unsigned)grid), C::kThreads, smem, stream, w, map,
