@@ -40,7 +40,7 @@ struct SampleArgs {
   int held;  // the row's logits fit the cluster's shared memory
 };
 
-constexpr int kSampleThreads = 512;
+constexpr int kSampleThreads = 1024;
 constexpr int kBins = 2048, kBinsPerThread = kBins / kSampleThreads;
 constexpr int kBinsPerOctave = 32;
 constexpr int kList = 1024;          // logits that are ordered at once
@@ -53,7 +53,7 @@ struct Bins {
 };
 struct SampleShared {
   Bins local, total;
-  u64 list[kList], sorted[kList];
+  u64 list[kList], spare[kList];
   u64 scan[kSampleThreads / 32];
   u64 scale[kBinsPerOctave];  // 2^(63 - i/32)
   float warp_top[kSampleThreads / 32];
@@ -63,7 +63,7 @@ struct SampleShared {
   // where a border was found: its bin, the sums before it, what is in it
   int at_bin;
   u64 before_n, before_w, before_q, inside_n;
-  u64 at_key, at_q, at_upto;  // its logit, that one's whole-number weight, the sum up to it
+  u64 at_key, at_upto;  // its logit, the sum up to it
 };
 
 template <int DT>
@@ -116,6 +116,52 @@ __device__ __forceinline__ void bin_add(Bins& h, int b, int q) {
 __device__ __forceinline__ u64 bin_sum(const Bins& h, int b) {
   const u64 n = h.count[b], q = ((u64)h.high[b] << 32) + h.low[b];
   return n * ((u64)kOne + kBias) - q;
+}
+
+// Sorts list[0, n), n <= kList, ascending, a key per thread: few by counting the
+// smaller ones, more by a bitonic network whose short steps are exchanges in a warp and
+// whose others go through list and spare in turn.
+__device__ __forceinline__ void sort_list(u64* list, u64* spare, int n) {
+  static_assert(kList == kSampleThreads, "a key per thread");
+  const int tid = threadIdx.x;
+  if (n <= 384) {
+    if (tid < n) {
+      const u64 v = list[tid];
+      int less = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) less += list[i] < v;
+      spare[less] = v;
+    }
+    __syncthreads();
+    if (tid < n) list[tid] = spare[tid];
+    __syncthreads();
+    return;
+  }
+  int size = 32;
+  while (size < n) size *= 2;
+  u64 v = tid < n ? list[tid] : ~0ull;
+  u64 *to = spare, *other = list;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2) {
+    const bool up = (tid & k) == 0;
+    for (int j = k / 2; j >= 32; j /= 2) {
+      to[tid] = v;
+      __syncthreads();
+      const u64 w = to[tid ^ j];
+      v = ((tid & j) == 0) == up ? (v < w ? v : w) : (v > w ? v : w);
+      u64* const t = to;
+      to = other;
+      other = t;
+    }
+    if ((tid & ~31) < size)
+      for (int j = min(k / 2, 16); j > 0; j /= 2) {
+        const u64 w = __shfl_xor_sync(~0u, v, j);
+        v = ((tid & j) == 0) == up ? (v < w ? v : w) : (v > w ? v : w);
+      }
+  }
+  __syncthreads();
+  if (tid < n) list[tid] = v;
+  __syncthreads();
 }
 
 // One cluster per row (and those after it).
@@ -242,14 +288,20 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     }
 
     // ---- bins: sums of every block's
-    auto bins_of = [&](auto which) {  // which(x, i): bin, or kBins; q is that of x's own bin
-      each([&](float x, int i) {
-        const int own = W.bin(x);
-        if (own < kBins) {
-          const int b = which(x, i, own);
-          if (b < kBins) bin_add(S.local, b, W.q(x, own));
-        }
-      });
+    auto bins_of = [&](bool sums, auto which) {  // which(x, i): bin, or kBins; q is that of x's own bin
+      if (sums)
+        each([&](float x, int i) {
+          const int own = W.bin(x);
+          if (own < kBins) {
+            const int b = which(x, i, own);
+            if (b < kBins) bin_add(S.local, b, W.q(x, own));
+          }
+        });
+      else
+        each([&](float x, int) {
+          const int own = W.bin(x);
+          if (own < kBins) atomicAdd(&S.local.count[own], 1u);
+        });
       cluster.sync();
       for (int b = rank * T + tid; b < kBins; b += C * T) {
         uint32_t n = 0, h = 0;
@@ -291,7 +343,84 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       before = low + upto - v;
       return all;
     };
-    bins_of([&](float, int, int own) { return own; });
+    auto weight_of = [&](u64 key) {  // of one logit, not rounded to the sums' units
+      const float x = key_logit(key);
+      const int b = W.bin(x);
+      return (double)((u64)kOne - (long long)W.q(x, b)) * (double)S.scale[b & (kBinsPerOctave - 1)] *
+             (double)exp2f((float)(room - 64 - b / kBinsPerOctave));
+    };
+    // ---- few logits are kept before top-p: those alone, in one list
+    if ((top_k > 0 && top_k <= kList) || min_p > 0.f) {
+      bins_of(false, [&](float, int, int own) { return own; });
+      u64 n = 0, before;
+      for (int k = 0; k < kBinsPerThread; ++k) n += S.total.count[tid * kBinsPerThread + k];
+      const u64 all = scan_n(n, before), want = top_k > 0 && (u64)top_k < all ? (u64)top_k : all;
+      for (int k = 0; k < kBinsPerThread && before < want; ++k) {
+        const int b = tid * kBinsPerThread + k;
+        const u64 c = S.total.count[b];
+        if (before + c >= want && c) {
+          S.at_bin = b;
+          S.inside_n = before + c;
+        }
+        before += c;
+      }
+      __syncthreads();
+      const int bin = S.at_bin;
+      if (S.inside_n <= kList) {  // the same in every block
+        SampleShared& F = *cluster.map_shared_rank(&S, 0);
+        each([&](float x, int i) {
+          if (W.bin(x) <= bin) {
+            const int at = atomicAdd(&F.list_n, 1);
+            if (at < kList) F.list[at] = order_key(x, i);
+          }
+        });
+        cluster.sync();
+        if (rank == 0) {
+          sort_list(S.list, S.spare, (int)S.inside_n);
+          constexpr int each_n = kList / T;
+          u64 v[each_n], mine = 0, v0;
+          for (int k = 0; k < each_n; ++k) {
+            const int i = tid * each_n + k;
+            v[k] = 0;
+            if (i < (int)want) {
+              const float x = key_logit(S.list[i]);
+              const int b = W.bin(x);
+              v[k] = weight((u64)kOne - (long long)W.q(x, b), b);
+            }
+            mine += v[k];
+          }
+          u64 sum = scan_n(mine, v0);
+          const u64 ahead = v0;
+          auto find = [&](u64 target) {  // the place where the running sum reaches it: S.at_key, ...
+            v0 = ahead;
+            for (int k = 0; k < each_n; ++k) {
+              if (v0 < target && v0 + v[k] >= target) {
+                S.at_key = S.list[tid * each_n + k];
+                S.at_upto = v0 + v[k];
+              }
+              v0 += v[k];
+            }
+            __syncthreads();
+          };
+          if (top_p < 1.f) {
+            find(max(1ull, (u64)ceil((double)top_p * (double)sum)));
+            sum = S.at_upto;
+            __syncthreads();
+          }
+          find((u64)((double)u * (double)sum) + 1);
+          if (tid == 0) {
+            a.token[row] = (int)(uint32_t)S.at_key;
+            if (a.logprob) {
+              const double p = weight_of(S.at_key) / (double)sum;
+              a.logprob[row] = p > 0.5 ? log1pf((float)(p - 1.0)) : logf((float)p);
+            }
+          }
+        }
+        continue;
+      }
+      __syncthreads();
+    }
+    bins_of(true, [&](float, int, int own) { return own; });
 
     // The bins' running sums: those before the thread's bins, and of all.
     u64 bins_n, bins_w, all_n, all_w;
@@ -310,10 +439,10 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     const u64 row_n = all_n, row_w = all_w;
     bool whole = true;  // S.total holds the bins of all logits
     // Finds the logit at which the running count (COUNT) or sum reaches
-    // `target`, 1 .. that of the row: S.at_key, S.at_q and S.at_upto.
+    // `target`, 1 .. that of the row: S.at_key and S.at_upto.
     auto locate = [&](bool count, u64 target) {
       if (!whole) {
-        bins_of([&](float, int, int own) { return own; });
+        bins_of(true, [&](float, int, int own) { return own; });
         whole = true;
       }
       {
@@ -343,7 +472,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       while (inside > kList) {
         whole = false;
         const int sh = max(0, 64 - 11 - __clzll(size));  // 2048 parts
-        bins_of([&](float x, int i, int own) {
+        bins_of(true, [&](float x, int i, int own) {
           const u64 k = order_key(x, i) - lo;
           return own == bin && k < size ? (int)(k >> sh) : kBins;
         });
@@ -386,19 +515,13 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       cluster.sync();
       if (rank == 0) {
         const int n = min(S.list_n, kList);
-        for (int i = tid; i < n; i += T) {
-          const u64 k = S.list[i];
-          int less = 0;
-          for (int j = 0; j < n; ++j) less += S.list[j] < k;
-          S.sorted[less] = k;
-        }
-        __syncthreads();
+        sort_list(S.list, S.spare, n);
         constexpr int each_n = kList / T;
         u64 q[each_n], mine = 0, q0;
 #pragma unroll
         for (int k = 0; k < each_n; ++k) {
           const int i = tid * each_n + k;
-          q[k] = i < n ? (u64)kOne - (long long)W.q(key_logit(S.sorted[i]), bin) : 0;
+          q[k] = i < n ? (u64)kOne - (long long)W.q(key_logit(S.list[i]), bin) : 0;
           mine += q[k];
         }
         scan_n(mine, q0);
@@ -409,8 +532,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
           const u64 was = count ? before_n + i : before_w + weight(q0, bin);
           const u64 is = count ? before_n + i + 1 : before_w + weight(q0 + q[k], bin);
           if (i < n && was < target && is >= target) {
-            S.at_key = S.sorted[i];
-            S.at_q = q[k];
+            S.at_key = S.list[i];
             S.at_upto = before_w + weight(q0 + q[k], bin);
           }
           q0 += q[k];
@@ -421,7 +543,6 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
           for (int r = 1; r < C; ++r) {
             SampleShared& o = *cluster.map_shared_rank(&S, r);
             o.at_key = S.at_key;
-            o.at_q = S.at_q;
             o.at_upto = S.at_upto;
           }
         }
@@ -442,10 +563,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     if (rank == 0 && tid == 0) {
       a.token[row] = (int)(uint32_t)S.at_key;
       if (a.logprob) {
-        const int bin = W.bin(key_logit(S.at_key));
-        const double w = (double)S.at_q * (double)S.scale[bin & (kBinsPerOctave - 1)] *
-                         (double)exp2f((float)(room - 64 - bin / kBinsPerOctave));
-        const double p = w / (double)sum;
+        const double p = weight_of(S.at_key) / (double)sum;
         a.logprob[row] = p > 0.5 ? log1pf((float)(p - 1.0)) : logf((float)p);
       }
     }
