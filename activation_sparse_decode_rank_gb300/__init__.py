@@ -389,5 +389,5 @@ from .serve import (  # noqa: E402
     PI_CACHE_MAX_SLOTS, PI_F32, PI_TOPK_MAX, PI_TREE_MAX, cache_workspace, logprob_workspace,
     make_cache_desc, pi_cache_append, pi_cache_compact, pi_cache_copy, pi_cache_desc, pi_cache_fork,
     pi_cache_workspace_size, pi_logprob_workspace_size, pi_paged_attention, pi_sample_workspace_size,
-    pi_selftest_attention_timeout, pi_token_logprobs, pi_token_sample, pi_tree_accept,
+    pi_selftest_attention_timeout, pi_selftest_tree_timeout, pi_token_logprobs, pi_token_sample, pi_tree_accept,
     pi_tree_attention, pi_tree_workspace_size, sample_workspace, tree_workspace)

@@ -250,9 +250,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, uint32_t parity, unsigned
   }
   return true;
 }
-// The same for waits that are short as a rule: looks a few times before it lets the
-// hardware suspend the warp.
-__device__ __forceinline__ bool mbar_spin(uint64_t* m, uint32_t parity, unsigned long long limit_ns) {
+// A few looks at a phase that is soon over, before a wait that lets the hardware
+// suspend the warp.
+__device__ __forceinline__ bool mbar_spin(uint64_t* m, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; i < 32; ++i) {
     uint32_t ok;
@@ -265,7 +265,7 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* m, uint32_t parity, unsigned
         : "memory");
     if (__all_sync(~0u, ok)) return true;
   }
-  return mbar_wait(m, parity, limit_ns);
+  return false;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -295,11 +295,6 @@ __device__ __forceinline__ float2 halves(u64 v) {
 __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   u64 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ u64 add2(u64 a, u64 b) {

@@ -135,9 +135,11 @@ __device__ __forceinline__ void row_add32(const TreeArgs& a, const float* q, con
 // first `sinks` are seen.
 template <int DT>
 __device__ __forceinline__ void row_add_cached(const TreeArgs& a, int slot, int g, const float* q, int t0, int t1,
-                                               int lo, RowSums& r) {
+                                               int lo, RowSums& r, int* beat) {
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int t = t0 + lane; t - lane < t1; t += 32) {
+    if (lane == 0) atomicAdd(beat, 1);
     const uint16_t* key = nullptr;
     if (t < t1 && (t >= lo || t < a.sinks)) {
       const int j = t / a.page_tokens;
@@ -256,6 +258,7 @@ struct TreeShared {
   uint64_t pair[4], qfull, fin;
   uint32_t taddr;
   int bad;
+  int beat;  // goes on while rows are gone through again, which others wait for
   TreeLine line;
   long long share0;
   uint32_t hide[kTreeHide][4];  // tokens of a tile whose page is out of range
@@ -552,15 +555,16 @@ __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, const TreeUnit& u
 // The segment [tile0, tile1) of row r once more, in fp32; the warp's lanes hold the
 // columns 8 lane .. of it.
 template <int DT, int TN, int MR>
-__device__ __forceinline__ RowSums tree_again(const TreeWork& w, const TreeUnit& u, int tile0, int tile1, int r) {
+__device__ __forceinline__ RowSums tree_again(const TreeWork& w, const TreeUnit& u, int tile0, int tile1, int r, int* beat) {
   const TreeArgs& a = w.a;
   const TreeRow x = tree_row(a, u, r, [&](int j) { return __ldg(a.parent + (size_t)u.slot * a.drafts + j); });
   RowSums s = {-INFINITY, 0.f, {}};
   const int f0 = max(tile0, 1) - 1, f1 = min(tile1 - 1, u.firsts);
-  if (f0 < f1) row_add_cached<DT>(a, u.slot, u.g, x.q, f0 * TN, min(u.v.first, f1 * TN), x.lo, s);
+  if (f0 < f1) row_add_cached<DT>(a, u.slot, u.g, x.q, f0 * TN, min(u.v.first, f1 * TN), x.lo, s, beat);
   const int w0 = max(tile0 - 1 - u.firsts, 0), w1 = tile1 - 1 - u.firsts;
   if (w0 < w1)
-    row_add_cached<DT>(a, u.slot, u.g, x.q, max(u.v.tail, u.start + w0 * TN), min(u.v.base, u.start + w1 * TN), x.lo, s);
+    row_add_cached<DT>(a, u.slot, u.g, x.q, max(u.v.tail, u.start + w0 * TN), min(u.v.base, u.start + w1 * TN), x.lo, s,
+                       beat);
   if (tile0 == 0) row_add_drafts<DT>(a, u.slot, u.v, u.g, x.q, x.seen, s);
   return s;
 }
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     mbar_init(&sh.qfull, 8);
     mbar_init(&sh.fin, 1);
     fence_mbar_init();
-    sh.bad = 0;
+    sh.bad = sh.beat = 0;
     w.span[blockIdx.x] = TreeSpan{0, 0, 0, 0};
   }
   long long share0, share1, unit_at;
@@ -696,10 +700,18 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     *(volatile int*)&sh.bad = 1;
     ok = false;
   };
-#define TREE_WAIT(bar, parity)                            \
-  if (!mbar_wait(bar, (uint32_t)(parity), w.limit_ns)) { \
-    gave_up();                                            \
-    break;                                                \
+  // A bounded wait, begun anew while rows are gone through again.
+  auto wait_for = [&](uint64_t* bar, uint32_t parity) {
+    for (;;) {
+      const int beat = __shfl_sync(~0u, *(volatile int*)&sh.beat, 0);
+      if (mbar_wait(bar, parity, w.limit_ns)) return true;
+      if (__shfl_sync(~0u, *(volatile int*)&sh.beat, 0) == beat) return false;
+    }
+  };
+#define TREE_WAIT(bar, parity)              \
+  if (!wait_for(bar, (uint32_t)(parity))) { \
+    gave_up();                              \
+    break;                                  \
   }
 
   if (warp < 8) {
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       sh.top[met & 1][h][row] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.pair[wq]);
-      if (!mbar_spin(&sh.pair[wq], (uint32_t)(met & 1), w.limit_ns)) return false;
+      if (!mbar_spin(&sh.pair[wq], (uint32_t)(met & 1)) && !wait_for(&sh.pair[wq], (uint32_t)(met & 1))) return false;
       theirs = sh.top[met & 1][1 - h][row];
       ++met;
       return true;
@@ -888,7 +900,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           alpha = m == -INFINITY ? 0.f : ex2(ref - next);
           m = up;
           ref = next;
-          const u64 scl2 = pair(scl, scl), next2 = pair(-next, -next);
+          const u64 next2 = pair(-next, -next);
           const uint32_t third = lanes + C::kThird + buf * (TN / 2) + first / 2;
           u64 sum[2] = {0, 0};
           auto weights_of = [&](int k) {  // of 32 columns from 16 k on
@@ -904,7 +916,9 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
               uint32_t part[16], last[8];
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                const float2 d = halves(add2(mul2(pair(v[16 * j + 2 * c], v[16 * j + 2 * c + 1]), scl2), next2));
+                // rounded before the difference, as the maximum is (a packed product would be
+                // fused with the sum: large scores' weights then lie anywhere)
+                const float2 d = halves(add2(pair(__fmul_rn(v[16 * j + 2 * c], scl), __fmul_rn(v[16 * j + 2 * c + 1], scl)), next2));
                 u64 p = pair(ex2(d.x), ex2(d.y));
                 sum[c & 1] = add2(sum[c & 1], p);
                 float2 f = halves(p);
@@ -932,7 +946,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         if (lane == 0 && tile) mbar_arrive(&sh.pfull[buf]);
         if (i > walk.tile0) {
           const int ob = (t - 1) % NO;
-          if (!mbar_wait(&sh.ofull[ob], (uint32_t)(((t - 1) / NO) & 1), w.limit_ns)) {
+          if (!wait_for(&sh.ofull[ob], (uint32_t)(((t - 1) / NO) & 1))) {
             gave_up();
             break;
           }
@@ -998,7 +1012,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       }
       for (uint32_t left = __ballot_sync(~0u, again); left; left &= left - 1) {
         const int r = (row & ~31) + __ffs(left) - 1;
-        const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, r);
+        const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, r, &sh.beat);
         const float inv = s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
         const int Rr = u.row0 + r, dr = Rr / a.group, c = 8 * lane - 128 * u.half;
         const size_t to_row = ((size_t)u.slot * a.drafts + dr) * a.heads + u.g * a.group + Rr - dr * a.group;
@@ -1032,7 +1046,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       if (lane % Q == 0) sh.few[met & 1][h][wq][own] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.pair[h]);
-      if (!mbar_spin(&sh.pair[h], (uint32_t)(met & 1), w.limit_ns)) return false;
+      if (!mbar_spin(&sh.pair[h], (uint32_t)(met & 1)) && !wait_for(&sh.pair[h], (uint32_t)(met & 1))) return false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) all[k] = sh.few[met & 1][h][k][own];
       ++met;
@@ -1215,7 +1229,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         if (lane == 0 && tile) mbar_arrive(&sh.pfull[buf]);
         if (i > walk.tile0) {
           const int ob = (t - 1) % NO;
-          if (!mbar_wait(&sh.ofull[ob], (uint32_t)(((t - 1) / NO) & 1), w.limit_ns)) {
+          if (!wait_for(&sh.ofull[ob], (uint32_t)(((t - 1) / NO) & 1))) {
             gave_up();
             break;
           }
@@ -1273,7 +1287,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
       // a row in four to each of the half's warps
       for (uint32_t left = __ballot_sync(~0u, again && lane % Q == 0 && (own & 3) == wq); left; left &= left - 1) {
         const int j = (__ffs(left) - 1) / Q;
-        const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, h * RH + j);
+        const RowSums s = tree_again<DT, TN, MR>(w, u, walk.tile0, walk.tile1, h * RH + j, &sh.beat);
         const float f = !direct ? 1.f : s.l > 0.f ? 1.f / s.l : s.l == s.l ? 0.f : s.l;
         const int to_row = __shfl_sync(~0u, out, j * Q);
         float* pr = part + j * (DV + 4);
@@ -1294,9 +1308,9 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
     int seg = 0, cols_before = 0, nv_before = 0;
     auto pv = [&](int p, int cols, int nv) {  // tile p's O
       const int buf = p & 1, st = p % SV, ob = p % NO;
-      if (!mbar_wait(&sh.vfull[st], (uint32_t)((p / SV) & 1), w.limit_ns) ||
-          !mbar_wait(&sh.pfull[buf], (uint32_t)((p >> 1) & 1), w.limit_ns) ||
-          (p >= NO && !mbar_wait(&sh.oempty[ob], (uint32_t)(((p / NO) - 1) & 1), w.limit_ns))) {
+      if (!wait_for(&sh.vfull[st], (uint32_t)((p / SV) & 1)) ||
+          !wait_for(&sh.pfull[buf], (uint32_t)((p >> 1) & 1)) ||
+          (p >= NO && !wait_for(&sh.oempty[ob], (uint32_t)(((p / NO) - 1) & 1)))) {
         gave_up();
         return;
       }
@@ -1645,12 +1659,14 @@ size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t
   return kTreeSpans + (size_t)kTreeGrid * 2 * (cache->head_dim > 128 ? 64 : 128) * (dv + 4) * 4;
 }
 
-pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots, int32_t heads,
-                            int32_t max_pages, int32_t drafts, const int32_t* parent, const int32_t* count,
-                            const float* q, const float* k_new, const float* v_new, const int32_t* table,
-                            const int32_t* len, void* pool, float scale, int32_t window, int32_t sinks,
-                            float* y, float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
-                            pi_stream stream) {
+}  // extern "C"
+
+static pi_status tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots, int32_t heads,
+                                int32_t max_pages, int32_t drafts, const int32_t* parent, const int32_t* count,
+                                const float* q, const float* k_new, const float* v_new, const int32_t* table,
+                                const int32_t* len, void* pool, float scale, int32_t window, int32_t sinks,
+                                float* y, float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                pi_stream stream, unsigned long long lose_ns) {
   pi_status st = check_cache(cache);
   if (st != PI_OK) return st;
   const pi_cache_desc& C = *cache;
@@ -1660,7 +1676,6 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   if (drafts < 1 || drafts > PI_TREE_MAX || window < 0 || sinks < 0) return PI_ERR_SHAPE;
   if (!q || !table || !len || !pool || !y || !dev_status || !ws || !k_new != !v_new) return PI_ERR_NULL;
   if (!all_aligned(parent, count, q, k_new, v_new, table, len, pool, y, lse, dev_status, ws)) return PI_ERR_ALIGN;
-  const int lose = 0;
   if (ws_bytes < pi_tree_workspace_size(cache, slots, heads, drafts)) return PI_ERR_WORKSPACE;
   TreeArgs a{};
   a.q = q;
@@ -1691,8 +1706,8 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   w.span = static_cast<TreeSpan*>(ws);
   w.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTreeSpans);
   w.halves = C.head_dim > 128 ? 2 : 1;
-  w.limit_ns = wait_limit();
-  w.lose = lose;
+  w.limit_ns = lose_ns ? lose_ns : wait_limit();
+  w.lose = lose_ns != 0;
   const long long rows = (long long)C.pages * 2 * C.kv_heads * C.page_tokens;
   CUtensorMap map = {}, edge_map = {};
   w.box = C.page_tokens & -C.page_tokens;
@@ -1703,11 +1718,33 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
   w.tma = w.box >= 8 && C.head_dim >= 64 && rows < (1ll << 31) &&
           tree_map(&map, a.pool, rows, C.head_dim, w.box) &&
           tree_map(&edge_map, a.pool, rows, C.head_dim, w.edge);
+  if (lose_ns && !w.tma) return PI_ERR_SHAPE;
   DevInfo di;
   st = dev_info(&di);
   if (st != PI_OK) return st;
   const bool f16 = C.dtype == PI_F16;
   return f16 ? launch_rows<0>(w, map, edge_map, di, stream) : launch_rows<1>(w, map, edge_map, di, stream);
+}
+
+extern "C" {
+
+pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t slots, int32_t heads,
+                            int32_t max_pages, int32_t drafts, const int32_t* parent, const int32_t* count,
+                            const float* q, const float* k_new, const float* v_new, const int32_t* table,
+                            const int32_t* len, void* pool, float scale, int32_t window, int32_t sinks,
+                            float* y, float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
+                            pi_stream stream) {
+  return tree_attention(cache, layer, slots, heads, max_pages, drafts, parent, count, q, k_new, v_new, table, len,
+                        pool, scale, window, sinks, y, lse, dev_status, ws, ws_bytes, stream, 0);
+}
+
+pi_status pi_selftest_tree_timeout(const pi_cache_desc* cache, int32_t slots, int32_t heads, int32_t max_pages,
+                                   int32_t drafts, const float* q, const int32_t* table, const int32_t* len,
+                                   void* pool, float* y, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                   int64_t limit_ns, pi_stream stream) {
+  if (limit_ns < 1000 || limit_ns > 5000000000LL) return PI_ERR_SHAPE;
+  return tree_attention(cache, 0, slots, heads, max_pages, drafts, nullptr, nullptr, q, nullptr, nullptr, table, len,
+                        pool, 1.f, 0, 0, y, nullptr, dev_status, ws, ws_bytes, stream, (unsigned long long)limit_ns);
 }
 
 }  // extern "C"

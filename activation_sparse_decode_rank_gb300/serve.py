@@ -45,6 +45,8 @@ SIGNATURES = {
     "pi_tree_attention": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P,
                                          _P, _P, ctypes.c_float, _I32, _I32, _P, _P, _P, _P, _SZ,
                                          _P]),
+    "pi_selftest_tree_timeout": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P,
+                                                _P, _SZ, _I64, _P]),
     "pi_tree_accept": (ctypes.c_int, [_CACHE, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P, _P]),
     "pi_sample_workspace_size": (_SZ, [_I32, _I32]),
@@ -213,6 +215,14 @@ def pi_tree_attention(cache, layer, slots, heads, max_pages, drafts, parent, cou
         ctypes.byref(cache), layer, slots, heads, max_pages, drafts, _ptr(parent), _ptr(count),
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(table), _ptr(len), _ptr(pool), scale, window, sinks,
         _ptr(y), _ptr(lse), _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+
+
+def pi_selftest_tree_timeout(cache, slots, heads, max_pages, drafts, q, table, len, pool, y,
+                             dev_status, ws, limit_ns, ws_bytes=None, stream=None) -> int:
+    return _fn("pi_selftest_tree_timeout")(
+        ctypes.byref(cache), slots, heads, max_pages, drafts, _ptr(q), _ptr(table), _ptr(len),
+        _ptr(pool), _ptr(y), _ptr(dev_status), _ptr(ws), _ws_bytes(ws, ws_bytes), limit_ns,
+        _stream(stream))
 
 
 def pi_tree_accept(cache, slots, max_pages, drafts, parent, count, tokens, choice, table, len, pool,

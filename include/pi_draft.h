@@ -63,6 +63,19 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
                             int32_t sinks, float* y, float* lse, int32_t* dev_status, void* ws,
                             size_t ws_bytes, pi_stream stream);
 
+/* Diagnostic of that call's failure path: pi_tree_attention (scale 1, chains, no
+ * window, no new rows) on a cache with head_dim >= 64 and page_tokens a multiple
+ * of 8, except that the copy of a box of keys is never ordered, so the waits for it
+ * run out after limit_ns nanoseconds (1e3 .. 5e9).  The block lets its copies and
+ * products under way end (2 s at most) and leaves, and PI_ERR_TIMEOUT lands in
+ * *dev_status; y is not meaningful.  Slot 0 must have a token before its drafts.
+ * Returns PI_OK when the launch was issued. */
+pi_status pi_selftest_tree_timeout(const pi_cache_desc* cache, int32_t slots, int32_t heads,
+                                   int32_t max_pages, int32_t drafts, const float* q,
+                                   const int32_t* table, const int32_t* len, void* pool, float* y,
+                                   int32_t* dev_status, void* ws, size_t ws_bytes,
+                                   int64_t limit_ns, pi_stream stream);
+
 /* Keeps the drafts that the chosen tokens confirm.  tokens[s][i] is draft i's
  * token, choice[s][i] the token chosen to follow it (from its logits; negative:
  * none).  Draft 0 is the tree's root, itself chosen before: it is taken.  From a

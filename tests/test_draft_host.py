@@ -87,6 +87,16 @@ def test_attention_refusals():
     assert attention(cache(dtype="f32")) == pi.PI_ERR_DTYPE
 
 
+def test_tree_selftest_refusals():
+    def f(c, limit, wsb=None):
+        size = pi.pi_tree_workspace_size(c, 4, 8, 5) if wsb is None else wsb
+        return pi.pi_selftest_tree_timeout(c, 4, 8, 10, 5, P, P, P, P, P, P, P, limit, size, stream=0)
+    assert f(cache(), 10) == pi.PI_ERR_SHAPE and f(cache(), 6 * 10 ** 9) == pi.PI_ERR_SHAPE
+    assert f(cache(), 10 ** 6, 0) == pi.PI_ERR_WORKSPACE
+    for c in (cache(head_dim=56), cache(page_tokens=7)):
+        assert f(c, 10 ** 6) == pi.PI_ERR_SHAPE
+
+
 def accept(c=None, **kw):
     a = dict(slots=4, max_pages=10, drafts=5, parent=P, count=P, tokens=P + 64, choice=P + 128,
              table=P + 4096, len=P + 256, pool=P + 65536, len_out=P + 8192, path=P + 8256,
