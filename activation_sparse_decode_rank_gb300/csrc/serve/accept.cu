@@ -10,7 +10,8 @@ namespace pis {
 // Confirmed drafts move up behind one another: step j's row goes to place j
 // <= its own, so a thread that copies its piece of the rows in the path's order,
 // reading a batch before writing it, overwrites no row that is still needed.
-// Bound: the moved rows' bytes.
+// Bound: the moved rows' bytes (64 slots, 48 layers of 8 heads of 128, some 100 rows:
+// 13.3 us, 52 % of a copy's rate; one slot 6.3 us, all of it the call).
 struct AcceptArgs {
   const int *parent, *count, *tokens, *choice, *table, *len;
   uint16_t* pool;

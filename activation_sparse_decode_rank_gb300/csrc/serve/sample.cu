@@ -15,11 +15,18 @@
 // Order without sorting.  Running sums over the 2048 bins (64 octaves; what lies
 // below weighs nothing) say in which bin a border lies.  The bin's logits alone are
 // collected, ordered by (logit, index) and gone through.  Where ties make them more
-// than the list holds, the bin is divided again by the bits of that key.
+// than the list holds, the bin is divided again by the bits of that key.  Rows that
+// top-k or min-p leave few logits of need no sums: they are counted by bin, and the
+// list holds all that are kept (1024 x 128256 fp32, such rows three of five: 630 us,
+// with sums for all 780).
 //
 // A row is a thread-block cluster's.  Its logits stay in the cluster's shared
 // memory, so that memory is read once, and few rows still use many SMs.  Rows
 // that do not fit are read again from global memory.
+//
+// Bound: instructions, some 50 per logit for its weight and bin, on one block of 1024
+// threads per SM.  Measured: 832 x 50272 fp16 without filters 208 us (memory 12), 64 x
+// 128256 bf16 56 us, 1 x 50273 fp32 25 us: a chain of eleven phases of a cluster.
 #include <cooperative_groups.h>
 
 #include "serve.cuh"

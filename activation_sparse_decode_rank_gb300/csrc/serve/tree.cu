@@ -179,27 +179,50 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 
 // ------------------------------------------------------------------ tensor cores
 //
-// The query rows of a kv head, drafts x heads of its group, are the 128 rows of
-// the fifth-generation tensor cores' tile: S = Q K^T (M = 128 rows, N = tokens),
-// O += P V, both accumulated in tensor memory.
+// Mathematics.  A query row's visible tokens may be split into any parts; part i
+// yields m_i = max a_t, l_i = sum exp(a_t - m_i), o_i = sum exp(a_t - m_i) v_t, and
+// parts join with the weights exp(m_i - max m).
+//
+// The query rows of a kv head are drafts x heads of its group.  Both products run
+// on the fifth-generation tensor cores, operands in shared memory by TMA, sums in
+// tensor memory, in one of two forms.
+//   Many rows (MR = 128; 64 for head dimensions past 128): S = Q K^T has the rows as
+//   the 128 rows of the product's tile and the tokens as its columns; a thread has a
+//   row of S, so maxima and sums are its own, and the weights return to the place of
+//   the scores that they come from, from where the second product O = P V reads them.
+//   Few rows (MR = 16, 32): S^T = K Q^T has the tokens as rows and query rows x parts as
+//   columns, a thread a token; O^T = V^T P^T, P through shared memory.  A tile then
+//   costs 16 instructions of 32 to 96 columns instead of 32 to 48 of 128, and all threads
+//   work whatever the number of rows.
+// 32 slots x 40 heads of 128, 13 drafts (13 rows), lengths to 2048, fp16: 178 us, in the
+// form of many rows 380; 16 slots, 32/8 heads, 26 drafts (104 rows), to 8001, bf16: 102,
+// as four units of 32 rows 267.
 //
 // A unit is (slot, kv head, MR query rows, up to 128 columns of V).  It goes
 // through tiles of TN tokens: the drafts' own, then those of the cache.  The
-// units' tiles, each unit preceded by kUnitCost positions for its fixed cost,
-// form one line of which every block takes an equal contiguous share; a unit
-// that several blocks share is joined by a second kernel.
+// units' tiles, each unit preceded by tree_cost() positions for its fixed cost,
+// form one line of which every block (one per SM: shared memory) takes an equal
+// contiguous share; a unit that several blocks share is joined by a second kernel.
 //
 // Precision.  q and the weights p are fp32 and enter as sums of 16-bit parts (two
 // in fp16, with q scaled by a power of two per row and p by 2^14; three in bf16),
-// low parts first.  A tile's O is read back and added to fp32 registers with a
-// rounded add: the tensor cores' own sums would drift over a long cache.
+// low parts first or in columns of their own.  A tile's O is read back and added to
+// fp32 registers with a rounded add: the tensor cores' own sums would drift over a
+// long cache.
 //
-// Roles of a block's warps.  0-7: load Q, softmax, and add up O; a thread has
-// half a row, warps w and w + 4 the same rows, which share their maximum.  8:
-// issues the MMAs: S of the next tile, then O of the last, so that the products run
-// while the warps 0-7 are at the tile in between.  From 9 on: fill K, or V: whole boxes
-// of tokens by TMA, everything else (drafts, the ends of what is seen, odd page sizes)
-// by hand, with zeros for values nobody sees.
+// Roles of a block's warps.  0-7: load Q, softmax, and add up O: warps w and w + 4
+// share the rows (few rows: the tokens) and halve the columns.  8: issues the MMAs, S
+// of the next tile, then O of the last, so that the products run while the warps 0-7
+// are at the tile in between.  From 9 on: fill K, or V: whole boxes of tokens by TMA,
+// everything else (drafts, the ends of what is seen, odd page sizes) by hand, with zeros
+// for values nobody sees.  New drafts' rows never come from the cache: no block waits for
+// another's store.
+//
+// Bound.  Few rows: HBM, beside a unit's start and end (some 10000 cycles against 2800
+// a tile): 57 % of a copy's rate at 32 slots x 40 heads.  Many rows: the weights'
+// instructions, some 4200 cycles a tile of 128 rows x 128 tokens, against 2200 of the
+// products: 8 slots, 64/8 heads, chains of 64 (512 rows), lengths to 32768, fp16: 467 us,
+// 543 TFLOP/s of the formula's operations, 1.1 PFLOP/s as executed.
 //
 // Operands that are not finite.  Rows whose sums come out NaN or infinite are
 // gone through again in fp32, token by token, by the warp that would write them.
@@ -1326,19 +1349,19 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           for (int ks = 0; ks < TN / 16; ++ks)
             if (16 * ks < cols) mma_ss(d, vd + (2048 >> 4) * ks, pd + (2048 >> 4) * ks, idesc, ks > 0);
         } else {
-        const uint64_t vd = tree_desc(vs, kPanelK);
-        const uint32_t idesc = tree_idesc<DT>(nv, true);
-        bool add = false;
+          const uint64_t vd = tree_desc(vs, kPanelK);
+          const uint32_t idesc = tree_idesc<DT>(nv, true);
+          bool add = false;
 #pragma unroll
-        for (int part = NP - 1; part >= 0; --part) {
-          const uint32_t pa = part == 2 ? tmem + C::kThird + buf * (TN / 2) : tmem + buf * TN + part * 8;
+          for (int part = NP - 1; part >= 0; --part) {
+            const uint32_t pa = part == 2 ? tmem + C::kThird + buf * (TN / 2) : tmem + buf * TN + part * 8;
 #pragma unroll
-          for (int ks = 0; ks < TN / 16; ++ks)
-            if (16 * ks < cols) {
-              mma_ts(d, pa + (part == 2 ? 8 : 16) * ks, vd + (2048 >> 4) * ks, idesc, add);
-              add = true;
-            }
-        }
+            for (int ks = 0; ks < TN / 16; ++ks)
+              if (16 * ks < cols) {
+                mma_ts(d, pa + (part == 2 ? 8 : 16) * ks, vd + (2048 >> 4) * ks, idesc, add);
+                add = true;
+              }
+          }
         }
         mma_commit(&sh.vempty[st]);
         mma_commit(&sh.ofull[ob]);
@@ -1368,17 +1391,17 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
                 mma_ss(tmem + buf * NQ, kdesc + (((k >> 2) * kPanelK + (k & 3) * 32) >> 4),
                        qd + (((k >> 2) * kPanelQ + (k & 3) * 32) >> 4), idesc, k > 0);
           } else {
-          const uint32_t idesc = tree_idesc<DT>(cols, false);
-          bool add = false;
+            const uint32_t idesc = tree_idesc<DT>(cols, false);
+            bool add = false;
 #pragma unroll
-          for (int part = NP - 1; part >= 0; --part)
+            for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k)
-              if (k < kd) {
-                mma_ss(tmem + buf * TN, qd + ((part * C::kQ + (k >> 2) * kPanelQ + (k & 3) * 32) >> 4),
-                       kdesc + (((k >> 2) * kPanelK + (k & 3) * 32) >> 4), idesc, add);
-                add = true;
-              }
+              for (int k = 0; k < DP / 16; ++k)
+                if (k < kd) {
+                  mma_ss(tmem + buf * TN, qd + ((part * C::kQ + (k >> 2) * kPanelQ + (k & 3) * 32) >> 4),
+                         kdesc + (((k >> 2) * kPanelK + (k & 3) * 32) >> 4), idesc, add);
+                  add = true;
+                }
           }
           mma_commit(&sh.kempty[st]);
           mma_commit(&sh.sfull[buf]);
