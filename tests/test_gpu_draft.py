@@ -9,8 +9,8 @@ Tolerances, from the arithmetic the headers promise (u = 2^-24):
     relative (numerator and denominator), so |dy| <= 3 e max|v| and
     |dlse| <= 2 e + 4 u |lse|.
   * a drawn token is the plain form's where the draw and the ends of the kept part
-    are 2^-30 or more from where they would change (sums are exact to 2^-36 of each
-    weight, so the sums themselves to 2^-36, and the plain form's to n 2^-53); where they
+    are 2^-30 or more from where they would change (sums are exact to 2^-35 of each
+    weight, so the sums themselves to 2^-35, and the plain form's to n 2^-53); where they
     are nearer the row is drawn anew.  Its log probability is off by at most 4 u
     (1 + |logprob|): a rounding each of w / sum, the logarithm's argument and its result.
   * whole numbers and stored 16-bit values are equal.
