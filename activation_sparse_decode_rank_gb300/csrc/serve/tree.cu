@@ -138,10 +138,11 @@ __device__ __forceinline__ void row_add_cached(const TreeArgs& a, int slot, int 
                                                int lo, RowSums& r, int* beat) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int t = t0 + lane; t - lane < t1; t += 32) {
+  for (unsigned at = 0; (int)at >= 0 && (int)at < t1 - t0; at += 32) {
+    const int t = t0 + (int)min(at + lane, (unsigned)(t1 - t0 - 1));
     if (lane == 0) atomicAdd(beat, 1);
     const uint16_t* key = nullptr;
-    if (t < t1 && (t >= lo || t < a.sinks)) {
+    if (at + lane < (unsigned)(t1 - t0) && (t >= lo || t < a.sinks)) {
       const int j = t / a.page_tokens;
       const int page = checked_page(__ldg(a.table + (size_t)slot * a.max_pages + j), a.pages, a.status);
       if (page >= 0)
@@ -473,7 +474,9 @@ struct TreeUnit {
 };
 template <int TN>
 __device__ __forceinline__ int tree_tiles(const TreeWork& w, const TreeSlot& v) {
-  return 1 + (v.first + TN - 1) / TN + (v.base > v.tail ? (v.base - (v.tail & -w.align) + TN - 1) / TN : 0);
+  // lengths up to 2^31 - 1: nothing is added that could pass them
+  const int start = v.tail & -w.align;
+  return 1 + (v.first ? (v.first - 1) / TN + 1 : 0) + (v.base > v.tail ? (v.base - start - 1) / TN + 1 : 0);
 }
 __device__ __forceinline__ int tree_units(const TreeWork& w, const TreeSlot& v, int mr) {
   return v.count ? w.a.kv_heads * ((v.count * w.a.group + mr - 1) / mr) * w.halves : 0;
@@ -497,7 +500,7 @@ struct TreeWalk {
     u.v = tree_slot(w.a, u.slot);
     units = tree_units(w, u.v, MR);
     u.start = u.v.tail & -w.align;
-    u.firsts = (u.v.first + TN - 1) / TN;
+    u.firsts = u.v.first ? (u.v.first - 1) / TN + 1 : 0;
     u.tiles = tree_tiles<TN>(w, u.v);
     fit();
   }
@@ -550,7 +553,7 @@ struct TreeWalk {
     if (i == 0) return (u.v.count + 15) & ~15;
     int lo, hi;
     const int t0 = cached(i, lo, hi);
-    return min(TN, (hi - t0 + 15) & ~15);
+    return (min(TN, hi - t0) + 15) & ~15;
   }
 };
 
@@ -583,11 +586,11 @@ __device__ __forceinline__ RowSums tree_again(const TreeWork& w, const TreeUnit&
   const TreeRow x = tree_row(a, u, r, [&](int j) { return __ldg(a.parent + (size_t)u.slot * a.drafts + j); });
   RowSums s = {-INFINITY, 0.f, {}};
   const int f0 = max(tile0, 1) - 1, f1 = min(tile1 - 1, u.firsts);
-  if (f0 < f1) row_add_cached<DT>(a, u.slot, u.g, x.q, f0 * TN, min(u.v.first, f1 * TN), x.lo, s, beat);
+  if (f0 < f1) row_add_cached<DT>(a, u.slot, u.g, x.q, f0 * TN, f1 == u.firsts ? u.v.first : f1 * TN, x.lo, s, beat);
   const int w0 = max(tile0 - 1 - u.firsts, 0), w1 = tile1 - 1 - u.firsts;
   if (w0 < w1)
-    row_add_cached<DT>(a, u.slot, u.g, x.q, max(u.v.tail, u.start + w0 * TN), min(u.v.base, u.start + w1 * TN), x.lo, s,
-                       beat);
+    row_add_cached<DT>(a, u.slot, u.g, x.q, max(u.v.tail, u.start + w0 * TN),
+                       tile1 == u.tiles ? u.v.base : u.start + w1 * TN, x.lo, s, beat);
   if (tile0 == 0) row_add_drafts<DT>(a, u.slot, u.v, u.g, x.q, x.seen, s);
   return s;
 }
@@ -880,7 +883,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           int any_lo = 0, hi = 0, t0 = 0;
           if (i > 0) t0 = walk.cached(i, any_lo, hi);
           const int from = i <= u.firsts ? 0 : lo;
-          bool all = i > 0 && t0 >= from && t0 + TN <= hi;
+          bool all = i > 0 && t0 >= from && hi - t0 >= TN;
 #pragma unroll
           for (int k = 0; k < TN / 32; ++k) all &= !sh.hide[t % kTreeHide][k];
           all = __all_sync(~0u, all);
@@ -1186,6 +1189,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           int any_lo = 0, hi = 0, t0 = 0;
           if (i > 0) t0 = walk.cached(i, any_lo, hi);
           const int tok = t0 + place;
+          const bool past = place >= hi - t0;
           const bool gone = sh.hide[t % kTreeHide][wq] >> lane & 1u;
           // a window's tokens from base + 1 on below the deepest row's are not seen by all
           if (i == 0) {
@@ -1193,14 +1197,14 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
             for (int j = 0; j < RH; ++j)
               v[j] = place < 64 && (seens[j] >> (place & 63) & 1) && !gone ? v[j] : -INFINITY;
           } else if (i <= u.firsts || a.window == 0) {
-            if (__any_sync(~0u, tok >= hi || gone)) {
+            if (__any_sync(~0u, past || gone)) {
 #pragma unroll
-              for (int j = 0; j < RH; ++j) v[j] = tok < hi && !gone ? v[j] : -INFINITY;
+              for (int j = 0; j < RH; ++j) v[j] = !past && !gone ? v[j] : -INFINITY;
             }
-          } else if (__any_sync(~0u, tok >= hi || gone || tok < u.v.base - a.window + PI_TREE_MAX)) {
+          } else if (__any_sync(~0u, past || gone || tok - PI_TREE_MAX < u.v.base - a.window)) {
 #pragma unroll
             for (int j = 0; j < RH; ++j)
-              v[j] = tok < hi && !gone && (tok >= los[j] || tok < sinks) ? v[j] : -INFINITY;
+              v[j] = !past && !gone && (tok >= los[j] || tok < sinks) ? v[j] : -INFINITY;
           }
           float tops[4];
           float most[RH];
@@ -1446,12 +1450,12 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         if (i == 0 || i >= walk.tile1) return x;
         x.t0 = walk.cached(i, x.lo, x.hi);
         if (!w.tma) return x;
-        x.whole = x.t0 >= x.lo && x.t0 + TN <= x.hi;
+        x.whole = x.t0 >= x.lo && x.hi - x.t0 >= TN;
         x.box = x.whole ? w.box : w.edge;
-        const int b0 = x.t0 + lane * x.box;
-        x.some = lane * x.box < TN && b0 + x.box > x.lo && b0 < x.hi;
+        const int at = lane * x.box;
+        x.some = at < TN && at + x.box > x.lo - x.t0 && at < x.hi - x.t0;
         if (x.some) {
-          const int j = index_of(b0);
+          const int b0 = x.t0 + at, j = index_of(b0);
           x.page = __ldg(a.table + (size_t)u.slot * a.max_pages + j);
           x.row = b0 - j * P;
         }
@@ -1473,7 +1477,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         unsigned char* const to = smem + (value ? C::kValues + st * C::kV : C::kStages + st * C::kK);
         const Boxes now = ahead;
         const int t0 = now.t0, lo = now.lo, hi = now.hi;
-        const int cols = i == 0 ? (u.v.count + 15) & ~15 : min(TN, (hi - t0 + 15) & ~15);
+        const int cols = i == 0 ? (u.v.count + 15) & ~15 : (min(TN, hi - t0) + 15) & ~15;
         const bool boxes = now.box && __all_sync(~0u, !now.some || (unsigned)now.page < (unsigned)a.pages);
         const bool fresh = i == 0 && a.k_new;
         ahead = boxes_of(i + 1);
@@ -1487,7 +1491,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
 #pragma unroll 1
             for (int k = 0; k < TN / 32; ++k) {
               const int tok = t0 + 32 * k + lane;
-              const uint32_t h = __ballot_sync(~0u, tok >= lo && tok < hi && !row_of(tok));
+              const uint32_t h = __ballot_sync(~0u, tok >= lo && 32 * k + lane < hi - t0 && !row_of(tok));
               if (lane == 0) sh.hide[t % kTreeHide][k] = h;
             }
           }
@@ -1499,7 +1503,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           auto piece = [&](int r, int e) {
             const int tok = t0 + r;
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (tok < lo || tok >= hi || e >= d1) return x;
+            if (tok < lo || r >= hi - t0 || e >= d1) return x;
             if (!fresh) {
               const uint16_t* row = row_of(tok);
               return row ? *reinterpret_cast<const uint4*>(row + e) : x;
@@ -1512,8 +1516,8 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
           const bool keep = fresh && u.row0 == 0 && (value || u.half == 0);
 #pragma unroll 1
           for (int r0 = 0; r0 < cols;) {
-            const int rows = boxes ? now.box : cols, b0 = t0 + r0, n = rows * pieces;
-            if (!boxes || b0 < lo || b0 + rows > hi) {
+            const int rows = boxes ? now.box : cols, n = rows * pieces;
+            if (!boxes || r0 < lo - t0 || r0 + rows > hi - t0) {
 #pragma unroll 1
               for (int e0 = 32 * pw + lane; e0 < n; e0 += 128 * warps) {
                 uint4 x[4];
@@ -1529,7 +1533,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   *reinterpret_cast<uint4*>(to + (c[k] >> 3) * kPanelK + r[k] * 128 + (((c[k] & 7) ^ (r[k] & 7)) << 4)) = x[k];
-                  if (keep && t0 + r[k] < hi && 8 * c[k] < d1)
+                  if (keep && r[k] < hi - t0 && 8 * c[k] < d1)
                     if (const uint16_t* row = row_of(t0 + r[k]))
                       *reinterpret_cast<uint4*>(const_cast<uint16_t*>(row) + 8 * c[k]) = x[k];
                 }
@@ -1542,8 +1546,8 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         __syncwarp();
         // TMA: a box of K where anything of it is seen, of V where all of it is
         const int r = bb * now.box;  // of the tile
-        const bool mine = boxes && r < cols && (now.whole || (value ? t0 + r >= lo && t0 + r + now.box <= hi
-                                                                    : t0 + r + now.box > lo && t0 + r < hi));
+        const bool mine = boxes && r < cols && (now.whole || (value ? r >= lo - t0 && r + now.box <= hi - t0
+                                                                    : r + now.box > lo - t0 && r < hi - t0));
         const int n = __popc(__ballot_sync(~0u, mine));
         if (lane == 0) mbar_expect(full + st, (uint32_t)(n * now.box * 128));
         __syncwarp();

@@ -241,6 +241,32 @@ def test_offsets_past_31_bits():
     t.check(*t.run())
 
 
+@pytest.mark.parametrize("shape", [(8, 2, 128, 112), (32, 1, 64, 112), (4, 1, 256, 112), (8, 2, 32, 126),
+                                   (32, 1, 64, 126)])
+@pytest.mark.parametrize("append", [False, True])
+@pytest.mark.parametrize("short", [0, 5])
+@pytest.mark.parametrize("infinite", [False, True])
+def test_lengths_next_to_the_largest(shape, append, short, infinite):
+    """Tokens up to 2^31: the numbers of the last tile's columns pass 31 bits."""
+    P = shape[3]
+    most = (2 ** 31 - 1) // P
+    base = 10 * P - 16 - short
+    t = Tree("f16", *shape, [base], None, 16, window=300, sinks=37, append=append, seed=14)
+    if infinite:  # the rows once more in fp32
+        put(t, 1, 0, base - 3, 2, math.inf)
+    # the sinks' page stays, the window's pages go to the row's end; none in between is valid
+    tab = torch.full((1, most), -7, dtype=torch.int32, device=DEV)
+    tab[0, 0] = int(t.np_table[0, 0])
+    tab[0, most - 9:] = i32(t.np_table[0, 1:10])
+    t.mp = most
+    y, lse = t.run(table=tab, len=i32([most * P - short]))
+    if infinite:
+        compare(t, y, lse)
+        assert int(t.status[0]) == 0
+    else:
+        t.check(y, lse)
+
+
 @pytest.mark.parametrize("args", [("f16", 8, 2, 64, 16), ("bf16", 64, 2, 128, 16), ("f16", 2, 1, 256, 8)])
 def test_lost_copy_times_out(args):
     t = Tree(*args, [300, 40], None, 4, shape="chain", seed=13)
