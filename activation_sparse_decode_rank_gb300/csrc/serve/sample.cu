@@ -17,7 +17,7 @@
 // collected, ordered by (logit, index) and gone through.  Where ties make them more
 // than the list holds, the bin is divided again by the bits of that key.  Rows that
 // top-k or min-p leave few logits of need no sums: they are counted by bin, and the
-// list holds all that are kept (1024 x 128256 fp32, such rows three of five: 630 us,
+// list holds all that are kept (1024 x 128256 fp32, such rows three of five: 618 us,
 // with sums for all 780).
 //
 // A row is a thread-block cluster's.  Its logits stay in the cluster's shared
@@ -25,8 +25,8 @@
 // that do not fit are read again from global memory.
 //
 // Bound: instructions, some 50 per logit for its weight and bin, on one block of 1024
-// threads per SM.  Measured: 832 x 50272 fp16 without filters 208 us (memory 12), 64 x
-// 128256 bf16 56 us, 1 x 50273 fp32 25 us: a chain of eleven phases of a cluster.
+// threads per SM.  Measured: 832 x 50272 fp16 without filters 209 us (memory 12), 64 x
+// 128256 bf16 52 to 61 us, 1 x 50273 fp32 25 to 27 us: a chain of eleven phases of a cluster.
 #include <cooperative_groups.h>
 
 #include "serve.cuh"

@@ -195,8 +195,8 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 //   columns, a thread a token; O^T = V^T P^T, P through shared memory.  A tile then
 //   costs 16 instructions of 32 to 96 columns instead of 32 to 48 of 128, and all threads
 //   work whatever the number of rows.
-// 32 slots x 40 heads of 128, 13 drafts (13 rows), lengths to 2048, fp16: 178 us, in the
-// form of many rows 380; 16 slots, 32/8 heads, 26 drafts (104 rows), to 8001, bf16: 102,
+// 32 slots x 40 heads of 128, 13 drafts (13 rows), lengths to 2048, fp16: 186 us, in the
+// form of many rows 380; 16 slots, 32/8 heads, 26 drafts (104 rows), to 8001, bf16: 110,
 // as four units of 32 rows 267.
 //
 // A unit is (slot, kv head, MR query rows, up to 128 columns of V).  It goes
@@ -220,10 +220,10 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 // another's store.
 //
 // Bound.  Few rows: HBM, beside a unit's start and end (some 10000 cycles against 2800
-// a tile): 57 % of a copy's rate at 32 slots x 40 heads.  Many rows: the weights'
+// a tile): 54 % of a copy's rate at 32 slots x 40 heads.  Many rows: the weights'
 // instructions, some 4200 cycles a tile of 128 rows x 128 tokens, against 2200 of the
-// products: 8 slots, 64/8 heads, chains of 64 (512 rows), lengths to 32768, fp16: 467 us,
-// 543 TFLOP/s of the formula's operations, 1.1 PFLOP/s as executed.
+// products: 8 slots, 64/8 heads, chains of 64 (512 rows), lengths to 32768, fp16: 493 us,
+// 515 TFLOP/s of the formula's operations, 1.0 PFLOP/s as executed.
 //
 // Operands that are not finite.  Rows whose sums come out NaN or infinite are
 // gone through again in fp32, token by token, by the warp that would write them.
@@ -255,8 +255,8 @@ struct TreeTile {  // MR: query rows of a unit
 constexpr int kTreeWarps = 13;   // at most
 constexpr int kTreeGrid = 192;   // most blocks
 // A unit's fixed cost, in tiles: Q, its drafts' rows, its output.  With 1 instead, 32
-// slots x 40 heads, 13 drafts, take 238 us (174), 8 slots, 64/8 heads, chains of 64,
-// 1084 us (470): a slot with nothing before its drafts is all fixed cost.
+// slots x 40 heads, 13 drafts, took 238 us (178), 8 slots, 64/8 heads, chains of 64,
+// 1084 us (467): a slot with nothing before its drafts is all fixed cost.
 __host__ __device__ __forceinline__ int tree_cost(int mr, int drafts) { return 4 + (mr <= 32 ? drafts / 8 : drafts / 4); }
 constexpr int kTreeWhole = 6;    // units of at most this many tiles are not split
 constexpr int kTreeShare = 3;    // least share of a block
