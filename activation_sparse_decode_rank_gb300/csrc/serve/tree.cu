@@ -1567,7 +1567,8 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         mbar_wait((value ? sh.vfull : sh.kfull) + i, (uint32_t)((t - 1 - i) / stages & 1), 500000000ull);
     }
     if (warp == 8) {
-      if (lane == 0) mma_commit(&sh.fin);
+      if (elected()) mma_commit(&sh.fin);  // it covers the MMAs of the lane that issued them
+      __syncwarp();
       mbar_wait(&sh.fin, 0, 2000000000ull);
     }
     __syncthreads();

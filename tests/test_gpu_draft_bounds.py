@@ -1,0 +1,42 @@
+"""The operators of include/pi_draft.h at the ends of what their header allows:
+waits that run out, extreme temperatures and queries, sums that have to be exact,
+shared workspaces, more rows than a launch has blocks."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import activation_sparse_decode_rank_gb300 as pi
+from test_gpu_draft import DEV, Tree, new_status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    pi.build()
+
+
+# ------------------------------------------------------------------ waits that run out
+def lose_copy(t, limit_ns):
+    """The self-test on t's problem: (status, milliseconds)."""
+    y = torch.empty((t.S, t.drafts, t.heads, t.D), device=DEV)
+    status = new_status()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    pi.check(pi.pi_selftest_tree_timeout(t.desc, t.S, t.heads, t.mp, t.drafts, t.qd, t.table, t.len, t.pool, y,
+                                         status, t.ws, limit_ns), "pi_selftest_tree_timeout")
+    end.record()
+    torch.cuda.synchronize()
+    return int(status[0]), start.elapsed_time(end)
+
+
+@pytest.mark.parametrize("args,drafts", [(("f16", 8, 2, 128, 16), 4), (("bf16", 64, 2, 128, 16), 16),
+                                         (("f16", 64, 2, 64, 32), 40), (("bf16", 4, 1, 256, 8), 16)])
+def test_waits_run_out_at_once(args, drafts):
+    # a limit of a microsecond: the block leaves while copies and products are under way
+    t = Tree(*args, [300, 200], None, drafts, shape="chain", seed=21)
+    got, ms = lose_copy(t, 1000)
+    assert got == pi.PI_ERR_TIMEOUT and ms < 6000
+    t.check(*t.run())  # the next call is as ever
