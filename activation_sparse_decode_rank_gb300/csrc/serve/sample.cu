@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     return __umul64hi(sum << room, S.scale[b & (kBinsPerOctave - 1)]) >> (b / kBinsPerOctave);
   };
 
-  for (int row = blockIdx.x / C; row < a.rows; row += gridDim.x / C) {
+  // 64 bits: up to 2^31 - 1 rows, and a step of up to 2^20 past the last
+  for (long long row = blockIdx.x / C; row < a.rows; row += gridDim.x / C) {
     cluster.sync();  // the last row's results are read
     float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
     const float u = __ldg(a.u + row);

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import activation_sparse_decode_rank_gb300 as pi
-from test_gpu_draft import DEV, Tree, new_status
+from test_gpu_draft import DEV, Tree, new_status, run_sample
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,26 @@ def test_waits_run_out_at_once(args, drafts):
     got, ms = lose_copy(t, 1000)
     assert got == pi.PI_ERR_TIMEOUT and ms < 6000
     t.check(*t.run())  # the next call is as ever
+
+
+# ------------------------------------------------------------------ sampling
+def test_sample_more_rows_than_a_grid():
+    # past 2^20 rows a block takes several; each row has settings of its own
+    R, V = (1 << 20) + 777, 3
+    g = np.random.default_rng(22)
+    x = g.integers(-1, 2, (R, V)).astype(np.float32)
+    u = g.random(R).astype(np.float32)
+    T = g.choice(np.float32([0.0, 1.0]), R)
+    tok, lp, status = run_sample(x, "f32", T, None, None, None, u)
+    order = np.argsort(-x, axis=1, kind="stable")
+    w = np.exp(np.take_along_axis(x, order, 1).astype(np.float64))
+    w[T == 0, 1:] = 0.0
+    sums = np.cumsum(w, 1)
+    goal = u.astype(np.float64)[:, None] * sums[:, -1:]
+    at = (sums <= goal).sum(1)
+    clear = (np.abs(sums - goal) > 2.0 ** -30 * sums[:, -1:]).all(1)
+    assert status == 0 and clear.sum() > R - 10
+    want = np.take_along_axis(order, at[:, None], 1)[:, 0]
+    assert (tok == want)[clear].all()
+    wl = np.log(np.take_along_axis(w, at[:, None], 1)[:, 0] / sums[:, -1])
+    assert (np.abs(lp - wl) <= 4 * 2.0 ** -24 * (1 + np.abs(wl)))[clear].all()
