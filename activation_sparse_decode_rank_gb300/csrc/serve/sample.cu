@@ -29,6 +29,7 @@
 // 128256 bf16 52 to 61 us, 1 x 50273 fp32 25 to 27 us: a chain of eleven phases of a cluster.
 #include <cooperative_groups.h>
 
+#include "sample_weight.cuh"
 #include "serve.cuh"
 
 namespace pis {
@@ -48,11 +49,9 @@ struct SampleArgs {
 };
 
 constexpr int kSampleThreads = 1024;
-constexpr int kBins = 2048, kBinsPerThread = kBins / kSampleThreads;
-constexpr int kBinsPerOctave = 32;
+constexpr int kBinsPerThread = kBins / kSampleThreads;
 constexpr int kList = 1024;          // logits that are ordered at once
 constexpr uint32_t kBias = 1u << 20; // of q, which rounding may take below 0
-constexpr float kOne = 0x1p36f;      // of a weight's fixed-point part
 
 // A bin's logits: their number and the sum of q + kBias.
 struct Bins {
@@ -88,32 +87,6 @@ __device__ __forceinline__ float key_logit(u64 k) {
   const uint32_t b = (uint32_t)(k >> 32);
   return __uint_as_float(b & 0x80000000u ? b : ~b & 0x7fffffffu);
 }
-
-// Weights of one row.
-struct Weights {
-  float top, least;   // least logit that min-p keeps
-  float ch, cl;       // log2(e) / T
-  // bin of a logit; kBins where its weight counts for nothing
-  __device__ __forceinline__ int bin(float x) const {
-    const float t = __fmul_rn(top - x, ch);
-    return x >= least && t < (float)(kBins / kBinsPerOctave) ? (int)(t * kBinsPerOctave) : kBins;
-  }
-  // q of a logit of bin b, as a whole number: off by less than 1.1 for all t < 64 (largest
-  // of 20000 random logits, temperatures 0.3 to 5: 1.0)
-  __device__ __forceinline__ int q(float x, int b) const {
-    const float d = top - x, dx = d - top;
-    const float e = (top - (d - dx)) - (x + dx);  // d + e = top - x
-    const float th = __fmul_rn(d, ch);
-    const float rl = fmaf(d, ch, -th) + fmaf(d, cl, e * ch);
-    const float rh = fmaf((float)b, -1.f / kBinsPerOctave, th);
-    constexpr float L = 0.6931471805599453f, Ll = -1.9046542e-9f;  // ln 2 - L
-    const float zh = __fmul_rn(rh, L), zl = fmaf(rh, L, -zh) + fmaf(rh, Ll, rl * L);
-    const float sq = __fmul_rn(0.5f * zh, zh), sl = fmaf(0.5f * zh, zh, -sq) + zh * zl;  // z^2 / 2
-    const float more = fmaf(zh, fmaf(zh, 1.f / 60.f, -1.f / 12.f), 1.f / 3.f);
-    const float high = zh - sq, low = ((zh - high) - sq) + fmaf(zh * sq, more, fmaf(sq, zl, zl - sl));
-    return __float2int_rn(high * kOne) + __float2int_rn(low * kOne);
-  }
-};
 
 __device__ __forceinline__ void bin_add(Bins& h, int b, int q) {
   const uint32_t v = (uint32_t)q + kBias;
@@ -288,13 +261,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     if (tid == 0) S.least = min_p > 0.f ? __double2float_ru(top + (double)temp * log((double)min_p)) : -INFINITY;
     __syncthreads();
     Weights W;
-    W.top = top;
-    W.least = S.least;
-    {
-      constexpr float L = 1.4426950408889634f, Ll = 1.9259630e-8f;  // log2(e) - L
-      W.ch = L / temp;
-      W.cl = (fmaf(-W.ch, temp, L) + Ll) / temp;
-    }
+    W.set(top, temp, S.least);
 
     // ---- bins: sums of every block's
     auto bins_of = [&](bool sums, auto which) {  // which(x, i): bin, or kBins; q is that of x's own bin
