@@ -32,20 +32,26 @@ PI_WEIGHT_FN int nearest(float v) {
 #endif
 }
 
-// Weights of one row.
+// Weights of one row.  Logits, their maximum and T are multiplied by 2^-64 where T is
+// above 2^64: two finite logits may be more than the largest float apart, and the low
+// part of log2(e) / T would have no bits left (what falls below 2^-149 is nothing beside
+// such a T).  With T <= 2^64 a difference that overflows weighs less than 2^-64.
 struct Weights {
   float top, least;   // least logit that min-p keeps
+  float unit;         // 2^-64 or 1
   float ch, cl;       // log2(e) / T
   PI_WEIGHT_FN void set(float maximum, float temperature, float least_kept) {
     constexpr float L = 1.4426950408889634f, Ll = 1.9259630e-8f;  // log2(e) - L
-    top = maximum;
+    unit = temperature > 0x1p64f ? 0x1p-64f : 1.f;
+    top = maximum * unit;
+    temperature *= unit;
     least = least_kept;
     ch = L / temperature;
     cl = (fmaf(-ch, temperature, L) + Ll) / temperature;
   }
   // bin of a logit; kBins where its weight counts for nothing
   PI_WEIGHT_FN int bin(float x) const {
-    const float t = product(top - x, ch);
+    const float t = product(fmaf(-unit, x, top), ch);
     return x >= least && t < (float)(kBins / kBinsPerOctave) ? (int)(t * kBinsPerOctave) : kBins;
   }
   // q of a logit of bin b, as a whole number.  With z = zh + zl, 1 - e^-z = zh - zh^2/2 +
@@ -54,8 +60,8 @@ struct Weights {
   // Off by less than 1.25 for all t < 64: 1 for the two roundings, the rest fp32's (0.1;
   // the largest of 6e7 random logits, 1.04).
   PI_WEIGHT_FN int q(float x, int b) const {
-    const float d = top - x, dx = d - top;
-    const float e = (top - (d - dx)) - (x + dx);  // d + e = top - x
+    const float d = fmaf(-unit, x, top), dx = d - top;
+    const float e = (top - (d - dx)) - fmaf(unit, x, dx);  // d + e = top - unit x
     const float th = product(d, ch);
     const float rl = fmaf(d, ch, -th) + fmaf(d, cl, product(e, ch));
     const float rh = fmaf((float)b, -1.f / kBinsPerOctave, th);

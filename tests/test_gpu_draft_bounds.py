@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import activation_sparse_decode_rank_gb300 as pi
-from test_gpu_draft import DEV, Tree, new_status, run_sample
+import drafthelp as plain
+from test_gpu_draft import DEV, U, Tree, new_status, rounded, run_sample
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,36 @@ def test_sample_more_rows_than_a_grid():
     assert (tok == want)[clear].all()
     wl = np.log(np.take_along_axis(w, at[:, None], 1)[:, 0] / sums[:, -1])
     assert (np.abs(lp - wl) <= 4 * 2.0 ** -24 * (1 + np.abs(wl)))[clear].all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sample_large_temperatures(dtype):
+    # finite logits further apart than the largest float, temperatures as large
+    g = np.random.default_rng(23)
+    R, V = 48, 64
+    x = np.zeros((R, V), np.float32)
+    T = np.zeros(R, np.float32)
+    for r in range(R):
+        x[r] = g.uniform(-3.3e38, 3.3e38, V)
+        x[r, :2] = 3e38, -3e38
+        T[r] = g.choice([2.0 ** 60, 2.0 ** 64, 2.0 ** 65, 1e30, 1e36, 1e37, 1e38, 3e38, 3.4028235e38])
+        if T[r] < 1e36:
+            x[r] = x[r] / np.float32(3e38) * T[r] * 5
+    x[0], x[1], x[2] = -1e38, -1e38, -1e38
+    x[:3, 7], x[:3, 9] = 3e38, -3e38
+    T[:3] = 1e38, 3e38, 3e38
+    k = g.choice([0, 0, 5, 40], R)
+    p = g.choice(np.float32([1.0, 1.0, 0.8]), R)
+    m = g.choice(np.float32([0.0, 0.0, 0.1, 0.2]), R)
+    u = g.random(R).astype(np.float32)
+    u[:3], k[:3], p[:3], m[:3] = 0.99999, 0, 1.0, [0.0, 0.1, 0.2]
+    tok, lp, status = run_sample(x, dtype, T, k, p, m, u)
+    xr = rounded(x, dtype)
+    checked = 0
+    for r in range(R):
+        want = plain.sample_row(xr[r], float(T[r]), int(k[r]), float(p[r]), float(m[r]), float(u[r]))
+        if want[2] >= 2.0 ** -30:
+            checked += 1
+            assert tok[r] == want[0], (r, T[r])
+            assert abs(lp[r] - want[1]) <= 4 * U * (1 + abs(want[1]))
+    assert status == 0 and checked >= 40

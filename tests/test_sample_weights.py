@@ -92,6 +92,23 @@ def test_weights_with_a_long_low_part(host, top, x, T):
     assert abs(host.error(top, x, T)) < 1.25
 
 
+@pytest.mark.parametrize("T0,T1", [(60, 68), (68, 121), (110, 121)])
+def test_weight_error_at_large_temperatures(host, T0, T1):
+    # log2(e) / T keeps its two parts; 44 T, the largest difference that counts, stays finite
+    at = (ctypes.c_double * 3)()
+    e = host.worst(8, 400000, 32, T0, T1, 0, at)
+    assert 0 < e < 1.25, (e, list(at))
+
+
+def test_differences_past_the_largest_float(host):
+    q = ctypes.c_int()
+    for T, t in ((1e38, 8.6561702), (3e38, 2.8853901), (3.4e38, 2.5459324)):
+        assert host.one(3e38, -3e38, T, ctypes.byref(q)) == int(32 * t)
+        assert abs(host.error(3e38, -3e38, T)) < 1.25
+    assert host.one(3e38, -3e38, 2.0 ** 64, ctypes.byref(q)) == 2048  # weighs nothing
+    assert host.one(3e38, -3e38, 1e19, ctypes.byref(q)) == 2048
+
+
 def test_largest_weight(host):
     q = ctypes.c_int()
     for top in (0.0, -3.5, 1e30, -1e-30):
