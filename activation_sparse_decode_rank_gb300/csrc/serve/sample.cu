@@ -10,23 +10,24 @@
 // r in [0, 1/32), and 2^-r = 1 - q with q < 0.0215 is a 36-bit fixed-point number:
 // z = r ln 2 and z^2 / 2 of the series of 1 - e^-z as sums of two fp32 numbers, the
 // rest (2^-19) in one.  A bin's weight is 2^(-b/32) (count - sum q): whole-number
-// sums, the same in any order, and one 64-bit product per bin, not per logit.
+// sums, the same in any order, and one product of 64 bits per bin, not per logit.  The
+// sums over bins have 128 bits, with 2^-99 of the largest weight as their unit: cut to
+// 64 bits, a vocabulary of 2^24 would leave weights below 2^-37 nothing.
 //
 // Order without sorting.  Running sums over the 2048 bins (64 octaves; what lies
 // below weighs nothing) say in which bin a border lies.  The bin's logits alone are
 // collected, ordered by (logit, index) and gone through.  Where ties make them more
 // than the list holds, the bin is divided again by the bits of that key.  Rows that
 // top-k or min-p leave few logits of need no sums: they are counted by bin, and the
-// list holds all that are kept (1024 x 128256 fp32, such rows three of five: 618 us,
-// with sums for all 780).
+// list holds all that are kept (1024 x 128256 fp32, such rows three of five: 575 us).
 //
 // A row is a thread-block cluster's.  Its logits stay in the cluster's shared
 // memory, so that memory is read once, and few rows still use many SMs.  Rows
 // that do not fit are read again from global memory.
 //
 // Bound: instructions, some 50 per logit for its weight and bin, on one block of 1024
-// threads per SM.  Measured: 832 x 50272 fp16 without filters 209 us (memory 12), 64 x
-// 128256 bf16 52 to 61 us, 1 x 50273 fp32 25 to 27 us: a chain of eleven phases of a cluster.
+// threads per SM.  Measured: 832 x 50272 fp16 without filters 202 us (memory 12), 64 x
+// 128256 bf16 48 to 60 us, 1 x 50273 fp32 23 to 24 us: a chain of eleven phases of a cluster.
 #include <cooperative_groups.h>
 
 #include "sample_weight.cuh"
@@ -53,6 +54,8 @@ constexpr int kBinsPerThread = kBins / kSampleThreads;
 constexpr int kList = 1024;          // logits that are ordered at once
 constexpr uint32_t kBias = 1u << 20; // of q, which rounding may take below 0
 
+typedef unsigned __int128 u128;
+
 // A bin's logits: their number and the sum of q + kBias.
 struct Bins {
   uint32_t count[kBins], low[kBins], high[kBins];
@@ -60,7 +63,7 @@ struct Bins {
 struct SampleShared {
   Bins local, total;
   u64 list[kList], spare[kList];
-  u64 scan[kSampleThreads / 32];
+  u128 scan[kSampleThreads / 32];
   u64 scale[kBinsPerOctave];  // 2^(63 - i/32)
   float warp_top[kSampleThreads / 32];
   float top, least;  // this block's maximum; the row's least logit that min-p keeps
@@ -68,8 +71,8 @@ struct SampleShared {
   int list_n;
   // where a border was found: its bin, the sums before it, what is in it
   int at_bin;
-  u64 before_n, before_w, before_q, inside_n;
-  u64 at_key, at_upto;  // its logit, the sum up to it
+  u128 before_w, at_upto;  // at_upto: the sum up to its logit
+  u64 before_n, before_q, inside_n, at_key;
 };
 
 template <int DT>
@@ -97,6 +100,24 @@ __device__ __forceinline__ void bin_add(Bins& h, int b, int q) {
 __device__ __forceinline__ u64 bin_sum(const Bins& h, int b) {
   const u64 n = h.count[b], q = ((u64)h.high[b] << 32) + h.low[b];
   return n * ((u64)kOne + kBias) - q;
+}
+
+__device__ __forceinline__ u64 shfl_from(u64 v, int l) { return __shfl_sync(~0u, v, l); }
+__device__ __forceinline__ u128 shfl_from(u128 v, int l) {
+  return (u128)__shfl_sync(~0u, (u64)(v >> 64), l) << 64 | __shfl_sync(~0u, (u64)v, l);
+}
+__device__ __forceinline__ double as_double(u128 v) { return (double)(u64)(v >> 64) * 0x1p64 + (double)(u64)v; }
+
+// floor(f sum), or (up) the least whole number not below f sum, 1 at least, for 0 <= f < 1
+// and sums below 2^124: exact, by f's 24 bits.  Below 2^-40 f counts as 0: the largest
+// logit alone weighs more than that of any row.
+__device__ __forceinline__ u128 part_of(float f, u128 sum, bool up) {
+  const uint32_t bits = __float_as_uint(f), s = 150 - (bits >> 23);  // f = m 2^-s
+  if (s > 63) return up;
+  const uint32_t m = (bits & 0x7fffffu) | 0x800000u;
+  const u128 low = (u128)m * (u64)sum, high = (u128)m * (u64)(sum >> 64) + (u64)(low >> 64);
+  const u64 rest = (u64)low & ((1ull << s) - 1);
+  return (high << (64 - s)) + ((u64)low >> s) + (up && rest ? 1 : 0);
 }
 
 // Sorts list[0, n), n <= kList, ascending, a key per thread: few by counting the
@@ -157,11 +178,10 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_enter();
   if (tid < kBinsPerOctave) S.scale[tid] = (u64)(exp2(-(double)tid / kBinsPerOctave) * 0x1p63);
-  // A sum of whole-number weights of bin b, at most vocab 2^36, in units that
-  // the sum of a row has room for.
-  const int room = 63 - 36 - (32 - __clz(a.vocab));
+  // A sum of whole-number weights of bin b, at most 2^24 2^36, in units of 2^-99 of the
+  // largest weight: bins of 64 octaves keep the bits that their logits have.
   auto weight = [&](u64 sum, int b) {
-    return __umul64hi(sum << room, S.scale[b & (kBinsPerOctave - 1)]) >> (b / kBinsPerOctave);
+    return (u128)sum * S.scale[b & (kBinsPerOctave - 1)] >> (b / kBinsPerOctave);
   };
 
   // 64 bits: up to 2^31 - 1 rows, and a step of up to 2^20 past the last
@@ -301,29 +321,35 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       __syncthreads();
     };
     // Exclusive sums over the threads; returns the sum of all.
-    auto scan_n = [&](u64 v, u64& before) {
-      u64 upto = v;
+    auto scan_n = [&](auto v, auto& before) {
+      static_assert(T / 32 == 32, "a lane per warp");
+      auto in_warp = [&](auto x) {  // inclusive
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 w = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += w;
-      }
+        for (int o = 1; o < 32; o <<= 1) {
+          const auto w = shfl_from(x, lane - o);
+          if (lane >= o) x += w;
+        }
+        return x;
+      };
+      const auto upto = in_warp(v);
       if (lane == 31) S.scan[warp] = upto;
       __syncthreads();
-      u64 all = 0, low = 0;
-      for (int w = 0; w < T / 32; ++w) {
-        low = w == warp ? all : low;
-        all += S.scan[w];
-      }
+      const auto warps = in_warp((decltype(v))S.scan[lane]);
       __syncthreads();
-      before = low + upto - v;
-      return all;
+      before = upto - v + (warp ? shfl_from(warps, warp - 1) : 0);
+      return shfl_from(warps, 31);
     };
-    auto weight_of = [&](u64 key) {  // of one logit, not rounded to the sums' units
+    auto weight_of = [&](u64 key) {  // of one logit
       const float x = key_logit(key);
       const int b = W.bin(x);
-      return (double)((u64)kOne - (long long)W.q(x, b)) * (double)S.scale[b & (kBinsPerOctave - 1)] *
-             (double)exp2f((float)(room - 64 - b / kBinsPerOctave));
+      return weight((u64)kOne - (long long)W.q(x, b), b);
+    };
+    auto finish = [&](u64 key, u128 sum) {
+      a.token[row] = (int)(uint32_t)key;
+      if (a.logprob) {
+        const double p = as_double(weight_of(key)) / as_double(sum);
+        a.logprob[row] = p > 0.5 ? log1pf((float)(p - 1.0)) : logf((float)p);
+      }
     };
     // ---- few logits are kept before top-p: those alone, in one list
     if ((top_k > 0 && top_k <= kList) || min_p > 0.f) {
@@ -354,20 +380,15 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
         if (rank == 0) {
           sort_list(S.list, S.spare, (int)S.inside_n);
           constexpr int each_n = kList / T;
-          u64 v[each_n], mine = 0, v0;
+          u128 v[each_n], mine = 0, v0;
           for (int k = 0; k < each_n; ++k) {
             const int i = tid * each_n + k;
-            v[k] = 0;
-            if (i < (int)want) {
-              const float x = key_logit(S.list[i]);
-              const int b = W.bin(x);
-              v[k] = weight((u64)kOne - (long long)W.q(x, b), b);
-            }
+            v[k] = i < (int)want ? weight_of(S.list[i]) : 0;
             mine += v[k];
           }
-          u64 sum = scan_n(mine, v0);
-          const u64 ahead = v0;
-          auto find = [&](u64 target) {  // the place where the running sum reaches it: S.at_key, ...
+          u128 sum = scan_n(mine, v0);
+          const u128 ahead = v0;
+          auto find = [&](u128 target) {  // the place where the running sum reaches it: S.at_key, ...
             v0 = ahead;
             for (int k = 0; k < each_n; ++k) {
               if (v0 < target && v0 + v[k] >= target) {
@@ -379,18 +400,12 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
             __syncthreads();
           };
           if (top_p < 1.f) {
-            find(max(1ull, (u64)ceil((double)top_p * (double)sum)));
+            find(part_of(top_p, sum, true));
             sum = S.at_upto;
             __syncthreads();
           }
-          find((u64)((double)u * (double)sum) + 1);
-          if (tid == 0) {
-            a.token[row] = (int)(uint32_t)S.at_key;
-            if (a.logprob) {
-              const double p = weight_of(S.at_key) / (double)sum;
-              a.logprob[row] = p > 0.5 ? log1pf((float)(p - 1.0)) : logf((float)p);
-            }
-          }
+          find(part_of(u, sum, false) + 1);
+          if (tid == 0) finish(S.at_key, sum);
         }
         continue;
       }
@@ -399,9 +414,12 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     bins_of(true, [&](float, int, int own) { return own; });
 
     // The bins' running sums: those before the thread's bins, and of all.
-    u64 bins_n, bins_w, all_n, all_w;
-    auto thread_sums = [&](auto f, u64& before_n, u64& before_w) {
-      u64 n = 0, w = 0;
+    u64 bins_n, row_n;
+    u128 bins_w, row_w;
+    auto thread_sums = [&](auto f, u64& before_n, u64& all_n, auto& before_w, auto& all_w) {
+      u64 n = 0;
+      auto w = all_w;
+      w = 0;
       for (int k = 0; k < kBinsPerThread; ++k) {
         const int b = tid * kBinsPerThread + k;
         if (!S.total.count[b]) continue;
@@ -411,23 +429,24 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       all_n = scan_n(n, before_n);
       all_w = scan_n(w, before_w);
     };
-    thread_sums([&](int b) { return weight(bin_sum(S.total, b), b); }, bins_n, bins_w);
-    const u64 row_n = all_n, row_w = all_w;
+    row_w = 0;
+    thread_sums([&](int b) { return weight(bin_sum(S.total, b), b); }, bins_n, row_n, bins_w, row_w);
     bool whole = true;  // S.total holds the bins of all logits
     // Finds the logit at which the running count (COUNT) or sum reaches
     // `target`, 1 .. that of the row: S.at_key and S.at_upto.
-    auto locate = [&](bool count, u64 target) {
+    auto locate = [&](bool count, u128 target) {
       if (!whole) {
         bins_of(true, [&](float, int, int own) { return own; });
         whole = true;
       }
       {
-        u64 n = bins_n, w = bins_w;
+        u64 n = bins_n;
+        u128 w = bins_w;
         for (int k = 0; k < kBinsPerThread && (count ? n : w) < target; ++k) {
           const int b = tid * kBinsPerThread + k;
           const u64 c = S.total.count[b];
           if (!c) continue;
-          const u64 next = w + weight(bin_sum(S.total, b), b);
+          const u128 next = w + weight(bin_sum(S.total, b), b);
           if ((count ? n + c : next) >= target) {
             S.at_bin = b;
             S.before_n = n;
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       }
       __syncthreads();
       const int bin = S.at_bin;
-      const u64 before_w = S.before_w;
+      const u128 before_w = S.before_w;
       u64 before_n = S.before_n, before_q = 0, inside = S.inside_n;
       __syncthreads();
       // keys [lo, lo + size), divided until few logits are left
@@ -452,8 +471,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
           const u64 k = order_key(x, i) - lo;
           return own == bin && k < size ? (int)(k >> sh) : kBins;
         });
-        u64 n, q;
-        thread_sums([&](int b) { return bin_sum(S.total, b); }, n, q);
+        u64 n, q, all_n, all_q = 0;
+        thread_sums([&](int b) { return bin_sum(S.total, b); }, n, all_n, q, all_q);
         n += before_n;
         q += before_q;
         for (int k = 0; k < kBinsPerThread && (count ? n : before_w + weight(q, bin)) < target; ++k) {
@@ -505,8 +524,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < each_n; ++k) {
           const int i = tid * each_n + k;
-          const u64 was = count ? before_n + i : before_w + weight(q0, bin);
-          const u64 is = count ? before_n + i + 1 : before_w + weight(q0 + q[k], bin);
+          const u128 was = count ? before_n + i : before_w + weight(q0, bin);
+          const u128 is = count ? before_n + i + 1 : before_w + weight(q0 + q[k], bin);
           if (i < n && was < target && is >= target) {
             S.at_key = S.list[i];
             S.at_upto = before_w + weight(q0 + q[k], bin);
@@ -526,23 +545,17 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
       cluster.sync();
     };
 
-    u64 sum = row_w;
+    u128 sum = row_w;
     if (top_k > 0 && (u64)top_k < row_n) {
       locate(true, top_k);
       sum = S.at_upto;
     }
     if (top_p < 1.f) {
-      locate(false, max(1ull, (u64)ceil((double)top_p * (double)sum)));
+      locate(false, part_of(top_p, sum, true));
       sum = S.at_upto;
     }
-    locate(false, (u64)((double)u * (double)sum) + 1);
-    if (rank == 0 && tid == 0) {
-      a.token[row] = (int)(uint32_t)S.at_key;
-      if (a.logprob) {
-        const double p = weight_of(S.at_key) / (double)sum;
-        a.logprob[row] = p > 0.5 ? log1pf((float)(p - 1.0)) : logf((float)p);
-      }
-    }
+    locate(false, part_of(u, sum, false) + 1);
+    if (rank == 0 && tid == 0) finish(S.at_key, sum);
   }
   cluster.sync();  // no block leaves while another reads its memory
 }

@@ -115,8 +115,9 @@ size_t pi_sample_workspace_size(int32_t rows, int32_t vocab);
  *        those kept;  logprob[r] = log(w / that sum).
  * temperature 0 takes the largest (logprob 0).  temperature [rows] fp32 or NULL
  * (1), top_k [rows] int32 or NULL, top_p and min_p [rows] fp32 or NULL (off), u
- * [rows] fp32; logprob may be NULL.  Sums are exact to 2^-35 of each weight, so
- * that a token is decided as in 64 bits.  A row whose logits are all -infinity,
+ * [rows] fp32; logprob may be NULL.  Sums are exact to 2^-35 of each weight, whatever
+ * the vocabulary: the token is that of exact sums where the draw and the end of what
+ * top-p keeps are further than 2^-34 of the sum from the next one's border.  A row whose logits are all -infinity,
  * or hold a NaN or +infinity, gives token -1 and logprob NaN; so does one whose
  * temperature is negative, infinite or NaN, whose u is outside [0, 1), or whose
  * top_p or min_p is NaN or negative or min_p above 1; all write PI_ERR_RANGE to

@@ -97,3 +97,60 @@ def test_sample_large_temperatures(dtype):
             assert tok[r] == want[0], (r, T[r])
             assert abs(lp[r] - want[1]) <= 4 * U * (1 + abs(want[1]))
     assert status == 0 and checked >= 40
+
+
+def half_row(g, V):
+    """Weights whose sum is 2 (1 + e), 2^-33.6 < e < 2^-32.9: the first logit weighs 1, the
+    second about 0.95, one logit in every 32nd of an octave from 2^-10 down to 2^-62 the
+    rest; what is not listed is -infinity.  A draw (or an end of top-p) of 0.5 lies e
+    behind the first logit's end, so it takes the second, while sums that are 2^-32 short
+    take the first."""
+    while True:
+        t = (10 + (np.arange(52 * 32) + g.random(52 * 32)) / 32) * -math.log(2.0)
+        x = np.concatenate([[0.0, 0.0], t]).astype(np.float32)
+        tail = np.exp(x[2:].astype(np.float64)).sum()
+        x[1] = np.float32(math.log(1 - tail))
+        e = (math.exp(float(x[1])) + tail - 1) / 2
+        if 2.0 ** -33.6 < e < 2.0 ** -32.9:
+            break
+    where = g.permutation(V)[:len(x)]
+    row = np.full(V, -np.inf, np.float32)
+    row[where] = x
+    return row, x, where
+
+
+@pytest.mark.parametrize("V", [2500, 128256, 2000003, (1 << 24) - 3])
+def test_sample_small_weights_count(V):
+    # exact sums whatever the vocabulary: a border within 2^-33 of the draw, the tail's
+    # weights down to 2^-62 of the largest
+    g = np.random.default_rng(V)
+    for top_p, u in ((1.0, 0.5), (0.5, 0.999)):
+        row, x, where = half_row(g, V)
+        want = plain.sample_row(x, 1.0, 0, top_p, 0.0, u)
+        assert want[0] == 1 and want[2] > 2.0 ** -35
+        tok, lp, status = run_sample(row[None], "f32", None, None, [top_p], None, [u])
+        assert status == 0 and tok[0] == where[1]
+        assert abs(lp[0] - want[1]) <= 4 * U * (1 + abs(want[1]))
+
+
+@pytest.mark.parametrize("V", [2500, (1 << 24) - 3])
+def test_sample_small_weights_count_in_a_list(V):
+    # few logits kept: a list, whose weights are as exact; top-k keeps 1000 of 2^-10 and less
+    g = np.random.default_rng(V + 1)
+    while True:
+        x = np.concatenate([[0.0, 0.0], -math.log(2.0) * (10 + np.arange(998) / 32 + g.random(998) / 32)])
+        x = x.astype(np.float32)
+        tail = np.exp(x[2:].astype(np.float64)).sum()
+        x[1] = np.float32(math.log(1 - tail))
+        e = (math.exp(float(x[1])) + tail - 1) / 2
+        if 2.0 ** -33.6 < e < 2.0 ** -32.9:
+            break
+    row = np.full(V, -100.0, np.float32)  # not kept
+    where = g.permutation(V)[:1000]
+    row[where] = x
+    for top_p, u in ((1.0, 0.5), (0.5, 0.999)):
+        want = plain.sample_row(x, 1.0, 0, top_p, 0.0, u)
+        assert want[0] == 1 and want[2] > 2.0 ** -35
+        tok, lp, status = run_sample(row[None], "f32", None, [1000], [top_p], None, [u])
+        assert status == 0 and tok[0] == where[1]
+        assert abs(lp[0] - want[1]) <= 4 * U * (1 + abs(want[1]))
