@@ -326,7 +326,7 @@ struct TreeWork {
   int align;       // tokens that a window's first tile begins at a multiple of
   int page_shift;  // log2(page_tokens), or -1
   unsigned long long limit_ns;
-  int lose;        // self-test: block 0's first box is never ordered
+  int lose;        // self-test: a box is never ordered
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
@@ -1551,7 +1551,9 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
         const int n = __popc(__ballot_sync(~0u, mine));
         if (lane == 0) mbar_expect(full + st, (uint32_t)(n * now.box * 128));
         __syncwarp();
-        if (mine && !(w.lose && blockIdx.x == 0 && t == 1 && !value && be == 0))
+        // the self-test's box: the first of the keys before slot 0's drafts, of its first unit
+        const bool lost = w.lose && !value && be == 0 && i == 1 && u.slot == 0 && u.unit == 0;
+        if (mine && !lost)
           tree_box(smem_u32(to + bp * kPanelK + r * 128), now.whole ? &map : &edge_map, d0 + 64 * bp, box_row, full + st);
       }
     }

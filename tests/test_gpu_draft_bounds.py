@@ -43,6 +43,18 @@ def test_waits_run_out_at_once(args, drafts):
     t.check(*t.run())  # the next call is as ever
 
 
+@pytest.mark.parametrize("args,lens,drafts", [
+    (("f16", 1, 1, 64, 16), [2047], 1),                 # a block's share may be a fixed cost alone
+    (("bf16", 8, 2, 128, 16), [5000, 7], 4),
+    (("f16", 64, 2, 128, 64), [4000, 0, 900], 32),
+    (("bf16", 4, 1, 256, 8), [3000, 1], 16)])
+def test_lost_copy_of_a_shared_unit(args, lens, drafts):
+    t = Tree(*args, lens, None, drafts, shape="chain", seed=24)
+    got, ms = lose_copy(t, 2_000_000)
+    assert got == pi.PI_ERR_TIMEOUT and ms < 6000
+    t.check(*t.run())  # the next call is as ever
+
+
 # ------------------------------------------------------------------ sampling
 def test_sample_more_rows_than_a_grid():
     # past 2^20 rows a block takes several; each row has settings of its own
