@@ -577,6 +577,7 @@ size_t pi_logprob_workspace_size(int32_t rows, int32_t vocab, int32_t topk) {
   if (rows < 0 || vocab < 1 || vocab > (1 << 24) || topk < 0 || topk > PI_TOPK_MAX || topk > vocab)
     return 0;
   // arrivals, zero between calls; parts' sums and lists
+  static_assert(kScoreParts * 4 == kCounters, "one workspace may serve several calls");
   return (size_t)kScoreParts * (4 + 16 + 32 * 8);
 }
 

@@ -137,9 +137,12 @@ inline unsigned long long wait_limit() {
 
 constexpr int kAttendGrid = 1024;  // most thread blocks of the attention
 
-// Byte offsets of the regions of a cache workspace.  `arrived` is zero
-// between calls and has one place and size for every cache, so that a
-// workspace may serve calls of several shapes; the rest is scratch.
+// The first bytes of the serving calls' workspaces: counters that are zero between
+// calls.  The rest is scratch, so that one workspace may serve all of them.
+constexpr size_t kCounters = 8 * kAttendGrid;
+
+// Byte offsets of the regions of a cache workspace.  `arrived` has one place
+// and size for every cache.
 struct CacheWs {
   size_t arrived, part, blocks, owner, rank, first, before, src, sums, total;
 };
@@ -155,7 +158,7 @@ inline CacheWs cache_ws(const pi_cache_desc& C, int slots, int heads) {
     return o;
   };
   (void)slots;
-  w.arrived = take(8 * kAttendGrid);
+  w.arrived = take(kCounters);
   const size_t scratch = off;
   w.part = take(heads ? (size_t)kAttendGrid * 2 * 8 * (C.head_dim + 4) * 4 : 0);
   const size_t end = off;

@@ -1674,7 +1674,9 @@ static bool tree_map(CUtensorMap* m, void* base, long long rows, int head_dim, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kTreeSpans = (kTreeGrid * sizeof(TreeSpan) + kAlign - 1) / kAlign * kAlign;
+// The spans' place in a workspace, and the parts' behind them.
+constexpr size_t kTreeSpans = kCounters;
+constexpr size_t kTreeParts = kTreeSpans + (kTreeGrid * sizeof(TreeSpan) + kAlign - 1) / kAlign * kAlign;
 
 }  // namespace pis
 
@@ -1686,7 +1688,7 @@ size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t
   if (check_cache(cache) != PI_OK || slots < 1 || slots > PI_CACHE_MAX_SLOTS) return 0;
   if (heads < 1 || heads > kMaxHeads || heads % cache->kv_heads || drafts < 1 || drafts > PI_TREE_MAX) return 0;
   const int dv = cache->head_dim <= 64 ? 64 : 128;
-  return kTreeSpans + (size_t)kTreeGrid * 2 * (cache->head_dim > 128 ? 64 : 128) * (dv + 4) * 4;
+  return kTreeParts + (size_t)kTreeGrid * 2 * (cache->head_dim > 128 ? 64 : 128) * (dv + 4) * 4;
 }
 
 }  // extern "C"
@@ -1733,8 +1735,8 @@ static pi_status tree_attention(const pi_cache_desc* cache, int32_t layer, int32
   a.scale = scale * 1.4426950408889634f;
   TreeWork w{};
   w.a = a;
-  w.span = static_cast<TreeSpan*>(ws);
-  w.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTreeSpans);
+  w.span = reinterpret_cast<TreeSpan*>(static_cast<char*>(ws) + kTreeSpans);
+  w.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kTreeParts);
   w.halves = C.head_dim > 128 ? 2 : 1;
   w.limit_ns = lose_ns ? lose_ns : wait_limit();
   w.lose = lose_ns != 0;

@@ -24,7 +24,10 @@ extern "C" {
 
 #define PI_TREE_MAX 64
 
-/* Bytes of workspace of pi_tree_attention; 0 for invalid sizes.  Host-only. */
+/* Bytes of workspace of pi_tree_attention; 0 for invalid sizes.  Host-only.  The
+ * size goes by head_dim alone: a workspace serves any slots, heads and drafts.  One
+ * buffer of the largest size may serve every call of pi_serve.h and of this header
+ * on its stream. */
 size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t heads,
                               int32_t drafts);
 

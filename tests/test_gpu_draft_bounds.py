@@ -9,7 +9,8 @@ import torch
 
 import activation_sparse_decode_rank_gb300 as pi
 import drafthelp as plain
-from test_gpu_draft import DEV, U, Tree, new_status, rounded, run_sample
+from test_gpu_draft import DEV, U, Tree, f32, i32, new_status, rounded, run_sample
+from test_gpu_serve import Cache
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +167,51 @@ def test_sample_small_weights_count_in_a_list(V):
         tok, lp, status = run_sample(row[None], "f32", None, [1000], [top_p], None, [u])
         assert status == 0 and tok[0] == where[1]
         assert abs(lp[0] - want[1]) <= 4 * U * (1 + abs(want[1]))
+
+
+# ------------------------------------------------------------------ workspaces
+@pytest.mark.parametrize("fill", [0, 1])
+def test_one_workspace_for_every_call(fill):
+    # tree attention between calls whose counters lie at the workspace's start
+    tree = [Tree("f16", 8, 2, 128, 16, [9001, 3, 700], None, 3, seed=25),
+            Tree("bf16", 32, 2, 64, 32, [5000], None, 20, append=True, seed=26)]
+    cache = Cache("f16", 8, 2, 64, 16, [6000, 3, 40], seed=27)
+    g = np.random.default_rng(28)
+    V, S = 60000, 3
+    x, tok = f32(g.standard_normal((2, V))), i32([5, V - 1])
+    u = f32(g.random(2))
+    own = [t.ws for t in tree] + [cache.ws, pi.logprob_workspace(2, V, 4, DEV)]
+    ws = torch.zeros(max(w.numel() * w.element_size() for w in own), dtype=torch.uint8, device=DEV)
+    if fill:  # beyond the counters it may hold anything
+        ws[8192:] = 0xff
+
+    def ints(*shape):
+        return torch.full(shape, 77, dtype=torch.int32, device=DEV)
+
+    def calls(shared):
+        out = []
+        for k, t in enumerate(tree + tree[:1]):
+            out += t.run(ws=ws if shared else t.ws)
+            cache.ws = ws if shared else own[2]
+            out += cache.run()
+            lp, ent, idx, top = (torch.zeros(2, device=DEV), torch.zeros(2, device=DEV), ints(2, 4),
+                                 torch.zeros((2, 4), device=DEV))
+            pi.check(pi.pi_token_logprobs(x, "f32", 2, V, V, tok, 4, lp, ent, idx, top, cache.status,
+                                          ws if shared else own[3]), "pi_token_logprobs")
+            drawn = ints(2)
+            pi.check(pi.pi_token_sample(x, "f32", 2, V, V, None, None, None, None, u, drawn, lp, cache.status,
+                                        ws if shared else own[3]), "pi_token_sample")
+            table, length, ref, pairs, counts = (ints(S, cache.mp), ints(S), ints(cache.pages), ints(S, 2),
+                                                 ints(4))
+            pi.check(pi.pi_cache_fork(cache.desc, S, cache.mp, i32([0, 0, 2]), i32([-1, 0, 5]), None, cache.table,
+                                      cache.len, table, length, ref, None, pairs, counts, cache.status,
+                                      ws if shared else own[2]), "pi_cache_fork")
+            out += [lp, ent, idx, top, drawn, table, length, ref, counts[:2]]
+        torch.cuda.synchronize()
+        return out
+    want, got = calls(False), calls(True)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    tree[0].check(*got[:2])
+    cache.check(*got[2:4])
+    assert int(ws[:8192].sum()) == 0
