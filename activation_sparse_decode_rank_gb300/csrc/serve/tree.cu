@@ -446,6 +446,11 @@ __device__ __forceinline__ u64 left2(u64 v, uint32_t r) {
   else h = make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
   return fma2(pair(h.x, h.y), pair(-1.f, -1.f), v);
 }
+// e for which 2^e takes a row's largest |q| into [2^13, 2^14); 126 at most, so that 2^-e is
+// no subnormal, and 0 where it is 0 or not finite.
+__device__ __forceinline__ int query_exponent(float top) {
+  return top > 0.f && top < INFINITY ? 140 - max(14, (int)(__float_as_uint(top) >> 23)) : 0;
+}
 // The rows' values of all lanes joined, N rows: row i's in the lanes 32 i / N and on.
 // Halves of the rows change places as halves of the lanes do.
 template <int N, typename F>
@@ -798,9 +803,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[b][e]));
             top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-            int ex = 140 - (int)(__float_as_uint(top) >> 23);  // the largest into [2^13, 2^14)
-            if (!(top > 0.f && top < INFINITY)) ex = 0;
-            ex = max(-100, min(100, ex));
+            const int ex = query_exponent(top);
             const float f = __uint_as_float((uint32_t)(ex + 127) << 23);
 #pragma unroll
             for (int e = 0; e < E; ++e) x[b][e] *= f;
@@ -1123,9 +1126,7 @@ __global__ void __launch_bounds__(TreeTile<DT, DP, MR>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[b][e]));
           top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-          int ex = 140 - (int)(__float_as_uint(top) >> 23);  // the largest into [2^13, 2^14)
-          if (!(top > 0.f && top < INFINITY)) ex = 0;
-          ex = max(-100, min(100, ex));
+          const int ex = query_exponent(top);
           const float f = __uint_as_float((uint32_t)(ex + 127) << 23);
 #pragma unroll
           for (int e = 0; e < E; ++e) x[b][e] *= f;

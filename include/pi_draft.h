@@ -53,7 +53,8 @@ size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t
  *   type, stored at the drafts' places in `layer`, and attended to as stored.
  *   The pages of those places must be the slot's alone (pi_cache_fork sees to it).
  * Precision, infinite operands, rows that are not visible and timeouts are as
- * in pi_paged_attention.  A page number out of range hides its tokens (drafts
+ * in pi_paged_attention (PI_BF16: rows of q whose elements are all below 2^-110 keep
+ * fewer bits).  A page number out of range hides its tokens (drafts
  * given by k_new are seen, but not stored), a parent out of range counts as -1, a
  * length or count out of range as no drafts; all write PI_ERR_INDEX to
  * *dev_status.  For the same lengths, counts and sizes results are the same bit

@@ -56,6 +56,19 @@ def test_lost_copy_of_a_shared_unit(args, lens, drafts):
     t.check(*t.run())  # the next call is as ever
 
 
+# ------------------------------------------------------------------ queries
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", [(8, 2, 128, 16), (32, 1, 64, 16), (4, 1, 256, 8)])
+@pytest.mark.parametrize("qscale", [2.0 ** -121, 2.0 ** -105, 2.0 ** 108, 2.0 ** 119])
+def test_small_and_large_queries_with_a_scale_to_match(dtype, shape, qscale):
+    # the scores are of the size of any others; bf16's third part would lie below 2^-133
+    if dtype == "bf16" and qscale < 2.0 ** -110:
+        pytest.skip("fewer bits by the header")
+    t = Tree(dtype, *shape, [200, 20], None, 6, qscale=qscale, seed=29)
+    t.scale = float(np.float32(1 / qscale / shape[2] ** 0.5))
+    t.check(*t.run())
+
+
 # ------------------------------------------------------------------ sampling
 def test_sample_more_rows_than_a_grid():
     # past 2^20 rows a block takes several; each row has settings of its own
