@@ -1710,6 +1710,7 @@ static pi_status tree_attention(const pi_cache_desc* cache, int32_t layer, int32
   if (!q || !table || !len || !pool || !y || !dev_status || !ws || !k_new != !v_new) return PI_ERR_NULL;
   if (!all_aligned(parent, count, q, k_new, v_new, table, len, pool, y, lse, dev_status, ws)) return PI_ERR_ALIGN;
   if (ws_bytes < pi_tree_workspace_size(cache, slots, heads, drafts)) return PI_ERR_WORKSPACE;
+  if (y == q) return PI_ERR_SHAPE;  // blocks that share rows read q while others write y
   TreeArgs a{};
   a.q = q;
   a.k_new = k_new;

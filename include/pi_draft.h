@@ -45,8 +45,8 @@ size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t
  *     a_t = scale q[s][i][h] . K[t][g]
  *     y[s][i][h] = sum_V exp(a_t) V[t][g] / sum_V exp(a_t),
  *     lse[s][i][h] = log sum_V exp(a_t).
- *   q [slots][drafts][heads][head_dim] fp32; y the same shape, fp32; lse NULL
- *   or [slots][drafts][heads] fp32.  Rows of drafts from count[s] on are neither
+ *   q [slots][drafts][heads][head_dim] fp32; y the same shape, fp32, in another
+ *   buffer; lse NULL or [slots][drafts][heads] fp32.  Rows of drafts from count[s] on are neither
  *   read nor written.
  *   k_new, v_new: NULL (the drafts' rows are in the cache already), or both
  *   [slots][drafts][kv_heads][head_dim] fp32: rows are rounded to the cache's
