@@ -11,7 +11,7 @@ namespace pis {
 // <= its own, so a thread that copies its piece of the rows in the path's order,
 // reading a batch before writing it, overwrites no row that is still needed.
 // Bound: the moved rows' bytes (64 slots, 48 layers of 8 heads of 128, some 100 rows:
-// 13.3 us, 52 % of a copy's rate; one slot 6.3 us, all of it the call).
+// 13.4 us, 52 % of a copy's rate; one slot 6.1 us, all of it the call).
 struct AcceptArgs {
   const int *parent, *count, *tokens, *choice, *table, *len;
   uint16_t* pool;
@@ -74,7 +74,6 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
   }
   __syncthreads();
   if (!a.pool) return;
-  (void)P;
   // rows that stay where they are come first on the path
   const int steps = s_n;
   int first = 0;

@@ -26,8 +26,9 @@
 // that do not fit are read again from global memory.
 //
 // Bound: instructions, some 50 per logit for its weight and bin, on one block of 1024
-// threads per SM.  Measured: 832 x 50272 fp16 without filters 202 us (memory 12), 64 x
-// 128256 bf16 48 to 60 us, 1 x 50273 fp32 23 to 24 us: a chain of eleven phases of a cluster.
+// threads per SM, which issues in 60 % of its cycles: barriers between the phases take
+// the rest.  Measured: 832 x 50272 fp16 without filters 202 us (memory 12), 64 x 128256 bf16
+// 47 to 60 us, 1 x 50273 fp32 21 to 25 us: a chain of eleven phases of a cluster.
 #include <cooperative_groups.h>
 
 #include "sample_weight.cuh"
@@ -193,12 +194,11 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
     const int top_k = a.top_k ? __ldg(a.top_k + row) : 0;
     const bool good = temp >= 0.f && temp < INFINITY && u >= 0.f && u < 1.f && top_p >= 0.f && min_p >= 0.f &&
                       min_p <= 1.f;
-    // the block's logits [e0, e1): whole aligned vectors but at the row's ends
+    // the block's vectors [v0, v1) of the row: whole and aligned but at the row's ends
     const char* base = static_cast<const char*>(a.logits) + row * a.stride * kSize;
     const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15) / kSize;
     const int nvec = (a.vocab + shift + VN - 1) / VN;
     const int v0 = (int)((long long)rank * nvec / C), v1 = (int)((long long)(rank + 1) * nvec / C);
-    const int e0 = max(0, v0 * VN - shift), e1 = min(a.vocab, v1 * VN - shift);
     const uint4* vecs = reinterpret_cast<const uint4*>(base - shift * kSize);
     // f(logit, index) for each
     auto each = [&](auto f) {
@@ -560,7 +560,9 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_kernel(const __grid_
   cluster.sync();  // no block leaves while another reads its memory
 }
 
-// Blocks of a row's cluster.
+// Blocks of a row's cluster: as many as its logits need, and more while SMs are idle and a
+// block has more than 4096 logits left (1 x 50273 fp32: 25.3 us; from 1024 on 27.1, from
+// 16384 on 27.9).
 static int sample_cluster(int rows, int vocab, int size, int sms, int room) {
   int c = 1;
   while (c < 8 && (long long)vocab * size > (long long)c * (room - 64)) c *= 2;

@@ -195,9 +195,11 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 //   columns, a thread a token; O^T = V^T P^T, P through shared memory.  A tile then
 //   costs 16 instructions of 32 to 96 columns instead of 32 to 48 of 128, and all threads
 //   work whatever the number of rows.
-// 32 slots x 40 heads of 128, 13 drafts (13 rows), lengths to 2048, fp16: 186 us, in the
-// form of many rows 380; 16 slots, 32/8 heads, 26 drafts (104 rows), to 8001, bf16: 110,
-// as four units of 32 rows 267.
+// 32 slots x 40 heads of 128, 13 drafts (13 rows), lengths to 2048, fp16: 183 us, in the
+// form of many rows 380.  The border: 16 slots, 32/8 heads of 128, 8001 tokens at most,
+// fp16 (bf16), with 24 rows 74 us (75) against 87 (108) in the form of many rows, with 32
+// 77 (78) against 85 (109); with 36 rows 87 (107) against 116 (118) as two units of 32, with
+// 64 92 (114) against 123 (124), with 128 114 (137) against 241 (244) as four.
 //
 // A unit is (slot, kv head, MR query rows, up to 128 columns of V).  It goes
 // through tiles of TN tokens: the drafts' own, then those of the cache.  The
@@ -220,10 +222,16 @@ __device__ __forceinline__ void row_add_drafts(const TreeArgs& a, int slot, cons
 // another's store.
 //
 // Bound.  Few rows: HBM, beside a unit's start and end (some 10000 cycles against 2800
-// a tile): 54 % of a copy's rate at 32 slots x 40 heads.  Many rows: the weights'
-// instructions, some 4200 cycles a tile of 128 rows x 128 tokens, against 2200 of the
-// products: 8 slots, 64/8 heads, chains of 64 (512 rows), lengths to 32768, fp16: 493 us,
-// 515 TFLOP/s of the formula's operations, 1.0 PFLOP/s as executed.
+// a tile, in series with them): 55 % of a copy's rate at 32 slots x 40 heads.  Many rows:
+// the softmax warps, some 4200 cycles a tile of 128 rows x 128 tokens against 2200 of the
+// products.  They issue in 38 % of the cycles and wait for tensor memory in most others:
+// 32 columns are loaded and waited for at a time, twice.  8 slots, 64/8 heads, chains of 64
+// (512 rows), lengths to 32768, fp16: 489 us, 520 TFLOP/s of the formula's operations, 1.0
+// PFLOP/s as executed.  With 33 to 64 rows half of those warps have no rows, and head
+// dimensions past 128 compute S and the weights once per half of V's columns.
+// Pages that are no multiple of 8 tokens and head dimensions below 64 have no boxes: all
+// rows by hand, a 16-byte load per thread and piece, 9 times as long (16 slots, 32/8 heads
+// of 128, 13 drafts, 4096 tokens, fp16: 73 us with pages of 16, 76 with 24, 678 with 7).
 //
 // Operands that are not finite.  Rows whose sums come out NaN or infinite are
 // gone through again in fp32, token by token, by the warp that would write them.
@@ -254,12 +262,20 @@ struct TreeTile {  // MR: query rows of a unit
 };
 constexpr int kTreeWarps = 13;   // at most
 constexpr int kTreeGrid = 192;   // most blocks
-// A unit's fixed cost, in tiles: Q, its drafts' rows, its output.  With 1 instead, 32
-// slots x 40 heads, 13 drafts, took 238 us (178), 8 slots, 64/8 heads, chains of 64,
-// 1084 us (467): a slot with nothing before its drafts is all fixed cost.
+// A unit's fixed cost, in tiles: Q, its drafts' rows, its output.  A slot with nothing
+// before its drafts is all fixed cost.  Measured at 32 slots x 40 heads, 13 drafts / 16
+// slots, 32/8 heads, 6 drafts / 32 drafts / 8 slots, 64/8 heads, chains of 64, fp16: 186 /
+// 74 / 114 / 488 us; with 2 for 4 188 / 82 / 110 / 487, with 6 191 / 76 / 116 / 496; drafts / 4
+// for few rows 197, drafts / 8 for many 109 / 536, without the slope 145 / 950.  Rows by hand
+// (odd pages, small heads) cost more than this; they have no rule of their own.
 __host__ __device__ __forceinline__ int tree_cost(int mr, int drafts) { return 4 + (mr <= 32 ? drafts / 8 : drafts / 4); }
-constexpr int kTreeWhole = 6;    // units of at most this many tiles are not split
-constexpr int kTreeShare = 3;    // least share of a block
+// Units of at most this many tiles are not split: one slot, 16 heads, 200 tokens 16.1 us
+// (split 21.4), 64 slots, 32/8 heads, to 600 tokens 70.7 (80.8); with 12 one slot of 700
+// tokens takes 26.6 for 23.6, 24 slots x 16 heads to 1000 tokens 47 for 52.
+constexpr int kTreeWhole = 6;
+// Least share of a block: one slot, 32/8 heads, 2048 tokens 25.3 us; with 1 29.7, with 6
+// 27.6 (700 tokens: 23.6 and 28.7).
+constexpr int kTreeShare = 3;
 constexpr int kTreeHide = 8;     // more than the tiles between the filling of K and the softmax
 
 // `total` positions over `blocks` blocks: the first `more` take one more.

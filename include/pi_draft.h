@@ -103,7 +103,9 @@ pi_status pi_tree_accept(const pi_cache_desc* cache, int32_t slots, int32_t max_
                          const int32_t* len, void* pool, int32_t* len_out, int32_t* path,
                          int32_t* accepted, int32_t* next, int32_t* dev_status, pi_stream stream);
 
-/* Bytes of workspace of pi_token_sample; 0 for invalid sizes.  Host-only. */
+/* Bytes of workspace of pi_token_sample; 0 for invalid sizes.  Host-only.  The call
+ * checks its workspace but does not write it at present: a row's sums stay on the
+ * SMs. */
 size_t pi_sample_workspace_size(int32_t rows, int32_t vocab);
 
 /* Draws a token per row of logits x (layout, dtype and alignment as in
