@@ -46,16 +46,16 @@ size_t pi_tree_workspace_size(const pi_cache_desc* cache, int32_t slots, int32_t
  *     y[s][i][h] = sum_V exp(a_t) V[t][g] / sum_V exp(a_t),
  *     lse[s][i][h] = log sum_V exp(a_t).
  *   q [slots][drafts][heads][head_dim] fp32; y the same shape, fp32, in another
- *   buffer; lse NULL or [slots][drafts][heads] fp32.  Rows of drafts from count[s] on are neither
- *   read nor written.
+ *   buffer; lse NULL or [slots][drafts][heads] fp32.  Rows of drafts from count[s]
+ *   on are neither read nor written.
  *   k_new, v_new: NULL (the drafts' rows are in the cache already), or both
  *   [slots][drafts][kv_heads][head_dim] fp32: rows are rounded to the cache's
  *   type, stored at the drafts' places in `layer`, and attended to as stored.
  *   The pages of those places must be the slot's alone (pi_cache_fork sees to it).
  * Precision, infinite operands, rows that are not visible and timeouts are as
  * in pi_paged_attention (PI_BF16: rows of q whose elements are all below 2^-110 keep
- * fewer bits).  A page number out of range hides its tokens (drafts
- * given by k_new are seen, but not stored), a parent out of range counts as -1, a
+ * fewer bits).  A page number out of range hides its tokens (drafts given by k_new
+ * are seen, but not stored), a parent out of range counts as -1, a
  * length or count out of range as no drafts; all write PI_ERR_INDEX to
  * *dev_status.  For the same lengths, counts and sizes results are the same bit
  * for bit. */
@@ -69,7 +69,7 @@ pi_status pi_tree_attention(const pi_cache_desc* cache, int32_t layer, int32_t s
 
 /* Diagnostic of that call's failure path: pi_tree_attention (scale 1, chains, no
  * window, no new rows) on a cache with head_dim >= 64 and page_tokens a multiple
- * of 8, except that the copy of a box of keys is never ordered, so the waits for it
+ * of 8, except that one more copy of keys is awaited, never ordered, so the waits for it
  * run out after limit_ns nanoseconds (1e3 .. 5e9).  The block lets its copies and
  * products under way end (2 s at most) and leaves, and PI_ERR_TIMEOUT lands in
  * *dev_status; y is not meaningful.  Slot 0 must have a token before its drafts.
@@ -123,8 +123,8 @@ size_t pi_sample_workspace_size(int32_t rows, int32_t vocab);
  * (1), top_k [rows] int32 or NULL, top_p and min_p [rows] fp32 or NULL (off), u
  * [rows] fp32; logprob may be NULL.  Sums are exact to 2^-35 of each weight, whatever
  * the vocabulary: the token is that of exact sums where the draw and the end of what
- * top-p keeps are further than 2^-34 of the sum from the next one's border.  A row whose logits are all -infinity,
- * or hold a NaN or +infinity, gives token -1 and logprob NaN; so does one whose
+ * top-p keeps are further than 2^-34 of the sum from the next one's border.  A row
+ * whose logits are all -infinity, or hold a NaN or +infinity, gives token -1 and logprob NaN; so does one whose
  * temperature is negative, infinite or NaN, whose u is outside [0, 1), or whose
  * top_p or min_p is NaN or negative or min_p above 1; all write PI_ERR_RANGE to
  * *dev_status.  Weights below 2^-64 count as 0, temperatures below 1e-30 as
