@@ -124,11 +124,11 @@ size_t pi_sample_workspace_size(int32_t rows, int32_t vocab);
  * [rows] fp32; logprob may be NULL.  Sums are exact to 2^-35 of each weight, whatever
  * the vocabulary: the token is that of exact sums where the draw and the end of what
  * top-p keeps are further than 2^-34 of the sum from the next one's border.  A row
- * whose logits are all -infinity, or hold a NaN or +infinity, gives token -1 and logprob NaN; so does one whose
- * temperature is negative, infinite or NaN, whose u is outside [0, 1), or whose
- * top_p or min_p is NaN or negative or min_p above 1; all write PI_ERR_RANGE to
- * *dev_status.  Weights below 2^-64 count as 0, temperatures below 1e-30 as
- * 1e-30.  rows >= 0, vocab 1..1 << 24. */
+ * whose logits are all -infinity, or hold a NaN or +infinity, gives token -1 and
+ * logprob NaN; so does one whose temperature is negative, infinite or NaN, whose u is
+ * outside [0, 1), or whose top_p or min_p is NaN or negative or min_p above 1; all
+ * write PI_ERR_RANGE to *dev_status.  Weights below 2^-64 count as 0, temperatures
+ * below 1e-30 as 1e-30.  rows >= 0, vocab 1..1 << 24. */
 pi_status pi_token_sample(const void* logits, int32_t dtype, int32_t rows, int32_t vocab,
                           int64_t stride, const float* temperature, const int32_t* top_k,
                           const float* top_p, const float* min_p, const float* u, int32_t* token,
